@@ -230,6 +230,60 @@ th_status th_prune_layer_alpha_workspace_size(int64_t c, int64_t b, int64_t n, i
 th_status th_gated_ffn_input(const void* X, const void* W_gate, const void* W_up, th_dtype dt,
                              int64_t n, int64_t d, int64_t f, void* Y, th_stream_t stream);
 
+/* Root-mean-square norm of the rows of a residual stream, what the q/k/v and the
+ * gate/up projections of a block read [BLOG, "The compression target: linear
+ * layers"]: Y_tq = X_tq / sqrt(mean_q X_tq^2 + eps) * weight_q. X [n,b] (row pitch
+ * ldx, dtype xdt), weight [b] in xdt, Y [n,b] (row pitch ldy, dtype ydt); sums and
+ * products in fp32, Y rounded once. Y may be X (same dtype and pitch); otherwise
+ * they must not overlap. n = 0 is allowed; n < 2^31, eps >= 0. 16-byte accesses
+ * where b % 8 == 0 and pointers and row pitches are 16-byte multiples, elementwise
+ * otherwise. Asynchronous on the stream. */
+th_status th_rms_norm(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t ldx,
+                      const void* weight, double eps, void* Y, th_dtype ydt, int64_t ldy,
+                      th_stream_t stream);
+
+/* Rotary positions of the queries and keys of n tokens, with an optional norm of
+ * each head in the same pass. Element e of head h of token t is at
+ * x[t * x_token + h * x_head + e] (strides in elements); y likewise. norm: [d]
+ * weights in the same dtype, or NULL for none. y may be x with the same strides;
+ * otherwise they must not overlap. */
+typedef struct {
+  const void* x;
+  void* y;
+  const void* norm;
+  int64_t heads;
+  int64_t x_token, x_head, y_token, y_head;
+} th_heads;
+typedef enum { TH_ROTARY_HALF = 0, TH_ROTARY_INTERLEAVED = 1 } th_rotary_layout;
+
+/* q and k (host structs; k may be NULL): heads of d elements, 1 <= d <= 256, dtype
+ * dt. A head with a norm becomes x / sqrt(mean x^2 + eps) * norm first. Then the
+ * pairs of its first rot elements (even, 0 <= rot <= d), (x_i, x_{i+rot/2}) for
+ * TH_ROTARY_HALF or (x_2i, x_2i+1) for TH_ROTARY_INTERLEAVED, i < rot/2, turn by
+ * the angle positions[t] * freqs[i]: (a, b) -> amplitude (a cos - b sin,
+ * b cos + a sin). The elements past rot keep their (normed) value. positions [n]
+ * int32 (device; any order and sign), or NULL for 0 .. n-1; freqs [rot/2] double
+ * (device), see th_rotary_freqs. Angles are reduced in fp64, the rest is fp32,
+ * outputs rounded once. n = 0 is allowed; n * heads < 2^31. Asynchronous. */
+th_status th_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n, int64_t d,
+                    int64_t rot, th_rotary_layout layout, const int32_t* positions,
+                    const double* freqs, double amplitude, double eps, th_stream_t stream);
+
+/* Frequencies for th_rotary, f_i = base^(-2i/rot) radians a position for i < rot/2,
+ * scaled for long contexts: with by_bands == 0 all of them are divided by `divide`
+ * (1 = unscaled); with by_bands != 0 a pair that makes r = original_length f_i /
+ * (2 pi) turns over the original length keeps its frequency for r >= fast_turns,
+ * has it divided by `divide` for r <= slow_turns, and between them is multiplied by
+ * keep + (1 - keep) / divide, keep = (r - slow_turns) / (fast_turns - slow_turns).
+ * scaling NULL: unscaled with base 10000. freqs: HOST, rot/2 doubles. Host only. */
+typedef struct {
+  double base;
+  double divide;
+  double original_length, slow_turns, fast_turns;
+  int32_t by_bands;
+} th_rotary_scaling;
+th_status th_rotary_freqs(int64_t rot, const th_rotary_scaling* scaling, double* freqs /* host */);
+
 /* Comparator: the column-sequential schedule of SparseGPT on the same Hessian and
  * factor [BLOG, "The scaling problem, and what SparseGPT changes": left to right,
  * every row at once, finished columns frozen, compensation only into active

@@ -17,6 +17,7 @@ TH_F32, TH_BF16 = 0, 1
 TH_UNSTRUCTURED, TH_NM = 0, 1
 TH_SCORE_OBS, TH_SCORE_WANDA = 0, 1
 TH_BASE_MAGNITUDE, TH_BASE_WANDA = 0, 1
+TH_ROTARY_HALF, TH_ROTARY_INTERLEAVED = 0, 1
 STATUS_NAMES = {0: "TH_OK", 1: "TH_ERR_INVALID_ARG", 2: "TH_ERR_NOT_SPD", 3: "TH_ERR_NONFINITE",
                 4: "TH_ERR_WORKSPACE", 5: "TH_ERR_HIP"}
 
@@ -40,6 +41,18 @@ class PruneParams(ctypes.Structure):
 class Stats(ctypes.Structure):
     _fields_ = [("lambda_used", ctypes.c_double), ("total_pruned", ctypes.c_int64),
                 ("nblocks", ctypes.c_int64)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("norm", ctypes.c_void_p),
+                ("heads", ctypes.c_int64), ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64)]
+
+
+class RotaryScaling(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("divide", ctypes.c_double),
+                ("original_length", ctypes.c_double), ("slow_turns", ctypes.c_double),
+                ("fast_turns", ctypes.c_double), ("by_bands", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -69,6 +82,10 @@ _SIG = {
     "th_prune_layer_alpha_workspace_size": [_I64, _I64, _I64, _I32, ctypes.POINTER(PruneParams),
                                             ctypes.c_double, ctypes.POINTER(ctypes.c_size_t)],
     "th_gated_ffn_input": [_P, _P, _P, _I32, _I64, _I64, _I64, _P, _P],
+    "th_rms_norm": [_P, _I32, _I64, _I64, _I64, _P, ctypes.c_double, _P, _I32, _I64, _P],
+    "th_rotary": [ctypes.POINTER(Heads), ctypes.POINTER(Heads), _I32, _I64, _I64, _I64, _I32, _P,
+                  _P, ctypes.c_double, ctypes.c_double, _P],
+    "th_rotary_freqs": [_I64, ctypes.POINTER(RotaryScaling), ctypes.POINTER(ctypes.c_double)],
     "th_prune_sparsegpt": [_P, _I32, _I64, _I64, _P, _I32, _I64, _P, ctypes.POINTER(PruneParams),
                            _P, _P, _P, ctypes.c_size_t, ctypes.POINTER(Stats),
                            ctypes.POINTER(_I64), _P],
@@ -146,6 +163,42 @@ def _require_cuda(*ts):
             raise ValueError("tensors must live on the GPU")
         if t is not None and not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
+
+
+def _require_rows(dev, *ts):
+    """Tensors of the forward steps: on dev, the last dimension contiguous (any outer strides)."""
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must live on the GPU")
+        if t.device != dev:
+            raise ValueError("tensors must live on one GPU")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError("the last dimension must be contiguous")
+
+
+def _require_shape(name, t, shape, dtype=None):
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _pitch(t, dim, dense):
+    """Stride of a dimension; a dimension of one element has its stride replaced by the dense one."""
+    return t.stride(dim) if t.shape[dim] > 1 else dense
+
+
+def _on_device(dev, fn, *args):
+    """Call fn with dev current, on dev's current stream (its last argument)."""
+    torch = _torch()
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _check(fn(*args, _stream(dev)))
+    return _check(fn(*args, _stream(dev)))
 
 
 def make_params(sparsity=0.5, pattern=None, block=128, lam=0.01, relative=True,
@@ -328,6 +381,74 @@ def gated_ffn_input(X, W_gate, W_up, Y=None):
     _check(lib().th_gated_ffn_input(_ptr(X), _ptr(W_gate), _ptr(W_up), _dtype_code(X), n, d, f,
                                     _ptr(Y), _stream(X.device)))
     return Y
+
+
+def rms_norm(X, weight, eps=1e-5, Y=None, out_dtype=None):
+    """Y = X / sqrt(mean(X^2) + eps) * weight by rows, X [n, b]; Y in out_dtype (default X's).
+    Y may be X."""
+    torch = _torch()
+    n, b = X.shape
+    if Y is None:
+        Y = torch.empty((n, b), dtype=out_dtype or X.dtype, device=X.device)
+    _require_rows(X.device, X, weight, Y)
+    _require_shape("weight", weight, (b,), X.dtype)
+    _require_shape("Y", Y, (n, b), out_dtype)
+    _on_device(X.device, lib().th_rms_norm, _ptr(X), _dtype_code(X), n, b, _pitch(X, 0, b),
+               _ptr(weight), float(eps), _ptr(Y), _dtype_code(Y), _pitch(Y, 0, b))
+    return Y
+
+
+def rotary_freqs(rot: int, base=10000.0, divide=1.0, bands=None, device=None):
+    """Frequencies of the rot/2 pairs (float64, rot/2 values, on device) for rotary().
+
+    divide: every frequency is divided by it; with bands = (original_length, slow_turns,
+    fast_turns) only those of pairs that turn slowly over the original length are."""
+    torch = _torch()
+    length, slow, fast = bands if bands is not None else (0.0, 0.0, 0.0)
+    g = RotaryScaling(float(base), float(divide), float(length), float(slow), float(fast),
+                      0 if bands is None else 1)
+    out = (ctypes.c_double * max(rot // 2, 1))()
+    _check(lib().th_rotary_freqs(rot, ctypes.byref(g), out))
+    return torch.tensor(out[:rot // 2], dtype=torch.float64, device=device)
+
+
+_ROTARY_LAYOUTS = {"half": TH_ROTARY_HALF, "interleaved": TH_ROTARY_INTERLEAVED}
+
+
+def _heads(x, y, norm) -> Heads:
+    n, h, d = x.shape
+    return Heads(x.data_ptr(), y.data_ptr(), None if norm is None else norm.data_ptr(), h,
+                 _pitch(x, 0, h * d), _pitch(x, 1, d), _pitch(y, 0, h * d), _pitch(y, 1, d))
+
+
+def rotary(q, k, freqs, positions=None, layout="half", amplitude=1.0, q_norm=None, k_norm=None,
+           eps=1e-6, q_out=None, k_out=None):
+    """Heads q [n, hq, d] and k [n, hk, d] (or None) normed where a weight is given, then their
+    first 2 * len(freqs) elements turned by positions * freqs (positions: int32 [n], default
+    0 .. n-1). Returns (q_out, k_out), which may be q and k themselves."""
+    torch = _torch()
+    n, hq, d = q.shape
+    if q_out is None:
+        q_out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if k is None and (k_out is not None or k_norm is not None):
+        raise ValueError("k_out and k_norm go with k")
+    _require_rows(q.device, q, k, freqs, positions, q_norm, k_norm, q_out, k_out)
+    _require_shape("q_out", q_out, q.shape, q.dtype)
+    _require_shape("freqs", freqs, (freqs.numel(),), torch.float64)
+    _require_shape("positions", positions, (n,), torch.int32)
+    _require_shape("q_norm", q_norm, (d,), q.dtype)
+    kh = None
+    if k is not None:
+        _require_shape("k", k, (n, k.shape[1], d), q.dtype)
+        _require_shape("k_out", k_out, k.shape, q.dtype)
+        _require_shape("k_norm", k_norm, (d,), q.dtype)
+        kh = ctypes.byref(_heads(k, k_out, k_norm))
+    _on_device(q.device, lib().th_rotary, ctypes.byref(_heads(q, q_out, q_norm)), kh,
+               _dtype_code(q), n, d, 2 * freqs.numel(), _ROTARY_LAYOUTS[layout], _ptr(positions),
+               _ptr(freqs), float(amplitude), float(eps))
+    return q_out, k_out
 
 
 def prune_sparsegpt_workspace_size(c, b, n, have_x, params: PruneParams) -> int:

@@ -818,6 +818,101 @@ th_status th_gated_ffn_input(const void* X, const void* W_gate, const void* W_up
   return TH_OK;
 }
 
+// ------------------------------------------------- the block's other forward steps
+
+th_status th_rms_norm(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t ldx,
+                      const void* weight, double eps, void* Y, th_dtype ydt, int64_t ldy,
+                      th_stream_t stream) {
+  if (!dtype_ok(xdt) || !dtype_ok(ydt)) return fail(TH_ERR_INVALID_ARG, "unknown dtype");
+  if (n < 0 || n >= ((int64_t)1 << 31) || b < 1)
+    return fail(TH_ERR_INVALID_ARG, "needs 0 <= n < 2^31 and b >= 1");
+  if (ldx < b || ldy < b) return fail(TH_ERR_INVALID_ARG, "a row pitch is smaller than b");
+  if (!(eps >= 0.0) || !std::isfinite(eps))
+    return fail(TH_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!weight || (n > 0 && (!X || !Y))) return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (X && X == Y && (xdt != ydt || ldx != ldy))
+    return fail(TH_ERR_INVALID_ARG, "in place needs one dtype and pitch");
+  if (n == 0) return TH_OK;
+  TH_HIP(launch_rms_norm(X, xdt, ldx, weight, Y, ydt, ldy, n, b, (float)eps, (hipStream_t)stream),
+         "rms norm");
+  return TH_OK;
+}
+
+th_status th_rotary_freqs(int64_t rot, const th_rotary_scaling* scaling, double* freqs) {
+  if (rot < 0 || rot % 2 || rot > 256)
+    return fail(TH_ERR_INVALID_ARG, "rot must be even, 0 <= rot <= 256");
+  if (rot > 0 && !freqs) return fail(TH_ERR_INVALID_ARG, "freqs is NULL");
+  const th_rotary_scaling plain = {10000.0, 1.0, 0.0, 0.0, 0.0, 0};
+  const th_rotary_scaling& g = scaling ? *scaling : plain;
+  if (!(g.base > 0.0) || !std::isfinite(g.base) || !(g.divide > 0.0) || !std::isfinite(g.divide))
+    return fail(TH_ERR_INVALID_ARG, "base and divide must be finite and > 0");
+  if (g.by_bands && (!(g.original_length > 0.0) || !std::isfinite(g.original_length) ||
+                     !(g.slow_turns >= 0.0) || !(g.fast_turns > g.slow_turns) ||
+                     !std::isfinite(g.fast_turns)))
+    return fail(TH_ERR_INVALID_ARG,
+                "bands need original_length > 0 and 0 <= slow_turns < fast_turns");
+  for (int64_t i = 0; i < rot / 2; ++i) {
+    const double f = std::pow(g.base, -2.0 * (double)i / (double)rot);
+    double keep = 0.0;
+    if (g.by_bands) {
+      const double turns = g.original_length * f / (2.0 * 3.14159265358979323846);
+      keep = (turns - g.slow_turns) / (g.fast_turns - g.slow_turns);
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+    }
+    freqs[i] = f * (keep + (1.0 - keep) / g.divide);
+  }
+  return TH_OK;
+}
+
+namespace {
+th_status check_heads(const th_heads* h, int64_t n, int64_t d, bool* work) {
+  if (h->heads < 0 || h->heads >= ((int64_t)1 << 31))
+    return fail(TH_ERR_INVALID_ARG, "heads must be >= 0");
+  if (h->x_token < 0 || h->x_head < 0 || h->y_token < 0 || h->y_head < 0)
+    return fail(TH_ERR_INVALID_ARG, "negative stride");
+  if (n == 0 || h->heads == 0) return TH_OK;
+  if (!h->x || !h->y) return fail(TH_ERR_INVALID_ARG, "x or y is NULL");
+  // rows of y that share memory would be written twice: whichever stride is the
+  // outer one has to step over the whole inner extent
+  const int64_t inner = h->y_head <= h->y_token || n == 1 ? h->y_head : h->y_token;
+  const int64_t outer = inner == h->y_head ? h->y_token : h->y_head;
+  const int64_t ni = inner == h->y_head ? h->heads : n, no = inner == h->y_head ? n : h->heads;
+  if ((ni > 1 && inner < d) || (no > 1 && outer < (ni - 1) * inner + d))
+    return fail(TH_ERR_INVALID_ARG, "the heads of y overlap");
+  if (h->x == h->y && (h->x_token != h->y_token || h->x_head != h->y_head))
+    return fail(TH_ERR_INVALID_ARG, "in place needs the same strides");
+  *work = true;
+  return TH_OK;
+}
+}  // namespace
+
+th_status th_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n, int64_t d,
+                    int64_t rot, th_rotary_layout layout, const int32_t* positions,
+                    const double* freqs, double amplitude, double eps, th_stream_t stream) {
+  if (!q) return fail(TH_ERR_INVALID_ARG, "q is NULL");
+  if (!dtype_ok(dt)) return fail(TH_ERR_INVALID_ARG, "unknown dtype");
+  if (n < 0 || d < 1 || d > 256) return fail(TH_ERR_INVALID_ARG, "needs n >= 0 and 1 <= d <= 256");
+  if (rot < 0 || rot > d || rot % 2)
+    return fail(TH_ERR_INVALID_ARG, "rot must be even, 0 <= rot <= d");
+  if (layout != TH_ROTARY_HALF && layout != TH_ROTARY_INTERLEAVED)
+    return fail(TH_ERR_INVALID_ARG, "unknown layout");
+  if (rot > 0 && !freqs) return fail(TH_ERR_INVALID_ARG, "freqs is NULL");
+  if (!std::isfinite(amplitude) || !(eps >= 0.0) || !std::isfinite(eps))
+    return fail(TH_ERR_INVALID_ARG, "amplitude must be finite, eps finite and >= 0");
+  bool work = false;
+  th_status st = check_heads(q, n, d, &work);
+  if (st == TH_OK && k) st = check_heads(k, n, d, &work);
+  if (st != TH_OK) return st;
+  if (!work) return TH_OK;
+  const int64_t heads = q->heads + (k ? k->heads : 0);
+  if (n >= (((int64_t)1 << 31) + heads - 1) / heads)
+    return fail(TH_ERR_INVALID_ARG, "n * heads must be < 2^31");
+  TH_HIP(launch_rotary(q, k, dt, n, d, rot, layout == TH_ROTARY_INTERLEAVED, positions, freqs,
+                       (float)amplitude, (float)eps, (hipStream_t)stream),
+         "rotary");
+  return TH_OK;
+}
+
 th_status th_reconstruction_error_workspace_size(int64_t c, int64_t b, int32_t have_x,
                                                  size_t* bytes) {
   if (!bytes || c < 1 || b < 1) return fail(TH_ERR_INVALID_ARG, "bad arguments");

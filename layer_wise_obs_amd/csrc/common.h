@@ -229,6 +229,16 @@ hipError_t launch_gated_ffn(const unsigned short* X, const unsigned short* Wg,
                             const unsigned short* Wu, unsigned short* Y, int64_t n, int64_t d,
                             int64_t f, hipStream_t s);
 
+// norm.hip
+hipError_t launch_rms_norm(const void* X, th_dtype xdt, int64_t ldx, const void* w, void* Y,
+                           th_dtype ydt, int64_t ldy, int64_t n, int64_t b, float eps,
+                           hipStream_t s);
+
+// rotary.hip
+hipError_t launch_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n, int64_t d,
+                         int64_t rot, int interleaved, const int32_t* positions,
+                         const double* freqs, float amplitude, float eps, hipStream_t s);
+
 // rows.hip
 hipError_t launch_row_energy(const void* W, th_dtype wdt, int64_t c, int64_t b, const float* g,
                              float* s, hipStream_t st);

@@ -6,3 +6,4 @@ the benchmark use it. It shares no code with the HIP library and does not import
 it.
 """
 from .thanos_oracle import *  # noqa: F401,F403
+from .forward import *  # noqa: F401,F403

@@ -1,0 +1,113 @@
+"""Argument checks of the block's forward steps (row norm, rotary positions), answered
+before anything touches the GPU, and the host-side frequencies of the rotation."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from layer_wise_obs_amd import _lib as L
+
+FAKE = 0x100000  # never dereferenced: every call below fails its checks first
+NAN, INF = float("nan"), float("inf")
+
+
+def _norm_args(**kw):
+    a = dict(X=FAKE, xdt=L.TH_BF16, n=4, b=64, ldx=64, w=FAKE, eps=1e-5, Y=2 * FAKE,
+             ydt=L.TH_BF16, ldy=64)
+    a.update(kw)
+    return list(a.values()) + [None]
+
+
+@pytest.mark.parametrize("bad", [
+    dict(X=None), dict(Y=None), dict(w=None), dict(xdt=2), dict(ydt=-1), dict(n=-1),
+    dict(n=1 << 31), dict(b=0), dict(ldx=63), dict(ldy=63), dict(eps=-1.0), dict(eps=NAN),
+    dict(eps=INF), dict(Y=FAKE, ydt=L.TH_F32), dict(Y=FAKE, ldy=128)])
+def test_rms_norm_refuses(bad):
+    assert L.lib().th_rms_norm(*_norm_args(**bad)) == L.TH_ERR_INVALID_ARG
+
+
+def test_no_rows_is_no_work():
+    assert L.lib().th_rms_norm(*_norm_args(n=0, X=None, Y=None)) == L.TH_OK
+    h = _heads(x=None, y=None)
+    assert L.lib().th_rotary(*_rotary_args(q=h, k=None, n=0)) == L.TH_OK
+    h = _heads(x=None, y=None, heads=0)
+    assert L.lib().th_rotary(*_rotary_args(q=h, k=h)) == L.TH_OK
+
+
+def _heads(**kw):
+    a = dict(x=FAKE, y=2 * FAKE, norm=None, heads=4, x_token=512, x_head=128, y_token=512,
+             y_head=128)
+    a.update(kw)
+    return L.Heads(*a.values())
+
+
+def _rotary_args(**kw):
+    a = dict(q=_heads(), k=_heads(heads=2), dt=L.TH_BF16, n=3, d=128, rot=128, layout=0,
+             pos=None, freqs=FAKE, amp=1.0, eps=1e-6)
+    a.update(kw)
+    a["q"] = None if a["q"] is None else ctypes.byref(a["q"])
+    a["k"] = None if a["k"] is None else ctypes.byref(a["k"])
+    return list(a.values()) + [None]
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=None), dict(dt=5), dict(n=-1), dict(n=(1 << 31) // 6 + 1), dict(d=0), dict(d=257),
+    dict(rot=127), dict(rot=130), dict(rot=-2), dict(layout=2), dict(freqs=None), dict(amp=NAN),
+    dict(eps=-1e-6), dict(eps=INF), dict(q=_heads(x=None)), dict(k=_heads(y=None)),
+    dict(q=_heads(heads=-1)), dict(q=_heads(x_head=-128)),
+    dict(q=_heads(y_head=127)), dict(q=_heads(y_token=511)), dict(k=_heads(y_token=0)),
+    dict(q=_heads(y=FAKE, y_token=1024))])
+def test_rotary_refuses(bad):
+    assert L.lib().th_rotary(*_rotary_args(**bad)) == L.TH_ERR_INVALID_ARG
+
+
+def test_head_major_outputs_are_not_refused_as_overlapping():
+    """y as [heads, n, d] (a cache's layout): the checks pass up to the dtype one."""
+    h = _heads(y_token=128, y_head=3 * 128)
+    assert L.lib().th_rotary(*_rotary_args(q=h, k=None, d=128, n=0)) == L.TH_OK
+    h = _heads(y_token=128, y_head=3 * 128 - 1)
+    assert L.lib().th_rotary(*_rotary_args(q=h, k=None)) == L.TH_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("rot,kw", [
+    (128, {}), (2, {}), (0, {}), (64, dict(base=500000.0)), (96, dict(divide=4.0)),
+    (128, dict(base=500000.0, divide=8.0, bands=(8192, 1.0, 4.0))),
+    (250, dict(divide=32.0, bands=(2048, 0.0, 2.5)))])
+def test_rotary_freqs_match_the_definition(rot, kw):
+    """Three roundings of fp64 and the power's own (below 4 units) at most."""
+    got = L.rotary_freqs(rot, **kw).numpy()
+    ref = O.rotary_freqs(rot, **kw)
+    assert got.shape == ref.shape == (rot // 2,)
+    assert np.all(np.abs(got - ref) <= 16 * np.finfo(np.float64).eps * ref)
+
+
+def test_rotary_freqs_bands_keep_fast_pairs_and_divide_slow_ones():
+    f = L.rotary_freqs(128, base=500000.0).numpy()
+    g = L.rotary_freqs(128, base=500000.0, divide=8.0, bands=(8192, 1.0, 4.0)).numpy()
+    turns = 8192 * f / (2 * math.pi)
+    assert (turns >= 4).any() and (turns <= 1).any() and ((turns > 1) & (turns < 4)).any()
+    assert np.array_equal(g[turns >= 4], f[turns >= 4])
+    assert np.array_equal(g[turns <= 1], f[turns <= 1] / 8.0)
+    mid = (turns > 1) & (turns < 4)
+    assert np.all((g[mid] < f[mid]) & (g[mid] > f[mid] / 8.0))
+
+
+@pytest.mark.parametrize("rot,kw", [
+    (3, {}), (258, {}), (-2, {}), (8, dict(base=0.0)), (8, dict(base=INF)), (8, dict(divide=0.0)),
+    (8, dict(divide=NAN)), (8, dict(bands=(0.0, 1.0, 4.0))), (8, dict(bands=(2048, 4.0, 4.0))),
+    (8, dict(bands=(2048, -1.0, 4.0))), (8, dict(bands=(NAN, 1.0, 4.0)))])
+def test_rotary_freqs_refuses(rot, kw):
+    with pytest.raises(L.ThanosError) as e:
+        L.rotary_freqs(rot, **kw)
+    assert e.value.status == L.TH_ERR_INVALID_ARG
+
+
+def test_binding_refuses_cpu_tensors():
+    x, w = torch.zeros(2, 8), torch.zeros(8)
+    with pytest.raises(ValueError):
+        L.rms_norm(x, w)
+    with pytest.raises(ValueError):
+        L.rotary(torch.zeros(2, 1, 8), None, torch.zeros(4, dtype=torch.float64))
