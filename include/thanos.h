@@ -230,6 +230,26 @@ th_status th_prune_layer_alpha_workspace_size(int64_t c, int64_t b, int64_t n, i
 th_status th_gated_ffn_input(const void* X, const void* W_gate, const void* W_up, th_dtype dt,
                              int64_t n, int64_t d, int64_t f, void* Y, th_stream_t stream);
 
+/* Linear layer with its epilogue: Y = act(X W^T + bias) + residual, what a block's
+ * (pruned) projections hand to the next layer [BLOG, "The compression target:
+ * linear layers"; "The layer-reconstruction lens"]. X [n,b] token-major (row pitch
+ * ldx), W [c,b], bias [c] or NULL, all bf16 (dt must be TH_BF16); residual [n,c]
+ * (row pitch ldr) or NULL and Y [n,c] (row pitch ldy) in ydt (bf16 or fp32).
+ * Products on the bf16 matrix cores with fp32 sums, epilogue in fp32, Y rounded
+ * once. gelu(z) = z Phi(z), with the error function; silu(z) = z / (1 + e^-z). Y may
+ * be the residual (same pitch); it must not overlap X, W or bias. Needs
+ * b % 8 == 0, b >= 8, ldx % 8 == 0, b and ldx < 2^22, and 16-byte aligned X and W;
+ * n = 0 is allowed. workspace (optional, may be NULL with workspace_bytes 0;
+ * 16-byte aligned) lets launches of few tiles split the contraction; size from
+ * th_linear_workspace_size (0 where it does not help). The pieces are summed in a
+ * fixed order, so repeated calls give identical bits. Asynchronous. */
+typedef enum { TH_ACT_NONE = 0, TH_ACT_RELU = 1, TH_ACT_SILU = 2, TH_ACT_GELU = 3 } th_activation;
+th_status th_linear_workspace_size(int64_t n, int64_t b, int64_t c, size_t* bytes /* host */);
+th_status th_linear(const void* X, int64_t ldx, const void* W, th_dtype dt, int64_t n, int64_t b,
+                    int64_t c, const void* bias, th_activation act, const void* residual,
+                    int64_t ldr, void* Y, th_dtype ydt, int64_t ldy, void* workspace,
+                    size_t workspace_bytes, th_stream_t stream);
+
 /* Root-mean-square norm of the rows of a residual stream, what the q/k/v and the
  * gate/up projections of a block read [BLOG, "The compression target: linear
  * layers"]: Y_tq = X_tq / sqrt(mean_q X_tq^2 + eps) * weight_q. X [n,b] (row pitch

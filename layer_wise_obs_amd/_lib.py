@@ -17,6 +17,7 @@ TH_F32, TH_BF16 = 0, 1
 TH_UNSTRUCTURED, TH_NM = 0, 1
 TH_SCORE_OBS, TH_SCORE_WANDA = 0, 1
 TH_BASE_MAGNITUDE, TH_BASE_WANDA = 0, 1
+TH_ACT_NONE, TH_ACT_RELU, TH_ACT_SILU, TH_ACT_GELU = range(4)
 TH_ROTARY_HALF, TH_ROTARY_INTERLEAVED = 0, 1
 STATUS_NAMES = {0: "TH_OK", 1: "TH_ERR_INVALID_ARG", 2: "TH_ERR_NOT_SPD", 3: "TH_ERR_NONFINITE",
                 4: "TH_ERR_WORKSPACE", 5: "TH_ERR_HIP"}
@@ -82,6 +83,9 @@ _SIG = {
     "th_prune_layer_alpha_workspace_size": [_I64, _I64, _I64, _I32, ctypes.POINTER(PruneParams),
                                             ctypes.c_double, ctypes.POINTER(ctypes.c_size_t)],
     "th_gated_ffn_input": [_P, _P, _P, _I32, _I64, _I64, _I64, _P, _P],
+    "th_linear_workspace_size": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "th_linear": [_P, _I64, _P, _I32, _I64, _I64, _I64, _P, _I32, _P, _I64, _P, _I32, _I64, _P,
+                  ctypes.c_size_t, _P],
     "th_rms_norm": [_P, _I32, _I64, _I64, _I64, _P, ctypes.c_double, _P, _I32, _I64, _P],
     "th_rotary": [ctypes.POINTER(Heads), ctypes.POINTER(Heads), _I32, _I64, _I64, _I64, _I32, _P,
                   _P, ctypes.c_double, ctypes.c_double, _P],
@@ -380,6 +384,45 @@ def gated_ffn_input(X, W_gate, W_up, Y=None):
         Y = torch.empty((n, f), dtype=torch.bfloat16, device=X.device)
     _check(lib().th_gated_ffn_input(_ptr(X), _ptr(W_gate), _ptr(W_up), _dtype_code(X), n, d, f,
                                     _ptr(Y), _stream(X.device)))
+    return Y
+
+
+def linear_workspace_size(n: int, b: int, c: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().th_linear_workspace_size(n, b, c, ctypes.byref(out)))
+    return out.value
+
+
+_ACTIVATIONS = {"none": TH_ACT_NONE, "relu": TH_ACT_RELU, "silu": TH_ACT_SILU,
+                "gelu": TH_ACT_GELU}
+
+
+def linear(X, W, bias=None, act="none", residual=None, Y=None, out_dtype=None, ws=None):
+    """Y = act(X W^T + bias) + residual for X [n, b], W [c, b] and bias [c] (bf16); residual and
+    Y [n, c] in out_dtype (bf16 or fp32, default X's). Y may be the residual."""
+    torch = _torch()
+    n, b = X.shape
+    c = W.shape[0]
+    dev = X.device
+    if Y is None:
+        if out_dtype is None:
+            out_dtype = X.dtype if residual is None else residual.dtype
+        Y = torch.empty((n, c), dtype=out_dtype, device=dev)
+    _require_rows(dev, X, bias, residual, Y, ws)
+    _require_cuda(W)
+    _require_shape("W", W, (c, b), X.dtype)
+    _require_shape("bias", bias, (c,), X.dtype)
+    _require_shape("Y", Y, (n, c), out_dtype)
+    _require_shape("residual", residual, (n, c), Y.dtype)
+    if W.device != dev:
+        raise ValueError("tensors must live on one GPU")
+    if ws is None:
+        nbytes = linear_workspace_size(n, b, c)
+        ws = workspace(nbytes, dev) if nbytes else None
+    _on_device(dev, lib().th_linear, _ptr(X), _pitch(X, 0, b), _ptr(W), _dtype_code(X), n, b, c,
+               _ptr(bias), _ACTIVATIONS[act], _ptr(residual),
+               0 if residual is None else _pitch(residual, 0, c), _ptr(Y), _dtype_code(Y),
+               _pitch(Y, 0, c), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
     return Y
 
 

@@ -820,6 +820,56 @@ th_status th_gated_ffn_input(const void* X, const void* W_gate, const void* W_up
 
 // ------------------------------------------------- the block's other forward steps
 
+namespace {
+th_status check_linear_sizes(int64_t n, int64_t b, int64_t c) {
+  if (n < 0 || c < 1 || b < 8 || b % 8)
+    return fail(TH_ERR_INVALID_ARG, "needs n >= 0, c >= 1, b >= 8 and b % 8 == 0");
+  if (b >= ((int64_t)1 << 22)) return fail(TH_ERR_INVALID_ARG, "b must be < 2^22");
+  if (n >= ((int64_t)1 << 38) || c >= ((int64_t)1 << 31) ||
+      cdiv(n, 128) * cdiv(c, 128) >= ((int64_t)1 << 30))
+    return fail(TH_ERR_INVALID_ARG, "n * c too large for one launch");
+  return TH_OK;
+}
+}  // namespace
+
+th_status th_linear_workspace_size(int64_t n, int64_t b, int64_t c, size_t* bytes) {
+  if (!bytes) return fail(TH_ERR_INVALID_ARG, "bytes is NULL");
+  th_status st = check_linear_sizes(n, b, c);
+  if (st != TH_OK) return st;
+  *bytes = n == 0 ? 0 : linear_workspace_floats(n, b, c) * sizeof(float);
+  return TH_OK;
+}
+
+th_status th_linear(const void* X, int64_t ldx, const void* W, th_dtype dt, int64_t n, int64_t b,
+                    int64_t c, const void* bias, th_activation act, const void* residual,
+                    int64_t ldr, void* Y, th_dtype ydt, int64_t ldy, void* workspace,
+                    size_t workspace_bytes, th_stream_t stream) {
+  if (dt != TH_BF16) return fail(TH_ERR_INVALID_ARG, "X and W: bf16 only");
+  if (!dtype_ok(ydt)) return fail(TH_ERR_INVALID_ARG, "unknown dtype");
+  th_status st = check_linear_sizes(n, b, c);
+  if (st != TH_OK) return st;
+  if (act < TH_ACT_NONE || act > TH_ACT_GELU) return fail(TH_ERR_INVALID_ARG, "unknown activation");
+  if (ldx < b || ldx % 8 || ldx >= ((int64_t)1 << 22))
+    return fail(TH_ERR_INVALID_ARG, "needs b <= ldx < 2^22 and ldx % 8 == 0");
+  if (ldy < c || (residual && ldr < c))
+    return fail(TH_ERR_INVALID_ARG, "a row pitch is smaller than c");
+  if (!W || (n > 0 && (!X || !Y))) return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (((uintptr_t)X | (uintptr_t)W) & 15)
+    return fail(TH_ERR_INVALID_ARG, "X and W must be 16-byte aligned");
+  if (Y && Y == residual && ldr != ldy)
+    return fail(TH_ERR_INVALID_ARG, "a residual in place needs Y's pitch");
+  if (workspace && ((uintptr_t)workspace & 15))
+    return fail(TH_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  if (n == 0) return TH_OK;
+  const size_t need = linear_workspace_floats(n, b, c) * sizeof(float);
+  if (workspace && workspace_bytes < need) return fail(TH_ERR_WORKSPACE, "workspace too small");
+  TH_HIP(launch_linear((const unsigned short*)X, ldx, (const unsigned short*)W, n, b, c,
+                       (const unsigned short*)bias, act, residual, ldr, Y, ydt, ldy,
+                       (float*)workspace, (hipStream_t)stream),
+         "linear");
+  return TH_OK;
+}
+
 th_status th_rms_norm(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t ldx,
                       const void* weight, double eps, void* Y, th_dtype ydt, int64_t ldy,
                       th_stream_t stream) {

@@ -229,6 +229,14 @@ hipError_t launch_gated_ffn(const unsigned short* X, const unsigned short* Wg,
                             const unsigned short* Wu, unsigned short* Y, int64_t n, int64_t d,
                             int64_t f, hipStream_t s);
 
+// linear.hip
+// workspace (floats) of the split contraction: 0 where it does not help
+size_t linear_workspace_floats(int64_t n, int64_t b, int64_t c);
+hipError_t launch_linear(const unsigned short* X, int64_t ldx, const unsigned short* W, int64_t n,
+                         int64_t b, int64_t c, const unsigned short* bias, int act,
+                         const void* residual, int64_t ldr, void* Y, th_dtype ydt, int64_t ldy,
+                         float* part, hipStream_t s);
+
 // norm.hip
 hipError_t launch_rms_norm(const void* X, th_dtype xdt, int64_t ldx, const void* w, void* Y,
                            th_dtype ydt, int64_t ldy, int64_t n, int64_t b, float eps,

@@ -1,4 +1,4 @@
-"""Argument checks of the block's forward steps (row norm, rotary positions), answered
+"""Argument checks of the block's forward steps (linear, row norm, rotary positions), answered
 before anything touches the GPU, and the host-side frequencies of the rotation."""
 import ctypes
 import math
@@ -29,7 +29,39 @@ def test_rms_norm_refuses(bad):
     assert L.lib().th_rms_norm(*_norm_args(**bad)) == L.TH_ERR_INVALID_ARG
 
 
+def _linear_args(**kw):
+    a = dict(X=FAKE, ldx=64, W=2 * FAKE, dt=L.TH_BF16, n=4, b=64, c=32, bias=None, act=0,
+             residual=None, ldr=0, Y=3 * FAKE, ydt=L.TH_BF16, ldy=32, ws=None, ws_bytes=0)
+    a.update(kw)
+    return list(a.values()) + [None]
+
+
+@pytest.mark.parametrize("bad", [
+    dict(X=None), dict(W=None), dict(Y=None), dict(dt=L.TH_F32), dict(dt=9), dict(ydt=3),
+    dict(n=-1), dict(b=0), dict(b=4, ldx=8), dict(b=60), dict(b=1 << 22, ldx=1 << 22), dict(c=0),
+    dict(ldx=56), dict(ldx=68), dict(ldx=1 << 22), dict(ldy=31), dict(act=4), dict(act=-1),
+    dict(X=FAKE + 8), dict(W=FAKE + 2), dict(residual=FAKE, ldr=31), dict(n=1 << 37),
+    dict(n=1 << 38, c=1, ldy=1), dict(c=1 << 31, ldy=1 << 31),
+    dict(residual=3 * FAKE, ldr=64), dict(ws=FAKE + 4, ws_bytes=1 << 20)])
+def test_linear_refuses(bad):
+    assert L.lib().th_linear(*_linear_args(**bad)) == L.TH_ERR_INVALID_ARG
+
+
+def test_linear_workspace_query():
+    lib, out = L.lib(), ctypes.c_size_t(0)
+    for n, b, c in ((-1, 64, 8), (4, 60, 8), (4, 64, 0), (4, 0, 8)):
+        assert lib.th_linear_workspace_size(n, b, c, ctypes.byref(out)) == L.TH_ERR_INVALID_ARG
+    assert lib.th_linear_workspace_size(4, 64, 8, None) == L.TH_ERR_INVALID_ARG
+    assert L.linear_workspace_size(0, 4096, 4096) == 0
+    assert L.linear_workspace_size(131072, 4096, 4096) == 0  # enough tiles: nothing is split
+    need = L.linear_workspace_size(777, 2056, 1023)
+    assert need > 0 and need % (777 * 1023 * 4) == 0
+    a = dict(n=777, b=2056, ldx=2056, c=1023, ldy=1023, ws=FAKE)
+    assert lib.th_linear(*_linear_args(ws_bytes=need - 1, **a)) == L.TH_ERR_WORKSPACE
+
+
 def test_no_rows_is_no_work():
+    assert L.lib().th_linear(*_linear_args(n=0, X=None, Y=None)) == L.TH_OK
     assert L.lib().th_rms_norm(*_norm_args(n=0, X=None, Y=None)) == L.TH_OK
     h = _heads(x=None, y=None)
     assert L.lib().th_rotary(*_rotary_args(q=h, k=None, n=0)) == L.TH_OK
