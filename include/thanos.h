@@ -304,6 +304,45 @@ typedef struct {
 } th_rotary_scaling;
 th_status th_rotary_freqs(int64_t rot, const th_rotary_scaling* scaling, double* freqs /* host */);
 
+/* Attention over packed sequences, what o_proj reads [BLOG, "The compression target:
+ * linear layers"; "The layer-reconstruction lens"]: per query and head
+ * O = softmax(scale Q K^T) V over the visible keys. Element e of head h of row t of
+ * Q is at Q[t * q_token + h * q_head + e] (strides in elements); K, V and O alike.
+ * Query head h reads key head h / (hq / hk).
+ *   Sequence s owns rows q_start[s] .. q_start[s+1]-1 of Q and O and rows
+ *   k_start[s] .. k_start[s+1]-1 of K and V (nseq + 1 ascending int32, device).
+ *   k_start NULL: the same as q_start. q_start NULL (then k_start NULL, nseq 1):
+ *   all rows are one sequence. With causal != 0 the last query of a sequence sees
+ *   its last key, the one before it one key fewer, and so on (a sequence may have
+ *   more keys than queries: single tokens over a cache; or fewer: its first queries
+ *   see none). Lengths of 0 are allowed.
+ * A query that sees no key gets zeros. What hidden keys and values hold never enters,
+ * infinities and NaN included. Rows of O before q_start[0] or from q_start[nseq] on
+ * are left as they are. Start values outside the tensors are moved to their ends, so
+ * a bad one never reads or writes outside them; where starts do not ascend, the rows
+ * concerned are unspecified. */
+typedef struct {
+  int64_t nq, nk;     /* rows of Q and O; rows of K and V */
+  int64_t hq, hk, d;  /* heads of Q and O; of K and V; elements per head */
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+  int64_t nseq;
+  int32_t causal;
+  double scale;       /* > 0, typically 1 / sqrt(d) */
+} th_attention_params;
+
+/* dt must be TH_BF16; 8 <= d <= 128, d % 8 == 0; hk divides hq; strides are multiples
+ * of 8 and Q, K, V, O 16-byte aligned; nq * hq / hk, nk < 2^31 - 2^16. O must not
+ * overlap the inputs. Scores, maxima, sums and O accumulate in fp32; the weights
+ * enter the second product rounded to bf16. workspace (optional, may be NULL with
+ * workspace_bytes 0; 16-byte aligned) lets launches of few queries split the keys;
+ * size from th_attention_workspace_size (0 where it does not help). The order of all
+ * sums is fixed, so repeated calls give identical bits. Asynchronous. */
+th_status th_attention_workspace_size(const th_attention_params* p, size_t* bytes /* host */);
+th_status th_attention(const void* Q, const void* K, const void* V, th_dtype dt,
+                       const int32_t* q_start, const int32_t* k_start,
+                       const th_attention_params* p, void* O, void* workspace,
+                       size_t workspace_bytes, th_stream_t stream);
+
 /* Comparator: the column-sequential schedule of SparseGPT on the same Hessian and
  * factor [BLOG, "The scaling problem, and what SparseGPT changes": left to right,
  * every row at once, finished columns frozen, compensation only into active

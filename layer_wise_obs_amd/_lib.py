@@ -56,6 +56,12 @@ class RotaryScaling(ctypes.Structure):
                 ("fast_turns", ctypes.c_double), ("by_bands", ctypes.c_int32)]
 
 
+class AttentionParams(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in (
+        "nq", "nk", "hq", "hk", "d", "q_token", "q_head", "k_token", "k_head", "v_token", "v_head",
+        "o_token", "o_head", "nseq")] + [("causal", ctypes.c_int32), ("scale", ctypes.c_double)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -90,6 +96,10 @@ _SIG = {
     "th_rotary": [ctypes.POINTER(Heads), ctypes.POINTER(Heads), _I32, _I64, _I64, _I64, _I32, _P,
                   _P, ctypes.c_double, ctypes.c_double, _P],
     "th_rotary_freqs": [_I64, ctypes.POINTER(RotaryScaling), ctypes.POINTER(ctypes.c_double)],
+    "th_attention_workspace_size": [ctypes.POINTER(AttentionParams),
+                                    ctypes.POINTER(ctypes.c_size_t)],
+    "th_attention": [_P, _P, _P, _I32, _P, _P, ctypes.POINTER(AttentionParams), _P, _P,
+                     ctypes.c_size_t, _P],
     "th_prune_sparsegpt": [_P, _I32, _I64, _I64, _P, _I32, _I64, _P, ctypes.POINTER(PruneParams),
                            _P, _P, _P, ctypes.c_size_t, ctypes.POINTER(Stats),
                            ctypes.POINTER(_I64), _P],
@@ -492,6 +502,47 @@ def rotary(q, k, freqs, positions=None, layout="half", amplitude=1.0, q_norm=Non
                _dtype_code(q), n, d, 2 * freqs.numel(), _ROTARY_LAYOUTS[layout], _ptr(positions),
                _ptr(freqs), float(amplitude), float(eps))
     return q_out, k_out
+
+
+def attention_workspace_size(params: AttentionParams) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().th_attention_workspace_size(ctypes.byref(params), ctypes.byref(out)))
+    return out.value
+
+
+def attention(Q, K, V, q_start=None, k_start=None, causal=True, scale=None, O=None, ws=None):
+    """O = softmax(scale Q K^T) V for Q [nq, hq, d], K and V [nk, hk, d] (bf16) of sequences packed
+    along the rows: q_start and k_start int32 [nseq + 1] on the GPU (k_start defaults to q_start;
+    without q_start all rows are one sequence). scale defaults to 1 / sqrt(d)."""
+    torch = _torch()
+    nq, hq, d = Q.shape
+    nk, hk, _ = K.shape
+    dev = Q.device
+    if O is None:
+        # rows that belong to no sequence are not written
+        O = torch.empty((nq, hq, d), dtype=Q.dtype, device=dev)
+    _require_rows(dev, Q, K, V, O, q_start, k_start, ws)
+    _require_shape("K", K, (nk, hk, d), Q.dtype)
+    _require_shape("V", V, (nk, hk, d), Q.dtype)
+    _require_shape("O", O, (nq, hq, d), Q.dtype)
+    nseq = 1
+    if q_start is not None:
+        nseq = q_start.numel() - 1
+        _require_shape("q_start", q_start, (nseq + 1,), torch.int32)
+        _require_shape("k_start", k_start, (nseq + 1,), torch.int32)
+    elif k_start is not None:
+        raise ValueError("k_start goes with q_start")
+    p = AttentionParams(nq, nk, hq, hk, d, _pitch(Q, 0, hq * d), _pitch(Q, 1, d),
+                        _pitch(K, 0, hk * d), _pitch(K, 1, d), _pitch(V, 0, hk * d),
+                        _pitch(V, 1, d), _pitch(O, 0, hq * d), _pitch(O, 1, d), nseq,
+                        1 if causal else 0, d ** -0.5 if scale is None else float(scale))
+    if ws is None:
+        nbytes = attention_workspace_size(p)
+        ws = workspace(nbytes, dev) if nbytes else None
+    _on_device(dev, lib().th_attention, _ptr(Q), _ptr(K), _ptr(V), _dtype_code(Q), _ptr(q_start),
+               _ptr(k_start), ctypes.byref(p), _ptr(O), _ptr(ws),
+               0 if ws is None else ws.numel() * ws.element_size())
+    return O
 
 
 def prune_sparsegpt_workspace_size(c, b, n, have_x, params: PruneParams) -> int:

@@ -1,0 +1,461 @@
+// Attention over packed sequences, O = softmax(scale Q K^T + mask) V, grouped heads
+// (g = hq / hk query heads read one key head), causal to the end of the keys: the
+// last query of a sequence sees its last key. What o_proj reads in a block whose
+// q/k/v projections are pruned ("Pruning LLMs with Thanos", sections "The
+// layer-reconstruction lens" and "The compression target: linear layers").
+//
+// One pass over the keys with a running reference m and sum l per query,
+//   p_j = 2^(c s_j - m),  l += p_j,  O += p_j v_j,  c = scale log2(e),
+// rescaled by 2^(m_old - m_new) when m moves. m only has to be near the maximum:
+// it moves when a score passes it by more than 8 (p <= 2^8 then), so most tiles
+// need no rescaling. m, l and O are fp32; p is rounded to bf16 for the matrix cores
+// (off by at most 2^-8 of itself, like the output's own rounding; fp32 weights would
+// need three times the matrix work).
+//
+// A workgroup takes 128 rows of one sequence and key head, a row being a (token,
+// query head of the group) pair, so K and V are read once for all g heads and
+// single tokens fill g rows. Each of the four waves owns 32 rows. The products are
+// formed transposed, S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_32x32x16_bf16:
+// a lane then holds scores of one query only (its softmax needs one exchange with
+// the other half wave), and its P values already are the operand of the second
+// product -- the contraction order over keys is free, so V's transposing LDS reads
+// (ds_read_b64_tr_b16, 4 keys each) follow the order P has in the registers.
+// Tiles of 64 keys are copied into LDS by direct loads, double-buffered; the 16-byte
+// pieces of a row are XOR-swizzled so that both kinds of operand reads use all banks.
+//
+// Where there are few workgroups, the keys of each are split over several; the
+// partial (m, l, O) are joined by a second kernel in a fixed order.
+#include "common.h"
+#include "lds_dma.h"
+
+namespace th {
+
+namespace {
+
+constexpr int kAThreads = 256;
+constexpr int kABM = 128;  // rows per workgroup
+constexpr int kAKT = 64;   // keys per tile
+constexpr float kAMove = 8.0f;  // log2 of how far p may pass 1 before m moves
+
+typedef short v4i16_t __attribute__((ext_vector_type(4)));
+typedef short v8i16_t __attribute__((ext_vector_type(8)));
+typedef unsigned short u16x4_t __attribute__((ext_vector_type(4)));
+
+struct AttnArgs {
+  const unsigned short *q, *k, *v;
+  unsigned short* o;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+  const int32_t *q_start, *k_start;  // NULL: one sequence of all rows
+  int64_t nq, nk;
+  int nseq, hk, g, d, causal, splits;
+  float c;        // scale * log2(e)
+  float* part_o;  // [splits][nq][hq][d]
+  float2* part_ml;
+};
+
+// Entry i of a start array, kept inside [0, n]: whatever it holds, no access leaves
+// the tensors.
+__device__ __forceinline__ int64_t start_at(const int32_t* s, int i, int64_t n) {
+  if (!s) return i ? n : 0;
+  const int64_t v = s[i];
+  return v < 0 ? 0 : (v > n ? n : v);
+}
+
+// The slots of sequence s begin at floor(q_start[s] g / BM) + s: at least as many
+// slots as the sequence has row blocks lie before the next one's. Returns the
+// sequence that holds `slot` (the last whose slots begin at or before it), or -1;
+// 64 starts are looked at a time.
+__device__ __forceinline__ int sequence_of(const AttnArgs& a, int64_t slot, int lane) {
+  int lo = 0, len = a.nseq;
+  auto begin = [&](int s) { return start_at(a.q_start, s, a.nq) * a.g / kABM + s; };
+  while (len > 0) {
+    const int step = (len + 63) >> 6;
+    const int at = lane * step;
+    const bool before = at < len && begin(lo + at) <= slot;
+    const int cnt = __popcll(__ballot(before));
+    if (cnt == 0) return -1;
+    lo += (cnt - 1) * step;
+    if (step == 1) return lo;
+    len = min(step, len - (cnt - 1) * step);
+  }
+  return -1;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Maximum over the two lanes (l, l + 32) that share a query.
+__device__ __forceinline__ float half_max(float x) {
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+
+__device__ __forceinline__ unsigned pack2(float a, float b) {
+  return (unsigned)f32_to_bf16_rne(a) | ((unsigned)f32_to_bf16_rne(b) << 16);
+}
+
+template <int D>
+__global__ __launch_bounds__(kAThreads, 2) void attention_kernel(AttnArgs a) {
+  constexpr int kPieces = D / 8;             // 16-byte pieces per row
+  constexpr int kRowB = D * 2;
+  constexpr int kTile = kAKT * kRowB;        // one operand's tile
+  constexpr int kLd = kTile / 4096;          // 1 KB loads per wave and operand
+  constexpr int kRowsPer = 64 / kPieces;     // rows per 1 KB
+  constexpr int kDB = D / 32, kKS = D / 16;
+  __shared__ __attribute__((aligned(1024))) unsigned char sm[4 * kTile];  // K0 K1 V0 V1
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int head = blockIdx.x % a.hk;
+  // the last slots first: a causal sequence's longest rows are its last
+  const int64_t slot = (int64_t)(gridDim.x / a.hk) - 1 - blockIdx.x / a.hk;
+  const int seq = sequence_of(a, slot, lane);
+  if (seq < 0) return;
+  const int64_t q0 = start_at(a.q_start, seq, a.nq), q1 = start_at(a.q_start, seq + 1, a.nq);
+  const int64_t k0 = start_at(a.k_start, seq, a.nk), k1 = start_at(a.k_start, seq + 1, a.nk);
+  const int lk = k1 > k0 ? (int)(k1 - k0) : 0;
+  const int64_t rows = q1 > q0 ? (q1 - q0) * a.g : 0;
+  const int64_t row0 = (slot - (q0 * a.g / kABM + seq)) * kABM;
+  if (row0 < 0 || row0 >= rows) return;
+  const int off = lk - (int)(q1 - q0);  // key of the same age as query 0
+
+  // keys [0, limit) are visible to a row
+  auto limit_of = [&](int64_t r) {
+    if (!a.causal) return lk;
+    const int64_t e = (int64_t)((unsigned)r / (unsigned)a.g) + off + 1;
+    return (int)(e < 0 ? 0 : (e < lk ? e : lk));
+  };
+  const int64_t row_end = row0 + kABM < rows ? row0 + kABM : rows;
+  const int keys = limit_of(row_end - 1);
+  const int per = (int)cdiv(cdiv(keys, kAKT), a.splits) * kAKT;
+  const int kbeg = min(keys, (int)blockIdx.y * per), kend = min(keys, kbeg + per);
+
+  // this lane's row
+  const int64_t wrow = row0 + wave * 32;
+  const bool wave_has = wrow < row_end;
+  const int64_t mine = wrow + (lane & 31);
+  const bool valid = mine < row_end;
+  const int64_t r = valid ? mine : row_end - 1;
+  const int64_t tok = (unsigned)r / (unsigned)a.g;  // nq g < 2^31
+  const int qh = head * a.g + (int)(r - tok * a.g);
+  const int visible = limit_of(r);
+  const int lim = min(visible, kend);
+  // rows ascend within a wave, and so do their limits
+  const int lim_first = __builtin_amdgcn_readfirstlane(lim);
+  const int lim_last = wave_has ? __builtin_amdgcn_readlane(lim, 31) : 0;
+  const int half = lane >> 5;
+
+  bf16x8_t qf[kKS];
+  {
+    const unsigned short* qp = a.q + (q0 + tok) * a.q_token + qh * a.q_head;
+#pragma unroll
+    for (int st = 0; st < kKS; ++st) {
+      const int e = st * 16 + half * 8;
+      u32x4_t u = u32x4_t{0u, 0u, 0u, 0u};
+      if (e < a.d) u = *(const u32x4_t*)(qp + e);
+      qf[st] = __builtin_bit_cast(bf16x8_t, u);
+    }
+  }
+
+  f32x16_t o[kDB];
+#pragma unroll
+  for (int i = 0; i < kDB; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+  float m = -INFINITY, l = 0.f;
+
+  // Loader: chunk wave + 4 i of a tile (1 KB, kRowsPer rows); lane l fills row
+  // kRowsPer chunk + l / kPieces at physical piece l % kPieces. K pieces are
+  // swizzled by the row so that 16 rows at one piece spread over all banks, V
+  // pieces so that 4 rows x 64 bytes do.
+  const int lr = lane / kPieces, lpp = lane % kPieces;
+  const int row_w = wave * kRowsPer + lr;  // + 4 i kRowsPer
+  const int swk = D == 128 ? (row_w & 15) : ((row_w >> 1) & 7);
+  const int swv = D == 128 ? ((row_w & 3) << 2) : (((row_w >> 1) & 1) << 2);
+  const int ck = (lpp ^ swk) * 8, cv = (lpp ^ swv) * 8;
+  const unsigned short* kb = a.k + k0 * a.k_token + head * a.k_head + ck;
+  const unsigned short* vb = a.v + k0 * a.v_token + head * a.v_head + cv;
+  const bool in_k = ck < a.d, in_v = cv < a.d;
+  if (a.d < D) {  // pieces past the head are zero in every tile
+    for (int i = tid; i < 4 * kTile / 16; i += kAThreads)
+      *(u32x4_t*)(sm + i * 16) = u32x4_t{0u, 0u, 0u, 0u};
+    __syncthreads();
+  }
+  auto issue = [&](int kt, int buf) {
+    const void *gk[kLd], *gv[kLd];
+#pragma unroll
+    for (int i = 0; i < kLd; ++i) {
+      int key = kt + row_w + 4 * i * kRowsPer;
+      key = key < lk ? key : lk - 1;  // rows past the keys are masked
+      gk[i] = kb + (int64_t)key * a.k_token;
+      gv[i] = vb + (int64_t)key * a.v_token;
+    }
+    unsigned char* dk = sm + buf * kTile + wave * 1024;
+    unsigned char* dv = sm + (2 + buf) * kTile + wave * 1024;
+    if (in_k) lds_dma_v<kLd>(gk, dk);
+    if (in_v) lds_dma_v<kLd>(gv, dv);
+  };
+
+  // operand addresses inside a tile; the step's piece bits are XORed in
+  const int krow = lane & 31;
+  const int kswz = D == 128 ? (krow & 15) : ((krow >> 1) & 7);
+  const int kaddr = krow * kRowB + ((half ^ kswz) << 4);
+  const int s16 = lane & 15;
+  const int vkey = 4 * half + (s16 >> 2);
+  const int vswz = D == 128 ? ((vkey & 3) << 2) : (((vkey >> 1) & 1) << 2);
+  const int vpiece = 2 * ((lane >> 4) & 1) + ((s16 & 3) >> 1);
+  const int vaddr = vkey * kRowB + ((vpiece ^ vswz) << 4) + (s16 & 1) * 8;
+
+  if (kbeg < kend) issue(kbeg, 0);
+  int buf = 0;
+  for (int kt = kbeg; kt < kend; kt += kAKT, buf ^= 1) {
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();  // this tile has landed; the other buffer was last read before it
+    if (kt + kAKT < kend) issue(kt + kAKT, buf ^ 1);
+    if (kt >= lim_last) continue;  // no row of this wave sees the tile
+    const unsigned char* ks = sm + buf * kTile;
+    const unsigned char* vs = sm + (2 + buf) * kTile;
+
+    f32x16_t s[2];
+#pragma unroll
+    for (int b2 = 0; b2 < 2; ++b2)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[b2][e] = 0.f;
+#pragma unroll
+    for (int st = 0; st < kKS; ++st)
+#pragma unroll
+      for (int b2 = 0; b2 < 2; ++b2) {
+        const bf16x8_t kf = *(const bf16x8_t*)(ks + b2 * 32 * kRowB + (kaddr ^ (st << 5)));
+        s[b2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[st], s[b2], 0, 0, 0);
+      }
+
+    const bool masked = kt + kAKT > lim_first;
+    if (masked) {
+#pragma unroll
+      for (int b2 = 0; b2 < 2; ++b2)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int key = kt + b2 * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
+          s[b2][e] = key < lim ? s[b2][e] : -INFINITY;
+        }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int b2 = 0; b2 < 2; ++b2)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b2][e]);
+    top = half_max(top) * a.c;
+    if (__any(top > m + kAMove)) {  // also the first tile, where m is -inf
+      const float mn = fmaxf(m, top);
+      const float f = exp2_fast(m - (mn == -INFINITY ? 0.f : mn));
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < kDB; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] *= f;
+      m = mn;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    bf16x8_t pf[4];
+#pragma unroll
+    for (int ks16 = 0; ks16 < 4; ++ks16) {
+      u32x4_t u;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int e = (ks16 & 1) * 8 + 2 * x;
+        const float p0 = exp2_fast(fmaf(s[ks16 >> 1][e], a.c, -ref));
+        const float p1 = exp2_fast(fmaf(s[ks16 >> 1][e + 1], a.c, -ref));
+        l += p0 + p1;
+        u[x] = pack2(p0, p1);
+      }
+      pf[ks16] = __builtin_bit_cast(bf16x8_t, u);
+    }
+
+    auto v_frag = [&](int ks16, int db) {
+      const unsigned char* p = vs + ks16 * 16 * kRowB + (vaddr ^ (db << 6));
+      const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) v4i16_t*)p);
+      const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) v4i16_t*)(p + 8 * kRowB));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    // A hidden key's p is 0, but 0 times an infinity or NaN in its V row is not: a
+    // tile with hidden keys is looked through, and where V holds such a value the
+    // products are taken key by key and kept for the rows that see the key.
+    bool special = false;
+    if (masked) {
+      unsigned bad = 0;
+#pragma unroll
+      for (int ks16 = 0; ks16 < 4; ++ks16)
+#pragma unroll
+        for (int db = 0; db < kDB; ++db) {
+          const v8i16_t vf = v_frag(ks16, db);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) bad |= (vf[x] & 0x7f80) == 0x7f80 ? 1u : 0u;
+        }
+      special = __any(bad);
+    }
+    if (!special) {
+#pragma unroll
+      for (int ks16 = 0; ks16 < 4; ++ks16)
+#pragma unroll
+        for (int db = 0; db < kDB; ++db)
+          o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8_t, v_frag(ks16, db)), pf[ks16], o[db], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int ks16 = 0; ks16 < 4; ++ks16)
+#pragma unroll
+        for (int db = 0; db < kDB; ++db) {
+          const v8i16_t vf = v_frag(ks16, db);
+#pragma unroll 1
+          for (int j = 0; j < 16; ++j) {  // key kt + 16 ks16 + j: element x of half h
+            const int jh = (j >> 2) & 1, jx = (j & 3) + 4 * (j >> 3);
+            v8i16_t one;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) one[x] = half == jh && x == jx ? vf[x] : (short)0;
+            f32x16_t z;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z[e] = 0.f;
+            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, one), pf[ks16],
+                                                        z, 0, 0, 0);
+            if (kt + 16 * ks16 + j < lim) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[db][e] += z[e];
+            }
+          }
+        }
+    }
+  }
+
+  l += __shfl_xor(l, 32);
+  if (!valid) return;
+  // element 8 (e / 4) + 4 half + e % 4 of each block of 32 is in register e
+  if (a.splits > 1) {
+    const int64_t at = ((int64_t)blockIdx.y * a.nq + q0 + tok) * (a.hk * a.g) + qh;
+    // l = -1 marks a piece that saw keys, all of them with scores of -inf
+    if (half == 0) a.part_ml[at] = make_float2(m, lim > kbeg && l == 0.f ? -1.f : l);
+    if (kbeg >= kend) return;
+#pragma unroll
+    for (int db = 0; db < kDB; ++db)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int e = db * 32 + 8 * x + 4 * half;
+        if (e < a.d)
+          *(f32x4_t*)(a.part_o + at * a.d + e) =
+              f32x4_t{o[db][4 * x], o[db][4 * x + 1], o[db][4 * x + 2], o[db][4 * x + 3]};
+      }
+    return;
+  }
+  const float inv = visible > 0 ? 1.0f / l : 0.f;
+  unsigned short* op = a.o + (q0 + tok) * a.o_token + qh * a.o_head;
+#pragma unroll
+  for (int db = 0; db < kDB; ++db)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int e = db * 32 + 8 * x + 4 * half;
+      if (e < a.d) {
+        u16x4_t w;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          w[y] = visible > 0 ? f32_to_bf16_rne(o[db][4 * x + y] * inv) : (unsigned short)0;
+        *(u16x4_t*)(op + e) = w;
+      }
+    }
+}
+
+// Joins the splits of a (token, query head): 32 lanes, 4 elements each.
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  const int hq = a.hk * a.g;
+  const int64_t tok = row / hq;
+  const int qh = (int)(row - tok * hq);
+  if (tok < start_at(a.q_start, 0, a.nq) || tok >= start_at(a.q_start, a.nseq, a.nq)) return;
+  const int e = (threadIdx.x & 31) * 4;
+  float m = -INFINITY, l = 0.f;
+  const int64_t step = a.nq * hq;
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_ml[s * step + row].x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  bool any = false;
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 ml = a.part_ml[s * step + row];
+    any |= ml.y != 0.f;  // 0: the piece saw no key
+    if (ml.y <= 0.f) continue;
+    const float f = exp2_fast(ml.x - ref);
+    l += ml.y * f;
+    if (e < a.d) o += *(const f32x4_t*)(a.part_o + (s * step + row) * a.d + e) * f;
+  }
+  if (e >= a.d) return;
+  // keys seen, but every score -inf: l is 0 and there is no softmax (NaN)
+  u16x4_t w;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) w[y] = any ? f32_to_bf16_rne(o[y] / l) : (unsigned short)0;
+  *(u16x4_t*)(a.o + tok * a.o_token + qh * a.o_head + e) = w;
+}
+
+constexpr int kAUnits = 256;  // compute units
+
+// Pieces the keys are split into: enough for two workgroups per compute unit, with
+// at least four tiles of keys each (by the sequences' average lengths, all that the
+// host knows).
+int splits_of(const th_attention_params* p) {
+  const int64_t g = p->hq / p->hk;
+  const int64_t seqs = p->nseq < p->nq ? p->nseq : p->nq;
+  const int64_t groups = seqs * cdiv(cdiv(p->nq, seqs) * g, kABM) * p->hk;
+  const int64_t tiles = cdiv(cdiv(p->nk, seqs), kAKT);
+  int64_t s = 2 * kAUnits / groups;
+  if (s > tiles / 4) s = tiles / 4;
+  if (s > 64) s = 64;
+  return s < 1 ? 1 : (int)s;
+}
+
+}  // namespace
+
+size_t attention_workspace_bytes(const th_attention_params* p) {
+  if (p->nq == 0) return 0;
+  const int s = splits_of(p);
+  if (s == 1) return 0;
+  return (size_t)s * p->nq * p->hq * ((size_t)p->d * sizeof(float) + sizeof(float2));
+}
+
+hipError_t launch_attention(const void* Q, const void* K, const void* V, const int32_t* q_start,
+                            const int32_t* k_start, const th_attention_params* p, void* O,
+                            void* workspace, hipStream_t s) {
+  AttnArgs a;
+  a.q = (const unsigned short*)Q;
+  a.k = (const unsigned short*)K;
+  a.v = (const unsigned short*)V;
+  a.o = (unsigned short*)O;
+  a.q_token = p->q_token;
+  a.q_head = p->q_head;
+  a.k_token = p->k_token;
+  a.k_head = p->k_head;
+  a.v_token = p->v_token;
+  a.v_head = p->v_head;
+  a.o_token = p->o_token;
+  a.o_head = p->o_head;
+  a.q_start = q_start;
+  a.k_start = k_start;
+  a.nq = p->nq;
+  a.nk = p->nk;
+  a.nseq = (int)p->nseq;
+  a.hk = (int)p->hk;
+  a.g = (int)(p->hq / p->hk);
+  a.d = (int)p->d;
+  a.causal = p->causal != 0;
+  a.c = (float)(p->scale * 1.4426950408889634);
+  a.splits = workspace ? splits_of(p) : 1;
+  a.part_ml = (float2*)workspace;
+  a.part_o = workspace ? (float*)(a.part_ml + (size_t)a.splits * p->nq * p->hq) : nullptr;
+  const int64_t slots = p->nq * a.g / kABM + p->nseq;
+  const dim3 grid((unsigned)(slots * p->hk), (unsigned)a.splits);
+  if (p->d <= 64)
+    hipLaunchKernelGGL((attention_kernel<64>), grid, dim3(kAThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((attention_kernel<128>), grid, dim3(kAThreads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)cdiv(p->nq * p->hq, 8)), dim3(256), 0, s,
+                     a);
+  return hipGetLastError();
+}
+
+}  // namespace th

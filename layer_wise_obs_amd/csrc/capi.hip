@@ -915,6 +915,14 @@ th_status th_rotary_freqs(int64_t rot, const th_rotary_scaling* scaling, double*
 }
 
 namespace {
+// Heads [rows, heads, d] written through these strides must not share memory.
+bool heads_overlap(int64_t rows, int64_t heads, int64_t d, int64_t token, int64_t head) {
+  const bool token_outer = heads == 1 || (rows > 1 && token >= head);
+  const int64_t inner = token_outer ? head : token, outer = token_outer ? token : head;
+  const int64_t ni = token_outer ? heads : rows, no = token_outer ? rows : heads;
+  return (ni > 1 && inner < d) || (no > 1 && outer < (ni - 1) * inner + d);
+}
+
 th_status check_heads(const th_heads* h, int64_t n, int64_t d, bool* work) {
   if (h->heads < 0 || h->heads >= ((int64_t)1 << 31))
     return fail(TH_ERR_INVALID_ARG, "heads must be >= 0");
@@ -922,12 +930,7 @@ th_status check_heads(const th_heads* h, int64_t n, int64_t d, bool* work) {
     return fail(TH_ERR_INVALID_ARG, "negative stride");
   if (n == 0 || h->heads == 0) return TH_OK;
   if (!h->x || !h->y) return fail(TH_ERR_INVALID_ARG, "x or y is NULL");
-  // rows of y that share memory would be written twice: whichever stride is the
-  // outer one has to step over the whole inner extent
-  const int64_t inner = h->y_head <= h->y_token || n == 1 ? h->y_head : h->y_token;
-  const int64_t outer = inner == h->y_head ? h->y_token : h->y_head;
-  const int64_t ni = inner == h->y_head ? h->heads : n, no = inner == h->y_head ? n : h->heads;
-  if ((ni > 1 && inner < d) || (no > 1 && outer < (ni - 1) * inner + d))
+  if (heads_overlap(n, h->heads, d, h->y_token, h->y_head))
     return fail(TH_ERR_INVALID_ARG, "the heads of y overlap");
   if (h->x == h->y && (h->x_token != h->y_token || h->x_head != h->y_head))
     return fail(TH_ERR_INVALID_ARG, "in place needs the same strides");
@@ -960,6 +963,65 @@ th_status th_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n
   TH_HIP(launch_rotary(q, k, dt, n, d, rot, layout == TH_ROTARY_INTERLEAVED, positions, freqs,
                        (float)amplitude, (float)eps, (hipStream_t)stream),
          "rotary");
+  return TH_OK;
+}
+
+namespace {
+th_status check_attention(const th_attention_params* p) {
+  const int64_t rows = ((int64_t)1 << 31) - ((int64_t)1 << 16);
+  if (!p) return fail(TH_ERR_INVALID_ARG, "params is NULL");
+  if (p->nq < 0 || p->nq >= rows || p->nk < 0 || p->nk >= rows)
+    return fail(TH_ERR_INVALID_ARG, "needs 0 <= nq, nk < 2^31 - 2^16");
+  if (p->hk < 1 || p->hq < 1 || p->hq % p->hk)
+    return fail(TH_ERR_INVALID_ARG, "needs hq, hk >= 1 and hk | hq");
+  if (p->d < 8 || p->d > 128 || p->d % 8)
+    return fail(TH_ERR_INVALID_ARG, "needs 8 <= d <= 128 and d % 8 == 0");
+  if (p->hq >= ((int64_t)1 << 16) || p->nq * (p->hq / p->hk) >= rows)
+    return fail(TH_ERR_INVALID_ARG, "nq * hq / hk must be < 2^31 - 2^16, hq < 2^16");
+  if (p->nseq < 1 || p->nseq >= ((int64_t)1 << 24))
+    return fail(TH_ERR_INVALID_ARG, "needs 1 <= nseq < 2^24");
+  if ((p->nq * (p->hq / p->hk) / 128 + p->nseq) * p->hk >= ((int64_t)1 << 30) ||
+      p->nq * p->hq >= ((int64_t)1 << 33))
+    return fail(TH_ERR_INVALID_ARG, "too many rows, heads and sequences for one launch");
+  const int64_t strides[8] = {p->q_token, p->q_head, p->k_token, p->k_head,
+                              p->v_token, p->v_head, p->o_token, p->o_head};
+  for (int64_t v : strides)
+    if (v < 0 || v % 8) return fail(TH_ERR_INVALID_ARG, "strides must be multiples of 8, >= 0");
+  if (heads_overlap(p->nq, p->hq, p->d, p->o_token, p->o_head))
+    return fail(TH_ERR_INVALID_ARG, "the heads of O overlap");
+  if (!(p->scale > 0.0) || !std::isfinite(p->scale))
+    return fail(TH_ERR_INVALID_ARG, "scale must be finite and > 0");
+  return TH_OK;
+}
+}  // namespace
+
+th_status th_attention_workspace_size(const th_attention_params* p, size_t* bytes) {
+  if (!bytes) return fail(TH_ERR_INVALID_ARG, "bytes is NULL");
+  th_status st = check_attention(p);
+  if (st != TH_OK) return st;
+  *bytes = attention_workspace_bytes(p);
+  return TH_OK;
+}
+
+th_status th_attention(const void* Q, const void* K, const void* V, th_dtype dt,
+                       const int32_t* q_start, const int32_t* k_start,
+                       const th_attention_params* p, void* O, void* workspace,
+                       size_t workspace_bytes, th_stream_t stream) {
+  if (dt != TH_BF16) return fail(TH_ERR_INVALID_ARG, "bf16 only");
+  th_status st = check_attention(p);
+  if (st != TH_OK) return st;
+  if (!q_start && (k_start || p->nseq != 1))
+    return fail(TH_ERR_INVALID_ARG, "without q_start: k_start NULL and nseq 1");
+  if ((p->nq > 0 && (!Q || !O)) || (p->nq > 0 && p->nk > 0 && (!K || !V)))
+    return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (((uintptr_t)Q | (uintptr_t)K | (uintptr_t)V | (uintptr_t)O | (uintptr_t)workspace) & 15)
+    return fail(TH_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  if (p->nq == 0) return TH_OK;
+  if (workspace && workspace_bytes < attention_workspace_bytes(p))
+    return fail(TH_ERR_WORKSPACE, "workspace too small");
+  TH_HIP(launch_attention(Q, K, V, q_start, k_start ? k_start : q_start, p, O, workspace,
+                          (hipStream_t)stream),
+         "attention");
   return TH_OK;
 }
 

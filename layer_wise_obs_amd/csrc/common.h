@@ -247,6 +247,13 @@ hipError_t launch_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int6
                          int64_t rot, int interleaved, const int32_t* positions,
                          const double* freqs, float amplitude, float eps, hipStream_t s);
 
+// attention.hip
+// workspace of the split keys: 0 where it does not help
+size_t attention_workspace_bytes(const th_attention_params* p);
+hipError_t launch_attention(const void* Q, const void* K, const void* V, const int32_t* q_start,
+                            const int32_t* k_start, const th_attention_params* p, void* O,
+                            void* workspace, hipStream_t s);
+
 // rows.hip
 hipError_t launch_row_energy(const void* W, th_dtype wdt, int64_t c, int64_t b, const float* g,
                              float* s, hipStream_t st);

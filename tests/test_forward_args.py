@@ -1,4 +1,5 @@
-"""Argument checks of the block's forward steps (linear, row norm, rotary positions), answered
+"""Argument checks of the block's forward steps (linear, row norm, rotary positions, attention),
+answered
 before anything touches the GPU, and the host-side frequencies of the rotation."""
 import ctypes
 import math
@@ -60,7 +61,46 @@ def test_linear_workspace_query():
     assert lib.th_linear(*_linear_args(ws_bytes=need - 1, **a)) == L.TH_ERR_WORKSPACE
 
 
+def _attention_params(**kw):
+    a = dict(nq=6, nk=9, hq=8, hk=2, d=64, q_token=512, q_head=64, k_token=128, k_head=64,
+             v_token=128, v_head=64, o_token=512, o_head=64, nseq=2, causal=1, scale=0.125)
+    a.update(kw)
+    return L.AttentionParams(*a.values())
+
+
+def _attention(Q=FAKE, K=FAKE, V=FAKE, dt=L.TH_BF16, qs=FAKE, ks=None, O=2 * FAKE, ws=None,
+               ws_bytes=0, **kw):
+    return L.lib().th_attention(Q, K, V, dt, qs, ks, ctypes.byref(_attention_params(**kw)), O, ws,
+                                ws_bytes, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(Q=None), dict(K=None), dict(V=None), dict(O=None), dict(dt=L.TH_F32), dict(Q=FAKE + 8),
+    dict(K=FAKE + 2), dict(V=FAKE + 8), dict(O=FAKE + 8), dict(ws=FAKE + 8, ws_bytes=1 << 30),
+    dict(qs=None), dict(qs=None, nseq=1, ks=FAKE), dict(nq=-1), dict(nk=-1), dict(nk=1 << 31),
+    dict(nq=1 << 62), dict(hq=0), dict(hk=0), dict(hk=3), dict(hq=-8), dict(d=4), dict(d=60),
+    dict(d=136, q_head=136, o_head=136, o_token=1088), dict(hq=1 << 17, o_token=1 << 24),
+    dict(nseq=0), dict(nseq=1 << 24), dict(q_token=-512), dict(k_head=60), dict(v_token=132),
+    dict(o_head=56), dict(o_token=504), dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN),
+    dict(scale=INF), dict(nq=1 << 30, hq=64, hk=8, o_token=4096)])
+def test_attention_refuses(bad):
+    assert _attention(**bad) == L.TH_ERR_INVALID_ARG
+
+
+def test_attention_workspace_query():
+    lib, out = L.lib(), ctypes.c_size_t(0)
+    p = _attention_params(scale=0.0)
+    assert lib.th_attention_workspace_size(ctypes.byref(p), ctypes.byref(out)) == L.TH_ERR_INVALID_ARG
+    assert lib.th_attention_workspace_size(None, ctypes.byref(out)) == L.TH_ERR_INVALID_ARG
+    assert L.attention_workspace_size(_attention_params()) == 0  # short: nothing is split
+    long = dict(nq=2, nk=100000)
+    need = L.attention_workspace_size(_attention_params(**long))
+    assert need > 0 and need % (2 * 8 * (64 + 2) * 4) == 0
+    assert _attention(ws=FAKE, ws_bytes=need - 1, **long) == L.TH_ERR_WORKSPACE
+
+
 def test_no_rows_is_no_work():
+    assert _attention(nq=0, Q=None, O=None) == L.TH_OK
     assert L.lib().th_linear(*_linear_args(n=0, X=None, Y=None)) == L.TH_OK
     assert L.lib().th_rms_norm(*_norm_args(n=0, X=None, Y=None)) == L.TH_OK
     h = _heads(x=None, y=None)
