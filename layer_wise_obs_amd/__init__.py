@@ -5,7 +5,8 @@ this package holds its ctypes binding, the build script and the seeded input
 generator.
 """
 from ._lib import (  # noqa: F401
-    ThanosError, debug_factor, debug_select_global, debug_select_nm, hessian_accumulate,
-    hessian_finalize, hessian_workspace_size, lib, make_params, prune_layer,
-    prune_layer_workspace_size, reconstruction_error, workspace,
+    ThanosError, attention, debug_factor, debug_select_global, debug_select_nm,
+    hessian_accumulate, hessian_finalize, hessian_workspace_size, lib, linear, make_params,
+    prune_layer, prune_layer_workspace_size, reconstruction_error, rms_norm, rotary,
+    rotary_freqs, workspace,
 )
