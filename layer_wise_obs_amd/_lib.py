@@ -179,26 +179,25 @@ def _require_cuda(*ts):
             raise ValueError("tensors must be contiguous")
 
 
-def _require_rows(dev, *ts):
-    """Tensors of the forward steps: on dev, the last dimension contiguous (any outer strides)."""
-    for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must live on the GPU")
-        if t.device != dev:
-            raise ValueError("tensors must live on one GPU")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError("the last dimension must be contiguous")
+def _device_index(t) -> int:
+    """GPU that the forward steps' call runs on: the one its first tensor lives on."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must live on the GPU")
+    return index
 
 
-def _require_shape(name, t, shape, dtype=None):
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape):
+def _require(index, name, t, shape, dtype):
+    """A tensor of the forward steps: on GPU index, of this shape and dtype, its last dimension
+    contiguous (any outer strides)."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on GPU {index}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
 def _pitch(t, dim, dense):
@@ -206,13 +205,26 @@ def _pitch(t, dim, dense):
     return t.stride(dim) if t.shape[dim] > 1 else dense
 
 
-def _on_device(dev, fn, *args):
-    """Call fn with dev current, on dev's current stream (its last argument)."""
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call_on(index, fn, *args):
+    """Call fn with GPU index current, on that GPU's current stream (its last argument)."""
     torch = _torch()
-    if dev.index is not None and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _check(fn(*args, _stream(dev)))
-    return _check(fn(*args, _stream(dev)))
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _check(fn(*args, torch.cuda.current_stream(index).cuda_stream))
+    _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+
+
+def _workspace_on(index, ws):
+    """(address, bytes) of a caller's workspace tensor."""
+    if ws.get_device() != index:
+        raise ValueError(f"ws must live on GPU {index}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def make_params(sparsity=0.5, pattern=None, block=128, lam=0.01, relative=True,
@@ -409,45 +421,50 @@ _ACTIVATIONS = {"none": TH_ACT_NONE, "relu": TH_ACT_RELU, "silu": TH_ACT_SILU,
 
 def linear(X, W, bias=None, act="none", residual=None, Y=None, out_dtype=None, ws=None):
     """Y = act(X W^T + bias) + residual for X [n, b], W [c, b] and bias [c] (bf16); residual and
-    Y [n, c] in out_dtype (bf16 or fp32, default X's). Y may be the residual."""
+    Y [n, c] in out_dtype (bf16 or fp32, default the residual's or X's). Y may be the residual."""
     torch = _torch()
+    index = _device_index(X)
     n, b = X.shape
     c = W.shape[0]
-    dev = X.device
+    if out_dtype is None:
+        out_dtype = next((t.dtype for t in (Y, residual) if t is not None), X.dtype)
     if Y is None:
-        if out_dtype is None:
-            out_dtype = X.dtype if residual is None else residual.dtype
-        Y = torch.empty((n, c), dtype=out_dtype, device=dev)
-    _require_rows(dev, X, bias, residual, Y, ws)
-    _require_cuda(W)
-    _require_shape("W", W, (c, b), X.dtype)
-    _require_shape("bias", bias, (c,), X.dtype)
-    _require_shape("Y", Y, (n, c), out_dtype)
-    _require_shape("residual", residual, (n, c), Y.dtype)
-    if W.device != dev:
-        raise ValueError("tensors must live on one GPU")
+        Y = torch.empty((n, c), dtype=out_dtype, device=X.device)
+    else:
+        _require(index, "Y", Y, (n, c), out_dtype)
+    _require(index, "X", X, (n, b), X.dtype)
+    _require(index, "W", W, (c, b), X.dtype)
+    if not W.is_contiguous():
+        raise ValueError("W must be contiguous")
+    if bias is not None:
+        _require(index, "bias", bias, (c,), X.dtype)
+    ldr = 0
+    if residual is not None:
+        _require(index, "residual", residual, (n, c), out_dtype)
+        ldr = _pitch(residual, 0, c)
     if ws is None:
         nbytes = linear_workspace_size(n, b, c)
-        ws = workspace(nbytes, dev) if nbytes else None
-    _on_device(dev, lib().th_linear, _ptr(X), _pitch(X, 0, b), _ptr(W), _dtype_code(X), n, b, c,
-               _ptr(bias), _ACTIVATIONS[act], _ptr(residual),
-               0 if residual is None else _pitch(residual, 0, c), _ptr(Y), _dtype_code(Y),
-               _pitch(Y, 0, c), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+        ws = workspace(nbytes, X.device) if nbytes else None
+    at, nbytes = (None, 0) if ws is None else _workspace_on(index, ws)
+    _call_on(index, lib().th_linear, X.data_ptr(), _pitch(X, 0, b), W.data_ptr(), _dtype_code(X),
+             n, b, c, _addr(bias), _ACTIVATIONS[act], _addr(residual), ldr, Y.data_ptr(),
+             _dtype_code(Y), _pitch(Y, 0, c), at, nbytes)
     return Y
 
 
 def rms_norm(X, weight, eps=1e-5, Y=None, out_dtype=None):
     """Y = X / sqrt(mean(X^2) + eps) * weight by rows, X [n, b]; Y in out_dtype (default X's).
     Y may be X."""
-    torch = _torch()
+    index = _device_index(X)
     n, b = X.shape
     if Y is None:
-        Y = torch.empty((n, b), dtype=out_dtype or X.dtype, device=X.device)
-    _require_rows(X.device, X, weight, Y)
-    _require_shape("weight", weight, (b,), X.dtype)
-    _require_shape("Y", Y, (n, b), out_dtype)
-    _on_device(X.device, lib().th_rms_norm, _ptr(X), _dtype_code(X), n, b, _pitch(X, 0, b),
-               _ptr(weight), float(eps), _ptr(Y), _dtype_code(Y), _pitch(Y, 0, b))
+        Y = _torch().empty((n, b), dtype=out_dtype or X.dtype, device=X.device)
+    else:
+        _require(index, "Y", Y, (n, b), out_dtype or Y.dtype)
+    _require(index, "X", X, (n, b), X.dtype)
+    _require(index, "weight", weight, (b,), X.dtype)
+    _call_on(index, lib().th_rms_norm, X.data_ptr(), _dtype_code(X), n, b, _pitch(X, 0, b),
+             weight.data_ptr(), float(eps), Y.data_ptr(), _dtype_code(Y), _pitch(Y, 0, b))
     return Y
 
 
@@ -480,27 +497,35 @@ def rotary(q, k, freqs, positions=None, layout="half", amplitude=1.0, q_norm=Non
     first 2 * len(freqs) elements turned by positions * freqs (positions: int32 [n], default
     0 .. n-1). Returns (q_out, k_out), which may be q and k themselves."""
     torch = _torch()
+    index = _device_index(q)
     n, hq, d = q.shape
+    _require(index, "q", q, (n, hq, d), q.dtype)
     if q_out is None:
         q_out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    if k is None and (k_out is not None or k_norm is not None):
-        raise ValueError("k_out and k_norm go with k")
-    _require_rows(q.device, q, k, freqs, positions, q_norm, k_norm, q_out, k_out)
-    _require_shape("q_out", q_out, q.shape, q.dtype)
-    _require_shape("freqs", freqs, (freqs.numel(),), torch.float64)
-    _require_shape("positions", positions, (n,), torch.int32)
-    _require_shape("q_norm", q_norm, (d,), q.dtype)
+    else:
+        _require(index, "q_out", q_out, (n, hq, d), q.dtype)
+    if q_norm is not None:
+        _require(index, "q_norm", q_norm, (d,), q.dtype)
+    pairs = freqs.shape[0]
+    _require(index, "freqs", freqs, (pairs,), torch.float64)
+    if positions is not None:
+        _require(index, "positions", positions, (n,), torch.int32)
     kh = None
     if k is not None:
-        _require_shape("k", k, (n, k.shape[1], d), q.dtype)
-        _require_shape("k_out", k_out, k.shape, q.dtype)
-        _require_shape("k_norm", k_norm, (d,), q.dtype)
-        kh = ctypes.byref(_heads(k, k_out, k_norm))
-    _on_device(q.device, lib().th_rotary, ctypes.byref(_heads(q, q_out, q_norm)), kh,
-               _dtype_code(q), n, d, 2 * freqs.numel(), _ROTARY_LAYOUTS[layout], _ptr(positions),
-               _ptr(freqs), float(amplitude), float(eps))
+        hk = k.shape[1]
+        _require(index, "k", k, (n, hk, d), q.dtype)
+        if k_out is None:
+            k_out = torch.empty((n, hk, d), dtype=q.dtype, device=q.device)
+        else:
+            _require(index, "k_out", k_out, (n, hk, d), q.dtype)
+        if k_norm is not None:
+            _require(index, "k_norm", k_norm, (d,), q.dtype)
+        kh = _heads(k, k_out, k_norm)
+    elif k_out is not None or k_norm is not None:
+        raise ValueError("k_out and k_norm go with k")
+    _call_on(index, lib().th_rotary, _heads(q, q_out, q_norm), kh, _dtype_code(q), n, d, 2 * pairs,
+             _ROTARY_LAYOUTS[layout], _addr(positions), freqs.data_ptr(), float(amplitude),
+             float(eps))
     return q_out, k_out
 
 
@@ -515,21 +540,22 @@ def attention(Q, K, V, q_start=None, k_start=None, causal=True, scale=None, O=No
     along the rows: q_start and k_start int32 [nseq + 1] on the GPU (k_start defaults to q_start;
     without q_start all rows are one sequence). scale defaults to 1 / sqrt(d)."""
     torch = _torch()
+    index = _device_index(Q)
     nq, hq, d = Q.shape
     nk, hk, _ = K.shape
-    dev = Q.device
-    if O is None:
-        # rows that belong to no sequence are not written
-        O = torch.empty((nq, hq, d), dtype=Q.dtype, device=dev)
-    _require_rows(dev, Q, K, V, O, q_start, k_start, ws)
-    _require_shape("K", K, (nk, hk, d), Q.dtype)
-    _require_shape("V", V, (nk, hk, d), Q.dtype)
-    _require_shape("O", O, (nq, hq, d), Q.dtype)
+    _require(index, "Q", Q, (nq, hq, d), Q.dtype)
+    _require(index, "K", K, (nk, hk, d), Q.dtype)
+    _require(index, "V", V, (nk, hk, d), Q.dtype)
+    if O is None:  # rows that belong to no sequence are not written
+        O = torch.empty((nq, hq, d), dtype=Q.dtype, device=Q.device)
+    else:
+        _require(index, "O", O, (nq, hq, d), Q.dtype)
     nseq = 1
     if q_start is not None:
-        nseq = q_start.numel() - 1
-        _require_shape("q_start", q_start, (nseq + 1,), torch.int32)
-        _require_shape("k_start", k_start, (nseq + 1,), torch.int32)
+        nseq = q_start.shape[0] - 1
+        _require(index, "q_start", q_start, (nseq + 1,), torch.int32)
+        if k_start is not None:
+            _require(index, "k_start", k_start, (nseq + 1,), torch.int32)
     elif k_start is not None:
         raise ValueError("k_start goes with q_start")
     p = AttentionParams(nq, nk, hq, hk, d, _pitch(Q, 0, hq * d), _pitch(Q, 1, d),
@@ -538,10 +564,10 @@ def attention(Q, K, V, q_start=None, k_start=None, causal=True, scale=None, O=No
                         1 if causal else 0, d ** -0.5 if scale is None else float(scale))
     if ws is None:
         nbytes = attention_workspace_size(p)
-        ws = workspace(nbytes, dev) if nbytes else None
-    _on_device(dev, lib().th_attention, _ptr(Q), _ptr(K), _ptr(V), _dtype_code(Q), _ptr(q_start),
-               _ptr(k_start), ctypes.byref(p), _ptr(O), _ptr(ws),
-               0 if ws is None else ws.numel() * ws.element_size())
+        ws = workspace(nbytes, Q.device) if nbytes else None
+    at, nbytes = (None, 0) if ws is None else _workspace_on(index, ws)
+    _call_on(index, lib().th_attention, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _dtype_code(Q),
+             _addr(q_start), _addr(k_start), p, O.data_ptr(), at, nbytes)
     return O
 
 
