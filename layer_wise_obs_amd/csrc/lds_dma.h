@@ -50,13 +50,13 @@ __device__ __forceinline__ uint64_t uniform_u64(uint64_t x) {
   return ((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((unsigned)(x >> 32)) << 32) |
          (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((unsigned)x);
 }
-// N loads (2 or 4) of 16 bytes per lane straight into LDS, in the saddr form: load m
+// N loads (1, 2 or 4) of 16 bytes per lane straight into LDS, in the saddr form: load m
 // takes byte offset vo[m] from the wave-uniform base g and writes the 1 KB chunk at
 // lds + 4096 m.
 template <int N>
 __device__ __forceinline__ void lds_dma_s(const unsigned (&vo)[N], const void* gbase,
                                           const void* lds) {
-  static_assert(N == 2 || N == 4, "two or four loads");
+  static_assert(N == 1 || N == 2 || N == 4, "one, two or four loads");
   const unsigned base = __builtin_amdgcn_readfirstlane(
       (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
   const uint64_t g = uniform_u64((uint64_t)(uintptr_t)gbase);
@@ -72,6 +72,13 @@ __device__ __forceinline__ void lds_dma_s(const unsigned (&vo)[N], const void* g
         : "=&s"(saved)
         : "s"(base), "v"(vo[0]), "v"(vo[1]), "v"(vo[2]), "v"(vo[3]), "s"(g)
         : "scc");
+  else if constexpr (N == 1)
+    __asm__ volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(base), "v"(vo[0]), "s"(g));
   else
     __asm__ volatile(
         "s_mov_b32 %0, m0\n\t"
