@@ -50,44 +50,28 @@ __device__ __forceinline__ uint64_t uniform_u64(uint64_t x) {
   return ((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((unsigned)(x >> 32)) << 32) |
          (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((unsigned)x);
 }
-// N loads (1, 2 or 4) of 16 bytes per lane straight into LDS, in the saddr form: load m
-// takes byte offset vo[m] from the wave-uniform base g and writes the 1 KB chunk at
-// lds + 4096 m.
-template <int N>
-__device__ __forceinline__ void lds_dma_s(const unsigned (&vo)[N], const void* gbase,
-                                          const void* lds) {
-  static_assert(N == 1 || N == 2 || N == 4, "one, two or four loads");
-  const unsigned base = __builtin_amdgcn_readfirstlane(
-      (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
-  const uint64_t g = uniform_u64((uint64_t)(uintptr_t)gbase);
-  unsigned saved;
-  if constexpr (N == 4)
-    __asm__ volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %6\n\t"
-        "s_add_u32 m0, %1, 4096\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %6\n\t"
-        "s_add_u32 m0, %1, 8192\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %6\n\t"
-        "s_add_u32 m0, %1, 12288\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %5, %6\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(base), "v"(vo[0]), "v"(vo[1]), "v"(vo[2]), "v"(vo[3]), "s"(g)
-        : "scc");
-  else if constexpr (N == 1)
-    __asm__ volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(base), "v"(vo[0]), "s"(g));
-  else
-    __asm__ volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %4\n\t"
-        "s_add_u32 m0, %1, 4096\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %4\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(base), "v"(vo[0]), "v"(vo[1]), "s"(g)
-        : "scc");
+// LDS byte address of a __shared__ object, for the loads below.
+__device__ __forceinline__ unsigned lds_address(const void* p) {
+  return (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// One load of 16 bytes per lane straight into LDS, in the saddr form: byte offset vo
+// (< 2^31) from the wave-uniform base g, into the 1 KB at LDS byte address lds
+// (wave-uniform). No result registers; completion is tracked by the callers' vmcnt
+// waits. M0 is declared clobbered rather than saved: two scalar moves fewer.
+__device__ __forceinline__ void lds_dma1(unsigned vo, const void* g, unsigned lds) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                   :
+                   : "s"(lds), "v"(vo), "s"(g)
+                   : "m0");
+}
+// One dword per lane into 256 bytes of LDS that nobody reads: brings the lanes' cache
+// lines into L2 without a result register.
+__device__ __forceinline__ void lds_dma_touch(unsigned vo, const void* g, unsigned lds) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                   :
+                   : "s"(lds), "v"(vo), "s"(g)
+                   : "m0");
 }
 
 __device__ __forceinline__ void lds_dma10s(const unsigned (&vo)[5], const void* gbase0,

@@ -24,7 +24,6 @@ namespace th {
 namespace {
 
 constexpr int kLK = 64;  // contraction per stage
-constexpr int kLThreads = 256;
 constexpr int kLGroup = 8;  // token tiles per group in the walk order
 constexpr int kLRow = kLK * 2;
 
@@ -120,13 +119,15 @@ __device__ __forceinline__ void finish8(float (&v)[8], int64_t t, int64_t q, int
 // Workgroup (x, split): tile x of the walk order, stages [split per, split per + per)
 // of the contraction. With part set, the tile's raw sums go to part[split][n][cp], cp
 // being c rounded up to 8.
-template <int WM, int WN, int S>
-__global__ __launch_bounds__(kLThreads) void linear_tile_kernel(
+template <int WM, int WN, int GN, int SA, int SB>
+__global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
     const unsigned short* __restrict__ X, int64_t ldx, const unsigned short* __restrict__ W,
     int64_t n, int64_t b, int64_t c, int ntm, int ntn, int per_xcd, int stages_per_split,
     float* __restrict__ part, LinEpilogue ep) {
-  constexpr int TM = 64 * WM, TN = 64 * WN;
-  constexpr int kA = TM * kLRow, kB = TN * kLRow, kStage = kA + kB;
+  constexpr int TM = 64 * WM, TN = 32 * WN * GN;
+  constexpr int kWaves = 2 * GN;
+  constexpr int LA = TM / 8 / kWaves, LB = TN / 8 / kWaves;  // 1 KB loads per wave and stage
+  constexpr int kA = TM * kLRow, kB = TN * kLRow;  // one stage of either operand
   const int wg = blockIdx.x;
   const int lin = (wg % 8) * per_xcd + wg / 8;
   if (lin >= ntm * ntn) return;
@@ -144,70 +145,74 @@ __global__ __launch_bounds__(kLThreads) void linear_tile_kernel(
   const int nk = min(stages_per_split, nk_all - s_begin);
   if (nk <= 0) return;  // no split of the launch is empty
 
-  __shared__ __attribute__((aligned(1024))) unsigned char sm[S * kStage];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
+  __shared__ __attribute__((aligned(1024))) unsigned char sm[SA * kA + SB * kB];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / GN, wn = wave % GN;
+  const unsigned smb = lds_address(sm);
 
-  // Loader: chunks of 1 KB (8 rows of 128 bytes); wave w loads chunks w + 4 m of
-  // either operand, m < 2 WM (2 WN). Lane l fills row 8 chunk + l/8 at physical piece
+  // Loader: chunks of 1 KB (8 rows of 128 bytes); wave w loads chunks
+  // w + kWaves m of either operand. Lane l fills row 8 chunk + l/8 at physical piece
   // l%8; (row / 2) & 7 is the same in each of its chunks.
   const int lrow = lane >> 3;
   const int lp = (lane & 7) ^ (((wave & 1) << 2) + (lane >> 4));
-  unsigned va[2][WM], vb[2][WN];
+  unsigned va[LA], vb[LB];
 #pragma unroll
-  for (int m = 0; m < 2 * WM; ++m) {
-    int64_t r = M0 + (wave + 4 * m) * 8 + lrow;
+  for (int m = 0; m < LA; ++m) {
+    int64_t r = M0 + (wave + kWaves * m) * 8 + lrow;
     r = r < n ? r : n - 1;  // rows past the end feed outputs that are never stored
-    va[m / WM][m % WM] = (unsigned)(((r - M0) * ldx + lp * 8) * 2);
+    va[m] = (unsigned)(((r - M0) * ldx + lp * 8) * 2);
   }
 #pragma unroll
-  for (int m = 0; m < 2 * WN; ++m) {
-    int64_t r = N0 + (wave + 4 * m) * 8 + lrow;
+  for (int m = 0; m < LB; ++m) {
+    int64_t r = N0 + (wave + kWaves * m) * 8 + lrow;
     r = r < c ? r : c - 1;
-    vb[m / WN][m % WN] = (unsigned)(((r - N0) * b + lp * 8) * 2);
+    vb[m] = (unsigned)(((r - N0) * b + lp * 8) * 2);
   }
-  const unsigned short* Xt = X + M0 * ldx;
-  const unsigned short* Wt = W + N0 * b;
-  // Stages past the last are loaded too (at most S - 1, never read), so that every
-  // stage has the same number of loads for the vmcnt waits; they re-read the last.
-  // Pieces past b re-read piece 0 of the stage; zero_tail clears them.
-  auto stage_k0 = [&](int it) {
+  // Stages past the last are loaded too (never read), so that every stage has the same
+  // number of loads for the vmcnt waits; they re-read the last. Pieces of the last
+  // stage past b re-read its piece 0; zero_tail clears them.
+  const int st_last = nk_all - 1;
+  const bool past = (int64_t)st_last * kLK + lp * 8 >= b;
+  const unsigned short *xs, *ws;  // the stages being issued
+  unsigned abase = 0, bbase = 0;
+  bool a_last = false, b_last = false;
+  auto stage_a = [&](int it) {
     const int st = s_begin + it;
-    return (int64_t)(st < nk_all ? st : nk_all - 1) * kLK;
-  };
-  auto issue_a = [&](int it) {
-    unsigned char* sbase = sm + (it % S) * kStage + wave * 1024;
-    const int64_t k0 = stage_k0(it);
-    const unsigned back = k0 + lp * 8 < b ? 0u : (unsigned)(lp * 16);
+    xs = X + M0 * ldx + (int64_t)(st < st_last ? st : st_last) * kLK;
+    abase = smb + (it % SA) * kA + wave * 1024;
+    if (st >= st_last && !a_last) {  // from here on every stage issued is the last one
+      a_last = true;
+      if (past) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      unsigned t[WM];
-#pragma unroll
-      for (int m = 0; m < WM; ++m) t[m] = va[h][m] - back;
-      lds_dma_s<WM>(t, Xt + k0, sbase + h * WM * 4096);
+        for (int m = 0; m < LA; ++m) va[m] -= lp * 16;
+      }
     }
   };
-  auto issue_b = [&](int it) {
-    unsigned char* sbase = sm + (it % S) * kStage + kA + wave * 1024;
-    const int64_t k0 = stage_k0(it);
-    const unsigned back = k0 + lp * 8 < b ? 0u : (unsigned)(lp * 16);
+  auto stage_b = [&](int it) {
+    const int st = s_begin + it;
+    ws = W + N0 * b + (int64_t)(st < st_last ? st : st_last) * kLK;
+    bbase = smb + SA * kA + (it % SB) * kB + wave * 1024;
+    if (st >= st_last && !b_last) {
+      b_last = true;
+      if (past) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      unsigned t[WN];
-#pragma unroll
-      for (int m = 0; m < WN; ++m) t[m] = vb[h][m] - back;
-      lds_dma_s<WN>(t, Wt + k0, sbase + h * WN * 4096);
+        for (int m = 0; m < LB; ++m) vb[m] -= lp * 16;
+      }
     }
   };
+  auto issue_a = [&](int m) { lds_dma1(va[m], xs, abase + m * kWaves * 1024); };
+  auto issue_b = [&](int m) { lds_dma1(vb[m], ws, bbase + m * kWaves * 1024); };
   // zero this wave's pieces of stage it that lie past b (its own loads have landed)
   auto zero_tail = [&](int it) {
     const int64_t k0 = (int64_t)(s_begin + it) * kLK;
     if (k0 + kLK <= b || k0 + lp * 8 < b) return;
-    unsigned char* sbase = sm + (it % S) * kStage + wave * 1024 + lane * 16;
+    unsigned char* za = sm + (it % SA) * kA + wave * 1024 + lane * 16;
+    unsigned char* zb = sm + SA * kA + (it % SB) * kB + wave * 1024 + lane * 16;
 #pragma unroll
-    for (int m = 0; m < 2 * WM; ++m) *(u32x4_t*)(sbase + m * 4096) = u32x4_t{0u, 0u, 0u, 0u};
+    for (int m = 0; m < LA; ++m) *(u32x4_t*)(za + m * kWaves * 1024) = u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int m = 0; m < 2 * WN; ++m) *(u32x4_t*)(sbase + kA + m * 4096) = u32x4_t{0u, 0u, 0u, 0u};
+    for (int m = 0; m < LB; ++m) *(u32x4_t*)(zb + m * kWaves * 1024) = u32x4_t{0u, 0u, 0u, 0u};
   };
 
   f32x16_t acc[WM][WN];
@@ -223,54 +228,84 @@ __global__ __launch_bounds__(kLThreads) void linear_tile_kernel(
   const int faddr = r32 * kLRow + ((half ^ ((r32 >> 1) & 7)) << 4);
   bf16x8_t a0[WM], b0[WN], a1[WM], b1[WN];
   auto read_frags = [&](int it, int sub, bf16x8_t (&a)[WM], bf16x8_t (&bb)[WN]) {
-    const unsigned char* st = sm + (it % S) * kStage + (faddr ^ (sub << 5));
+    const unsigned char* fa = sm + (it % SA) * kA + (faddr ^ (sub << 5));
+    const unsigned char* fb = sm + SA * kA + (it % SB) * kB + (faddr ^ (sub << 5));
 #pragma unroll
-    for (int i = 0; i < WM; ++i) a[i] = *(const bf16x8_t*)(st + (wm * WM + i) * 32 * kLRow);
+    for (int i = 0; i < WM; ++i) a[i] = *(const bf16x8_t*)(fa + (wm * WM + i) * 32 * kLRow);
 #pragma unroll
-    for (int j = 0; j < WN; ++j) bb[j] = *(const bf16x8_t*)(st + kA + (wn * WN + j) * 32 * kLRow);
+    for (int j = 0; j < WN; ++j) bb[j] = *(const bf16x8_t*)(fb + (wn * WN + j) * 32 * kLRow);
   };
-  auto mfmas = [&](const bf16x8_t (&a)[WM], const bf16x8_t (&bb)[WN]) {
+  // One substep's products. The order is pinned: the operand reads of the next
+  // substep go first, then the loads of a coming stage between the products, so
+  // that reads and loads issue while the matrix cores are busy.
+  auto mfmas = [&](const bf16x8_t (&a)[WM], const bf16x8_t (&bb)[WN], auto&& between) {
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < WM; ++i)
-#pragma unroll
-      for (int j = 0; j < WN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], bb[j], acc[i][j], 0, 0, 0);
+    for (int x = 0; x < WM * WN; ++x) {
+      const int i = x / WN, j = x % WN;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], bb[j], acc[i][j], 0, 0, 0);
+      between(x);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
-  // all but the newest S - 2 stages of this wave's loads have landed
+  // `per` loads after each product, B's before A's
+  auto load_one = [&](int m) {
+    if (m < LB) issue_b(m);
+    else if (m < LB + LA) issue_a(m - LB);
+  };
+  constexpr int kPer = (LA + LB + WM * WN - 1) / (WM * WN);
+  auto loads = [&](int x) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) load_one(x * kPer + m);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto no_loads = [](int) {};
+  // this wave's loads of the next stage have landed; of later stages they may be in
+  // flight (those of A where it runs further ahead: they are issued after B's)
   auto wait_loads = [&] {
-    constexpr int left = (S - 2) * 2 * (WM + WN);
-    static_assert(left == 0 || left == 8 || left == 16, "vmcnt immediates");
+    constexpr int left = (SA - 2) * LA + (SB - 2) * LB;
+    static_assert(SA == SB || SB == 2, "the newest loads belong to later stages");
+    static_assert(left == 0 || left == 4 || left == 8, "vmcnt immediates");
     if constexpr (left == 0)
       __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    else if constexpr (left == 8)
-      __asm__ volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    else if constexpr (left == 4)
+      __asm__ volatile("s_waitcnt vmcnt(4)" ::: "memory");
     else
-      __asm__ volatile("s_waitcnt vmcnt(16)" ::: "memory");
+      __asm__ volatile("s_waitcnt vmcnt(8)" ::: "memory");
   };
 
+  // prologue: B's stages 0 .. SB-2, then A's 0 .. SA-2, all waited for
 #pragma unroll
-  for (int it = 0; it < S - 1; ++it) {
-    issue_a(it);
-    issue_b(it);
+  for (int it = 0; it < SB - 1; ++it) {
+    stage_b(it);
+#pragma unroll
+    for (int m = 0; m < LB; ++m) issue_b(m);
   }
-  wait_loads();
+#pragma unroll
+  for (int it = 0; it < SA - 1; ++it) {
+    stage_a(it);
+#pragma unroll
+    for (int m = 0; m < LA; ++m) issue_a(m);
+  }
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
   zero_tail(0);
   __syncthreads();
   read_frags(0, 0, a0, b0);
   for (int it = 0; it < nk; ++it) {
-    issue_a(it + S - 1);  // its buffer was last read before the barrier of it-1
+    stage_b(it + SB - 1);  // into buffers last read before the barrier of it - 1
+    stage_a(it + SA - 1);
     read_frags(it, 1, a1, b1);
-    mfmas(a0, b0);
-    issue_b(it + S - 1);
+    mfmas(a0, b0, loads);
     read_frags(it, 2, a0, b0);
-    mfmas(a1, b1);
+    mfmas(a1, b1, no_loads);
     read_frags(it, 3, a1, b1);
-    mfmas(a0, b0);
+    mfmas(a0, b0, no_loads);
     wait_loads();
     zero_tail(it + 1);
     __syncthreads();
     read_frags(it + 1, 0, a0, b0);
-    mfmas(a1, b1);
+    mfmas(a1, b1, no_loads);
   }
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();  // every wave's loads have landed: the stages may be reused
@@ -280,7 +315,7 @@ __global__ __launch_bounds__(kLThreads) void linear_tile_kernel(
   // read back, a lane has 8 consecutive channels of one token. The row pitch puts
   // the two halves of a write 128 bytes apart in the banks.
   constexpr int kCols = 32 * WN, kPitch = kCols + 8;
-  static_assert(4 * 32 * kPitch * 4 <= S * kStage, "strips fit the stages");
+  static_assert(kWaves * 32 * kPitch * 4 <= SA * kA + SB * kB, "strips fit the stages");
   float* strip = (float*)sm + wave * 32 * kPitch;
   constexpr int kLanes = kCols / 8;      // lanes per token
   constexpr int kTok = 64 / kLanes;      // tokens per pass
@@ -432,14 +467,14 @@ LinPlan plan_of(int64_t n, int64_t b, int64_t c, bool can_split) {
   return p;
 }
 
-template <int WM, int WN, int S>
+template <int WM, int WN, int GN, int SA, int SB>
 hipError_t launch_tiles(const unsigned short* X, int64_t ldx, const unsigned short* W, int64_t n,
                         int64_t b, int64_t c, const LinPlan& p, float* part, const LinEpilogue& ep,
                         hipStream_t s) {
-  const int ntm = (int)cdiv(n, 64 * WM), ntn = (int)cdiv(c, 64 * WN);
+  const int ntm = (int)cdiv(n, 64 * WM), ntn = (int)cdiv(c, 32 * WN * GN);
   const int per_xcd = (int)cdiv((int64_t)ntm * ntn, 8);
-  hipLaunchKernelGGL((linear_tile_kernel<WM, WN, S>),
-                     dim3((unsigned)(8 * per_xcd), (unsigned)p.splits), dim3(kLThreads), 0, s, X,
+  hipLaunchKernelGGL((linear_tile_kernel<WM, WN, GN, SA, SB>),
+                     dim3((unsigned)(8 * per_xcd), (unsigned)p.splits), dim3(128 * GN), 0, s, X,
                      ldx, W, n, b, c, ntm, ntn, per_xcd, p.per, part, ep);
   return hipGetLastError();
 }
@@ -483,9 +518,9 @@ hipError_t launch_linear(const unsigned short* X, int64_t ldx, const unsigned sh
           : n <= 32 ? launch_skinny<2>(X, ldx, W, n, b, c, ep, s)
                     : launch_skinny<4>(X, ldx, W, n, b, c, ep, s);
       break;
-    case kLin64: e = launch_tiles<1, 1, 4>(X, ldx, W, n, b, c, p, raw, ep, s); break;
-    case kLin128: e = launch_tiles<2, 2, 2>(X, ldx, W, n, b, c, p, raw, ep, s); break;
-    default: e = launch_tiles<4, 4, 2>(X, ldx, W, n, b, c, p, raw, ep, s); break;
+    case kLin64: e = launch_tiles<1, 1, 2, 4, 4>(X, ldx, W, n, b, c, p, raw, ep, s); break;
+    case kLin128: e = launch_tiles<2, 2, 2, 2, 2>(X, ldx, W, n, b, c, p, raw, ep, s); break;
+    default: e = launch_tiles<4, 2, 4, 3, 2>(X, ldx, W, n, b, c, p, raw, ep, s); break;
   }
   if (e != hipSuccess || !raw) return e;
   const int64_t items = n * cdiv(c, 8);
