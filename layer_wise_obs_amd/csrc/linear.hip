@@ -7,13 +7,14 @@
 // a layer is what its pruned predecessors produce.
 //
 // Tiles of (64 WM) tokens x (64 WN) channels on four waves (2 x 2, each
-// 32 WM x 32 WN of v_mfma_f32_32x32x16_bf16 blocks). The contraction is contiguous
+// 32 WM x 32 WN of v_mfma_f32_16x16x32_bf16 blocks: at this card's power limit they
+// run at 1.86 GHz, the 32x32x16 form at 1.66). The contraction is contiguous
 // in both operands, so an MFMA operand (8 consecutive k of a row per lane) is one
 // 16-byte LDS read. Stages of 64 k (128-byte rows, whole cache lines) are filled by
 // direct global->LDS loads, S stages deep; the 16-byte pieces of a row are
 // XOR-swizzled by (row / 2) & 7, so the operand reads (16 rows at one piece per 16
-// lanes) use all 64 banks. Fragments are double-buffered over the four 16-wide
-// substeps of a stage. Tiles are walked in groups of 8 token tiles per channel tile,
+// lanes) use all 64 banks. Fragments are double-buffered over the two 32-wide
+// substeps of a stage. Tiles are walked in groups of 4 token tiles per channel tile,
 // each XCD a contiguous range of that order, so that the workgroups of an XCD share
 // X and W slices in its L2.
 #include "common.h"
@@ -24,7 +25,7 @@ namespace th {
 namespace {
 
 constexpr int kLK = 64;  // contraction per stage
-constexpr int kLGroup = 8;  // token tiles per group in the walk order
+constexpr int kLGroup = 4;  // token tiles per group in the walk order
 constexpr int kLRow = kLK * 2;
 
 struct LinEpilogue {
@@ -126,6 +127,7 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
     float* __restrict__ part, LinEpilogue ep) {
   constexpr int TM = 64 * WM, TN = 32 * WN * GN;
   constexpr int kWaves = 2 * GN;
+  constexpr int FM = 2 * WM, FN = 2 * WN;  // 16 x 16 blocks of a wave
   constexpr int LA = TM / 8 / kWaves, LB = TN / 8 / kWaves;  // 1 KB loads per wave and stage
   constexpr int kA = TM * kLRow, kB = TN * kLRow;  // one stage of either operand
   const int wg = blockIdx.x;
@@ -215,50 +217,51 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
     for (int m = 0; m < LB; ++m) *(u32x4_t*)(zb + m * kWaves * 1024) = u32x4_t{0u, 0u, 0u, 0u};
   };
 
-  f32x16_t acc[WM][WN];
+  f32x4_t acc[FM][FN];
 #pragma unroll
-  for (int i = 0; i < WM; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < WN; ++j)
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int r16 = lane & 15, quad = lane >> 4;
+  // operand address of a 16-row block: its row is a multiple of 16, so the swizzle is
+  // the lane's own and a substep only XORs a piece bit
+  const int faddr = r16 * kLRow + ((quad ^ ((r16 >> 1) & 7)) << 4);
+  bf16x8_t a0[FM], b0[FN], a1[FM], b1[FN];
+  auto read_frags = [&](int it, int sub, bf16x8_t (&a)[FM], bf16x8_t (&bb)[FN]) {
+    const unsigned char* fa = sm + (it % SA) * kA + (faddr ^ (sub << 6));
+    const unsigned char* fb = sm + SA * kA + (it % SB) * kB + (faddr ^ (sub << 6));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-  const int r32 = lane & 31, half = lane >> 5;
-  // operand address of a 32-row block: its row is a multiple of 32, so the swizzle is
-  // the lane's own and a substep only XORs piece bits
-  const int faddr = r32 * kLRow + ((half ^ ((r32 >> 1) & 7)) << 4);
-  bf16x8_t a0[WM], b0[WN], a1[WM], b1[WN];
-  auto read_frags = [&](int it, int sub, bf16x8_t (&a)[WM], bf16x8_t (&bb)[WN]) {
-    const unsigned char* fa = sm + (it % SA) * kA + (faddr ^ (sub << 5));
-    const unsigned char* fb = sm + SA * kA + (it % SB) * kB + (faddr ^ (sub << 5));
+    for (int i = 0; i < FM; ++i) a[i] = *(const bf16x8_t*)(fa + (wm * FM + i) * 16 * kLRow);
 #pragma unroll
-    for (int i = 0; i < WM; ++i) a[i] = *(const bf16x8_t*)(fa + (wm * WM + i) * 32 * kLRow);
-#pragma unroll
-    for (int j = 0; j < WN; ++j) bb[j] = *(const bf16x8_t*)(fb + (wn * WN + j) * 32 * kLRow);
+    for (int j = 0; j < FN; ++j) bb[j] = *(const bf16x8_t*)(fb + (wn * FN + j) * 16 * kLRow);
   };
   // One substep's products. The order is pinned: the operand reads of the next
   // substep go first, then the loads of a coming stage between the products, so
   // that reads and loads issue while the matrix cores are busy.
-  auto mfmas = [&](const bf16x8_t (&a)[WM], const bf16x8_t (&bb)[WN], auto&& between) {
+  auto mfmas = [&](const bf16x8_t (&a)[FM], const bf16x8_t (&bb)[FN], auto&& between) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int x = 0; x < WM * WN; ++x) {
-      const int i = x / WN, j = x % WN;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], bb[j], acc[i][j], 0, 0, 0);
+    for (int x = 0; x < FM * FN; ++x) {
+      const int i = x / FN, j = x % FN;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], bb[j], acc[i][j], 0, 0, 0);
       between(x);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // `per` loads after each product, B's before A's
+  // one load after every kGap-th product, B's before A's
+  constexpr int kGap = FM * FN / (LA + LB) > 0 ? FM * FN / (LA + LB) : 1;
+  constexpr int kPer = (LA + LB + FM * FN - 1) / (FM * FN);
   auto load_one = [&](int m) {
     if (m < LB) issue_b(m);
     else if (m < LB + LA) issue_a(m - LB);
   };
-  constexpr int kPer = (LA + LB + WM * WN - 1) / (WM * WN);
   auto loads = [&](int x) {
-    __builtin_amdgcn_sched_barrier(0);
+    if (x % kGap == 0) {
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int m = 0; m < kPer; ++m) load_one(x * kPer + m);
-    __builtin_amdgcn_sched_barrier(0);
+      for (int m = 0; m < kPer; ++m) load_one(x / kGap * kPer + m);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   auto no_loads = [](int) {};
   // this wave's loads of the next stage have landed; of later stages they may be in
@@ -297,10 +300,6 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
     stage_a(it + SA - 1);
     read_frags(it, 1, a1, b1);
     mfmas(a0, b0, loads);
-    read_frags(it, 2, a0, b0);
-    mfmas(a1, b1, no_loads);
-    read_frags(it, 3, a1, b1);
-    mfmas(a0, b0, no_loads);
     wait_loads();
     zero_tail(it + 1);
     __syncthreads();
@@ -311,10 +310,10 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
   __syncthreads();  // every wave's loads have landed: the stages may be reused
 
   // Epilogue through LDS, one 32-token strip of the wave's block at a time: the lane
-  // holds channel r32 of each 32 x 32 block and tokens 8 (e / 4) + 4 half + (e % 4);
-  // read back, a lane has 8 consecutive channels of one token. The row pitch puts
-  // the two halves of a write 128 bytes apart in the banks.
-  constexpr int kCols = 32 * WN, kPitch = kCols + 8;
+  // holds channel l % 16 of each 16 x 16 block and tokens 4 (l / 16) + e; read back, a
+  // lane has 8 consecutive channels of one token. The row pitch puts the four quarters
+  // of a write 64 bytes apart in the banks.
+  constexpr int kCols = 32 * WN, kPitch = kCols + 4;
   static_assert(kWaves * 32 * kPitch * 4 <= SA * kA + SB * kB, "strips fit the stages");
   float* strip = (float*)sm + wave * 32 * kPitch;
   constexpr int kLanes = kCols / 8;      // lanes per token
@@ -323,10 +322,12 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
 #pragma unroll
   for (int i = 0; i < WM; ++i) {
 #pragma unroll
-    for (int j = 0; j < WN; ++j)
+    for (int i2 = 0; i2 < 2; ++i2)
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        strip[((e >> 2) * 8 + half * 4 + (e & 3)) * kPitch + j * 32 + r32] = acc[i][j][e];
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          strip[(i2 * 16 + quad * 4 + e) * kPitch + j * 16 + r16] = acc[2 * i + i2][j][e];
     wave_sync();
 #pragma unroll 1
     for (int t0 = 0; t0 < 32; t0 += kTok) {
