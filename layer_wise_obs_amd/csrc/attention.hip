@@ -32,14 +32,13 @@ namespace th {
 
 namespace {
 
-constexpr int kAThreads = 256;
-constexpr int kABM = 128;  // rows per workgroup
 constexpr int kAKT = 64;   // keys per tile
 constexpr float kAMove = 8.0f;  // log2 of how far p may pass 1 before m moves
 
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
 typedef short v8i16_t __attribute__((ext_vector_type(8)));
 typedef unsigned short u16x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 
 struct AttnArgs {
   const unsigned short *q, *k, *v;
@@ -65,9 +64,10 @@ __device__ __forceinline__ int64_t start_at(const int32_t* s, int i, int64_t n) 
 // slots as the sequence has row blocks lie before the next one's. Returns the
 // sequence that holds `slot` (the last whose slots begin at or before it), or -1;
 // 64 starts are looked at a time.
+template <int BM>
 __device__ __forceinline__ int sequence_of(const AttnArgs& a, int64_t slot, int lane) {
   int lo = 0, len = a.nseq;
-  auto begin = [&](int s) { return start_at(a.q_start, s, a.nq) * a.g / kABM + s; };
+  auto begin = [&](int s) { return start_at(a.q_start, s, a.nq) * a.g / BM + s; };
   while (len > 0) {
     const int step = (len + 63) >> 6;
     const int at = lane * step;
@@ -85,34 +85,49 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 
 // Maximum over the two lanes (l, l + 32) that share a query.
 __device__ __forceinline__ float half_max(float x) {
-  return fmaxf(x, __shfl_xor(x, 32));
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+// v_max3_f32: two maxima in one instruction, NaN operands ignored like fmaxf's (which
+// the compiler precedes by a canonicalising maximum of either operand). The compiler
+// does not know the instruction, so it puts no wait between a matrix product and it: a
+// and the products of b and c must have been waited for by an ordinary operation that
+// `a` depends on.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  __asm__("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
 }
 
-__device__ __forceinline__ unsigned pack2(float a, float b) {
-  return (unsigned)f32_to_bf16_rne(a) | ((unsigned)f32_to_bf16_rne(b) << 16);
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ bf16x2_t pack2(float a, float b) {
+  return bf16x2_t{(__bf16)a, (__bf16)b};  // v_cvt_pk_bf16_f32, round to nearest even
 }
 
-template <int D>
-__global__ __launch_bounds__(kAThreads, 2) void attention_kernel(AttnArgs a) {
+// NW waves of 32 rows; ST tiles of keys in LDS.
+template <int D, int NW, int ST>
+__global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
+  constexpr int kBM = 32 * NW;
   constexpr int kPieces = D / 8;             // 16-byte pieces per row
   constexpr int kRowB = D * 2;
   constexpr int kTile = kAKT * kRowB;        // one operand's tile
-  constexpr int kLd = kTile / 4096;          // 1 KB loads per wave and operand
+  constexpr int kLd = kTile / 1024 / NW;     // 1 KB loads per wave and operand
   constexpr int kRowsPer = 64 / kPieces;     // rows per 1 KB
   constexpr int kDB = D / 32, kKS = D / 16;
-  __shared__ __attribute__((aligned(1024))) unsigned char sm[4 * kTile];  // K0 K1 V0 V1
+  __shared__ __attribute__((aligned(1024))) unsigned char sm[2 * ST * kTile];  // K tiles, V tiles
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int head = blockIdx.x % a.hk;
   // the last slots first: a causal sequence's longest rows are its last
   const int64_t slot = (int64_t)(gridDim.x / a.hk) - 1 - blockIdx.x / a.hk;
-  const int seq = sequence_of(a, slot, lane);
+  const int seq = sequence_of<kBM>(a, slot, lane);
   if (seq < 0) return;
   const int64_t q0 = start_at(a.q_start, seq, a.nq), q1 = start_at(a.q_start, seq + 1, a.nq);
   const int64_t k0 = start_at(a.k_start, seq, a.nk), k1 = start_at(a.k_start, seq + 1, a.nk);
   const int lk = k1 > k0 ? (int)(k1 - k0) : 0;
   const int64_t rows = q1 > q0 ? (q1 - q0) * a.g : 0;
-  const int64_t row0 = (slot - (q0 * a.g / kABM + seq)) * kABM;
+  const int64_t row0 = (slot - (q0 * a.g / kBM + seq)) * kBM;
   if (row0 < 0 || row0 >= rows) return;
   const int off = lk - (int)(q1 - q0);  // key of the same age as query 0
 
@@ -122,7 +137,7 @@ __global__ __launch_bounds__(kAThreads, 2) void attention_kernel(AttnArgs a) {
     const int64_t e = (int64_t)((unsigned)r / (unsigned)a.g) + off + 1;
     return (int)(e < 0 ? 0 : (e < lk ? e : lk));
   };
-  const int64_t row_end = row0 + kABM < rows ? row0 + kABM : rows;
+  const int64_t row_end = row0 + kBM < rows ? row0 + kBM : rows;
   const int keys = limit_of(row_end - 1);
   const int per = (int)cdiv(cdiv(keys, kAKT), a.splits) * kAKT;
   const int kbeg = min(keys, (int)blockIdx.y * per), kend = min(keys, kbeg + per);
@@ -161,36 +176,37 @@ __global__ __launch_bounds__(kAThreads, 2) void attention_kernel(AttnArgs a) {
     for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
   float m = -INFINITY, l = 0.f;
 
-  // Loader: chunk wave + 4 i of a tile (1 KB, kRowsPer rows); lane l fills row
+  // Loader: chunk wave + NW i of a tile (1 KB, kRowsPer rows); lane l fills row
   // kRowsPer chunk + l / kPieces at physical piece l % kPieces. K pieces are
   // swizzled by the row so that 16 rows at one piece spread over all banks, V
-  // pieces so that 4 rows x 64 bytes do.
+  // pieces so that 4 rows x 64 bytes do; either is the same in a lane's chunks.
   const int lr = lane / kPieces, lpp = lane % kPieces;
-  const int row_w = wave * kRowsPer + lr;  // + 4 i kRowsPer
+  const int row_w = wave * kRowsPer + lr;  // + NW i kRowsPer
   const int swk = D == 128 ? (row_w & 15) : ((row_w >> 1) & 7);
   const int swv = D == 128 ? ((row_w & 3) << 2) : (((row_w >> 1) & 1) << 2);
+  static_assert(D == 64 || NW * kRowsPer % 16 == 0, "one K swizzle per lane");
   const int ck = (lpp ^ swk) * 8, cv = (lpp ^ swv) * 8;
   const unsigned short* kb = a.k + k0 * a.k_token + head * a.k_head + ck;
   const unsigned short* vb = a.v + k0 * a.v_token + head * a.v_head + cv;
   const bool in_k = ck < a.d, in_v = cv < a.d;
   if (a.d < D) {  // pieces past the head are zero in every tile
-    for (int i = tid; i < 4 * kTile / 16; i += kAThreads)
+    for (int i = tid; i < 2 * ST * kTile / 16; i += 64 * NW)
       *(u32x4_t*)(sm + i * 16) = u32x4_t{0u, 0u, 0u, 0u};
     __syncthreads();
   }
+  const unsigned smb = lds_address(sm);
   auto issue = [&](int kt, int buf) {
-    const void *gk[kLd], *gv[kLd];
+    const unsigned dk = smb + buf * kTile + wave * 1024;
+    const unsigned dv = smb + (ST + buf) * kTile + wave * 1024;
 #pragma unroll
     for (int i = 0; i < kLd; ++i) {
-      int key = kt + row_w + 4 * i * kRowsPer;
+      int key = kt + row_w + NW * i * kRowsPer;
       key = key < lk ? key : lk - 1;  // rows past the keys are masked
-      gk[i] = kb + (int64_t)key * a.k_token;
-      gv[i] = vb + (int64_t)key * a.v_token;
+      const unsigned short* gk = kb + (int64_t)key * a.k_token;
+      const unsigned short* gv = vb + (int64_t)key * a.v_token;
+      if (in_k) lds_dma1v(gk, dk + i * NW * 1024);
+      if (in_v) lds_dma1v(gv, dv + i * NW * 1024);
     }
-    unsigned char* dk = sm + buf * kTile + wave * 1024;
-    unsigned char* dv = sm + (2 + buf) * kTile + wave * 1024;
-    if (in_k) lds_dma_v<kLd>(gk, dk);
-    if (in_v) lds_dma_v<kLd>(gv, dv);
   };
 
   // operand addresses inside a tile; the step's piece bits are XORed in
@@ -203,16 +219,18 @@ __global__ __launch_bounds__(kAThreads, 2) void attention_kernel(AttnArgs a) {
   const int vpiece = 2 * ((lane >> 4) & 1) + ((s16 & 3) >> 1);
   const int vaddr = vkey * kRowB + ((vpiece ^ vswz) << 4) + (s16 & 1) * 8;
 
-  if (kbeg < kend) issue(kbeg, 0);
-  int buf = 0;
-  for (int kt = kbeg; kt < kend; kt += kAKT, buf ^= 1) {
-    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();  // this tile has landed; the other buffer was last read before it
-    if (kt + kAKT < kend) issue(kt + kAKT, buf ^ 1);
-    if (kt >= lim_last) continue;  // no row of this wave sees the tile
-    const unsigned char* ks = sm + buf * kTile;
-    const unsigned char* vs = sm + (2 + buf) * kTile;
-
+  const unsigned char *ks, *vs;  // the tile at hand
+  auto v_frag = [&](int ks16, int db) {
+    const unsigned char* p = vs + ks16 * 16 * kRowB + (vaddr ^ (db << 6));
+    const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) v4i16_t*)p);
+    const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) v4i16_t*)(p + 8 * kRowB));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  // One tile of 64 keys from kt; MASKED: some row of the wave does not see all of them.
+  auto tile = [&](int kt, auto MASKED) __attribute__((always_inline)) {
+    constexpr bool masked = decltype(MASKED)::value;
     f32x16_t s[2];
 #pragma unroll
     for (int b2 = 0; b2 < 2; ++b2)
@@ -224,10 +242,9 @@ __global__ __launch_bounds__(kAThreads, 2) void attention_kernel(AttnArgs a) {
       for (int b2 = 0; b2 < 2; ++b2) {
         const bf16x8_t kf = *(const bf16x8_t*)(ks + b2 * 32 * kRowB + (kaddr ^ (st << 5)));
         s[b2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[st], s[b2], 0, 0, 0);
+        if (b2 == 1 && st % 2 == 1) __builtin_amdgcn_sched_barrier(0);
       }
-
-    const bool masked = kt + kAKT > lim_first;
-    if (masked) {
+    if constexpr (masked) {
 #pragma unroll
       for (int b2 = 0; b2 < 2; ++b2)
 #pragma unroll
@@ -236,11 +253,9 @@ __global__ __launch_bounds__(kAThreads, 2) void attention_kernel(AttnArgs a) {
           s[b2][e] = key < lim ? s[b2][e] : -INFINITY;
         }
     }
-    float top = -INFINITY;
+    float top = fmaxf(s[0][0], s[1][0]);  // waits for the products of both blocks
 #pragma unroll
-    for (int b2 = 0; b2 < 2; ++b2)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b2][e]);
+    for (int e = 1; e < 16; ++e) top = max3(top, s[0][e], s[1][e]);
     top = half_max(top) * a.c;
     if (__any(top > m + kAMove)) {  // also the first tile, where m is -inf
       const float mn = fmaxf(m, top);
@@ -252,77 +267,97 @@ __global__ __launch_bounds__(kAThreads, 2) void attention_kernel(AttnArgs a) {
         for (int e = 0; e < 16; ++e) o[i][e] *= f;
       m = mn;
     }
-    const float ref = m == -INFINITY ? 0.f : m;
+    const float ref = m == -INFINITY ? 0.f : -m;
     bf16x8_t pf[4];
 #pragma unroll
     for (int ks16 = 0; ks16 < 4; ++ks16) {
-      u32x4_t u;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int e = (ks16 & 1) * 8 + 2 * x;
-        const float p0 = exp2_fast(fmaf(s[ks16 >> 1][e], a.c, -ref));
-        const float p1 = exp2_fast(fmaf(s[ks16 >> 1][e + 1], a.c, -ref));
-        l += p0 + p1;
-        u[x] = pack2(p0, p1);
+        const bf16x2_t p = pack2(exp2_fast(fmaf(s[ks16 >> 1][e], a.c, ref)),
+                                 exp2_fast(fmaf(s[ks16 >> 1][e + 1], a.c, ref)));
+        // the sum takes the rounded weights, which are the ones that V meets
+        l = __builtin_amdgcn_fdot2_f32_bf16(p, bf16x2_t{(__bf16)1.0f, (__bf16)1.0f}, l, false);
+        pf[ks16][2 * x] = p[0];
+        pf[ks16][2 * x + 1] = p[1];
       }
-      pf[ks16] = __builtin_bit_cast(bf16x8_t, u);
     }
-
-    auto v_frag = [&](int ks16, int db) {
-      const unsigned char* p = vs + ks16 * 16 * kRowB + (vaddr ^ (db << 6));
-      const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) v4i16_t*)p);
-      const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) v4i16_t*)(p + 8 * kRowB));
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    };
-    // A hidden key's p is 0, but 0 times an infinity or NaN in its V row is not: a
-    // tile with hidden keys is looked through, and where V holds such a value the
+    // A hidden key's p is 0, but 0 times an infinity or NaN in its V row is not: in a
+    // tile with hidden keys V is looked through, and where it holds such a value the
     // products are taken key by key and kept for the rows that see the key.
-    bool special = false;
-    if (masked) {
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (masked) {
       unsigned bad = 0;
 #pragma unroll
-      for (int ks16 = 0; ks16 < 4; ++ks16)
+      for (int ks16 = 0; ks16 < 4; ++ks16) {
+        if (kt + 16 * ks16 + 16 <= lim_first) continue;  // every row sees these keys
 #pragma unroll
         for (int db = 0; db < kDB; ++db) {
-          const v8i16_t vf = v_frag(ks16, db);
+          const u32x4_t u = __builtin_bit_cast(u32x4_t, v_frag(ks16, db));
+          // an exponent of all ones, plus one in its last place, sets the sign bit
 #pragma unroll
-          for (int x = 0; x < 8; ++x) bad |= (vf[x] & 0x7f80) == 0x7f80 ? 1u : 0u;
+          for (int x = 0; x < 4; ++x) bad |= (u[x] & 0x7f807f80u) + 0x00800080u;
         }
-      special = __any(bad);
-    }
-    if (!special) {
+      }
+      if (__any((bad & 0x80008000u) != 0)) {
 #pragma unroll
-      for (int ks16 = 0; ks16 < 4; ++ks16)
+        for (int ks16 = 0; ks16 < 4; ++ks16)
 #pragma unroll
-        for (int db = 0; db < kDB; ++db)
-          o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              __builtin_bit_cast(bf16x8_t, v_frag(ks16, db)), pf[ks16], o[db], 0, 0, 0);
-    } else {
-#pragma unroll
-      for (int ks16 = 0; ks16 < 4; ++ks16)
-#pragma unroll
-        for (int db = 0; db < kDB; ++db) {
-          const v8i16_t vf = v_frag(ks16, db);
+          for (int db = 0; db < kDB; ++db) {
+            const v8i16_t vf = v_frag(ks16, db);
 #pragma unroll 1
-          for (int j = 0; j < 16; ++j) {  // key kt + 16 ks16 + j: element x of half h
-            const int jh = (j >> 2) & 1, jx = (j & 3) + 4 * (j >> 3);
-            v8i16_t one;
+            for (int j = 0; j < 16; ++j) {  // key kt + 16 ks16 + j: element x of half h
+              const int jh = (j >> 2) & 1, jx = (j & 3) + 4 * (j >> 3);
+              v8i16_t one;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) one[x] = half == jh && x == jx ? vf[x] : (short)0;
-            f32x16_t z;
+              for (int x = 0; x < 8; ++x) one[x] = half == jh && x == jx ? vf[x] : (short)0;
+              f32x16_t z;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) z[e] = 0.f;
-            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, one), pf[ks16],
-                                                        z, 0, 0, 0);
-            if (kt + 16 * ks16 + j < lim) {
+              for (int e = 0; e < 16; ++e) z[e] = 0.f;
+              z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, one),
+                                                          pf[ks16], z, 0, 0, 0);
+              if (kt + 16 * ks16 + j < lim) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[db][e] += z[e];
+                for (int e = 0; e < 16; ++e) o[db][e] += z[e];
+              }
             }
           }
-        }
+        return;
+      }
     }
+#pragma unroll
+    for (int ks16 = 0; ks16 < 4; ++ks16)
+#pragma unroll
+      for (int db = 0; db < kDB; ++db)
+        o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_bit_cast(bf16x8_t, v_frag(ks16, db)), pf[ks16], o[db], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i)
+    if (kbeg + i * kAKT < kend) issue(kbeg + i * kAKT, i);
+  int buf = 0;
+  for (int kt = kbeg; kt < kend; kt += kAKT) {
+    // this tile has landed (at most ST - 2 later ones are in flight)
+    static_assert(ST == 2 || (ST == 3 && kLd <= 2), "vmcnt immediates");
+    if (ST == 2 || kt + kAKT >= kend)
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    else if (kLd == 2)
+      __asm__ volatile("s_waitcnt vmcnt(4)" ::: "memory");
+    else
+      __asm__ volatile("s_waitcnt vmcnt(2)" ::: "memory");
+    __syncthreads();  // the buffer filled next was last read before this barrier
+    const int next = buf == 0 ? ST - 1 : buf - 1;
+    if (kt + (ST - 1) * kAKT < kend) issue(kt + (ST - 1) * kAKT, next);
+    ks = sm + buf * kTile;
+    vs = sm + (ST + buf) * kTile;
+    buf = buf == ST - 1 ? 0 : buf + 1;
+    if (kt >= lim_last) continue;  // no row of this wave sees the tile
+    if (kt + kAKT <= lim_first)
+      tile(kt, std::integral_constant<bool, false>{});
+    else
+      tile(kt, std::integral_constant<bool, true>{});
   }
 
   l += __shfl_xor(l, 32);
@@ -352,11 +387,12 @@ __global__ __launch_bounds__(kAThreads, 2) void attention_kernel(AttnArgs a) {
     for (int x = 0; x < 4; ++x) {
       const int e = db * 32 + 8 * x + 4 * half;
       if (e < a.d) {
-        u16x4_t w;
+        bf16x2_t w[2];
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-          w[y] = visible > 0 ? f32_to_bf16_rne(o[db][4 * x + y] * inv) : (unsigned short)0;
-        *(u16x4_t*)(op + e) = w;
+        for (int y = 0; y < 2; ++y)
+          w[y] = visible > 0 ? pack2(o[db][4 * x + 2 * y] * inv, o[db][4 * x + 2 * y + 1] * inv)
+                             : pack2(0.f, 0.f);
+        *(bf16x4_t*)(op + e) = __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3);
       }
     }
 }
@@ -391,6 +427,14 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   *(u16x4_t*)(a.o + tok * a.o_token + qh * a.o_head + e) = w;
 }
 
+template <int D, int NW, int ST>
+void launch_rows(const AttnArgs& a, hipStream_t s) {
+  const int64_t slots = a.nq * a.g / (32 * NW) + a.nseq;
+  hipLaunchKernelGGL((attention_kernel<D, NW, ST>),
+                     dim3((unsigned)(slots * a.hk), (unsigned)a.splits), dim3(64 * NW), 0, s, a);
+}
+
+constexpr int kABM = 128;      // rows per workgroup
 constexpr int kAUnits = 256;  // compute units
 
 // Pieces the keys are split into: enough for two workgroups per compute unit, with
@@ -445,12 +489,10 @@ hipError_t launch_attention(const void* Q, const void* K, const void* V, const i
   a.splits = workspace ? splits_of(p) : 1;
   a.part_ml = (float2*)workspace;
   a.part_o = workspace ? (float*)(a.part_ml + (size_t)a.splits * p->nq * p->hq) : nullptr;
-  const int64_t slots = p->nq * a.g / kABM + p->nseq;
-  const dim3 grid((unsigned)(slots * p->hk), (unsigned)a.splits);
   if (p->d <= 64)
-    hipLaunchKernelGGL((attention_kernel<64>), grid, dim3(kAThreads), 0, s, a);
+    launch_rows<64, 4, 2>(a, s);
   else
-    hipLaunchKernelGGL((attention_kernel<128>), grid, dim3(kAThreads), 0, s, a);
+    launch_rows<128, 4, 2>(a, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)cdiv(p->nq * p->hq, 8)), dim3(256), 0, s,

@@ -65,14 +65,6 @@ __device__ __forceinline__ void lds_dma1(unsigned vo, const void* g, unsigned ld
                    : "s"(lds), "v"(vo), "s"(g)
                    : "m0");
 }
-// One dword per lane into 256 bytes of LDS that nobody reads: brings the lanes' cache
-// lines into L2 without a result register.
-__device__ __forceinline__ void lds_dma_touch(unsigned vo, const void* g, unsigned lds) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-                   :
-                   : "s"(lds), "v"(vo), "s"(g)
-                   : "m0");
-}
 
 __device__ __forceinline__ void lds_dma10s(const unsigned (&vo)[5], const void* gbase0,
                                            const void* gbase1, const void* lds) {
@@ -100,35 +92,13 @@ __device__ __forceinline__ void lds_dma10s(const unsigned (&vo)[5], const void* 
 }
 
 
-// N loads (2 or 4) of 16 bytes per lane straight into LDS from one address per
-// lane: load m writes the 1 KB chunk at lds + 4096 m. Lanes that are off write
-// nothing; the others keep their places.
-template <int N>
-__device__ __forceinline__ void lds_dma_v(const void* const (&g)[N], const void* lds) {
-  static_assert(N == 2 || N == 4, "two or four loads");
-  const unsigned base = __builtin_amdgcn_readfirstlane(
-      (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
-  unsigned saved;
-  if constexpr (N == 4)
-    __asm__ volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\t"
-        "s_add_u32 m0, %1, 4096\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, off\n\t"
-        "s_add_u32 m0, %1, 8192\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, off\n\t"
-        "s_add_u32 m0, %1, 12288\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %5, off\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(base), "v"(g[0]), "v"(g[1]), "v"(g[2]), "v"(g[3])
-        : "scc");
-  else
-    __asm__ volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\t"
-        "s_add_u32 m0, %1, 4096\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, off\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(base), "v"(g[0]), "v"(g[1])
-        : "scc");
+// The same from one 64-bit address per lane. Lanes that are off write nothing; the
+// others keep their places.
+__device__ __forceinline__ void lds_dma1v(const void* g, unsigned lds) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                   :
+                   : "s"(lds), "v"(g)
+                   : "m0");
 }
 
 }  // namespace th
