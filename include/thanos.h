@@ -331,7 +331,8 @@ typedef struct {
 } th_attention_params;
 
 /* dt must be TH_BF16; 8 <= d <= 128, d % 8 == 0; hk divides hq; strides are multiples
- * of 8 and Q, K, V, O 16-byte aligned; nq * hq / hk, nk < 2^31 - 2^16. O must not
+ * of 8 (k_token, v_token < 2^24) and Q, K, V, O 16-byte aligned; nq * hq / hk,
+ * nk < 2^31 - 2^16. O must not
  * overlap the inputs. Scores, maxima, sums and O accumulate in fp32; the weights
  * enter the second product rounded to bf16. workspace (optional, may be NULL with
  * workspace_bytes 0; 16-byte aligned) lets launches of few queries split the keys;

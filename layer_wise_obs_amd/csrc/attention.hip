@@ -104,8 +104,8 @@ __device__ __forceinline__ bf16x2_t pack2(float a, float b) {
   return bf16x2_t{(__bf16)a, (__bf16)b};  // v_cvt_pk_bf16_f32, round to nearest even
 }
 
-// NW waves of 32 rows; ST tiles of keys in LDS.
-template <int D, int NW, int ST>
+// NW waves of 32 rows; ST tiles of keys in LDS; PAD: the head is shorter than D.
+template <int D, int NW, int ST, bool PAD>
 __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   constexpr int kBM = 32 * NW;
   constexpr int kPieces = D / 8;             // 16-byte pieces per row
@@ -186,26 +186,39 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   const int swv = D == 128 ? ((row_w & 3) << 2) : (((row_w >> 1) & 1) << 2);
   static_assert(D == 64 || NW * kRowsPer % 16 == 0, "one K swizzle per lane");
   const int ck = (lpp ^ swk) * 8, cv = (lpp ^ swv) * 8;
-  const unsigned short* kb = a.k + k0 * a.k_token + head * a.k_head + ck;
-  const unsigned short* vb = a.v + k0 * a.v_token + head * a.v_head + cv;
-  const bool in_k = ck < a.d, in_v = cv < a.d;
-  if (a.d < D) {  // pieces past the head are zero in every tile
+  const unsigned short* kb = a.k + k0 * a.k_token + head * a.k_head;
+  const unsigned short* vb = a.v + k0 * a.v_token + head * a.v_head;
+  const bool in_k = !PAD || ck < a.d, in_v = !PAD || cv < a.d;
+  if constexpr (PAD) {  // pieces past the head are zero in every tile
     for (int i = tid; i < 2 * ST * kTile / 16; i += 64 * NW)
       *(u32x4_t*)(sm + i * 16) = u32x4_t{0u, 0u, 0u, 0u};
     __syncthreads();
   }
   const unsigned smb = lds_address(sm);
-  auto issue = [&](int kt, int buf) {
-    const unsigned dk = smb + buf * kTile + wave * 1024;
-    const unsigned dv = smb + (ST + buf) * kTile + wave * 1024;
+  // byte offsets from the tile's first key (64 rows of less than 2^24 elements)
+  unsigned vk[kLd], vv[kLd];
+  auto offsets = [&](int last) {  // rows past `last` read that one: they are masked
 #pragma unroll
     for (int i = 0; i < kLd; ++i) {
-      int key = kt + row_w + NW * i * kRowsPer;
-      key = key < lk ? key : lk - 1;  // rows past the keys are masked
-      const unsigned short* gk = kb + (int64_t)key * a.k_token;
-      const unsigned short* gv = vb + (int64_t)key * a.v_token;
-      if (in_k) lds_dma1v(gk, dk + i * NW * 1024);
-      if (in_v) lds_dma1v(gv, dv + i * NW * 1024);
+      const unsigned row = min(row_w + NW * i * kRowsPer, last);
+      vk[i] = (row * (unsigned)a.k_token + ck) * 2;
+      vv[i] = (row * (unsigned)a.v_token + cv) * 2;
+    }
+  };
+  offsets(kAKT - 1);
+  auto issue = [&](int kt, int buf) {
+    if (kt + kAKT > lk) offsets(lk - 1 - kt);  // the sequence's last tile
+    const unsigned short* gk = kb + (int64_t)kt * a.k_token;
+    const unsigned short* gv = vb + (int64_t)kt * a.v_token;
+    const unsigned dk = smb + buf * kTile + wave * 1024;
+    const unsigned dv = smb + (ST + buf) * kTile + wave * 1024;
+    if (in_k) {
+#pragma unroll
+      for (int i = 0; i < kLd; ++i) lds_dma1(vk[i], gk, dk + i * NW * 1024);
+    }
+    if (in_v) {
+#pragma unroll
+      for (int i = 0; i < kLd; ++i) lds_dma1(vv[i], gv, dv + i * NW * 1024);
     }
   };
 
@@ -228,23 +241,36 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
         (__attribute__((address_space(3))) v4i16_t*)(p + 8 * kRowB));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  // One tile of 64 keys from kt; MASKED: some row of the wave does not see all of them.
-  auto tile = [&](int kt, auto MASKED) __attribute__((always_inline)) {
-    constexpr bool masked = decltype(MASKED)::value;
+  // One tile of 64 keys from kt.
+  auto tile = [&](int kt) __attribute__((always_inline)) {
+    // Scores: the operands of two steps (four blocks) are read while the products of
+    // the two before run; the order is pinned.
     f32x16_t s[2];
+    bf16x8_t kf[2][4];
+    auto read_k = [&](int st2, bf16x8_t (&f)[4]) {
 #pragma unroll
-    for (int b2 = 0; b2 < 2; ++b2)
+      for (int x = 0; x < 4; ++x)
+        f[x] = *(const bf16x8_t*)(ks + (x & 1) * 32 * kRowB + (kaddr ^ ((2 * st2 + (x >> 1)) << 5)));
+    };
+    read_k(0, kf[0]);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[b2][e] = 0.f;
+    for (int st2 = 0; st2 < kKS / 2; ++st2) {
+      if (st2 + 1 < kKS / 2) read_k(st2 + 1, kf[(st2 + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int st = 0; st < kKS; ++st)
-#pragma unroll
-      for (int b2 = 0; b2 < 2; ++b2) {
-        const bf16x8_t kf = *(const bf16x8_t*)(ks + b2 * 32 * kRowB + (kaddr ^ (st << 5)));
-        s[b2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[st], s[b2], 0, 0, 0);
-        if (b2 == 1 && st % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+      for (int x = 0; x < 4; ++x) {
+        const f32x16_t zero = {};
+        const int b2 = x & 1;
+        s[b2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[st2 & 1][x], qf[2 * st2 + (x >> 1)],
+                                                        st2 == 0 && x < 2 ? zero : s[b2], 0, 0, 0);
       }
-    if constexpr (masked) {
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // A hidden key's p is 0, but 0 times an infinity or NaN in its V row is not: in a
+    // tile with hidden keys V is looked through, and where it holds such a value the
+    // products are taken key by key and kept for the rows that see the key.
+    bool special = false;
+    if (kt + kAKT > lim_first) {  // some row of the wave does not see every key
 #pragma unroll
       for (int b2 = 0; b2 < 2; ++b2)
 #pragma unroll
@@ -252,7 +278,24 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
           const int key = kt + b2 * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
           s[b2][e] = key < lim ? s[b2][e] : -INFINITY;
         }
+      unsigned bad = 0;
+#pragma unroll 1
+      for (int ks16 = 0; ks16 < 4; ++ks16) {
+        if (kt + 16 * ks16 + 16 <= lim_first) continue;  // every row sees these keys
+#pragma unroll
+        for (int db = 0; db < kDB; ++db) {
+          const u32x4_t u = __builtin_bit_cast(u32x4_t, v_frag(ks16, db));
+          // an exponent of all ones, plus one in its last place, sets the sign bit
+#pragma unroll
+          for (int x = 0; x < 4; ++x) bad |= (u[x] & 0x7f807f80u) + 0x00800080u;
+        }
+      }
+      special = __any((bad & 0x80008000u) != 0);
     }
+    // the first step's part of V is under way during the softmax
+    v8i16_t vf[2][kDB];
+#pragma unroll
+    for (int db = 0; db < kDB; ++db) vf[0][db] = v_frag(0, db);
     float top = fmaxf(s[0][0], s[1][0]);  // waits for the products of both blocks
 #pragma unroll
     for (int e = 1; e < 16; ++e) top = max3(top, s[0][e], s[1][e]);
@@ -282,56 +325,42 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
         pf[ks16][2 * x + 1] = p[1];
       }
     }
-    // A hidden key's p is 0, but 0 times an infinity or NaN in its V row is not: in a
-    // tile with hidden keys V is looked through, and where it holds such a value the
-    // products are taken key by key and kept for the rows that see the key.
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (masked) {
-      unsigned bad = 0;
+    if (special) {
 #pragma unroll
-      for (int ks16 = 0; ks16 < 4; ++ks16) {
-        if (kt + 16 * ks16 + 16 <= lim_first) continue;  // every row sees these keys
+      for (int ks16 = 0; ks16 < 4; ++ks16)
 #pragma unroll
         for (int db = 0; db < kDB; ++db) {
-          const u32x4_t u = __builtin_bit_cast(u32x4_t, v_frag(ks16, db));
-          // an exponent of all ones, plus one in its last place, sets the sign bit
-#pragma unroll
-          for (int x = 0; x < 4; ++x) bad |= (u[x] & 0x7f807f80u) + 0x00800080u;
-        }
-      }
-      if (__any((bad & 0x80008000u) != 0)) {
-#pragma unroll
-        for (int ks16 = 0; ks16 < 4; ++ks16)
-#pragma unroll
-          for (int db = 0; db < kDB; ++db) {
-            const v8i16_t vf = v_frag(ks16, db);
+          const v8i16_t vx = v_frag(ks16, db);
 #pragma unroll 1
-            for (int j = 0; j < 16; ++j) {  // key kt + 16 ks16 + j: element x of half h
-              const int jh = (j >> 2) & 1, jx = (j & 3) + 4 * (j >> 3);
-              v8i16_t one;
+          for (int j = 0; j < 16; ++j) {  // key kt + 16 ks16 + j: element x of half h
+            const int jh = (j >> 2) & 1, jx = (j & 3) + 4 * (j >> 3);
+            v8i16_t one;
 #pragma unroll
-              for (int x = 0; x < 8; ++x) one[x] = half == jh && x == jx ? vf[x] : (short)0;
-              f32x16_t z;
+            for (int x = 0; x < 8; ++x) one[x] = half == jh && x == jx ? vx[x] : (short)0;
+            const f32x16_t zero = {};
+            const f32x16_t z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                __builtin_bit_cast(bf16x8_t, one), pf[ks16], zero, 0, 0, 0);
+            if (kt + 16 * ks16 + j < lim) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) z[e] = 0.f;
-              z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, one),
-                                                          pf[ks16], z, 0, 0, 0);
-              if (kt + 16 * ks16 + j < lim) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[db][e] += z[e];
-              }
+              for (int e = 0; e < 16; ++e) o[db][e] += z[e];
             }
           }
-        return;
-      }
+        }
+      return;
     }
 #pragma unroll
-    for (int ks16 = 0; ks16 < 4; ++ks16)
+    for (int ks16 = 0; ks16 < 4; ++ks16) {
+      if (ks16 < 3) {
+#pragma unroll
+        for (int db = 0; db < kDB; ++db) vf[(ks16 + 1) & 1][db] = v_frag(ks16 + 1, db);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int db = 0; db < kDB; ++db)
         o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            __builtin_bit_cast(bf16x8_t, v_frag(ks16, db)), pf[ks16], o[db], 0, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
+            __builtin_bit_cast(bf16x8_t, vf[ks16 & 1][db]), pf[ks16], o[db], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
 #pragma unroll
@@ -354,10 +383,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
     vs = sm + (ST + buf) * kTile;
     buf = buf == ST - 1 ? 0 : buf + 1;
     if (kt >= lim_last) continue;  // no row of this wave sees the tile
-    if (kt + kAKT <= lim_first)
-      tile(kt, std::integral_constant<bool, false>{});
-    else
-      tile(kt, std::integral_constant<bool, true>{});
+    tile(kt);
   }
 
   l += __shfl_xor(l, 32);
@@ -397,41 +423,66 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
     }
 }
 
-// Joins the splits of a (token, query head): 32 lanes, 4 elements each.
+// Joins the splits of a (token, query head): eight groups of 32 lanes (4 elements
+// each) take every eighth split, group 0 adds the groups in order.
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  __shared__ float part[8][132];  // 128 elements, l, any
+  const int64_t row = blockIdx.x;
   const int hq = a.hk * a.g;
   const int64_t tok = row / hq;
   const int qh = (int)(row - tok * hq);
   if (tok < start_at(a.q_start, 0, a.nq) || tok >= start_at(a.q_start, a.nseq, a.nq)) return;
-  const int e = (threadIdx.x & 31) * 4;
-  float m = -INFINITY, l = 0.f;
+  const int grp = threadIdx.x / 32, lane = threadIdx.x & 31, e = lane * 4;
   const int64_t step = a.nq * hq;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_ml[s * step + row].x);
+  float m = -INFINITY;
+  for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.part_ml[s * step + row].x);
+#pragma unroll
+  for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x, 32));
   const float ref = m == -INFINITY ? 0.f : m;
   f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  bool any = false;
-  for (int s = 0; s < a.splits; ++s) {
+  float l = 0.f, any = 0.f;
+  for (int s = grp; s < a.splits; s += 8) {
     const float2 ml = a.part_ml[s * step + row];
-    any |= ml.y != 0.f;  // 0: the piece saw no key
-    if (ml.y <= 0.f) continue;
+    if (ml.y != 0.f) any = 1.f;  // 0: the piece saw no key
+    if (ml.y <= 0.f) continue;   // -1: only scores of -inf
     const float f = exp2_fast(ml.x - ref);
     l += ml.y * f;
     if (e < a.d) o += *(const f32x4_t*)(a.part_o + (s * step + row) * a.d + e) * f;
   }
-  if (e >= a.d) return;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) part[grp][e + y] = o[y];
+  if (lane == 0) {
+    part[grp][128] = l;
+    part[grp][129] = any;
+  }
+  __syncthreads();
+  if (grp || e >= a.d) return;
+  for (int s = 1; s < 8; ++s) {
+#pragma unroll
+    for (int y = 0; y < 4; ++y) o[y] += part[s][e + y];
+  }
+  l = 0.f;
+  any = 0.f;
+  for (int s = 0; s < 8; ++s) {
+    l += part[s][128];
+    any += part[s][129];
+  }
   // keys seen, but every score -inf: l is 0 and there is no softmax (NaN)
   u16x4_t w;
 #pragma unroll
-  for (int y = 0; y < 4; ++y) w[y] = any ? f32_to_bf16_rne(o[y] / l) : (unsigned short)0;
+  for (int y = 0; y < 4; ++y) w[y] = any > 0.f ? f32_to_bf16_rne(o[y] / l) : (unsigned short)0;
   *(u16x4_t*)(a.o + tok * a.o_token + qh * a.o_head + e) = w;
 }
 
+template <int D, int NW, int ST, bool PAD>
+void launch_kernel(const AttnArgs& a, hipStream_t s) {
+  const int64_t slots = a.nq * a.g / (32 * NW) + a.nseq;
+  hipLaunchKernelGGL((attention_kernel<D, NW, ST, PAD>),
+                     dim3((unsigned)(slots * a.hk), (unsigned)a.splits), dim3(64 * NW), 0, s, a);
+}
 template <int D, int NW, int ST>
 void launch_rows(const AttnArgs& a, hipStream_t s) {
-  const int64_t slots = a.nq * a.g / (32 * NW) + a.nseq;
-  hipLaunchKernelGGL((attention_kernel<D, NW, ST>),
-                     dim3((unsigned)(slots * a.hk), (unsigned)a.splits), dim3(64 * NW), 0, s, a);
+  a.d < D ? launch_kernel<D, NW, ST, true>(a, s) : launch_kernel<D, NW, ST, false>(a, s);
 }
 
 constexpr int kABM = 128;      // rows per workgroup
@@ -495,8 +546,7 @@ hipError_t launch_attention(const void* Q, const void* K, const void* V, const i
     launch_rows<128, 4, 2>(a, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)cdiv(p->nq * p->hq, 8)), dim3(256), 0, s,
-                     a);
+  hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)(p->nq * p->hq)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -987,6 +987,8 @@ th_status check_attention(const th_attention_params* p) {
                               p->v_token, p->v_head, p->o_token, p->o_head};
   for (int64_t v : strides)
     if (v < 0 || v % 8) return fail(TH_ERR_INVALID_ARG, "strides must be multiples of 8, >= 0");
+  if (p->k_token >= ((int64_t)1 << 24) || p->v_token >= ((int64_t)1 << 24))
+    return fail(TH_ERR_INVALID_ARG, "k_token and v_token must be < 2^24");
   if (heads_overlap(p->nq, p->hq, p->d, p->o_token, p->o_head))
     return fail(TH_ERR_INVALID_ARG, "the heads of O overlap");
   if (!(p->scale > 0.0) || !std::isfinite(p->scale))

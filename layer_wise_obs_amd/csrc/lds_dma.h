@@ -91,14 +91,4 @@ __device__ __forceinline__ void lds_dma10s(const unsigned (&vo)[5], const void* 
       : "scc");
 }
 
-
-// The same from one 64-bit address per lane. Lanes that are off write nothing; the
-// others keep their places.
-__device__ __forceinline__ void lds_dma1v(const void* g, unsigned lds) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                   :
-                   : "s"(lds), "v"(g)
-                   : "m0");
-}
-
 }  // namespace th

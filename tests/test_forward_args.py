@@ -56,7 +56,7 @@ def test_linear_workspace_query():
     assert L.linear_workspace_size(0, 4096, 4096) == 0
     assert L.linear_workspace_size(131072, 4096, 4096) == 0  # enough tiles: nothing is split
     need = L.linear_workspace_size(777, 2056, 1023)
-    assert need > 0 and need % (777 * 1023 * 4) == 0
+    assert need > 0 and need % (777 * 1024 * 4) == 0
     a = dict(n=777, b=2056, ldx=2056, c=1023, ldy=1023, ws=FAKE)
     assert lib.th_linear(*_linear_args(ws_bytes=need - 1, **a)) == L.TH_ERR_WORKSPACE
 
@@ -81,7 +81,7 @@ def _attention(Q=FAKE, K=FAKE, V=FAKE, dt=L.TH_BF16, qs=FAKE, ks=None, O=2 * FAK
     dict(nq=1 << 62), dict(hq=0), dict(hk=0), dict(hk=3), dict(hq=-8), dict(d=4), dict(d=60),
     dict(d=136, q_head=136, o_head=136, o_token=1088), dict(hq=1 << 17, o_token=1 << 24),
     dict(nseq=0), dict(nseq=1 << 24), dict(q_token=-512), dict(k_head=60), dict(v_token=132),
-    dict(o_head=56), dict(o_token=504), dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN),
+    dict(k_token=1 << 24), dict(v_token=1 << 30), dict(o_head=56), dict(o_token=504), dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN),
     dict(scale=INF), dict(nq=1 << 30, hq=64, hk=8, o_token=4096)])
 def test_attention_refuses(bad):
     assert _attention(**bad) == L.TH_ERR_INVALID_ARG

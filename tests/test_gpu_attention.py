@@ -237,11 +237,11 @@ def test_attention_captured_and_replayed_with_new_lengths():
 
 def test_attention_offsets_past_32_bits():
     print("[case] attention keys past 2^32 elements", flush=True)
-    pitch, d = (1 << 30) + 8, 64
-    buf = torch.empty(5 * pitch + 2 * d, dtype=BF, device=DEV)
-    K = buf.as_strided((5, 1, d), (pitch, d, 1))
-    V = buf.as_strided((5, 1, d), (pitch, d, 1), d)
-    k, v, q = _randn((5, 1, d), 31), _randn((5, 1, d), 32), _randn((5, 3, d), 33)
+    n, pitch, d = 600, (1 << 23) + 8, 64
+    buf = torch.empty(n * pitch + 2 * d, dtype=BF, device=DEV)
+    K = buf.as_strided((n, 1, d), (pitch, d, 1))
+    V = buf.as_strided((n, 1, d), (pitch, d, 1), d)
+    k, v, q = _randn((n, 1, d), 31), _randn((n, 1, d), 32), _randn((5, 3, d), 33)
     K.copy_(k.to(DEV))
     V.copy_(v.to(DEV))
-    _check(L.attention(q.to(DEV), K, V), q, k, v, [0, 5], [0, 5])
+    _check(L.attention(q.to(DEV), K, V), q, k, v, [0, 5], [0, n])
