@@ -170,11 +170,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   }
 
   f32x16_t o[kDB];
-#pragma unroll
-  for (int i = 0; i < kDB; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
-  float m = -INFINITY, l = 0.f;
+  float m, l;
+  unsigned bad = 0;  // sign bits: V values met that are not finite, in tiles with hidden keys
 
   // Loader: chunk wave + NW i of a tile (1 KB, kRowsPer rows); lane l fills row
   // kRowsPer chunk + l / kPieces at physical piece l % kPieces. K pieces are
@@ -205,20 +202,20 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
       vv[i] = (row * (unsigned)a.v_token + cv) * 2;
     }
   };
-  offsets(kAKT - 1);
-  auto issue = [&](int kt, int buf) {
+  // The next tile's loads, one by one: i < kLd of K, then kLd of V.
+  const unsigned short *gk = kb, *gv = vb;
+  unsigned dk = 0;
+  auto next_tile = [&](int kt, int buf) {
     if (kt + kAKT > lk) offsets(lk - 1 - kt);  // the sequence's last tile
-    const unsigned short* gk = kb + (int64_t)kt * a.k_token;
-    const unsigned short* gv = vb + (int64_t)kt * a.v_token;
-    const unsigned dk = smb + buf * kTile + wave * 1024;
-    const unsigned dv = smb + (ST + buf) * kTile + wave * 1024;
-    if (in_k) {
-#pragma unroll
-      for (int i = 0; i < kLd; ++i) lds_dma1(vk[i], gk, dk + i * NW * 1024);
-    }
-    if (in_v) {
-#pragma unroll
-      for (int i = 0; i < kLd; ++i) lds_dma1(vv[i], gv, dv + i * NW * 1024);
+    gk = kb + (int64_t)kt * a.k_token;
+    gv = vb + (int64_t)kt * a.v_token;
+    dk = smb + buf * kTile + wave * 1024;
+  };
+  auto load = [&](int i) {
+    if (i < kLd) {
+      if (in_k) lds_dma1(vk[i], gk, dk + i * NW * 1024);
+    } else {
+      if (in_v) lds_dma1(vv[i - kLd], gv, dk + ST * kTile + (i - kLd) * NW * 1024);
     }
   };
 
@@ -242,35 +239,45 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
   // One tile of 64 keys from kt.
-  auto tile = [&](int kt) __attribute__((always_inline)) {
-    // Scores: the operands of two steps (four blocks) are read while the products of
-    // the two before run; the order is pinned.
+  auto tile = [&](int kt, bool more, auto CAREFUL) __attribute__((always_inline)) {
+    constexpr bool careful = decltype(CAREFUL)::value;
+    // Scores: operands are read three steps ahead, the next tile's loads go between
+    // the products; the order is pinned.
     f32x16_t s[2];
-    bf16x8_t kf[2][4];
-    auto read_k = [&](int st2, bf16x8_t (&f)[4]) {
+    bf16x8_t kf[4][2];
+    auto read_k = [&](int st) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        f[x] = *(const bf16x8_t*)(ks + (x & 1) * 32 * kRowB + (kaddr ^ ((2 * st2 + (x >> 1)) << 5)));
+      for (int b2 = 0; b2 < 2; ++b2)
+        kf[st & 3][b2] = *(const bf16x8_t*)(ks + b2 * 32 * kRowB + (kaddr ^ (st << 5)));
     };
-    read_k(0, kf[0]);
+    auto scores = [&](auto LOADS) __attribute__((always_inline)) {
 #pragma unroll
-    for (int st2 = 0; st2 < kKS / 2; ++st2) {
-      if (st2 + 1 < kKS / 2) read_k(st2 + 1, kf[(st2 + 1) & 1]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int st = 0; st < 3; ++st) read_k(st);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const f32x16_t zero = {};
-        const int b2 = x & 1;
-        s[b2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[st2 & 1][x], qf[2 * st2 + (x >> 1)],
-                                                        st2 == 0 && x < 2 ? zero : s[b2], 0, 0, 0);
+      for (int st = 0; st < kKS; ++st) {
+        if (st + 3 < kKS) read_k(st + 3);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b2 = 0; b2 < 2; ++b2) {
+          const f32x16_t zero = {};
+          s[b2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[st & 3][b2], qf[st], st ? s[b2] : zero,
+                                                          0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(LOADS)::value) {
+#pragma unroll
+          for (int i = 0; i < 2 * kLd; ++i)
+            if (i * kKS / (2 * kLd) == st) load(i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // A hidden key's p is 0, but 0 times an infinity or NaN in its V row is not: in a
-    // tile with hidden keys V is looked through, and where it holds such a value the
-    // products are taken key by key and kept for the rows that see the key.
-    bool special = false;
-    if (kt + kAKT > lim_first) {  // some row of the wave does not see every key
+    };
+    if (more)
+      scores(std::integral_constant<bool, true>{});
+    else
+      scores(std::integral_constant<bool, false>{});
+    const bool masked = kt + kAKT > lim_first;  // some row of the wave does not see every key
+    if (masked) {
 #pragma unroll
       for (int b2 = 0; b2 < 2; ++b2)
 #pragma unroll
@@ -278,24 +285,28 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
           const int key = kt + b2 * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
           s[b2][e] = key < lim ? s[b2][e] : -INFINITY;
         }
-      unsigned bad = 0;
+      if constexpr (!careful) {
 #pragma unroll 1
-      for (int ks16 = 0; ks16 < 4; ++ks16) {
-        if (kt + 16 * ks16 + 16 <= lim_first) continue;  // every row sees these keys
+        for (int ks16 = 0; ks16 < 4; ++ks16) {
+          if (kt + 16 * ks16 + 16 <= lim_first) continue;  // every row sees these keys
 #pragma unroll
-        for (int db = 0; db < kDB; ++db) {
-          const u32x4_t u = __builtin_bit_cast(u32x4_t, v_frag(ks16, db));
-          // an exponent of all ones, plus one in its last place, sets the sign bit
+          for (int db = 0; db < kDB; ++db) {
+            const u32x4_t u = __builtin_bit_cast(u32x4_t, v_frag(ks16, db));
+            // an exponent of all ones, plus one in its last place, sets the sign bit
 #pragma unroll
-          for (int x = 0; x < 4; ++x) bad |= (u[x] & 0x7f807f80u) + 0x00800080u;
+            for (int x = 0; x < 4; ++x) bad |= (u[x] & 0x7f807f80u) + 0x00800080u;
+          }
         }
       }
-      special = __any((bad & 0x80008000u) != 0);
     }
-    // the first step's part of V is under way during the softmax
-    v8i16_t vf[2][kDB];
+    // the first steps' part of V is under way during the softmax
+    v8i16_t vf[3][kDB];
+    auto read_v = [&](int ks16) {
 #pragma unroll
-    for (int db = 0; db < kDB; ++db) vf[0][db] = v_frag(0, db);
+      for (int db = 0; db < kDB; ++db) vf[ks16 % 3][db] = v_frag(ks16, db);
+    };
+    read_v(0);
+    read_v(1);
     float top = fmaxf(s[0][0], s[1][0]);  // waits for the products of both blocks
 #pragma unroll
     for (int e = 1; e < 16; ++e) top = max3(top, s[0][e], s[1][e]);
@@ -325,66 +336,88 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
         pf[ks16][2 * x + 1] = p[1];
       }
     }
-    if (special) {
+    if constexpr (careful) {
+      if (masked) {
 #pragma unroll
-      for (int ks16 = 0; ks16 < 4; ++ks16)
+        for (int ks16 = 0; ks16 < 4; ++ks16)
 #pragma unroll
-        for (int db = 0; db < kDB; ++db) {
-          const v8i16_t vx = v_frag(ks16, db);
+          for (int db = 0; db < kDB; ++db) {
+            const v8i16_t vx = v_frag(ks16, db);
 #pragma unroll 1
-          for (int j = 0; j < 16; ++j) {  // key kt + 16 ks16 + j: element x of half h
-            const int jh = (j >> 2) & 1, jx = (j & 3) + 4 * (j >> 3);
-            v8i16_t one;
+            for (int j = 0; j < 16; ++j) {  // key kt + 16 ks16 + j: element x of half h
+              const int jh = (j >> 2) & 1, jx = (j & 3) + 4 * (j >> 3);
+              v8i16_t one;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) one[x] = half == jh && x == jx ? vx[x] : (short)0;
-            const f32x16_t zero = {};
-            const f32x16_t z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(bf16x8_t, one), pf[ks16], zero, 0, 0, 0);
-            if (kt + 16 * ks16 + j < lim) {
+              for (int x = 0; x < 8; ++x) one[x] = half == jh && x == jx ? vx[x] : (short)0;
+              const f32x16_t zero = {};
+              const f32x16_t z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  __builtin_bit_cast(bf16x8_t, one), pf[ks16], zero, 0, 0, 0);
+              if (kt + 16 * ks16 + j < lim) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[db][e] += z[e];
+                for (int e = 0; e < 16; ++e) o[db][e] += z[e];
+              }
             }
           }
-        }
-      return;
+        return;
+      }
     }
 #pragma unroll
     for (int ks16 = 0; ks16 < 4; ++ks16) {
-      if (ks16 < 3) {
-#pragma unroll
-        for (int db = 0; db < kDB; ++db) vf[(ks16 + 1) & 1][db] = v_frag(ks16 + 1, db);
-      }
+      if (ks16 < 2) read_v(ks16 + 2);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int db = 0; db < kDB; ++db)
         o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            __builtin_bit_cast(bf16x8_t, vf[ks16 & 1][db]), pf[ks16], o[db], 0, 0, 0);
+            __builtin_bit_cast(bf16x8_t, vf[ks16 % 3][db]), pf[ks16], o[db], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 
+  // One pass over the keys. A hidden key's p is 0, but 0 times an infinity or NaN in its
+  // V row is not: the first pass looks through V in tiles with hidden keys, and where it
+  // holds such a value the workgroup passes again, taking those tiles' products key by
+  // key and keeping them for the rows that see the key.
+  auto pass = [&](auto CAREFUL) __attribute__((always_inline)) {
+    m = -INFINITY;
+    l = 0.f;
 #pragma unroll
-  for (int i = 0; i < ST - 1; ++i)
-    if (kbeg + i * kAKT < kend) issue(kbeg + i * kAKT, i);
-  int buf = 0;
-  for (int kt = kbeg; kt < kend; kt += kAKT) {
-    // this tile has landed (at most ST - 2 later ones are in flight)
-    static_assert(ST == 2 || (ST == 3 && kLd <= 2), "vmcnt immediates");
-    if (ST == 2 || kt + kAKT >= kend)
-      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    else if (kLd == 2)
-      __asm__ volatile("s_waitcnt vmcnt(4)" ::: "memory");
-    else
-      __asm__ volatile("s_waitcnt vmcnt(2)" ::: "memory");
-    __syncthreads();  // the buffer filled next was last read before this barrier
-    const int next = buf == 0 ? ST - 1 : buf - 1;
-    if (kt + (ST - 1) * kAKT < kend) issue(kt + (ST - 1) * kAKT, next);
-    ks = sm + buf * kTile;
-    vs = sm + (ST + buf) * kTile;
-    buf = buf == ST - 1 ? 0 : buf + 1;
-    if (kt >= lim_last) continue;  // no row of this wave sees the tile
-    tile(kt);
-  }
+    for (int i = 0; i < kDB; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+    offsets(kAKT - 1);
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i)
+      if (kbeg + i * kAKT < kend) {
+        next_tile(kbeg + i * kAKT, i);
+#pragma unroll
+        for (int x = 0; x < 2 * kLd; ++x) load(x);
+      }
+    int buf = 0;
+    for (int kt = kbeg; kt < kend; kt += kAKT) {
+      // this tile has landed (at most ST - 2 later ones are in flight)
+      static_assert(ST == 2 || ST == 3 && kLd <= 2, "vmcnt immediates");
+      if (ST == 2 || kt + kAKT >= kend)
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      else if (kLd == 2)
+        __asm__ volatile("s_waitcnt vmcnt(4)" ::: "memory");
+      else
+        __asm__ volatile("s_waitcnt vmcnt(2)" ::: "memory");
+      __syncthreads();  // the buffer filled next was last read before this barrier
+      const bool more = kt + (ST - 1) * kAKT < kend;
+      if (more) next_tile(kt + (ST - 1) * kAKT, buf == 0 ? ST - 1 : buf - 1);
+      ks = sm + buf * kTile;
+      vs = sm + (ST + buf) * kTile;
+      buf = buf == ST - 1 ? 0 : buf + 1;
+      if (kt < lim_last) {
+        tile(kt, more, CAREFUL);
+      } else if (more) {  // no row of this wave sees the tile
+#pragma unroll
+        for (int x = 0; x < 2 * kLd; ++x) load(x);
+      }
+    }
+  };
+  pass(std::integral_constant<bool, false>{});
+  if (__syncthreads_or((bad & 0x80008000u) != 0)) pass(std::integral_constant<bool, true>{});
 
   l += __shfl_xor(l, 32);
   if (!valid) return;

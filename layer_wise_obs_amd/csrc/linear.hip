@@ -248,27 +248,32 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // one load after every kGap-th product, B's before A's
-  constexpr int kGap = FM * FN / (LA + LB) > 0 ? FM * FN / (LA + LB) : 1;
-  constexpr int kPer = (LA + LB + FM * FN - 1) / (FM * FN);
-  auto load_one = [&](int m) {
-    if (m < LB) issue_b(m);
-    else if (m < LB + LA) issue_a(m - LB);
-  };
-  auto loads = [&](int x) {
-    if (x % kGap == 0) {
+  // the loads of one operand's stage, spread evenly over a substep's products
+  auto loads_a = [&](int x) {
+    constexpr int gap = FM * FN / LA > 0 ? FM * FN / LA : 1, per = (LA + FM * FN - 1) / (FM * FN);
+    if (x % gap == 0) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int m = 0; m < kPer; ++m) load_one(x / kGap * kPer + m);
+      for (int m = 0; m < per; ++m)
+        if (x / gap * per + m < LA) issue_a(x / gap * per + m);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto no_loads = [](int) {};
-  // this wave's loads of the next stage have landed; of later stages they may be in
-  // flight (those of A where it runs further ahead: they are issued after B's)
+  auto loads_b = [&](int x) {
+    constexpr int gap = FM * FN / LB > 0 ? FM * FN / LB : 1, per = (LB + FM * FN - 1) / (FM * FN);
+    if (x % gap == 0) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < per; ++m)
+        if (x / gap * per + m < LB) issue_b(x / gap * per + m);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Order of the loads: A(SA-1), B(SB), A(SA), B(SB+1), ... At the wait of stage it, A
+  // and B of stage it + 1 have to have landed; newer are A(it + 2) .. A(it + SA - 1) and
+  // B(it + 2) .. B(it + SB - 1).
   auto wait_loads = [&] {
     constexpr int left = (SA - 2) * LA + (SB - 2) * LB;
-    static_assert(SA == SB || SB == 2, "the newest loads belong to later stages");
     static_assert(left == 0 || left == 4 || left == 8, "vmcnt immediates");
     if constexpr (left == 0)
       __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -278,7 +283,7 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
       __asm__ volatile("s_waitcnt vmcnt(8)" ::: "memory");
   };
 
-  // prologue: B's stages 0 .. SB-2, then A's 0 .. SA-2, all waited for
+  // prologue: B's stages 0 .. SB-2, A's 0 .. SA-2, waited for; then B(SB-1)
 #pragma unroll
   for (int it = 0; it < SB - 1; ++it) {
     stage_b(it);
@@ -294,17 +299,25 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
   zero_tail(0);
   __syncthreads();
+  stage_b(SB - 1);
+#pragma unroll
+  for (int m = 0; m < LB; ++m) issue_b(m);
   read_frags(0, 0, a0, b0);
+  // A stage: half its products, then (its last operands read, the next stage landed,
+  // the barrier) the other half. A's next stage goes into the buffer freed by the
+  // barrier of stage it - 1 during the first half, B's into the one freed by this
+  // stage's barrier during the second: a quarter of the address unit's rate, where all
+  // loads in one half would take half of it in bursts.
   for (int it = 0; it < nk; ++it) {
-    stage_b(it + SB - 1);  // into buffers last read before the barrier of it - 1
     stage_a(it + SA - 1);
     read_frags(it, 1, a1, b1);
-    mfmas(a0, b0, loads);
+    mfmas(a0, b0, loads_a);
     wait_loads();
     zero_tail(it + 1);
     __syncthreads();
+    stage_b(it + SB);
     read_frags(it + 1, 0, a0, b0);
-    mfmas(a1, b1, no_loads);
+    mfmas(a1, b1, loads_b);
   }
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();  // every wave's loads have landed: the stages may be reused
