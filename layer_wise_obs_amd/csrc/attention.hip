@@ -60,25 +60,51 @@ __device__ __forceinline__ int64_t start_at(const int32_t* s, int i, int64_t n) 
   return v < 0 ? 0 : (v > n ? n : v);
 }
 
+struct Sequence {
+  int index;              // -1: the slot belongs to none
+  int64_t q0, q1, k0, k1;  // its rows of Q and K
+};
+
 // The slots of sequence s begin at floor(q_start[s] g / BM) + s: at least as many
-// slots as the sequence has row blocks lie before the next one's. Returns the
-// sequence that holds `slot` (the last whose slots begin at or before it), or -1;
-// 64 starts are looked at a time.
+// slots as the sequence has row blocks lie before the next one's. A slot belongs to
+// the last sequence whose slots begin at or before it; up to 63 sequences are found
+// with one load of either start array (a lane holds a start), more by looking at 64
+// at a time.
 template <int BM>
-__device__ __forceinline__ int sequence_of(const AttnArgs& a, int64_t slot, int lane) {
+__device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, int64_t slot, int lane) {
+  Sequence r;
+  r.index = -1;
+  if (a.nseq < 64) {
+    const int i = min(lane, a.nseq);
+    const int q = (int)start_at(a.q_start, i, a.nq), k = (int)start_at(a.k_start, i, a.nk);
+    const bool before = lane < a.nseq && (int64_t)q * a.g / BM + lane <= slot;
+    const int cnt = __popcll(__ballot(before));
+    if (cnt == 0) return r;
+    r.index = cnt - 1;
+    r.q0 = __builtin_amdgcn_readlane(q, cnt - 1);
+    r.q1 = __builtin_amdgcn_readlane(q, cnt);
+    r.k0 = __builtin_amdgcn_readlane(k, cnt - 1);
+    r.k1 = __builtin_amdgcn_readlane(k, cnt);
+    return r;
+  }
   int lo = 0, len = a.nseq;
-  auto begin = [&](int s) { return start_at(a.q_start, s, a.nq) * a.g / BM + s; };
-  while (len > 0) {
+  for (;;) {
     const int step = (len + 63) >> 6;
     const int at = lane * step;
-    const bool before = at < len && begin(lo + at) <= slot;
+    const bool before =
+        at < len && start_at(a.q_start, lo + at, a.nq) * a.g / BM + lo + at <= slot;
     const int cnt = __popcll(__ballot(before));
-    if (cnt == 0) return -1;
+    if (cnt == 0) return r;
     lo += (cnt - 1) * step;
-    if (step == 1) return lo;
+    if (step == 1) break;
     len = min(step, len - (cnt - 1) * step);
   }
-  return -1;
+  r.index = lo;
+  r.q0 = start_at(a.q_start, lo, a.nq);
+  r.q1 = start_at(a.q_start, lo + 1, a.nq);
+  r.k0 = start_at(a.k_start, lo, a.nk);
+  r.k1 = start_at(a.k_start, lo + 1, a.nk);
+  return r;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -104,8 +130,9 @@ __device__ __forceinline__ bf16x2_t pack2(float a, float b) {
   return bf16x2_t{(__bf16)a, (__bf16)b};  // v_cvt_pk_bf16_f32, round to nearest even
 }
 
-// NW waves of 32 rows; ST tiles of keys in LDS; PAD: the head is shorter than D.
-template <int D, int NW, int ST, bool PAD>
+// D elements per row in LDS, of which the first DC enter the products (d <= DC); NW
+// waves of 32 rows; ST tiles of keys in LDS; PAD: the head is shorter than D.
+template <int D, int DC, int NW, int ST, bool PAD>
 __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   constexpr int kBM = 32 * NW;
   constexpr int kPieces = D / 8;             // 16-byte pieces per row
@@ -113,7 +140,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   constexpr int kTile = kAKT * kRowB;        // one operand's tile
   constexpr int kLd = kTile / 1024 / NW;     // 1 KB loads per wave and operand
   constexpr int kRowsPer = 64 / kPieces;     // rows per 1 KB
-  constexpr int kDB = D / 32, kKS = D / 16;
+  constexpr int kDB = DC / 32, kKS = DC / 16;
   __shared__ __attribute__((aligned(1024))) unsigned char sm[2 * ST * kTile];  // K tiles, V tiles
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -121,13 +148,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   const int head = blockIdx.x % a.hk;
   // the last slots first: a causal sequence's longest rows are its last
   const int64_t slot = (int64_t)(gridDim.x / a.hk) - 1 - blockIdx.x / a.hk;
-  const int seq = sequence_of<kBM>(a, slot, lane);
-  if (seq < 0) return;
-  const int64_t q0 = start_at(a.q_start, seq, a.nq), q1 = start_at(a.q_start, seq + 1, a.nq);
-  const int64_t k0 = start_at(a.k_start, seq, a.nk), k1 = start_at(a.k_start, seq + 1, a.nk);
+  const Sequence sq = sequence_of<kBM>(a, slot, lane);
+  if (sq.index < 0) return;
+  const int64_t q0 = sq.q0, q1 = sq.q1, k0 = sq.k0, k1 = sq.k1;
   const int lk = k1 > k0 ? (int)(k1 - k0) : 0;
   const int64_t rows = q1 > q0 ? (q1 - q0) * a.g : 0;
-  const int64_t row0 = (slot - (q0 * a.g / kBM + seq)) * kBM;
+  const int64_t row0 = (slot - (q0 * a.g / kBM + sq.index)) * kBM;
   if (row0 < 0 || row0 >= rows) return;
   const int off = lk - (int)(q1 - q0);  // key of the same age as query 0
 
@@ -420,9 +446,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   if (__syncthreads_or((bad & 0x80008000u) != 0)) pass(std::integral_constant<bool, true>{});
 
   l += __shfl_xor(l, 32);
-  if (!valid) return;
   // element 8 (e / 4) + 4 half + e % 4 of each block of 32 is in register e
   if (a.splits > 1) {
+    if (!valid) return;
     const int64_t at = ((int64_t)blockIdx.y * a.nq + q0 + tok) * (a.hk * a.g) + qh;
     // l = -1 marks a piece that saw keys, all of them with scores of -inf
     if (half == 0) a.part_ml[at] = make_float2(m, lim > kbeg && l == 0.f ? -1.f : l);
@@ -438,22 +464,35 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
       }
     return;
   }
+  // Through LDS (free after the last barrier), so that a store instruction writes whole
+  // rows: 4 elements per lane of 32 rows each took 4.5 us per round of workgroups.
+  constexpr int kOutB = kRowB + 16;  // row pitch: rows 4 banks apart
+  static_assert(NW * 32 * kOutB <= 2 * ST * kTile, "rows fit the tiles");
+  unsigned char* ob = sm + wave * 32 * kOutB;
   const float inv = visible > 0 ? 1.0f / l : 0.f;
-  unsigned short* op = a.o + (q0 + tok) * a.o_token + qh * a.o_head;
 #pragma unroll
   for (int db = 0; db < kDB; ++db)
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int e = db * 32 + 8 * x + 4 * half;
-      if (e < a.d) {
-        bf16x2_t w[2];
+      bf16x2_t w[2];
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-          w[y] = visible > 0 ? pack2(o[db][4 * x + 2 * y] * inv, o[db][4 * x + 2 * y + 1] * inv)
-                             : pack2(0.f, 0.f);
-        *(bf16x4_t*)(op + e) = __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3);
-      }
+      for (int y = 0; y < 2; ++y)
+        w[y] = visible > 0 ? pack2(o[db][4 * x + 2 * y] * inv, o[db][4 * x + 2 * y + 1] * inv)
+                           : pack2(0.f, 0.f);
+      *(bf16x4_t*)(ob + (lane & 31) * kOutB + (db * 32 + 8 * x + 4 * half) * 2) =
+          __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3);
     }
+  wave_sync();
+  const int rows_here = (int)(row_end - wrow);  // of this wave's 32
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += kRowsPer) {
+    const int rr = r0 + lr;
+    const int64_t t = q0 + (unsigned)__shfl((int)tok, rr);
+    const int hh = __shfl(qh, rr);
+    if (rr < rows_here && lpp * 8 < a.d)
+      *(u32x4_t*)(a.o + t * a.o_token + hh * a.o_head + lpp * 8) =
+          *(const u32x4_t*)(ob + rr * kOutB + lpp * 16);
+  }
 }
 
 // Joins the splits of a (token, query head): eight groups of 32 lanes (4 elements
@@ -507,31 +546,34 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   *(u16x4_t*)(a.o + tok * a.o_token + qh * a.o_head + e) = w;
 }
 
-template <int D, int NW, int ST, bool PAD>
+template <int D, int DC, int NW, int ST, bool PAD>
 void launch_kernel(const AttnArgs& a, hipStream_t s) {
   const int64_t slots = a.nq * a.g / (32 * NW) + a.nseq;
-  hipLaunchKernelGGL((attention_kernel<D, NW, ST, PAD>),
+  hipLaunchKernelGGL((attention_kernel<D, DC, NW, ST, PAD>),
                      dim3((unsigned)(slots * a.hk), (unsigned)a.splits), dim3(64 * NW), 0, s, a);
-}
-template <int D, int NW, int ST>
-void launch_rows(const AttnArgs& a, hipStream_t s) {
-  a.d < D ? launch_kernel<D, NW, ST, true>(a, s) : launch_kernel<D, NW, ST, false>(a, s);
 }
 
 constexpr int kABM = 128;      // rows per workgroup
 constexpr int kAUnits = 256;  // compute units
 
-// Pieces the keys are split into: enough for two workgroups per compute unit, with
-// at least four tiles of keys each (by the sequences' average lengths, all that the
-// host knows).
+// Pieces the keys are split into, by the sequences' average lengths (all that the host
+// knows). Where a sequence's rows fill one workgroup at most (single tokens), reading
+// the keys bounds the call, and many small pieces even out the sequences' lengths:
+// eight workgroups per compute unit, pieces of two tiles or more (16 sequences over
+// 300001 keys: 355 us with two workgroups per unit, 282 with eight). Where rows fill
+// several workgroups, the products bound it and the partial results cost: two
+// workgroups per unit, pieces of four tiles or more.
 int splits_of(const th_attention_params* p) {
   const int64_t g = p->hq / p->hk;
   const int64_t seqs = p->nseq < p->nq ? p->nseq : p->nq;
-  const int64_t groups = seqs * cdiv(cdiv(p->nq, seqs) * g, kABM) * p->hk;
+  const int64_t blocks = cdiv(cdiv(p->nq, seqs) * g, kABM);
+  const int64_t groups = seqs * blocks * p->hk;
   const int64_t tiles = cdiv(cdiv(p->nk, seqs), kAKT);
-  int64_t s = 2 * kAUnits / groups;
-  if (s > tiles / 4) s = tiles / 4;
-  if (s > 64) s = 64;
+  const bool few = blocks == 1;
+  int64_t s = (few ? 8 : 2) * kAUnits / groups;
+  const int64_t most = few ? tiles / 2 : tiles / 4;
+  if (s > most) s = most;
+  if (s > 128) s = 128;
   return s < 1 ? 1 : (int)s;
 }
 
@@ -573,10 +615,16 @@ hipError_t launch_attention(const void* Q, const void* K, const void* V, const i
   a.splits = workspace ? splits_of(p) : 1;
   a.part_ml = (float2*)workspace;
   a.part_o = workspace ? (float*)(a.part_ml + (size_t)a.splits * p->nq * p->hq) : nullptr;
-  if (p->d <= 64)
-    launch_rows<64, 4, 2>(a, s);
+  if (p->d < 64)
+    launch_kernel<64, 64, 4, 2, true>(a, s);
+  else if (p->d == 64)
+    launch_kernel<64, 64, 4, 2, false>(a, s);
+  else if (p->d <= 96)
+    launch_kernel<128, 96, 4, 2, true>(a, s);
+  else if (p->d < 128)
+    launch_kernel<128, 128, 4, 2, true>(a, s);
   else
-    launch_rows<128, 4, 2>(a, s);
+    launch_kernel<128, 128, 4, 2, false>(a, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)(p->nq * p->hq)), dim3(256), 0, s, a);
