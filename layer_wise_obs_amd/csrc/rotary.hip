@@ -10,7 +10,8 @@
 // Bound by memory: one read and one write of the heads. p f_i is formed and
 // reduced to turns in fp64 (p f_i reaches 10^6 radians, where fp32 is off by 0.06),
 // then sine and cosine are fp32. They depend on the token and the pair only, so a
-// workgroup computes them once per token into LDS for all its heads of q and k.
+// workgroup computes them once per token into LDS for all its heads of q and k, while
+// its first heads are on their way.
 // A head is held by a group of lanes with 8 consecutive elements each (16 bytes of
 // bf16); a half-layout partner sits in another lane of the group.
 #include "common.h"
@@ -22,7 +23,8 @@ namespace {
 constexpr int kRThreads = 256;
 constexpr int kRMaxTokens = 16;  // tokens per workgroup, at most
 constexpr int kRMaxPairs = 128;
-constexpr int kRBatch = 4;       // heads whose loads are in flight together
+constexpr int kRBatch = 2;       // heads whose loads are in flight together (2: 403 us for
+                                 // 65536 tokens x 64 heads of 128, 5.3 TB/s; 4: 417; 8: 416)
 
 struct RotSide {
   const void* x;
@@ -38,7 +40,7 @@ struct RotArgs {
   int d, rot, interleaved, tokens;
   const int32_t* pos;
   const double* freqs;
-  float amplitude, eps;
+  float amplitude, eps, inv_d;
 };
 
 // (cos, sin) of position p at frequency f, in fp32 from an angle reduced in fp64.
@@ -50,24 +52,36 @@ __device__ __forceinline__ float2 turn_of(double p, double f, float amplitude) {
   return make_float2(c * amplitude, s * amplitude);
 }
 
-__device__ __forceinline__ void unpack8(const u32x4_t& u, float (&v)[8]) {
+// Eight elements as they are in memory, and as floats.
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<unsigned short> {
+  u32x4_t u;
+  __device__ __forceinline__ void load(const unsigned short* p) { u = *(const u32x4_t*)p; }
+  __device__ __forceinline__ void to(float (&v)[8]) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
   }
-}
-__device__ __forceinline__ void get8(const unsigned short* p, float (&v)[8]) {
-  unpack8(*(const u32x4_t*)p, v);
-}
-__device__ __forceinline__ void get8(const float* p, float (&v)[8]) {
-  const f32x4_t a = ((const f32x4_t*)p)[0], b = ((const f32x4_t*)p)[1];
+};
+template <>
+struct Raw8<float> {
+  f32x4_t a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = ((const f32x4_t*)p)[0];
+    b = ((const f32x4_t*)p)[1];
+  }
+  __device__ __forceinline__ void to(float (&v)[8]) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[4 + i] = b[i];
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
   }
-}
+};
 __device__ __forceinline__ void put8(unsigned short* p, const float (&v)[8]) {
   u32x4_t u;
 #pragma unroll
@@ -91,21 +105,38 @@ __global__ __launch_bounds__(kRThreads) void rotary_kernel(RotArgs a) {
   __shared__ float2 cs[kRMaxTokens * kRMaxPairs];
   const int pairs = a.rot >> 1;
   const int64_t token0 = (int64_t)blockIdx.x * a.tokens;
-  for (int i = threadIdx.x; i < a.tokens * pairs; i += kRThreads) {
-    const int t = i / pairs, p = i - t * pairs;
-    const int64_t tok = token0 + t;
-    if (tok < a.n)
-      cs[i] = turn_of(a.pos ? (double)a.pos[tok] : (double)tok, a.freqs[p], a.amplitude);
-  }
-  __syncthreads();
   constexpr int groups = kRThreads / G;
   const int phases = groups / a.tokens;
   const int grp = threadIdx.x / G, lane = threadIdx.x % G;
   const int t = grp / phases, phase = grp - t * phases;
   const int64_t tok = token0 + t;
-  if (t >= a.tokens || tok >= a.n) return;
   const int e0 = lane * 8;
   const bool mine = e0 < a.d, turned = e0 < a.rot;
+  const bool works = t < a.tokens && tok < a.n;
+  const int all = a.side[0].heads + a.side[1].heads;
+  // heads phase, phase + phases, ...: kRBatch of them in flight, the first ones while
+  // the angles are formed
+  Raw8<T> raw[kRBatch];
+  auto fetch = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kRBatch; ++u) {
+      const int h = h0 + u * phases;
+      if (works && mine && h < all) {
+        const bool k = h >= a.side[0].heads;
+        const RotSide& sd = a.side[k ? 1 : 0];
+        raw[u].load((const T*)sd.x + tok * sd.xt + (int64_t)(k ? h - a.side[0].heads : h) * sd.xh + e0);
+      }
+    }
+  };
+  fetch(phase);
+  for (int i = threadIdx.x; i < a.tokens * pairs; i += kRThreads) {
+    const int ti = i / pairs, p = i - ti * pairs;
+    const int64_t tt = token0 + ti;
+    if (tt < a.n)
+      cs[i] = turn_of(a.pos ? (double)a.pos[tt] : (double)tt, a.freqs[p], a.amplitude);
+  }
+  __syncthreads();
+  if (!works) return;
   // this lane's pairs: 8 of them (half) or 4 (interleaved), the same for every head
   float cosv[INTERLEAVED ? 4 : 8], sinv[INTERLEAVED ? 4 : 8];
   const bool upper = !INTERLEAVED && e0 >= pairs;  // second element of its pairs
@@ -119,99 +150,94 @@ __global__ __launch_bounds__(kRThreads) void rotary_kernel(RotArgs a) {
   }
   const int hops = pairs / 8;  // half: the partner's distance in lanes
   const int partner = (threadIdx.x & 63) + (upper ? -hops : hops);
-  const int all = a.side[0].heads + a.side[1].heads;
   for (int h0 = phase; h0 < all; h0 += phases * kRBatch) {
-    float v[kRBatch][8];
-#pragma unroll
-    for (int u = 0; u < kRBatch; ++u) {
-      const int h = h0 + u * phases;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-      if (h < all && mine) {
-        const bool k = h >= a.side[0].heads;
-        const RotSide& sd = a.side[k ? 1 : 0];
-        get8((const T*)sd.x + tok * sd.xt + (int64_t)(k ? h - a.side[0].heads : h) * sd.xh + e0, v[u]);
-      }
-    }
+    if (h0 != phase) fetch(h0);
 #pragma unroll
     for (int u = 0; u < kRBatch; ++u) {
       const int h = h0 + u * phases;
       if (h >= all) break;
       const bool k = h >= a.side[0].heads;
       const RotSide& sd = a.side[k ? 1 : 0];
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (mine) raw[u].to(v);
       if (sd.w) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += v[u][i] * v[u][i];
+        for (int i = 0; i < 8; ++i) s += v[i] * v[i];
 #pragma unroll
         for (int m = G / 2; m; m >>= 1) s += __shfl_xor(s, m);
-        const float scale = 1.0f / sqrtf(s / (float)a.d + a.eps);
+        const float scale = rsqrtf(s * a.inv_d + a.eps);
         if (mine) {
+          Raw8<T> wr;
           float w[8];
-          get8((const T*)sd.w + e0, w);
+          wr.load((const T*)sd.w + e0);
+          wr.to(w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * scale * w[i];
+          for (int i = 0; i < 8; ++i) v[i] = v[i] * scale * w[i];
         }
       }
       if constexpr (INTERLEAVED) {
         if (turned) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float x = v[u][2 * i], y = v[u][2 * i + 1];
-            v[u][2 * i] = x * cosv[i] - y * sinv[i];
-            v[u][2 * i + 1] = y * cosv[i] + x * sinv[i];
+            const float x = v[2 * i], y = v[2 * i + 1];
+            v[2 * i] = x * cosv[i] - y * sinv[i];
+            v[2 * i + 1] = y * cosv[i] + x * sinv[i];
           }
         }
       } else {
         float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = __shfl(v[u][i], partner);
+        for (int i = 0; i < 8; ++i) o[i] = __shfl(v[i], partner);
         if (turned) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            v[u][i] = upper ? v[u][i] * cosv[i] + o[i] * sinv[i] : v[u][i] * cosv[i] - o[i] * sinv[i];
+            v[i] = upper ? v[i] * cosv[i] + o[i] * sinv[i] : v[i] * cosv[i] - o[i] * sinv[i];
         }
       }
       if (mine)
-        put8((T*)sd.y + tok * sd.yt + (int64_t)(k ? h - a.side[0].heads : h) * sd.yh + e0, v[u]);
+        put8((T*)sd.y + tok * sd.yt + (int64_t)(k ? h - a.side[0].heads : h) * sd.yh + e0, v);
     }
   }
 }
 
-// Any head size, pitch and alignment: one wave per head, one pair per lane and step.
+// Any head size, pitch and alignment: a workgroup per token, a wave per head at a
+// time, one pair per lane and step.
 template <class T>
 __global__ __launch_bounds__(kRThreads) void rotary_any_kernel(RotArgs a) {
-  const int all = a.side[0].heads + a.side[1].heads;
-  const int64_t row = (int64_t)blockIdx.x * (kRThreads / 64) + threadIdx.x / 64;
-  const int64_t tok = row / all;
-  const int lane = threadIdx.x & 63;
-  if (tok >= a.n) return;
-  int h = (int)(row - tok * all);
-  const bool k = h >= a.side[0].heads;
-  const RotSide& sd = a.side[k ? 1 : 0];
-  if (k) h -= a.side[0].heads;
-  const T* x = (const T*)sd.x + tok * sd.xt + (int64_t)h * sd.xh;
-  T* y = (T*)sd.y + tok * sd.yt + (int64_t)h * sd.yh;
-  const T* w = (const T*)sd.w;
-  float scale = 1.0f;
-  if (w) {
-    float s = 0.f;
-    for (int e = lane; e < a.d; e += 64) s += get1(x + e) * get1(x + e);
-#pragma unroll
-    for (int m = 32; m; m >>= 1) s += __shfl_xor(s, m);
-    scale = 1.0f / sqrtf(s / (float)a.d + a.eps);
-  }
-  auto normed = [&](int e) { return w ? get1(x + e) * scale * get1(w + e) : get1(x + e); };
+  __shared__ float2 cs[kRMaxPairs];
+  const int64_t tok = blockIdx.x;
   const int pairs = a.rot >> 1;
   const double p = a.pos ? (double)a.pos[tok] : (double)tok;
-  for (int i = lane; i < pairs; i += 64) {
-    const int ea = a.interleaved ? 2 * i : i, eb = a.interleaved ? 2 * i + 1 : i + pairs;
-    const float2 c = turn_of(p, a.freqs[i], a.amplitude);
-    const float va = normed(ea), vb = normed(eb);
-    put1(y + ea, va * c.x - vb * c.y);
-    put1(y + eb, vb * c.x + va * c.y);
+  for (int i = threadIdx.x; i < pairs; i += kRThreads) cs[i] = turn_of(p, a.freqs[i], a.amplitude);
+  __syncthreads();
+  const int all = a.side[0].heads + a.side[1].heads;
+  const int lane = threadIdx.x & 63;
+  for (int hh = threadIdx.x / 64; hh < all; hh += kRThreads / 64) {
+    const bool k = hh >= a.side[0].heads;
+    const RotSide& sd = a.side[k ? 1 : 0];
+    const int h = k ? hh - a.side[0].heads : hh;
+    const T* x = (const T*)sd.x + tok * sd.xt + (int64_t)h * sd.xh;
+    T* y = (T*)sd.y + tok * sd.yt + (int64_t)h * sd.yh;
+    const T* w = (const T*)sd.w;
+    float scale = 1.0f;
+    if (w) {
+      float s = 0.f;
+      for (int e = lane; e < a.d; e += 64) s += get1(x + e) * get1(x + e);
+#pragma unroll
+      for (int m = 32; m; m >>= 1) s += __shfl_xor(s, m);
+      scale = rsqrtf(s * a.inv_d + a.eps);
+    }
+    auto normed = [&](int e) { return w ? get1(x + e) * scale * get1(w + e) : get1(x + e); };
+    for (int i = lane; i < pairs; i += 64) {
+      const int ea = a.interleaved ? 2 * i : i, eb = a.interleaved ? 2 * i + 1 : i + pairs;
+      const float2 c = cs[i];
+      const float va = normed(ea), vb = normed(eb);
+      put1(y + ea, va * c.x - vb * c.y);
+      put1(y + eb, vb * c.x + va * c.y);
+    }
+    for (int e = a.rot + lane; e < a.d; e += 64) put1(y + e, normed(e));
   }
-  for (int e = a.rot + lane; e < a.d; e += 64) put1(y + e, normed(e));
 }
 
 template <class T, int G>
@@ -242,9 +268,7 @@ hipError_t launch_typed(const RotArgs& a, hipStream_t s) {
           (((uintptr_t)sd.x | (uintptr_t)sd.y | (uintptr_t)sd.w) & 15) == 0;
   }
   if (!vec) {
-    const int64_t rows = a.n * (a.side[0].heads + a.side[1].heads);
-    hipLaunchKernelGGL((rotary_any_kernel<T>), dim3((unsigned)cdiv(rows, kRThreads / 64)),
-                       dim3(kRThreads), 0, s, a);
+    hipLaunchKernelGGL((rotary_any_kernel<T>), dim3((unsigned)a.n), dim3(kRThreads), 0, s, a);
     return hipGetLastError();
   }
   if (a.d <= 64) return launch_group<T, 8>(a, s);
@@ -274,6 +298,7 @@ hipError_t launch_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int6
   a.freqs = freqs;
   a.amplitude = amplitude;
   a.eps = eps;
+  a.inv_d = 1.0f / (float)d;
   return dt == TH_BF16 ? launch_typed<unsigned short>(a, s) : launch_typed<float>(a, s);
 }
 
