@@ -274,11 +274,11 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
   // B(it + 2) .. B(it + SB - 1).
   auto wait_loads = [&] {
     constexpr int left = (SA - 2) * LA + (SB - 2) * LB;
-    static_assert(left == 0 || left == 4 || left == 8, "vmcnt immediates");
-    if constexpr (left == 0)
-      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    else if constexpr (left == 4)
+    static_assert(left == 4 || left == 6 || left == 8, "vmcnt immediates");
+    if constexpr (left == 4)
       __asm__ volatile("s_waitcnt vmcnt(4)" ::: "memory");
+    else if constexpr (left == 6)
+      __asm__ volatile("s_waitcnt vmcnt(6)" ::: "memory");
     else
       __asm__ volatile("s_waitcnt vmcnt(8)" ::: "memory");
   };
@@ -385,71 +385,78 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restric
   finish8(v, t, q, c - q < 8 ? (int)(c - q) : 8, ep);
 }
 
-// Skinny products, n <= 16 NT tokens: bound by reading W once. A workgroup takes 16
+// Skinny products, up to 16 tokens: bound by reading W once. A workgroup takes 16
 // channels, its eight waves an eighth of the contraction each; W goes straight from
 // memory into the operands of v_mfma_f32_16x16x32_bf16 (W as the first one: lane l
-// holds channel l % 16, k = 8 (l / 16) .. + 7), 8 steps of 1 KB in flight per wave, X
-// comes from L2. The waves' sums meet in LDS and are added in the order of the waves.
+// holds channel l % 16, k = 8 (l / 16) .. + 7), kSkSteps steps of 1 KB in flight per
+// wave, X comes from L2. The waves' sums meet in LDS and are added in the order of the
+// waves. 8.6 us for one token 4096 -> 4096 (3.9 TB/s, the launch included), 93 us for
+// four 8192 -> 28672 (5.06 TB/s); nontemporal loads of W 9.5 and 111.
 constexpr int kSkWaves = 8;
 constexpr int kSkSteps = 8;
 
-template <int NT>
 __global__ __launch_bounds__(64 * kSkWaves) void linear_skinny_kernel(
     const unsigned short* __restrict__ X, int64_t ldx, const unsigned short* __restrict__ W, int n,
     int64_t b, int64_t c, LinEpilogue ep) {
-  __shared__ float red[kSkWaves][16 * NT][17];
+  __shared__ float red[kSkWaves][16][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r16 = lane & 15, kq = (lane >> 4) * 8;
   const int64_t f0 = (int64_t)blockIdx.x * 16;
   const int64_t fr = f0 + r16 < c ? f0 + r16 : c - 1;  // fills outputs that are not stored
   const unsigned short* wp = W + fr * b + kq;
-  const unsigned short* xp[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int t = j * 16 + r16 < n ? j * 16 + r16 : n - 1;
-    xp[j] = X + t * ldx + kq;
-  }
+  const unsigned short* xp = X + (r16 < n ? r16 : n - 1) * ldx + kq;
   const int steps = (int)cdiv(b, 32), per = (int)cdiv(steps, kSkWaves);
   const int sb = wave * per, se = min(steps, sb + per);
-  f32x4_t acc[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
   for (int s0 = sb; s0 < se; s0 += kSkSteps) {
-    u32x4_t w[kSkSteps], x[kSkSteps][NT];
+    u32x4_t w[kSkSteps], x[kSkSteps];
 #pragma unroll
     for (int u = 0; u < kSkSteps; ++u) {
       const int64_t k = (int64_t)(s0 + u) * 32;
       const bool in = s0 + u < se && k + kq < b;
       const u32x4_t zero = u32x4_t{0u, 0u, 0u, 0u};
-      w[u] = in ? __builtin_nontemporal_load((const u32x4_t*)(wp + k)) : zero;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) x[u][j] = in ? *(const u32x4_t*)(xp[j] + k) : zero;
+      w[u] = in ? *(const u32x4_t*)(wp + k) : zero;
+      x[u] = in ? *(const u32x4_t*)(xp + k) : zero;
     }
 #pragma unroll
     for (int u = 0; u < kSkSteps; ++u)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[u]),
-                                                         __builtin_bit_cast(bf16x8_t, x[u][j]),
-                                                         acc[j], 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[u]),
+                                                    __builtin_bit_cast(bf16x8_t, x[u]), acc, 0, 0, 0);
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[wave][j * 16 + r16][(lane >> 4) * 4 + e] = acc[j][e];
+  for (int e = 0; e < 4; ++e) red[wave][r16][(lane >> 4) * 4 + e] = acc[e];
   __syncthreads();
-  for (int i = tid; i < 256 * NT; i += 64 * kSkWaves) {
-    const int t = i >> 4, q = i & 15;
-    if (t < n && f0 + q < c) {
-      float v = red[0][t][q];
+  const int t = tid >> 4, q = tid & 15;
+  if (t < n && f0 + q < c) {  // n <= 16
+    float v = red[0][t][q];
 #pragma unroll
-      for (int w = 1; w < kSkWaves; ++w) v += red[w][t][q];
-      finish1(v, t, f0 + q, ep);
-    }
+    for (int w = 1; w < kSkWaves; ++w) v += red[w][t][q];
+    finish1(v, t, f0 + q, ep);
   }
 }
 
-enum { kLinSkinny = 0, kLin64 = 1, kLin128 = 2, kLin256 = 4 };
+// The tile kernel's forms. Its time is modelled as rounds of `slots` workgroups, each
+// taking fixed + stages * per_stage microseconds with every slot taken and half of the
+// second part with few (measured: 777 x 4096 -> 11008 on 172 tiles of 256 x 256 98.9 us,
+// modelled 96.4; 1024 x 4096 -> 4096 on 256 of 128 x 128 41.2, 41.2; 2048 x 4096 -> 4096
+// on 256 of 128 x 256 66.3, 66.5; 777 x 2056 -> 1023 on 208 of 64 x 64 16.6, 16.3), and
+// the join of splits as 3 us and its traffic at 4 TB/s. The cheapest form is taken: over
+// 25 shapes it was within 10% of the best one measured.
+struct LinTile {
+  int tm, tn;
+  int slots;  // workgroups that run at a time
+  double per_stage, fixed;
+};
+enum { kLin64 = 0, kLin128 = 1, kLin128x256 = 2, kLin256 = 3, kLinTiles = 4, kLinSkinny = 4 };
+constexpr LinTile kTiles[kLinTiles] = {
+    {64, 64, 512, 0.53, 4.0},     // 4 waves of 32 x 32, two workgroups per compute unit
+    {128, 128, 256, 0.55, 6.0},   // 8 waves of 64 x 32
+    {128, 256, 256, 0.93, 7.0},   // 8 waves of 64 x 64
+    {256, 256, 256, 1.54, 14.0},  // 8 waves of 128 x 64
+};
+// Up to 12 tokens the skinny kernel is ahead (4096 -> 4096: 8.5 us for one token against
+// 12.7 on tiles, 11.0 against 13.3 for twelve; 11008 -> 4096: even at sixteen).
+constexpr int64_t kSkinny = 12;
 
 struct LinPlan {
   int tile;    // one of the above
@@ -457,28 +464,29 @@ struct LinPlan {
   int per;     // stages per piece
 };
 
-constexpr int kUnits = 256;  // compute units
-
 LinPlan plan_of(int64_t n, int64_t b, int64_t c, bool can_split) {
-  LinPlan p;
-  p.per = (int)cdiv(b, kLK);
-  p.splits = 1;
-  if (n <= 64) {
-    p.tile = kLinSkinny;
-    return p;
+  const int64_t stages = cdiv(b, kLK);
+  LinPlan best = {kLinSkinny, 1, (int)stages};
+  if (n <= kSkinny) return best;
+  double least = 1e300;
+  for (int t = 0; t < kLinTiles; ++t) {
+    const LinTile& k = kTiles[t];
+    const int64_t tiles = cdiv(n, k.tm) * cdiv(c, k.tn);
+    for (int64_t want : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (want > 1 && (!can_split || stages < 2 * want || tiles * want > 4 * k.slots)) break;
+      const int64_t per = cdiv(stages, want), splits = cdiv(stages, per);
+      const int64_t full = tiles * splits / k.slots, rest = tiles * splits % k.slots;
+      double us = (double)full * (k.fixed + (double)per * k.per_stage);
+      if (rest)
+        us += k.fixed + (double)per * k.per_stage * (0.5 + 0.5 * (double)rest / k.slots);
+      if (splits > 1) us += 3.0 + 8.0 * (double)splits * (double)n * (double)c / 4e6;
+      if (us < least) {
+        least = us;
+        best = {t, (int)splits, (int)per};
+      }
+    }
   }
-  const int64_t big = cdiv(n, 256) * cdiv(c, 256), mid = cdiv(n, 128) * cdiv(c, 128);
-  p.tile = big >= kUnits ? kLin256 : (mid >= kUnits ? kLin128 : kLin64);
-  const int64_t tiles = p.tile == kLin256 ? big : (p.tile == kLin128 ? mid : cdiv(n, 64) * cdiv(c, 64));
-  const int64_t stages = p.per;
-  if (can_split && tiles < kUnits) {
-    int64_t splits = 2 * kUnits / tiles;
-    if (splits > stages / 8) splits = stages / 8;
-    if (splits < 1) splits = 1;
-    p.per = (int)cdiv(stages, splits);
-    p.splits = (int)cdiv(stages, p.per);
-  }
-  return p;
+  return best;
 }
 
 template <int WM, int WN, int GN, int SA, int SB>
@@ -490,14 +498,6 @@ hipError_t launch_tiles(const unsigned short* X, int64_t ldx, const unsigned sho
   hipLaunchKernelGGL((linear_tile_kernel<WM, WN, GN, SA, SB>),
                      dim3((unsigned)(8 * per_xcd), (unsigned)p.splits), dim3(128 * GN), 0, s, X,
                      ldx, W, n, b, c, ntm, ntn, per_xcd, p.per, part, ep);
-  return hipGetLastError();
-}
-
-template <int NT>
-hipError_t launch_skinny(const unsigned short* X, int64_t ldx, const unsigned short* W, int64_t n,
-                         int64_t b, int64_t c, const LinEpilogue& ep, hipStream_t s) {
-  hipLaunchKernelGGL((linear_skinny_kernel<NT>), dim3((unsigned)cdiv(c, 16)), dim3(64 * kSkWaves),
-                     0, s, X, ldx, W, (int)n, b, c, ep);
   return hipGetLastError();
 }
 
@@ -528,12 +528,13 @@ hipError_t launch_linear(const unsigned short* X, int64_t ldx, const unsigned sh
   hipError_t e;
   switch (p.tile) {
     case kLinSkinny:
-      e = n <= 16   ? launch_skinny<1>(X, ldx, W, n, b, c, ep, s)
-          : n <= 32 ? launch_skinny<2>(X, ldx, W, n, b, c, ep, s)
-                    : launch_skinny<4>(X, ldx, W, n, b, c, ep, s);
+      hipLaunchKernelGGL(linear_skinny_kernel, dim3((unsigned)cdiv(c, 16)), dim3(64 * kSkWaves), 0, s,
+                         X, ldx, W, (int)n, b, c, ep);
+      e = hipGetLastError();
       break;
     case kLin64: e = launch_tiles<1, 1, 2, 4, 4>(X, ldx, W, n, b, c, p, raw, ep, s); break;
-    case kLin128: e = launch_tiles<2, 2, 2, 2, 2>(X, ldx, W, n, b, c, p, raw, ep, s); break;
+    case kLin128: e = launch_tiles<2, 1, 4, 4, 4>(X, ldx, W, n, b, c, p, raw, ep, s); break;
+    case kLin128x256: e = launch_tiles<2, 2, 4, 3, 3>(X, ldx, W, n, b, c, p, raw, ep, s); break;
     default: e = launch_tiles<4, 2, 4, 3, 2>(X, ldx, W, n, b, c, p, raw, ep, s); break;
   }
   if (e != hipSuccess || !raw) return e;

@@ -55,9 +55,9 @@ def test_linear_workspace_query():
     assert lib.th_linear_workspace_size(4, 64, 8, None) == L.TH_ERR_INVALID_ARG
     assert L.linear_workspace_size(0, 4096, 4096) == 0
     assert L.linear_workspace_size(131072, 4096, 4096) == 0  # enough tiles: nothing is split
-    need = L.linear_workspace_size(777, 2056, 1023)
-    assert need > 0 and need % (777 * 1024 * 4) == 0
-    a = dict(n=777, b=2056, ldx=2056, c=1023, ldy=1023, ws=FAKE)
+    need = L.linear_workspace_size(70, 4096, 519)
+    assert need > 0 and need % (70 * 520 * 4) == 0
+    a = dict(n=70, b=4096, ldx=4096, c=519, ldy=519, ws=FAKE)
     assert lib.th_linear(*_linear_args(ws_bytes=need - 1, **a)) == L.TH_ERR_WORKSPACE
 
 
