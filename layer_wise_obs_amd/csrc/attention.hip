@@ -495,6 +495,294 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   }
 }
 
+// Few rows (single tokens over a cache): a workgroup takes 32 rows of one sequence and
+// key head, and its four waves every fourth tile of 32 keys, each with two tiles of its
+// own in LDS and no barrier in the loop; their (m, l, O) meet in LDS at the end. Bound
+// by reading K and V; against 128-row workgroups, whose other three waves had no rows,
+// a token over 300 keys of 32 heads went from 12.5 to 10.8 us. Everything else is as above.
+template <int D, int DC, bool PAD>
+__global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
+  constexpr int kBM = 32, kKeys = 32, kWaves = 4;
+  constexpr int kPieces = D / 8, kRowB = D * 2;
+  constexpr int kTile = kKeys * kRowB;     // one operand's tile
+  constexpr int kLd = kTile / 1024;        // 1 KB loads per operand
+  constexpr int kRowsPer = 64 / kPieces;
+  constexpr int kDB = DC / 32, kKS = DC / 16;
+  constexpr int kOutW = D + 4;             // row pitch of the joined O, floats
+  static_assert(32 * kOutW * 4 <= 4 * kTile, "O fits a wave's tiles");
+  __shared__ __attribute__((aligned(1024))) unsigned char sm[kWaves * 4 * kTile];
+  __shared__ float sm_m[kWaves][32], sm_l[kWaves][32];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int head = blockIdx.x % a.hk;
+  const int64_t slot = (int64_t)(gridDim.x / a.hk) - 1 - blockIdx.x / a.hk;
+  const Sequence sq = sequence_of<kBM>(a, slot, lane);
+  if (sq.index < 0) return;
+  const int64_t q0 = sq.q0, q1 = sq.q1, k0 = sq.k0, k1 = sq.k1;
+  const int lk = k1 > k0 ? (int)(k1 - k0) : 0;
+  const int64_t rows = q1 > q0 ? (q1 - q0) * a.g : 0;
+  const int64_t row0 = (slot - (q0 * a.g / kBM + sq.index)) * kBM;
+  if (row0 < 0 || row0 >= rows) return;
+  const int off = lk - (int)(q1 - q0);
+  auto limit_of = [&](int64_t r) {
+    if (!a.causal) return lk;
+    const int64_t e = (int64_t)((unsigned)r / (unsigned)a.g) + off + 1;
+    return (int)(e < 0 ? 0 : (e < lk ? e : lk));
+  };
+  const int64_t row_end = row0 + kBM < rows ? row0 + kBM : rows;
+  const int keys = limit_of(row_end - 1);
+  const int per = (int)cdiv(cdiv(keys, kKeys), a.splits) * kKeys;
+  const int kbeg = min(keys, (int)blockIdx.y * per), kend = min(keys, kbeg + per);
+  const int64_t mine = row0 + (lane & 31);
+  const int64_t r = mine < row_end ? mine : row_end - 1;
+  const int64_t tok = (unsigned)r / (unsigned)a.g;
+  const int qh = head * a.g + (int)(r - tok * a.g);
+  const int lim = min(limit_of(r), kend);
+  const int lim_first = __builtin_amdgcn_readfirstlane(lim);
+  const int half = lane >> 5;
+
+  bf16x8_t qf[kKS];
+  {
+    const unsigned short* qp = a.q + (q0 + tok) * a.q_token + qh * a.q_head;
+#pragma unroll
+    for (int st = 0; st < kKS; ++st) {
+      const int e = st * 16 + half * 8;
+      u32x4_t u = u32x4_t{0u, 0u, 0u, 0u};
+      if (e < a.d) u = *(const u32x4_t*)(qp + e);
+      qf[st] = __builtin_bit_cast(bf16x8_t, u);
+    }
+  }
+
+  // Loader: load i fills rows kRowsPer i .. of the wave's own tile, pieces swizzled as
+  // above.
+  unsigned char* own = sm + wave * 4 * kTile;  // K0 V0 K1 V1
+  if constexpr (PAD) {
+    for (int i = lane; i < 4 * kTile / 16; i += 64) *(u32x4_t*)(own + i * 16) = u32x4_t{0u, 0u, 0u, 0u};
+    wave_sync();
+  }
+  const int lr = lane / kPieces, lpp = lane % kPieces;
+  auto k_piece = [&](int i) {
+    const int row = i * kRowsPer + lr;
+    return (lpp ^ (D == 128 ? (row & 15) : ((row >> 1) & 7))) * 8;
+  };
+  const int cv = (lpp ^ (D == 128 ? ((lr & 3) << 2) : (((lr >> 1) & 1) << 2))) * 8;
+  const unsigned short* kb = a.k + k0 * a.k_token + head * a.k_head;
+  const unsigned short* vb = a.v + k0 * a.v_token + head * a.v_head;
+  const unsigned ob = lds_address(sm) + wave * 4 * kTile;
+  auto issue = [&](int kt, int buf) {
+    const unsigned short* gk = kb + (int64_t)kt * a.k_token;
+    const unsigned short* gv = vb + (int64_t)kt * a.v_token;
+    const int last = min(kKeys, lk - kt) - 1;  // rows past the keys read the last: masked
+#pragma unroll
+    for (int i = 0; i < kLd; ++i) {
+      const unsigned row = min(i * kRowsPer + lr, last);
+      const int ck = k_piece(i);
+      if (!PAD || ck < a.d)
+        lds_dma1((row * (unsigned)a.k_token + ck) * 2, gk, ob + 2 * buf * kTile + i * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < kLd; ++i) {
+      const unsigned row = min(i * kRowsPer + lr, last);
+      if (!PAD || cv < a.d)
+        lds_dma1((row * (unsigned)a.v_token + cv) * 2, gv, ob + (2 * buf + 1) * kTile + i * 1024);
+    }
+  };
+  const int krow = lane & 31;
+  const int kswz = D == 128 ? (krow & 15) : ((krow >> 1) & 7);
+  const int kaddr = krow * kRowB + ((half ^ kswz) << 4);
+  const int s16 = lane & 15;
+  const int vkey = 4 * half + (s16 >> 2);
+  const int vswz = D == 128 ? ((vkey & 3) << 2) : (((vkey >> 1) & 1) << 2);
+  const int vpiece = 2 * ((lane >> 4) & 1) + ((s16 & 3) >> 1);
+  const int vaddr = vkey * kRowB + ((vpiece ^ vswz) << 4) + (s16 & 1) * 8;
+
+  f32x16_t o[kDB];
+  float m, l;
+  unsigned bad = 0;
+  auto tile = [&](int kt, int buf, auto CAREFUL) __attribute__((always_inline)) {
+    constexpr bool careful = decltype(CAREFUL)::value;
+    const unsigned char* ks = own + 2 * buf * kTile;
+    const unsigned char* vs = ks + kTile;
+    auto v_frag = [&](int ks16, int db) {
+      const unsigned char* p = vs + ks16 * 16 * kRowB + (vaddr ^ (db << 6));
+      const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) v4i16_t*)p);
+      const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) v4i16_t*)(p + 8 * kRowB));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    f32x16_t s2[2] = {{}, {}};  // two chains of products
+#pragma unroll
+    for (int st = 0; st < kKS; ++st) {
+      const bf16x8_t kf = *(const bf16x8_t*)(ks + (kaddr ^ (st << 5)));
+      s2[st & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[st], s2[st & 1], 0, 0, 0);
+    }
+    f32x16_t s;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = s2[0][e] + s2[1][e];
+    const bool masked = kt + kKeys > lim_first;
+    if (masked) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        s[e] = kt + 8 * (e >> 2) + 4 * half + (e & 3) < lim ? s[e] : -INFINITY;
+      if constexpr (!careful) {
+#pragma unroll
+        for (int ks16 = 0; ks16 < 2; ++ks16)
+#pragma unroll
+          for (int db = 0; db < kDB; ++db) {
+            const u32x4_t u = __builtin_bit_cast(u32x4_t, v_frag(ks16, db));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) bad |= (u[x] & 0x7f807f80u) + 0x00800080u;
+          }
+      }
+    }
+    float top = s[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
+    top = half_max(top) * a.c;
+    if (__any(top > m + kAMove)) {
+      const float mn = fmaxf(m, top);
+      const float f = exp2_fast(m - (mn == -INFINITY ? 0.f : mn));
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < kDB; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] *= f;
+      m = mn;
+    }
+    const float ref = m == -INFINITY ? 0.f : -m;
+    bf16x8_t pf[2];
+#pragma unroll
+    for (int ks16 = 0; ks16 < 2; ++ks16)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int e = ks16 * 8 + 2 * x;
+        const bf16x2_t p = pack2(exp2_fast(fmaf(s[e], a.c, ref)), exp2_fast(fmaf(s[e + 1], a.c, ref)));
+        l = __builtin_amdgcn_fdot2_f32_bf16(p, bf16x2_t{(__bf16)1.0f, (__bf16)1.0f}, l, false);
+        pf[ks16][2 * x] = p[0];
+        pf[ks16][2 * x + 1] = p[1];
+      }
+    if constexpr (careful) {
+      if (masked) {
+#pragma unroll
+        for (int ks16 = 0; ks16 < 2; ++ks16)
+#pragma unroll
+          for (int db = 0; db < kDB; ++db) {
+            const v8i16_t vx = v_frag(ks16, db);
+#pragma unroll 1
+            for (int j = 0; j < 16; ++j) {
+              const int jh = (j >> 2) & 1, jx = (j & 3) + 4 * (j >> 3);
+              v8i16_t one;
+#pragma unroll
+              for (int x = 0; x < 8; ++x) one[x] = half == jh && x == jx ? vx[x] : (short)0;
+              const f32x16_t zero = {};
+              const f32x16_t z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  __builtin_bit_cast(bf16x8_t, one), pf[ks16], zero, 0, 0, 0);
+              if (kt + 16 * ks16 + j < lim) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[db][e] += z[e];
+              }
+            }
+          }
+        return;
+      }
+    }
+#pragma unroll
+    for (int ks16 = 0; ks16 < 2; ++ks16)
+#pragma unroll
+      for (int db = 0; db < kDB; ++db)
+        o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_bit_cast(bf16x8_t, v_frag(ks16, db)), pf[ks16], o[db], 0, 0, 0);
+  };
+  auto pass = [&](auto CAREFUL) __attribute__((always_inline)) {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kDB; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+    constexpr int step = kWaves * kKeys;
+    int kt = kbeg + wave * kKeys, buf = 0;
+    if (kt < kend) issue(kt, 0);
+    for (; kt < kend; kt += step, buf ^= 1) {
+      if (kt + step < kend) {
+        // the other buffer's reads are done before it is filled again
+        __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        issue(kt + step, buf ^ 1);
+        if constexpr (kLd == 8)
+          __asm__ volatile("s_waitcnt vmcnt(16)" ::: "memory");
+        else
+          __asm__ volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      } else {
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+      tile(kt, buf, CAREFUL);
+    }
+  };
+  static_assert(kLd == 8 || kLd == 4, "vmcnt immediates");
+  pass(std::integral_constant<bool, false>{});
+  if (__syncthreads_or((bad & 0x80008000u) != 0)) {
+    pass(std::integral_constant<bool, true>{});
+    __syncthreads();
+  }
+
+  // Join of the waves: each puts its O (32 rows) over its own tiles.
+  l += __shfl_xor(l, 32);
+  float* po = (float*)own;
+#pragma unroll
+  for (int db = 0; db < kDB; ++db)
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      *(f32x4_t*)(po + (lane & 31) * kOutW + db * 32 + 8 * x + 4 * half) =
+          f32x4_t{o[db][4 * x], o[db][4 * x + 1], o[db][4 * x + 2], o[db][4 * x + 3]};
+  if (half == 0) {
+    sm_m[wave][lane] = m;
+    sm_l[wave][lane] = l;
+  }
+  __syncthreads();
+  const int rr = tid >> 3;  // eight threads per row
+  if (row0 + rr >= row_end) return;
+  const int64_t rg = row0 + rr;
+  const int64_t ot = (unsigned)rg / (unsigned)a.g;
+  const int oh = head * a.g + (int)(rg - ot * a.g);
+  const int vis = limit_of(rg);
+  float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, sm_m[w][rr]);
+  const float rt = mt == -INFINITY ? 0.f : mt;
+  float f[kWaves];
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    // a wave whose scores were all -inf (or that saw no key) weighs nothing, a NaN stays
+    const float lw = sm_l[w][rr];
+    f[w] = lw == 0.f ? 0.f : exp2_fast(sm_m[w][rr] - rt);
+    lt += lw * f[w];
+  }
+  const int64_t at = ((int64_t)blockIdx.y * a.nq + q0 + ot) * (a.hk * a.g) + oh;
+  if (a.splits > 1 && (tid & 7) == 0)
+    a.part_ml[at] = make_float2(mt, min(vis, kend) > kbeg && lt == 0.f ? -1.f : lt);
+  const float inv = vis > 0 ? 1.0f / lt : 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {  // elements 4 (tid % 8) + 32 i
+    const int e = (tid & 7) * 4 + 32 * i;
+    if (e >= a.d) break;
+    f32x4_t v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+      if (f[w] != 0.f)
+        v += *(const f32x4_t*)((const float*)(sm + w * 4 * kTile) + rr * kOutW + e) * f[w];
+    if (a.splits > 1) {
+      *(f32x4_t*)(a.part_o + at * a.d + e) = v;
+    } else {
+      const bf16x2_t w0 = vis > 0 ? pack2(v[0] * inv, v[1] * inv) : pack2(0.f, 0.f);
+      const bf16x2_t w1 = vis > 0 ? pack2(v[2] * inv, v[3] * inv) : pack2(0.f, 0.f);
+      *(bf16x4_t*)(a.o + (q0 + ot) * a.o_token + oh * a.o_head + e) =
+          __builtin_shufflevector(w0, w1, 0, 1, 2, 3);
+    }
+  }
+}
+
 // Joins the splits of a (token, query head): eight groups of 32 lanes (4 elements
 // each) take every eighth split, group 0 adds the groups in order.
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
@@ -553,35 +841,54 @@ void launch_kernel(const AttnArgs& a, hipStream_t s) {
                      dim3((unsigned)(slots * a.hk), (unsigned)a.splits), dim3(64 * NW), 0, s, a);
 }
 
-constexpr int kABM = 128;      // rows per workgroup
+template <int D, int DC, bool PAD>
+void launch_few(const AttnArgs& a, hipStream_t s) {
+  const int64_t slots = a.nq * a.g / 32 + a.nseq;
+  hipLaunchKernelGGL((attention_few_kernel<D, DC, PAD>),
+                     dim3((unsigned)(slots * a.hk), (unsigned)a.splits), dim3(256), 0, s, a);
+}
+
 constexpr int kAUnits = 256;  // compute units
 
-// Pieces the keys are split into, by the sequences' average lengths (all that the host
-// knows). Where a sequence's rows fill one workgroup at most (single tokens), reading
-// the keys bounds the call, and many small pieces even out the sequences' lengths:
-// eight workgroups per compute unit, pieces of two tiles or more (16 sequences over
-// 300001 keys: 355 us with two workgroups per unit, 282 with eight). Where rows fill
-// several workgroups, the products bound it and the partial results cost: two
-// workgroups per unit, pieces of four tiles or more.
-int splits_of(const th_attention_params* p) {
+struct AttnPlan {
+  bool few;    // 32-row workgroups whose waves share the keys
+  int splits;  // pieces of the keys
+};
+
+// By the sequences' average lengths, all that the host knows. Up to 32 rows a sequence
+// the call is bound by reading the keys: the few-rows kernel (one workgroup per compute
+// unit at a time), its keys in pieces of 192 or more while those do not fill the units,
+// else of 512 or more up to four rounds, which even out the sequences' lengths. (16
+// sequences over 300001 keys, 8 key heads: 287, 272, 292, 330 us with two, four, eight,
+// sixteen rounds; one over 4096 keys, 32 heads: 22 us in 8 pieces, 28 in 16; four over
+// 4000 keys, 8 heads: 19, 15, 13 us in pieces of 512, 256, 128; one over 32768 keys, one
+// head: 22 us in 64 pieces, 27 in 128.) With more rows the products bound it and partial
+// results cost: two workgroups per unit, pieces of four tiles of 64 or more.
+AttnPlan plan_of(const th_attention_params* p) {
   const int64_t g = p->hq / p->hk;
   const int64_t seqs = p->nseq < p->nq ? p->nseq : p->nq;
-  const int64_t blocks = cdiv(cdiv(p->nq, seqs) * g, kABM);
-  const int64_t groups = seqs * blocks * p->hk;
-  const int64_t tiles = cdiv(cdiv(p->nk, seqs), kAKT);
-  const bool few = blocks == 1;
-  int64_t s = (few ? 8 : 2) * kAUnits / groups;
-  const int64_t most = few ? tiles / 2 : tiles / 4;
-  if (s > most) s = most;
-  if (s > 128) s = 128;
-  return s < 1 ? 1 : (int)s;
+  const int64_t rows = cdiv(p->nq, seqs) * g, keys = cdiv(p->nk, seqs);
+  AttnPlan r;
+  r.few = rows <= 32;
+  const int64_t groups = seqs * cdiv(rows, r.few ? 32 : 128) * p->hk;
+  auto pieces = [&](int64_t workgroups, int64_t least) {
+    const int64_t s = workgroups / groups < keys / least ? workgroups / groups : keys / least;
+    return s < 1 ? (int64_t)1 : (s > 64 ? (int64_t)64 : s);
+  };
+  if (r.few) {
+    const int64_t one = pieces(kAUnits, 192), more = pieces(4 * kAUnits, 512);
+    r.splits = (int)(one > more ? one : more);
+  } else {
+    r.splits = (int)pieces(2 * kAUnits, 4 * 64);
+  }
+  return r;
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(const th_attention_params* p) {
   if (p->nq == 0) return 0;
-  const int s = splits_of(p);
+  const int s = plan_of(p).splits;
   if (s == 1) return 0;
   return (size_t)s * p->nq * p->hq * ((size_t)p->d * sizeof(float) + sizeof(float2));
 }
@@ -612,19 +919,30 @@ hipError_t launch_attention(const void* Q, const void* K, const void* V, const i
   a.d = (int)p->d;
   a.causal = p->causal != 0;
   a.c = (float)(p->scale * 1.4426950408889634);
-  a.splits = workspace ? splits_of(p) : 1;
+  const AttnPlan plan = plan_of(p);
+  a.splits = workspace ? plan.splits : 1;
   a.part_ml = (float2*)workspace;
   a.part_o = workspace ? (float*)(a.part_ml + (size_t)a.splits * p->nq * p->hq) : nullptr;
-  if (p->d < 64)
+  if (plan.few) {
+    if (p->d < 64)
+      launch_few<64, 64, true>(a, s);
+    else if (p->d == 64)
+      launch_few<64, 64, false>(a, s);
+    else if (p->d < 128)
+      launch_few<128, 128, true>(a, s);
+    else
+      launch_few<128, 128, false>(a, s);
+  } else if (p->d < 64) {
     launch_kernel<64, 64, 4, 2, true>(a, s);
-  else if (p->d == 64)
+  } else if (p->d == 64) {
     launch_kernel<64, 64, 4, 2, false>(a, s);
-  else if (p->d <= 96)
+  } else if (p->d <= 96) {
     launch_kernel<128, 96, 4, 2, true>(a, s);
-  else if (p->d < 128)
+  } else if (p->d < 128) {
     launch_kernel<128, 128, 4, 2, true>(a, s);
-  else
+  } else {
     launch_kernel<128, 128, 4, 2, false>(a, s);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)(p->nq * p->hq)), dim3(256), 0, s, a);

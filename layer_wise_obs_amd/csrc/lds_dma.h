@@ -50,22 +50,6 @@ __device__ __forceinline__ uint64_t uniform_u64(uint64_t x) {
   return ((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((unsigned)(x >> 32)) << 32) |
          (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((unsigned)x);
 }
-// LDS byte address of a __shared__ object, for the loads below.
-__device__ __forceinline__ unsigned lds_address(const void* p) {
-  return (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
-}
-
-// One load of 16 bytes per lane straight into LDS, in the saddr form: byte offset vo
-// (< 2^31) from the wave-uniform base g, into the 1 KB at LDS byte address lds
-// (wave-uniform). No result registers; completion is tracked by the callers' vmcnt
-// waits. M0 is declared clobbered rather than saved: two scalar moves fewer.
-__device__ __forceinline__ void lds_dma1(unsigned vo, const void* g, unsigned lds) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                   :
-                   : "s"(lds), "v"(vo), "s"(g)
-                   : "m0");
-}
-
 __device__ __forceinline__ void lds_dma10s(const unsigned (&vo)[5], const void* gbase0,
                                            const void* gbase1, const void* lds) {
   const unsigned base = __builtin_amdgcn_readfirstlane(
@@ -89,6 +73,26 @@ __device__ __forceinline__ void lds_dma10s(const unsigned (&vo)[5], const void* 
       : "=&s"(saved)
       : "s"(base), "v"(vo[0]), "v"(vo[1]), "v"(vo[2]), "v"(vo[3]), "v"(vo[4]), "s"(g0), "s"(g1)
       : "scc");
+}
+
+// LDS byte address of a __shared__ object, for the loads below.
+__device__ __forceinline__ unsigned lds_address(const void* p) {
+  return (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// One load of 16 bytes per lane straight into LDS, in the saddr form: byte offset vo
+// (< 2^31) from the wave-uniform base g, into the 1 KB at LDS byte address lds
+// (wave-uniform). Lanes that are off write nothing, the others keep their places. No
+// result registers; completion is tracked by the callers' vmcnt waits.
+__device__ __forceinline__ void lds_dma1(unsigned vo, const void* g, unsigned lds) {
+  const unsigned base = __builtin_amdgcn_readfirstlane(lds);
+  const uint64_t gb = uniform_u64((uint64_t)(uintptr_t)g);
+  unsigned saved;
+  __asm__ volatile(
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+      "global_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(base), "v"(vo), "s"(gb));
 }
 
 }  // namespace th
