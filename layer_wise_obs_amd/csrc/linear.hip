@@ -227,46 +227,49 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
   // the lane's own and a substep only XORs a piece bit
   const int faddr = r16 * kLRow + ((quad ^ ((r16 >> 1) & 7)) << 4);
   bf16x8_t a0[FM], b0[FN], a1[FM], b1[FN];
-  auto read_frags = [&](int it, int sub, bf16x8_t (&a)[FM], bf16x8_t (&bb)[FN]) {
-    const unsigned char* fa = sm + (it % SA) * kA + (faddr ^ (sub << 6));
-    const unsigned char* fb = sm + SA * kA + (it % SB) * kB + (faddr ^ (sub << 6));
-#pragma unroll
-    for (int i = 0; i < FM; ++i) a[i] = *(const bf16x8_t*)(fa + (wm * FM + i) * 16 * kLRow);
-#pragma unroll
-    for (int j = 0; j < FN; ++j) bb[j] = *(const bf16x8_t*)(fb + (wn * FN + j) * 16 * kLRow);
+  // operand y of a substep: the FN blocks of W, then the FM of X
+  auto read_one = [&](int it, int sub, int y, bf16x8_t (&a)[FM], bf16x8_t (&bb)[FN]) {
+    if (y < FN)
+      bb[y] = *(const bf16x8_t*)(sm + SA * kA + (it % SB) * kB + (faddr ^ (sub << 6)) +
+                                 (wn * FN + y) * 16 * kLRow);
+    else
+      a[y - FN] = *(const bf16x8_t*)(sm + (it % SA) * kA + (faddr ^ (sub << 6)) +
+                                     (wm * FM + y - FN) * 16 * kLRow);
   };
-  // One substep's products. The order is pinned: the operand reads of the next
-  // substep go first, then the loads of a coming stage between the products, so
-  // that reads and loads issue while the matrix cores are busy.
-  auto mfmas = [&](const bf16x8_t (&a)[FM], const bf16x8_t (&bb)[FN], auto&& between) {
+  // One substep's products, with the next substep's operand reads (of stage it2, substep
+  // sub2) and a coming stage's loads between them. The order is pinned, products first:
+  // after a barrier the matrix cores start at once.
+  auto mfmas = [&](const bf16x8_t (&a)[FM], const bf16x8_t (&bb)[FN], int it2, int sub2,
+                   bf16x8_t (&a2)[FM], bf16x8_t (&b2)[FN], auto&& load) {
+    constexpr int per = (FM + FN + FM * FN - 1) / (FM * FN);  // reads after a product
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int x = 0; x < FM * FN; ++x) {
       const int i = x / FN, j = x % FN;
       acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], bb[j], acc[i][j], 0, 0, 0);
-      between(x);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int y = 0; y < per; ++y)
+        if (x * per + y < FM + FN) read_one(it2, sub2, x * per + y, a2, b2);
+      load(x);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
   };
   // the loads of one operand's stage, spread evenly over a substep's products
   auto loads_a = [&](int x) {
     constexpr int gap = FM * FN / LA > 0 ? FM * FN / LA : 1, per = (LA + FM * FN - 1) / (FM * FN);
     if (x % gap == 0) {
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int m = 0; m < per; ++m)
         if (x / gap * per + m < LA) issue_a(x / gap * per + m);
-      __builtin_amdgcn_sched_barrier(0);
     }
   };
   auto loads_b = [&](int x) {
     constexpr int gap = FM * FN / LB > 0 ? FM * FN / LB : 1, per = (LB + FM * FN - 1) / (FM * FN);
     if (x % gap == 0) {
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int m = 0; m < per; ++m)
         if (x / gap * per + m < LB) issue_b(x / gap * per + m);
-      __builtin_amdgcn_sched_barrier(0);
     }
   };
   // Order of the loads: A(SA-1), B(SB), A(SA), B(SB+1), ... At the wait of stage it, A
@@ -302,7 +305,8 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
   stage_b(SB - 1);
 #pragma unroll
   for (int m = 0; m < LB; ++m) issue_b(m);
-  read_frags(0, 0, a0, b0);
+#pragma unroll
+  for (int y = 0; y < FM + FN; ++y) read_one(0, 0, y, a0, b0);
   // A stage: half its products, then (its last operands read, the next stage landed,
   // the barrier) the other half. A's next stage goes into the buffer freed by the
   // barrier of stage it - 1 during the first half, B's into the one freed by this
@@ -310,14 +314,12 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
   // loads in one half would take half of it in bursts.
   for (int it = 0; it < nk; ++it) {
     stage_a(it + SA - 1);
-    read_frags(it, 1, a1, b1);
-    mfmas(a0, b0, loads_a);
+    mfmas(a0, b0, it, 1, a1, b1, loads_a);
     wait_loads();
     zero_tail(it + 1);
     __syncthreads();
     stage_b(it + SB);
-    read_frags(it + 1, 0, a0, b0);
-    mfmas(a1, b1, loads_b);
+    mfmas(a1, b1, it + 1, 0, a0, b0, loads_b);
   }
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();  // every wave's loads have landed: the stages may be reused
