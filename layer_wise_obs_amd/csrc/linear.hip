@@ -331,11 +331,16 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
   constexpr int kCols = 32 * WN, kPitch = kCols + 4;
   static_assert(kWaves * 32 * kPitch * 4 <= SA * kA + SB * kB, "strips fit the stages");
   float* strip = (float*)sm + wave * 32 * kPitch;
-  constexpr int kLanes = kCols / 8;      // lanes per token
-  constexpr int kTok = 64 / kLanes;      // tokens per pass
+  constexpr int kLanes = kCols / 8;   // lanes per token
+  constexpr int kTok = 64 / kLanes;   // tokens per pass
+  constexpr int kPass = 32 / kTok;
   const int64_t cp = (c + 7) & ~(int64_t)7;
-#pragma unroll
-  for (int i = 0; i < WM; ++i) {
+  const int tl = lane / kLanes, ql = (lane % kLanes) * 8;
+  const int64_t q = N0 + wn * kCols + ql;
+  const int count = c - q < 8 ? (int)(c - q) : 8;
+  auto token = [&](int i, int p) { return M0 + wm * 32 * WM + i * 32 + p * kTok + tl; };
+  auto values = [&](int p) { return strip + (p * kTok + tl) * kPitch + ql; };
+  auto write_strip = [&](int i) {
 #pragma unroll
     for (int i2 = 0; i2 < 2; ++i2)
 #pragma unroll
@@ -344,26 +349,115 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
         for (int e = 0; e < 4; ++e)
           strip[(i2 * 16 + quad * 4 + e) * kPitch + j * 16 + r16] = acc[2 * i + i2][j][e];
     wave_sync();
+  };
+  if (part) {
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+      write_strip(i);
 #pragma unroll 1
-    for (int t0 = 0; t0 < 32; t0 += kTok) {
-      const int tr = t0 + lane / kLanes;
-      const int64_t t = M0 + wm * 32 * WM + i * 32 + tr;
-      const int64_t q = N0 + wn * kCols + (lane % kLanes) * 8;
-      if (t < n && q < c) {
-        const f32x4_t* p = (const f32x4_t*)(strip + tr * kPitch + (lane % kLanes) * 8);
-        const f32x4_t lo = p[0], hi = p[1];
-        if (part) {
-          f32x4_t* o = (f32x4_t*)(part + ((int64_t)blockIdx.y * n + t) * cp + q);
-          o[0] = lo;
-          o[1] = hi;
-        } else {
-          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          finish8(v, t, q, c - q < 8 ? (int)(c - q) : 8, ep);
+      for (int p = 0; p < kPass; ++p) {
+        if (token(i, p) < n && count > 0) {
+          const f32x4_t* v = (const f32x4_t*)values(p);
+          f32x4_t* o = (f32x4_t*)(part + ((int64_t)blockIdx.y * n + token(i, p)) * cp + q);
+          o[0] = v[0];
+          o[1] = v[1];
         }
       }
+      wave_sync();
     }
-    wave_sync();
+    return;
   }
+  if (!ep.vec) {
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+      write_strip(i);
+#pragma unroll 1
+      for (int p = 0; p < kPass; ++p) {
+        if (token(i, p) < n && count > 0) {
+          float v[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] = values(p)[x];
+          finish8(v, token(i, p), q, count, ep);
+        }
+      }
+      wave_sync();
+    }
+    return;
+  }
+  // The residuals of all strips (fp32: of two at a time) are on their way before the
+  // first one is used: read strip by strip they cost 16 round trips to memory a tile.
+  auto finish = [&](auto F32) __attribute__((always_inline)) {
+    constexpr bool f32 = decltype(F32)::value;
+    constexpr int kHeld = f32 && WM > 2 ? 2 : WM;
+    u32x4_t res[kHeld][kPass][f32 ? 2 : 1];
+#pragma unroll
+    for (int i0 = 0; i0 < WM; i0 += kHeld) {
+      if (ep.residual) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+          for (int p = 0; p < kPass; ++p)
+            if (token(i0 + i, p) < n && count > 0) {
+              const int64_t at = token(i0 + i, p) * ep.ldr + q;
+              if constexpr (f32) {
+                res[i][p][0] = ((const u32x4_t*)((const float*)ep.residual + at))[0];
+                res[i][p][1] = ((const u32x4_t*)((const float*)ep.residual + at))[1];
+              } else {
+                res[i][p][0] = *(const u32x4_t*)((const unsigned short*)ep.residual + at);
+              }
+            }
+      }
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        write_strip(i0 + i);
+        if (ep.bias || ep.act != TH_ACT_NONE) {  // in place, by the lane that reads it next
+#pragma unroll 1
+          for (int p = 0; p < kPass; ++p) {
+            float* v = values(p);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const float b8 = ep.bias && count > 0 ? bf16_to_f32(ep.bias[q + x]) : 0.f;
+              v[x] = activate(v[x] + b8, ep.act);
+            }
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < kPass; ++p) {
+          if (token(i0 + i, p) >= n || count <= 0) continue;
+          const f32x4_t* vp = (const f32x4_t*)values(p);
+          const f32x4_t lo = vp[0], hi = vp[1];
+          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          const int64_t at = token(i0 + i, p) * ep.ldy + q;
+          if constexpr (f32) {
+            if (ep.residual) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) v[x] += __uint_as_float(res[i][p][x >> 2][x & 3]);
+            }
+            f32x4_t* y = (f32x4_t*)((float*)ep.y + at);
+            y[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+            y[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+          } else {
+            if (ep.residual) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                v[2 * x] += __uint_as_float(res[i][p][0][x] << 16);
+                v[2 * x + 1] += __uint_as_float(res[i][p][0][x] & 0xffff0000u);
+              }
+            }
+            bf16x8_t y;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) y[x] = (__bf16)v[x];
+            *(bf16x8_t*)((unsigned short*)ep.y + at) = y;
+          }
+        }
+        wave_sync();
+      }
+    }
+  };
+  if (ep.y_f32)
+    finish(std::integral_constant<bool, true>{});
+  else
+    finish(std::integral_constant<bool, false>{});
 }
 
 // Sum of the splits' raw products in order, then the epilogue: 8 channels per thread.
