@@ -188,21 +188,30 @@ def _device_index(t) -> int:
 
 
 def _require(index, name, t, shape, dtype):
-    """A tensor of the forward steps: on GPU index, of this shape and dtype, its last dimension
-    contiguous (any outer strides)."""
+    """Strides of a tensor of the forward steps: on GPU index, of this shape and dtype, its last
+    dimension contiguous (any outer strides)."""
+    strides = t.stride()
+    if (t.get_device() == index and t.shape == shape and t.dtype == dtype
+            and (strides[-1] == 1 or shape[-1] <= 1)):
+        return strides
     if t.get_device() != index:
         raise ValueError(f"{name} must live on GPU {index}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+    raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
-def _pitch(t, dim, dense):
-    """Stride of a dimension; a dimension of one element has its stride replaced by the dense one."""
-    return t.stride(dim) if t.shape[dim] > 1 else dense
+def _fresh(torch, t):
+    """A new dense tensor of t's shape, dtype and GPU."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _row_pitch(strides, n, dense):
+    """Row stride of a tensor [n, dense]; a single row's, which no access uses, is given as the
+    dense one."""
+    return strides[0] if n > 1 else dense
 
 
 def _addr(t):
@@ -212,7 +221,7 @@ def _addr(t):
 def _call_on(index, fn, *args):
     """Call fn with GPU index current, on that GPU's current stream (its last argument)."""
     torch = _torch()
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _check(fn(*args, torch.cuda.current_stream(index).cuda_stream))
     _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
@@ -428,43 +437,44 @@ def linear(X, W, bias=None, act="none", residual=None, Y=None, out_dtype=None, w
     c = W.shape[0]
     if out_dtype is None:
         out_dtype = next((t.dtype for t in (Y, residual) if t is not None), X.dtype)
-    if Y is None:
-        Y = torch.empty((n, c), dtype=out_dtype, device=X.device)
-    else:
-        _require(index, "Y", Y, (n, c), out_dtype)
-    _require(index, "X", X, (n, b), X.dtype)
+    ldx = _row_pitch(_require(index, "X", X, (n, b), X.dtype), n, b)
     _require(index, "W", W, (c, b), X.dtype)
     if not W.is_contiguous():
         raise ValueError("W must be contiguous")
     if bias is not None:
         _require(index, "bias", bias, (c,), X.dtype)
-    ldr = 0
+    ldr = ldy = c
     if residual is not None:
-        _require(index, "residual", residual, (n, c), out_dtype)
-        ldr = _pitch(residual, 0, c)
+        ldr = _row_pitch(_require(index, "residual", residual, (n, c), out_dtype), n, c)
+    if Y is None:
+        Y = torch.empty((n, c), dtype=out_dtype, device=X.device)
+    else:
+        ldy = _row_pitch(_require(index, "Y", Y, (n, c), out_dtype), n, c)
     if ws is None:
         nbytes = linear_workspace_size(n, b, c)
         ws = workspace(nbytes, X.device) if nbytes else None
     at, nbytes = (None, 0) if ws is None else _workspace_on(index, ws)
-    _call_on(index, lib().th_linear, X.data_ptr(), _pitch(X, 0, b), W.data_ptr(), _dtype_code(X),
-             n, b, c, _addr(bias), _ACTIVATIONS[act], _addr(residual), ldr, Y.data_ptr(),
-             _dtype_code(Y), _pitch(Y, 0, c), at, nbytes)
+    _call_on(index, lib().th_linear, X.data_ptr(), ldx, W.data_ptr(), _dtype_code(X), n, b, c,
+             _addr(bias), _ACTIVATIONS[act], _addr(residual), ldr, Y.data_ptr(), _dtype_code(Y),
+             ldy, at, nbytes)
     return Y
 
 
 def rms_norm(X, weight, eps=1e-5, Y=None, out_dtype=None):
     """Y = X / sqrt(mean(X^2) + eps) * weight by rows, X [n, b]; Y in out_dtype (default X's).
     Y may be X."""
+    torch = _torch()
     index = _device_index(X)
     n, b = X.shape
-    if Y is None:
-        Y = _torch().empty((n, b), dtype=out_dtype or X.dtype, device=X.device)
-    else:
-        _require(index, "Y", Y, (n, b), out_dtype or Y.dtype)
-    _require(index, "X", X, (n, b), X.dtype)
+    ldx = _row_pitch(_require(index, "X", X, (n, b), X.dtype), n, b)
     _require(index, "weight", weight, (b,), X.dtype)
-    _call_on(index, lib().th_rms_norm, X.data_ptr(), _dtype_code(X), n, b, _pitch(X, 0, b),
-             weight.data_ptr(), float(eps), Y.data_ptr(), _dtype_code(Y), _pitch(Y, 0, b))
+    ldy = b
+    if Y is None:
+        Y = torch.empty((n, b), dtype=out_dtype or X.dtype, device=X.device)
+    else:
+        ldy = _row_pitch(_require(index, "Y", Y, (n, b), out_dtype or Y.dtype), n, b)
+    _call_on(index, lib().th_rms_norm, X.data_ptr(), _dtype_code(X), n, b, ldx, weight.data_ptr(),
+             float(eps), Y.data_ptr(), _dtype_code(Y), ldy)
     return Y
 
 
@@ -485,10 +495,10 @@ def rotary_freqs(rot: int, base=10000.0, divide=1.0, bands=None, device=None):
 _ROTARY_LAYOUTS = {"half": TH_ROTARY_HALF, "interleaved": TH_ROTARY_INTERLEAVED}
 
 
-def _heads(x, y, norm) -> Heads:
-    n, h, d = x.shape
-    return Heads(x.data_ptr(), y.data_ptr(), None if norm is None else norm.data_ptr(), h,
-                 _pitch(x, 0, h * d), _pitch(x, 1, d), _pitch(y, 0, h * d), _pitch(y, 1, d))
+def _pitches(strides, n, h, d):
+    """Token and head strides of a tensor [n, h, d]; those of a dimension of one element, which
+    no access uses, are given as the dense ones."""
+    return strides[0] if n > 1 else h * d, strides[1] if h > 1 else d
 
 
 def rotary(q, k, freqs, positions=None, layout="half", amplitude=1.0, q_norm=None, k_norm=None,
@@ -498,32 +508,33 @@ def rotary(q, k, freqs, positions=None, layout="half", amplitude=1.0, q_norm=Non
     0 .. n-1). Returns (q_out, k_out), which may be q and k themselves."""
     torch = _torch()
     index = _device_index(q)
-    n, hq, d = q.shape
-    _require(index, "q", q, (n, hq, d), q.dtype)
-    if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
-    else:
-        _require(index, "q_out", q_out, (n, hq, d), q.dtype)
-    if q_norm is not None:
-        _require(index, "q_norm", q_norm, (d,), q.dtype)
+    n, _, d = q.shape
+    dtype = q.dtype
+
+    def heads(name, x, out, norm):
+        h = x.shape[1]
+        strides = _require(index, name, x, (n, h, d), dtype)
+        if norm is not None:
+            _require(index, name + "_norm", norm, (d,), dtype)
+        if out is None:
+            out = _fresh(torch, x)
+            out_pitches = h * d, d
+        else:
+            out_pitches = _pitches(_require(index, name + "_out", out, (n, h, d), dtype), n, h, d)
+        return out, Heads(x.data_ptr(), out.data_ptr(), _addr(norm), h,
+                          *_pitches(strides, n, h, d), *out_pitches)
+
     pairs = freqs.shape[0]
     _require(index, "freqs", freqs, (pairs,), torch.float64)
     if positions is not None:
         _require(index, "positions", positions, (n,), torch.int32)
+    q_out, qh = heads("q", q, q_out, q_norm)
     kh = None
     if k is not None:
-        hk = k.shape[1]
-        _require(index, "k", k, (n, hk, d), q.dtype)
-        if k_out is None:
-            k_out = torch.empty((n, hk, d), dtype=q.dtype, device=q.device)
-        else:
-            _require(index, "k_out", k_out, (n, hk, d), q.dtype)
-        if k_norm is not None:
-            _require(index, "k_norm", k_norm, (d,), q.dtype)
-        kh = _heads(k, k_out, k_norm)
+        k_out, kh = heads("k", k, k_out, k_norm)
     elif k_out is not None or k_norm is not None:
         raise ValueError("k_out and k_norm go with k")
-    _call_on(index, lib().th_rotary, _heads(q, q_out, q_norm), kh, _dtype_code(q), n, d, 2 * pairs,
+    _call_on(index, lib().th_rotary, qh, kh, _dtype_code(q), n, d, 2 * pairs,
              _ROTARY_LAYOUTS[layout], _addr(positions), freqs.data_ptr(), float(amplitude),
              float(eps))
     return q_out, k_out
@@ -543,13 +554,15 @@ def attention(Q, K, V, q_start=None, k_start=None, causal=True, scale=None, O=No
     index = _device_index(Q)
     nq, hq, d = Q.shape
     nk, hk, _ = K.shape
-    _require(index, "Q", Q, (nq, hq, d), Q.dtype)
-    _require(index, "K", K, (nk, hk, d), Q.dtype)
-    _require(index, "V", V, (nk, hk, d), Q.dtype)
+    dtype = Q.dtype
+    q_s = _pitches(_require(index, "Q", Q, (nq, hq, d), dtype), nq, hq, d)
+    k_s = _pitches(_require(index, "K", K, (nk, hk, d), dtype), nk, hk, d)
+    v_s = _pitches(_require(index, "V", V, (nk, hk, d), dtype), nk, hk, d)
     if O is None:  # rows that belong to no sequence are not written
-        O = torch.empty((nq, hq, d), dtype=Q.dtype, device=Q.device)
+        O = _fresh(torch, Q)
+        o_s = hq * d, d
     else:
-        _require(index, "O", O, (nq, hq, d), Q.dtype)
+        o_s = _pitches(_require(index, "O", O, (nq, hq, d), dtype), nq, hq, d)
     nseq = 1
     if q_start is not None:
         nseq = q_start.shape[0] - 1
@@ -558,10 +571,8 @@ def attention(Q, K, V, q_start=None, k_start=None, causal=True, scale=None, O=No
             _require(index, "k_start", k_start, (nseq + 1,), torch.int32)
     elif k_start is not None:
         raise ValueError("k_start goes with q_start")
-    p = AttentionParams(nq, nk, hq, hk, d, _pitch(Q, 0, hq * d), _pitch(Q, 1, d),
-                        _pitch(K, 0, hk * d), _pitch(K, 1, d), _pitch(V, 0, hk * d),
-                        _pitch(V, 1, d), _pitch(O, 0, hq * d), _pitch(O, 1, d), nseq,
-                        1 if causal else 0, d ** -0.5 if scale is None else float(scale))
+    p = AttentionParams(nq, nk, hq, hk, d, *q_s, *k_s, *v_s, *o_s, nseq, 1 if causal else 0,
+                        d ** -0.5 if scale is None else float(scale))
     if ws is None:
         nbytes = attention_workspace_size(p)
         ws = workspace(nbytes, Q.device) if nbytes else None
