@@ -239,7 +239,7 @@ th_status th_gated_ffn_input(const void* X, const void* W_gate, const void* W_up
  * once. gelu(z) = z Phi(z), with the error function; silu(z) = z / (1 + e^-z). Y may
  * be the residual (same pitch); it must not overlap X, W or bias. Needs
  * b % 8 == 0, b >= 8, ldx % 8 == 0, b and ldx < 2^22, and 16-byte aligned X and W;
- * n = 0 is allowed. workspace (optional, may be NULL with workspace_bytes 0;
+ * n < 2^31, c < 2^27 and at most 2^24 - 16 blocks of 64 x 64 outputs; n = 0 is allowed. workspace (optional, may be NULL with workspace_bytes 0;
  * 16-byte aligned) lets launches of few tiles split the contraction; size from
  * th_linear_workspace_size (0 where it does not help). The pieces are summed in a
  * fixed order, so repeated calls give identical bits. Asynchronous. */
@@ -332,8 +332,8 @@ typedef struct {
 
 /* dt must be TH_BF16; 8 <= d <= 128, d % 8 == 0; hk divides hq; strides are multiples
  * of 8 (k_token, v_token < 2^24) and Q, K, V, O 16-byte aligned; nq * hq / hk,
- * nk < 2^31 - 2^16. O must not
- * overlap the inputs. Scores, maxima, sums and O accumulate in fp32; the weights
+ * nk < 2^31 - 2^16; hk times the row blocks (of 32 rows where the sequences average
+ * no more, else of 128), plus hk nseq, < 2^24. O must not overlap the inputs. Scores, maxima, sums and O accumulate in fp32; the weights
  * enter the second product rounded to bf16. workspace (optional, may be NULL with
  * workspace_bytes 0; 16-byte aligned) lets launches of few queries split the keys;
  * size from th_attention_workspace_size (0 where it does not help). The order of all

@@ -886,6 +886,11 @@ AttnPlan plan_of(const th_attention_params* p) {
 
 }  // namespace
 
+int64_t attention_workgroups(const th_attention_params* p) {
+  if (p->nq == 0) return 0;
+  return (p->nq * (p->hq / p->hk) / (plan_of(p).few ? 32 : 128) + p->nseq) * p->hk;
+}
+
 size_t attention_workspace_bytes(const th_attention_params* p) {
   if (p->nq == 0) return 0;
   const int s = plan_of(p).splits;

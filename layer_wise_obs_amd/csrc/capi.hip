@@ -825,8 +825,10 @@ th_status check_linear_sizes(int64_t n, int64_t b, int64_t c) {
   if (n < 0 || c < 1 || b < 8 || b % 8)
     return fail(TH_ERR_INVALID_ARG, "needs n >= 0, c >= 1, b >= 8 and b % 8 == 0");
   if (b >= ((int64_t)1 << 22)) return fail(TH_ERR_INVALID_ARG, "b must be < 2^22");
-  if (n >= ((int64_t)1 << 38) || c >= ((int64_t)1 << 31) ||
-      cdiv(n, 128) * cdiv(c, 128) >= ((int64_t)1 << 30))
+  // a launch has less than 2^32 threads: at most 256 for 64 x 64 outputs, in ranges of a
+  // multiple of 8 workgroups; 512 for 16 outputs of few tokens
+  if (n >= ((int64_t)1 << 31) || c >= ((int64_t)1 << 27) ||
+      cdiv(n, 64) * cdiv(c, 64) > ((int64_t)1 << 24) - 16)
     return fail(TH_ERR_INVALID_ARG, "n * c too large for one launch");
   return TH_OK;
 }
@@ -856,6 +858,8 @@ th_status th_linear(const void* X, int64_t ldx, const void* W, th_dtype dt, int6
   if (!W || (n > 0 && (!X || !Y))) return fail(TH_ERR_INVALID_ARG, "NULL argument");
   if (((uintptr_t)X | (uintptr_t)W) & 15)
     return fail(TH_ERR_INVALID_ARG, "X and W must be 16-byte aligned");
+  if (Y && (Y == X || Y == W || Y == bias))
+    return fail(TH_ERR_INVALID_ARG, "Y must not be an input but the residual");
   if (Y && Y == residual && ldr != ldy)
     return fail(TH_ERR_INVALID_ARG, "a residual in place needs Y's pitch");
   if (workspace && ((uintptr_t)workspace & 15))
@@ -882,6 +886,7 @@ th_status th_rms_norm(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t
   if (!weight || (n > 0 && (!X || !Y))) return fail(TH_ERR_INVALID_ARG, "NULL argument");
   if (X && X == Y && (xdt != ydt || ldx != ldy))
     return fail(TH_ERR_INVALID_ARG, "in place needs one dtype and pitch");
+  if (Y && Y == weight) return fail(TH_ERR_INVALID_ARG, "Y must not be the weight");
   if (n == 0) return TH_OK;
   TH_HIP(launch_rms_norm(X, xdt, ldx, weight, Y, ydt, ldy, n, b, (float)eps, (hipStream_t)stream),
          "rms norm");
@@ -980,8 +985,8 @@ th_status check_attention(const th_attention_params* p) {
     return fail(TH_ERR_INVALID_ARG, "nq * hq / hk must be < 2^31 - 2^16, hq < 2^16");
   if (p->nseq < 1 || p->nseq >= ((int64_t)1 << 24))
     return fail(TH_ERR_INVALID_ARG, "needs 1 <= nseq < 2^24");
-  if ((p->nq * (p->hq / p->hk) / 128 + p->nseq) * p->hk >= ((int64_t)1 << 30) ||
-      p->nq * p->hq >= ((int64_t)1 << 33))
+  // a launch has less than 2^32 threads, 256 to a workgroup
+  if (attention_workgroups(p) >= ((int64_t)1 << 24))
     return fail(TH_ERR_INVALID_ARG, "too many rows, heads and sequences for one launch");
   const int64_t strides[8] = {p->q_token, p->q_head, p->k_token, p->k_head,
                               p->v_token, p->v_head, p->o_token, p->o_head};
@@ -1018,6 +1023,7 @@ th_status th_attention(const void* Q, const void* K, const void* V, th_dtype dt,
     return fail(TH_ERR_INVALID_ARG, "NULL argument");
   if (((uintptr_t)Q | (uintptr_t)K | (uintptr_t)V | (uintptr_t)O | (uintptr_t)workspace) & 15)
     return fail(TH_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  if (O && (O == Q || O == K || O == V)) return fail(TH_ERR_INVALID_ARG, "O must not be an input");
   if (p->nq == 0) return TH_OK;
   if (workspace && workspace_bytes < attention_workspace_bytes(p))
     return fail(TH_ERR_WORKSPACE, "workspace too small");

@@ -106,6 +106,10 @@ __device__ __forceinline__ float bcast(float v, int lane) {
 
 __host__ __device__ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Workgroups (of up to 256 threads) that one launch of the row-wise kernels takes at most:
+// a grid has less than 2^32 threads.
+constexpr int64_t kMaxGroups = (int64_t)1 << 23;
+
 // ---------------------------------------------------------------- launchers
 // hessian.hip
 int syrk_bf16_splits(int64_t t, int64_t b);
@@ -249,6 +253,7 @@ hipError_t launch_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int6
 
 // attention.hip
 // workspace of the split keys: 0 where it does not help
+int64_t attention_workgroups(const th_attention_params* p);
 size_t attention_workspace_bytes(const th_attention_params* p);
 hipError_t launch_attention(const void* Q, const void* K, const void* V, const int32_t* q_start,
                             const int32_t* k_start, const th_attention_params* p, void* O,

@@ -128,16 +128,20 @@ hipError_t launch_typed(const void* X, int64_t ldx, const void* w, void* Y, int6
   // 16-byte accesses: 8 bf16 or 4 fp32 elements
   const bool vec = b % 8 == 0 && ldx % (16 / sizeof(TI)) == 0 && ldy % (16 / sizeof(TO)) == 0 &&
                    (((uintptr_t)X | (uintptr_t)w | (uintptr_t)Y) & 15) == 0;
-  const dim3 grid((unsigned)n);
-  if (!vec)
-    hipLaunchKernelGGL((rms_norm_any_kernel<TI, TO>), grid, dim3(256), 0, s, (const TI*)X, ldx,
-                       (const TI*)w, (TO*)Y, ldy, b, eps);
-  else if (b <= 1024)
-    hipLaunchKernelGGL((rms_norm_kernel<TI, TO, 64>), grid, dim3(64), 0, s, (const TI*)X, ldx,
-                       (const TI*)w, (TO*)Y, ldy, b, eps);
-  else
-    hipLaunchKernelGGL((rms_norm_kernel<TI, TO, 256>), grid, dim3(256), 0, s, (const TI*)X, ldx,
-                       (const TI*)w, (TO*)Y, ldy, b, eps);
+  const TI* x = (const TI*)X;
+  TO* y = (TO*)Y;
+  for (; n > 0; n -= kMaxGroups, x += kMaxGroups * ldx, y += kMaxGroups * ldy) {
+    const dim3 grid((unsigned)(n < kMaxGroups ? n : kMaxGroups));
+    if (!vec)
+      hipLaunchKernelGGL((rms_norm_any_kernel<TI, TO>), grid, dim3(256), 0, s, x, ldx,
+                         (const TI*)w, y, ldy, b, eps);
+    else if (b <= 1024)
+      hipLaunchKernelGGL((rms_norm_kernel<TI, TO, 64>), grid, dim3(64), 0, s, x, ldx, (const TI*)w,
+                         y, ldy, b, eps);
+    else
+      hipLaunchKernelGGL((rms_norm_kernel<TI, TO, 256>), grid, dim3(256), 0, s, x, ldx,
+                         (const TI*)w, y, ldy, b, eps);
+  }
   return hipGetLastError();
 }
 

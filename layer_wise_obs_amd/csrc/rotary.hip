@@ -36,7 +36,7 @@ struct RotSide {
 
 struct RotArgs {
   RotSide side[2];
-  int64_t n;
+  int64_t from, n;  // tokens [from, n), at most kMaxGroups workgroups of them
   int d, rot, interleaved, tokens;
   const int32_t* pos;
   const double* freqs;
@@ -104,7 +104,7 @@ template <class T, int G, bool INTERLEAVED>
 __global__ __launch_bounds__(kRThreads) void rotary_kernel(RotArgs a) {
   __shared__ float2 cs[kRMaxTokens * kRMaxPairs];
   const int pairs = a.rot >> 1;
-  const int64_t token0 = (int64_t)blockIdx.x * a.tokens;
+  const int64_t token0 = a.from + (int64_t)blockIdx.x * a.tokens;
   constexpr int groups = kRThreads / G;
   const int phases = groups / a.tokens;
   const int grp = threadIdx.x / G, lane = threadIdx.x % G;
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(kRThreads) void rotary_kernel(RotArgs a) {
 template <class T>
 __global__ __launch_bounds__(kRThreads) void rotary_any_kernel(RotArgs a) {
   __shared__ float2 cs[kRMaxPairs];
-  const int64_t tok = blockIdx.x;
+  const int64_t tok = a.from + blockIdx.x;
   const int pairs = a.rot >> 1;
   const double p = a.pos ? (double)a.pos[tok] : (double)tok;
   for (int i = threadIdx.x; i < pairs; i += kRThreads) cs[i] = turn_of(p, a.freqs[i], a.amplitude);
@@ -249,16 +249,19 @@ hipError_t launch_group(RotArgs a, hipStream_t s) {
   while (phases < groups && phases * kRBatch < all) phases *= 2;
   a.tokens = groups / phases;
   if (a.tokens > kRMaxTokens) a.tokens = kRMaxTokens;
-  const dim3 grid((unsigned)cdiv(a.n, a.tokens));
-  if (a.interleaved)
-    hipLaunchKernelGGL((rotary_kernel<T, G, true>), grid, dim3(kRThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((rotary_kernel<T, G, false>), grid, dim3(kRThreads), 0, s, a);
+  for (; a.from < a.n; a.from += kMaxGroups * a.tokens) {
+    const int64_t left = cdiv(a.n - a.from, a.tokens);
+    const dim3 grid((unsigned)(left < kMaxGroups ? left : kMaxGroups));
+    if (a.interleaved)
+      hipLaunchKernelGGL((rotary_kernel<T, G, true>), grid, dim3(kRThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((rotary_kernel<T, G, false>), grid, dim3(kRThreads), 0, s, a);
+  }
   return hipGetLastError();
 }
 
 template <class T>
-hipError_t launch_typed(const RotArgs& a, hipStream_t s) {
+hipError_t launch_typed(RotArgs a, hipStream_t s) {
   // 16-byte accesses need whole chunks of 8 elements on either side of a pair
   const int64_t el = 16 / sizeof(T);
   bool vec = a.d % 8 == 0 && a.rot % 8 == 0 && (a.interleaved || a.rot % 16 == 0);
@@ -268,7 +271,12 @@ hipError_t launch_typed(const RotArgs& a, hipStream_t s) {
           (((uintptr_t)sd.x | (uintptr_t)sd.y | (uintptr_t)sd.w) & 15) == 0;
   }
   if (!vec) {
-    hipLaunchKernelGGL((rotary_any_kernel<T>), dim3((unsigned)a.n), dim3(kRThreads), 0, s, a);
+    for (; a.from < a.n; a.from += kMaxGroups) {
+      const int64_t left = a.n - a.from;
+      hipLaunchKernelGGL((rotary_any_kernel<T>),
+                         dim3((unsigned)(left < kMaxGroups ? left : kMaxGroups)), dim3(kRThreads), 0,
+                         s, a);
+    }
     return hipGetLastError();
   }
   if (a.d <= 64) return launch_group<T, 8>(a, s);
@@ -289,6 +297,7 @@ hipError_t launch_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int6
   RotArgs a;
   a.side[0] = side_of(q);
   a.side[1] = side_of(k);
+  a.from = 0;
   a.n = n;
   a.d = (int)d;
   a.rot = (int)rot;

@@ -48,6 +48,46 @@ def test_linear_refuses(bad):
     assert L.lib().th_linear(*_linear_args(**bad)) == L.TH_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("n,b,c", [  # a launch has less than 2^32 threads
+    (1, 8, 1 << 27), (1 << 31, 8, 8), ((1 << 30) - 960, 8, 8), (1 << 18, 64, 1 << 18),
+    (((1 << 24) - 16) * 64 + 1, 8, 64)])
+def test_linear_refuses_more_than_a_launch_takes(n, b, c):
+    assert L.lib().th_linear(*_linear_args(n=n, b=b, ldx=b, c=c, ldy=c)) == L.TH_ERR_INVALID_ARG
+    out = ctypes.c_size_t(0)
+    assert (L.lib().th_linear_workspace_size(n, b, c, ctypes.byref(out)) == L.TH_ERR_INVALID_ARG)
+
+
+@pytest.mark.parametrize("n,b,c", [
+    (1, 8, (1 << 27) - 1), (((1 << 24) - 16) * 64, 8, 64), (64, 64, (1 << 27) - 1)])
+def test_linear_accepts_what_a_launch_takes(n, b, c):
+    assert L.linear_workspace_size(n, b, c) == 0
+
+
+@pytest.mark.parametrize("call", [
+    lambda: L.lib().th_linear(*_linear_args(Y=FAKE, ldy=64)),
+    lambda: L.lib().th_linear(*_linear_args(Y=2 * FAKE)),
+    lambda: L.lib().th_linear(*_linear_args(bias=3 * FAKE)),
+    lambda: L.lib().th_rms_norm(*_norm_args(X=3 * FAKE, Y=FAKE)),
+    lambda: _attention(Q=2 * FAKE), lambda: _attention(K=2 * FAKE), lambda: _attention(V=2 * FAKE)])
+def test_outputs_that_are_inputs_are_refused(call):
+    assert call() == L.TH_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw,ok", [
+    (dict(nq=8, nseq=(1 << 24) - 1, hq=1, hk=1, o_token=64), True),
+    (dict(nq=8, nseq=1 << 23, hq=2, hk=2, o_token=128), False),
+    # row blocks of a key head: floor(nq / 128) + 1, times 4: 2^24 - 4, then 2^24
+    (dict(nq=(1 << 29) - 129, nk=0, nseq=1, hq=4, hk=4, d=8, o_token=32, o_head=8), True),
+    (dict(nq=(1 << 29) - 64, nk=0, nseq=1, hq=4, hk=4, d=8, o_token=32, o_head=8), False),
+    (dict(nq=1 << 29, nk=0, nseq=1, hq=4, hk=4, d=8, o_token=32, o_head=8), False),
+    (dict(nq=1 << 23, nk=0, nseq=1 << 23, hq=1, hk=1, d=8, o_token=8), True),
+    (dict(nq=1 << 28, nk=0, nseq=1 << 23, hq=1, hk=1, d=8, o_token=8), False)])
+def test_attention_workgroups_of_a_launch(kw, ok):
+    p, out = _attention_params(**kw), ctypes.c_size_t(0)
+    got = L.lib().th_attention_workspace_size(ctypes.byref(p), ctypes.byref(out))
+    assert got == (L.TH_OK if ok else L.TH_ERR_INVALID_ARG)
+
+
 def test_linear_workspace_query():
     lib, out = L.lib(), ctypes.c_size_t(0)
     for n, b, c in ((-1, 64, 8), (4, 60, 8), (4, 64, 0), (4, 0, 8)):

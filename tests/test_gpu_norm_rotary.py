@@ -196,3 +196,32 @@ def test_strides_past_32_bits_and_another_stream():
     side.synchronize()
     _rot_check(y, src, np.arange(n), freqs.cpu().numpy(), "half", 1.0, None, 1e-6)
     _close(z, O.rms_norm(src[:, 0], np.ones(d), 1e-5), _norm_rel(d))
+
+
+def test_rms_norm_more_rows_than_a_launch_takes():
+    n, b = (1 << 24) + 3, 8
+    X = torch.empty(n, b, dtype=BF, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(1))
+    w = torch.arange(1, b + 1, dtype=BF, device=DEV)
+    Y = L.rms_norm(X, w)
+    for a in (0, (1 << 23) - 2, 1 << 23, (1 << 24) - 2, n - 4):  # ends of the launches' ranges
+        _close(Y[a:a + 4], O.rms_norm(X[a:a + 4].cpu(), w.cpu(), 1e-5), _norm_rel(b))
+    # every other row against the same call on a part
+    half = L.rms_norm(X[n // 2:], w)
+    assert torch.equal(Y[n // 2:], half)
+
+
+@pytest.mark.parametrize("d,n", [(6, (1 << 24) + 5), (8, (1 << 28) + 21)])
+def test_rotary_more_tokens_than_a_launch_takes(d, n):
+    x = torch.empty(n, 1, d, dtype=BF, device=DEV)
+    x[:] = torch.arange(1, d + 1, device=DEV).to(BF)
+    freqs = L.rotary_freqs(2, device=DEV)  # one pair, one radian a position
+    y, _ = L.rotary(x, None, freqs, q_out=x)
+    step = 1 << (23 if d == 6 else 27)
+    for a in (0, step - 2, step, 2 * step - 2, n - 4):
+        p = torch.arange(a, a + 4, dtype=torch.float64)
+        want = torch.stack([p.cos() - 2 * p.sin(), 2 * p.cos() + p.sin()], 1)
+        got = y[a:a + 4, 0].double().cpu()
+        # the angle in turns is off by 2^-53 of itself, the sine and cosine by 2^-21 with it,
+        # the two products by three roundings, the output by half a step
+        assert ((got[:, :2] - want).abs() <= 2.0 ** -8 * want.abs() + 3 * 2.0 ** -20).all()
+        assert torch.equal(got[:, 2:], torch.arange(3, d + 1, dtype=torch.float64).expand(4, -1))
