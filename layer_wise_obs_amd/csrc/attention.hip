@@ -114,6 +114,11 @@ __device__ __forceinline__ float half_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
+// Maximum over the four lanes (l % 16 + 16 i) that share a query.
+__device__ __forceinline__ float quad_max(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
 // v_max3_f32: two maxima in one instruction, NaN operands ignored like fmaxf's (which
 // the compiler precedes by a canonicalising maximum of either operand). The compiler
 // does not know the instruction, so it puts no wait between a matrix product and it: a
@@ -140,7 +145,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   constexpr int kTile = kAKT * kRowB;        // one operand's tile
   constexpr int kLd = kTile / 1024 / NW;     // 1 KB loads per wave and operand
   constexpr int kRowsPer = 64 / kPieces;     // rows per 1 KB
-  constexpr int kDB = DC / 32, kKS = DC / 16;
+  constexpr int kCB = DC / 16, kKS = (DC + 31) / 32;  // blocks of 16 channels, steps of 32
   __shared__ __attribute__((aligned(1024))) unsigned char sm[2 * ST * kTile];  // K tiles, V tiles
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -168,45 +173,52 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   const int per = (int)cdiv(cdiv(keys, kAKT), a.splits) * kAKT;
   const int kbeg = min(keys, (int)blockIdx.y * per), kend = min(keys, kbeg + per);
 
-  // this lane's row
+  // this lane's rows: r16 of each block of 16
   const int64_t wrow = row0 + wave * 32;
   const bool wave_has = wrow < row_end;
-  const int64_t mine = wrow + (lane & 31);
-  const bool valid = mine < row_end;
-  const int64_t r = valid ? mine : row_end - 1;
-  const int64_t tok = (unsigned)r / (unsigned)a.g;  // nq g < 2^31
-  const int qh = head * a.g + (int)(r - tok * a.g);
-  const int visible = limit_of(r);
-  const int lim = min(visible, kend);
+  const int r16 = lane & 15, quad = lane >> 4;
+  int64_t tok[2];
+  int qh[2], visible[2], lim[2];
+  bool valid[2];
+#pragma unroll
+  for (int rb = 0; rb < 2; ++rb) {
+    const int64_t mine = wrow + rb * 16 + r16;
+    valid[rb] = mine < row_end;
+    const int64_t r = valid[rb] ? mine : row_end - 1;
+    tok[rb] = (unsigned)r / (unsigned)a.g;  // nq g < 2^31
+    qh[rb] = head * a.g + (int)(r - tok[rb] * a.g);
+    visible[rb] = limit_of(r);
+    lim[rb] = min(visible[rb], kend);
+  }
   // rows ascend within a wave, and so do their limits
-  const int lim_first = __builtin_amdgcn_readfirstlane(lim);
-  const int lim_last = wave_has ? __builtin_amdgcn_readlane(lim, 31) : 0;
-  const int half = lane >> 5;
+  const int lim_first = __builtin_amdgcn_readfirstlane(lim[0]);
+  const int lim_last = wave_has ? __builtin_amdgcn_readlane(lim[1], 15) : 0;
 
-  bf16x8_t qf[kKS];
-  {
-    const unsigned short* qp = a.q + (q0 + tok) * a.q_token + qh * a.q_head;
+  bf16x8_t qf[kKS][2];
+#pragma unroll
+  for (int rb = 0; rb < 2; ++rb) {
+    const unsigned short* qp = a.q + (q0 + tok[rb]) * a.q_token + qh[rb] * a.q_head;
 #pragma unroll
     for (int st = 0; st < kKS; ++st) {
-      const int e = st * 16 + half * 8;
+      const int e = st * 32 + quad * 8;
       u32x4_t u = u32x4_t{0u, 0u, 0u, 0u};
       if (e < a.d) u = *(const u32x4_t*)(qp + e);
-      qf[st] = __builtin_bit_cast(bf16x8_t, u);
+      qf[st][rb] = __builtin_bit_cast(bf16x8_t, u);
     }
   }
 
-  f32x16_t o[kDB];
-  float m, l;
+  f32x4_t o[kCB][2];
+  float m[2], l[2];
   unsigned bad = 0;  // sign bits: V values met that are not finite, in tiles with hidden keys
 
   // Loader: chunk wave + NW i of a tile (1 KB, kRowsPer rows); lane l fills row
   // kRowsPer chunk + l / kPieces at physical piece l % kPieces. K pieces are
   // swizzled by the row so that 16 rows at one piece spread over all banks, V
-  // pieces so that 4 rows x 64 bytes do; either is the same in a lane's chunks.
+  // pieces so that 8 rows x 32 bytes do; either is the same in a lane's chunks.
   const int lr = lane / kPieces, lpp = lane % kPieces;
   const int row_w = wave * kRowsPer + lr;  // + NW i kRowsPer
   const int swk = D == 128 ? (row_w & 15) : ((row_w >> 1) & 7);
-  const int swv = D == 128 ? ((row_w & 3) << 2) : (((row_w >> 1) & 1) << 2);
+  const int swv = D == 128 ? ((row_w & 7) << 1) : (((row_w >> 1) & 3) << 1);
   static_assert(D == 64 || NW * kRowsPer % 16 == 0, "one K swizzle per lane");
   const int ck = (lpp ^ swk) * 8, cv = (lpp ^ swv) * 8;
   const unsigned short* kb = a.k + k0 * a.k_token + head * a.k_head;
@@ -246,55 +258,54 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   };
 
   // operand addresses inside a tile; the step's piece bits are XORed in
-  const int krow = lane & 31;
-  const int kswz = D == 128 ? (krow & 15) : ((krow >> 1) & 7);
-  const int kaddr = krow * kRowB + ((half ^ kswz) << 4);
-  const int s16 = lane & 15;
-  const int vkey = 4 * half + (s16 >> 2);
-  const int vswz = D == 128 ? ((vkey & 3) << 2) : (((vkey >> 1) & 1) << 2);
-  const int vpiece = 2 * ((lane >> 4) & 1) + ((s16 & 3) >> 1);
-  const int vaddr = vkey * kRowB + ((vpiece ^ vswz) << 4) + (s16 & 1) * 8;
+  const int kswz = D == 128 ? r16 : ((r16 >> 1) & 7);
+  const int kaddr = r16 * kRowB + ((quad ^ kswz) << 4);
+  const int vkey = 4 * quad + (r16 >> 2);
+  const int vswz = D == 128 ? ((vkey & 7) << 1) : (((vkey >> 1) & 3) << 1);
+  const int vaddr = vkey * kRowB + ((((r16 & 3) >> 1) ^ vswz) << 4) + (r16 & 1) * 8;
 
   const unsigned char *ks, *vs;  // the tile at hand
-  auto v_frag = [&](int ks16, int db) {
-    const unsigned char* p = vs + ks16 * 16 * kRowB + (vaddr ^ (db << 6));
+  // channels 16 cb + r16 of 32 keys from 32 kc: 4 quad + x, then 16 + 4 quad + x
+  auto v_frag = [&](int kc, int cb) {
+    const unsigned char* p = vs + kc * 32 * kRowB + (vaddr ^ (cb << 5));
     const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         (__attribute__((address_space(3))) v4i16_t*)p);
     const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) v4i16_t*)(p + 8 * kRowB));
+        (__attribute__((address_space(3))) v4i16_t*)(p + 16 * kRowB));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
   // One tile of 64 keys from kt.
   auto tile = [&](int kt, bool more, auto CAREFUL) __attribute__((always_inline)) {
     constexpr bool careful = decltype(CAREFUL)::value;
-    // Scores: operands are read three steps ahead, the next tile's loads go between
-    // the products; the order is pinned.
-    f32x16_t s[2];
-    bf16x8_t kf[4][2];
-    auto read_k = [&](int st) {
-#pragma unroll
-      for (int b2 = 0; b2 < 2; ++b2)
-        kf[st & 3][b2] = *(const bf16x8_t*)(ks + b2 * 32 * kRowB + (kaddr ^ (st << 5)));
+    // Scores of four blocks of 16 keys: operands are read a step ahead, the next tile's
+    // loads go between the products; the order is pinned.
+    f32x4_t s[4][2];
+    bf16x8_t kf[2][4];
+    auto read_k = [&](int st, int kb16) {
+      kf[st & 1][kb16] = *(const bf16x8_t*)(ks + kb16 * 16 * kRowB + (kaddr ^ (st << 6)));
     };
     auto scores = [&](auto LOADS) __attribute__((always_inline)) {
 #pragma unroll
-      for (int st = 0; st < 3; ++st) read_k(st);
+      for (int kb16 = 0; kb16 < 4; ++kb16) read_k(0, kb16);
 #pragma unroll
       for (int st = 0; st < kKS; ++st) {
-        if (st + 3 < kKS) read_k(st + 3);
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int b2 = 0; b2 < 2; ++b2) {
-          const f32x16_t zero = {};
-          s[b2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[st & 3][b2], qf[st], st ? s[b2] : zero,
-                                                          0, 0, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (decltype(LOADS)::value) {
-#pragma unroll
-          for (int i = 0; i < 2 * kLd; ++i)
-            if (i * kKS / (2 * kLd) == st) load(i);
+        for (int kb16 = 0; kb16 < 4; ++kb16) {
+          if (st + 1 < kKS) read_k(st + 1, kb16);
           __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int rb = 0; rb < 2; ++rb) {
+            const f32x4_t zero = {};
+            s[kb16][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                kf[st & 1][kb16], qf[st][rb], st ? s[kb16][rb] : zero, 0, 0, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (decltype(LOADS)::value) {
+#pragma unroll
+            for (int i = 0; i < 2 * kLd; ++i)
+              if (i * 4 * kKS / (2 * kLd) == st * 4 + kb16) load(i);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
       }
     };
@@ -305,19 +316,20 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
     const bool masked = kt + kAKT > lim_first;  // some row of the wave does not see every key
     if (masked) {
 #pragma unroll
-      for (int b2 = 0; b2 < 2; ++b2)
+      for (int kb16 = 0; kb16 < 4; ++kb16)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int key = kt + b2 * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
-          s[b2][e] = key < lim ? s[b2][e] : -INFINITY;
-        }
+        for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[kb16][rb][e] =
+                kt + kb16 * 16 + 4 * quad + e < lim[rb] ? s[kb16][rb][e] : -INFINITY;
       if constexpr (!careful) {
 #pragma unroll 1
-        for (int ks16 = 0; ks16 < 4; ++ks16) {
-          if (kt + 16 * ks16 + 16 <= lim_first) continue;  // every row sees these keys
+        for (int kc = 0; kc < 2; ++kc) {
+          if (kt + 32 * kc + 32 <= lim_first) continue;  // every row sees these keys
 #pragma unroll
-          for (int db = 0; db < kDB; ++db) {
-            const u32x4_t u = __builtin_bit_cast(u32x4_t, v_frag(ks16, db));
+          for (int cb = 0; cb < kCB; ++cb) {
+            const u32x4_t u = __builtin_bit_cast(u32x4_t, v_frag(kc, cb));
             // an exponent of all ones, plus one in its last place, sets the sign bit
 #pragma unroll
             for (int x = 0; x < 4; ++x) bad |= (u[x] & 0x7f807f80u) + 0x00800080u;
@@ -325,62 +337,74 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
         }
       }
     }
-    // the first steps' part of V is under way during the softmax
-    v8i16_t vf[3][kDB];
-    auto read_v = [&](int ks16) {
+    // the first half of V is under way during the softmax
+    v8i16_t vf[kCB];
 #pragma unroll
-      for (int db = 0; db < kDB; ++db) vf[ks16 % 3][db] = v_frag(ks16, db);
-    };
-    read_v(0);
-    read_v(1);
-    float top = fmaxf(s[0][0], s[1][0]);  // waits for the products of both blocks
+    for (int cb = 0; cb < kCB; ++cb) vf[cb] = v_frag(0, cb);
+    float top[2];
 #pragma unroll
-    for (int e = 1; e < 16; ++e) top = max3(top, s[0][e], s[1][e]);
-    top = half_max(top) * a.c;
-    if (__any(top > m + kAMove)) {  // also the first tile, where m is -inf
-      const float mn = fmaxf(m, top);
-      const float f = exp2_fast(m - (mn == -INFINITY ? 0.f : mn));
-      l *= f;
+    for (int rb = 0; rb < 2; ++rb) top[rb] = fmaxf(s[2][rb][0], s[3][rb][0]);
+    // the ordinary maxima above wait for the last products, which come after all others
 #pragma unroll
-      for (int i = 0; i < kDB; ++i)
+    for (int rb = 0; rb < 2; ++rb) {
+      top[rb] = max3(top[rb], s[0][rb][0], s[1][rb][0]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[i][e] *= f;
-      m = mn;
-    }
-    const float ref = m == -INFINITY ? 0.f : -m;
-    bf16x8_t pf[4];
-#pragma unroll
-    for (int ks16 = 0; ks16 < 4; ++ks16) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int e = (ks16 & 1) * 8 + 2 * x;
-        const bf16x2_t p = pack2(exp2_fast(fmaf(s[ks16 >> 1][e], a.c, ref)),
-                                 exp2_fast(fmaf(s[ks16 >> 1][e + 1], a.c, ref)));
-        // the sum takes the rounded weights, which are the ones that V meets
-        l = __builtin_amdgcn_fdot2_f32_bf16(p, bf16x2_t{(__bf16)1.0f, (__bf16)1.0f}, l, false);
-        pf[ks16][2 * x] = p[0];
-        pf[ks16][2 * x + 1] = p[1];
+      for (int e = 1; e < 4; ++e) {
+        top[rb] = max3(top[rb], s[0][rb][e], s[1][rb][e]);
+        top[rb] = max3(top[rb], s[2][rb][e], s[3][rb][e]);
       }
+      top[rb] = quad_max(top[rb]) * a.c;
+    }
+    if (__any(top[0] > m[0] + kAMove || top[1] > m[1] + kAMove)) {  // also the first tile
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb) {
+        const float mn = fmaxf(m[rb], top[rb]);
+        const float f = exp2_fast(m[rb] - (mn == -INFINITY ? 0.f : mn));
+        l[rb] *= f;
+#pragma unroll
+        for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[cb][rb][e] *= f;
+        m[rb] = mn;
+      }
+    }
+    bf16x8_t pf[2][2];
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+      const float ref = m[rb] == -INFINITY ? 0.f : -m[rb];
+#pragma unroll
+      for (int kb16 = 0; kb16 < 4; ++kb16)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const bf16x2_t p = pack2(exp2_fast(fmaf(s[kb16][rb][2 * x], a.c, ref)),
+                                   exp2_fast(fmaf(s[kb16][rb][2 * x + 1], a.c, ref)));
+          // the sum takes the rounded weights, which are the ones that V meets
+          l[rb] = __builtin_amdgcn_fdot2_f32_bf16(p, bf16x2_t{(__bf16)1.0f, (__bf16)1.0f}, l[rb],
+                                                  false);
+          pf[kb16 >> 1][rb][(kb16 & 1) * 4 + 2 * x] = p[0];
+          pf[kb16 >> 1][rb][(kb16 & 1) * 4 + 2 * x + 1] = p[1];
+        }
     }
     if constexpr (careful) {
       if (masked) {
 #pragma unroll
-        for (int ks16 = 0; ks16 < 4; ++ks16)
+        for (int kc = 0; kc < 2; ++kc)
 #pragma unroll
-          for (int db = 0; db < kDB; ++db) {
-            const v8i16_t vx = v_frag(ks16, db);
+          for (int cb = 0; cb < kCB; ++cb) {
+            const v8i16_t vx = v_frag(kc, cb);
 #pragma unroll 1
-            for (int j = 0; j < 16; ++j) {  // key kt + 16 ks16 + j: element x of half h
-              const int jh = (j >> 2) & 1, jx = (j & 3) + 4 * (j >> 3);
+            for (int j = 0; j < 32; ++j) {  // element j % 8 of lanes 16 (j / 8) ..
+              const int jq = j >> 3, jx = j & 7;
+              const int key = kt + 32 * kc + 4 * jq + (jx & 3) + 16 * (jx >> 2);
               v8i16_t one;
 #pragma unroll
-              for (int x = 0; x < 8; ++x) one[x] = half == jh && x == jx ? vx[x] : (short)0;
-              const f32x16_t zero = {};
-              const f32x16_t z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                  __builtin_bit_cast(bf16x8_t, one), pf[ks16], zero, 0, 0, 0);
-              if (kt + 16 * ks16 + j < lim) {
+              for (int x = 0; x < 8; ++x) one[x] = quad == jq && x == jx ? vx[x] : (short)0;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[db][e] += z[e];
+              for (int rb = 0; rb < 2; ++rb) {
+                const f32x4_t zero = {};
+                const f32x4_t z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8_t, one), pf[kc][rb], zero, 0, 0, 0);
+                if (key < lim[rb]) o[cb][rb] += z;
               }
             }
           }
@@ -388,15 +412,17 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
       }
     }
 #pragma unroll
-    for (int ks16 = 0; ks16 < 4; ++ks16) {
-      if (ks16 < 2) read_v(ks16 + 2);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int kc = 0; kc < 2; ++kc)
 #pragma unroll
-      for (int db = 0; db < kDB; ++db)
-        o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            __builtin_bit_cast(bf16x8_t, vf[ks16 % 3][db]), pf[ks16], o[db], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+      for (int cb = 0; cb < kCB; ++cb) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb)
+          o[cb][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8_t, vf[cb]), pf[kc][rb], o[cb][rb], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (kc == 0) vf[cb] = v_frag(1, cb);
+      }
   };
 
   // One pass over the keys. A hidden key's p is 0, but 0 times an infinity or NaN in its
@@ -404,12 +430,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   // holds such a value the workgroup passes again, taking those tiles' products key by
   // key and keeping them for the rows that see the key.
   auto pass = [&](auto CAREFUL) __attribute__((always_inline)) {
-    m = -INFINITY;
-    l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kDB; ++i)
+    for (int rb = 0; rb < 2; ++rb) {
+      m[rb] = -INFINITY;
+      l[rb] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+      for (int cb = 0; cb < kCB; ++cb) o[cb][rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
     offsets(kAKT - 1);
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i)
@@ -445,23 +472,27 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   pass(std::integral_constant<bool, false>{});
   if (__syncthreads_or((bad & 0x80008000u) != 0)) pass(std::integral_constant<bool, true>{});
 
-  l += __shfl_xor(l, 32);
-  // element 8 (e / 4) + 4 half + e % 4 of each block of 32 is in register e
+#pragma unroll
+  for (int rb = 0; rb < 2; ++rb) {
+    l[rb] += __shfl_xor(l[rb], 16);
+    l[rb] += __shfl_xor(l[rb], 32);
+  }
+  // element 4 quad + e of each block of 16 is in register e
   if (a.splits > 1) {
-    if (!valid) return;
-    const int64_t at = ((int64_t)blockIdx.y * a.nq + q0 + tok) * (a.hk * a.g) + qh;
-    // l = -1 marks a piece that saw keys, all of them with scores of -inf
-    if (half == 0) a.part_ml[at] = make_float2(m, lim > kbeg && l == 0.f ? -1.f : l);
-    if (kbeg >= kend) return;
 #pragma unroll
-    for (int db = 0; db < kDB; ++db)
+    for (int rb = 0; rb < 2; ++rb) {
+      if (!valid[rb]) continue;
+      const int64_t at = ((int64_t)blockIdx.y * a.nq + q0 + tok[rb]) * (a.hk * a.g) + qh[rb];
+      // l = -1 marks a piece that saw keys, all of them with scores of -inf
+      if (quad == 0)
+        a.part_ml[at] = make_float2(m[rb], lim[rb] > kbeg && l[rb] == 0.f ? -1.f : l[rb]);
+      if (kbeg >= kend) continue;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int e = db * 32 + 8 * x + 4 * half;
-        if (e < a.d)
-          *(f32x4_t*)(a.part_o + at * a.d + e) =
-              f32x4_t{o[db][4 * x], o[db][4 * x + 1], o[db][4 * x + 2], o[db][4 * x + 3]};
+      for (int cb = 0; cb < kCB; ++cb) {
+        const int e = cb * 16 + 4 * quad;
+        if (e < a.d) *(f32x4_t*)(a.part_o + at * a.d + e) = o[cb][rb];
       }
+    }
     return;
   }
   // Through LDS (free after the last barrier), so that a store instruction writes whole
@@ -469,26 +500,27 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   constexpr int kOutB = kRowB + 16;  // row pitch: rows 4 banks apart
   static_assert(NW * 32 * kOutB <= 2 * ST * kTile, "rows fit the tiles");
   unsigned char* ob = sm + wave * 32 * kOutB;
-  const float inv = visible > 0 ? 1.0f / l : 0.f;
 #pragma unroll
-  for (int db = 0; db < kDB; ++db)
+  for (int rb = 0; rb < 2; ++rb) {
+    const bool any = visible[rb] > 0;
+    const float inv = any ? 1.0f / l[rb] : 0.f;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int cb = 0; cb < kCB; ++cb) {
       bf16x2_t w[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y)
-        w[y] = visible > 0 ? pack2(o[db][4 * x + 2 * y] * inv, o[db][4 * x + 2 * y + 1] * inv)
-                           : pack2(0.f, 0.f);
-      *(bf16x4_t*)(ob + (lane & 31) * kOutB + (db * 32 + 8 * x + 4 * half) * 2) =
+        w[y] = any ? pack2(o[cb][rb][2 * y] * inv, o[cb][rb][2 * y + 1] * inv) : pack2(0.f, 0.f);
+      *(bf16x4_t*)(ob + (rb * 16 + r16) * kOutB + (cb * 16 + 4 * quad) * 2) =
           __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3);
     }
+  }
   wave_sync();
   const int rows_here = (int)(row_end - wrow);  // of this wave's 32
 #pragma unroll 1
   for (int r0 = 0; r0 < 32; r0 += kRowsPer) {
-    const int rr = r0 + lr;
-    const int64_t t = q0 + (unsigned)__shfl((int)tok, rr);
-    const int hh = __shfl(qh, rr);
+    const int rr = r0 + lr;  // of one block of 16: kRowsPer divides it
+    const int64_t t = q0 + (unsigned)__shfl((int)(r0 < 16 ? tok[0] : tok[1]), rr & 15);
+    const int hh = __shfl(r0 < 16 ? qh[0] : qh[1], rr & 15);
     if (rr < rows_here && lpp * 8 < a.d)
       *(u32x4_t*)(a.o + t * a.o_token + hh * a.o_head + lpp * 8) =
           *(const u32x4_t*)(ob + rr * kOutB + lpp * 16);
@@ -937,16 +969,26 @@ hipError_t launch_attention(const void* Q, const void* K, const void* V, const i
       launch_few<128, 128, true>(a, s);
     else
       launch_few<128, 128, false>(a, s);
-  } else if (p->d < 64) {
-    launch_kernel<64, 64, 4, 2, true>(a, s);
-  } else if (p->d == 64) {
-    launch_kernel<64, 64, 4, 2, false>(a, s);
-  } else if (p->d <= 96) {
-    launch_kernel<128, 96, 4, 2, true>(a, s);
-  } else if (p->d < 128) {
-    launch_kernel<128, 128, 4, 2, true>(a, s);
   } else {
-    launch_kernel<128, 128, 4, 2, false>(a, s);
+    switch (cdiv(p->d, 16)) {
+      case 1:
+      case 2: launch_kernel<64, 32, 4, 2, true>(a, s); break;
+      case 3: launch_kernel<64, 48, 4, 2, true>(a, s); break;
+      case 4:
+        if (p->d < 64)
+          launch_kernel<64, 64, 4, 2, true>(a, s);
+        else
+          launch_kernel<64, 64, 4, 2, false>(a, s);
+        break;
+      case 5: launch_kernel<128, 80, 4, 2, true>(a, s); break;
+      case 6: launch_kernel<128, 96, 4, 2, true>(a, s); break;
+      case 7: launch_kernel<128, 112, 4, 2, true>(a, s); break;
+      default:
+        if (p->d < 128)
+          launch_kernel<128, 128, 4, 2, true>(a, s);
+        else
+          launch_kernel<128, 128, 4, 2, false>(a, s);
+    }
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;

@@ -82,6 +82,17 @@ def test_attention_matches_definition(lens, hq, hk, d, causal):
     _check(got, Q, K, V, qs, ks, causal)
 
 
+@pytest.mark.parametrize("d", list(range(8, 129, 8)))
+@pytest.mark.parametrize("lens", [[(70, 70), (0, 5), (40, 150)], [(1, 75), (2, 2)]])
+def test_attention_every_head_size(lens, d):
+    print(f"[case] attention lens={lens} d={d}", flush=True)
+    qs, ks = _starts([a for a, _ in lens]), _starts([b for _, b in lens])
+    Q, K, V = (_randn((n, h, d), d + i) for i, (n, h) in enumerate(
+        [(qs[-1], 6), (ks[-1], 2), (ks[-1], 2)]))
+    got = L.attention(Q.to(DEV), K.to(DEV), V.to(DEV), _i32(qs), k_start=_i32(ks))
+    _check(got, Q, K, V, qs, ks)
+
+
 def test_attention_default_starts_and_scale():
     """k_start defaults to q_start; without either all rows are one sequence."""
     print("[case] attention defaults", flush=True)
