@@ -220,14 +220,21 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
   const int swk = D == 128 ? (row_w & 15) : ((row_w >> 1) & 7);
   const int swv = D == 128 ? ((row_w & 7) << 1) : (((row_w >> 1) & 3) << 1);
   static_assert(D == 64 || NW * kRowsPer % 16 == 0, "one K swizzle per lane");
-  const int ck = (lpp ^ swk) * 8, cv = (lpp ^ swv) * 8;
+  const int ck = (lpp ^ swk) * 8;
+  int cv = (lpp ^ swv) * 8;
   const unsigned short* kb = a.k + k0 * a.k_token + head * a.k_head;
   const unsigned short* vb = a.v + k0 * a.v_token + head * a.v_head;
-  const bool in_k = !PAD || ck < a.d, in_v = !PAD || cv < a.d;
-  if constexpr (PAD) {  // pieces past the head are zero in every tile
-    for (int i = tid; i < 2 * ST * kTile / 16; i += 64 * NW)
-      *(u32x4_t*)(sm + i * 16) = u32x4_t{0u, 0u, 0u, 0u};
-    __syncthreads();
+  // K's pieces past the head are zero in every tile and never loaded; V's repeat its
+  // first piece: they make channels that are not stored
+  const bool in_k = !PAD || ck < a.d;
+  if (PAD && cv >= a.d) cv = 0;
+  if constexpr (PAD) {
+    for (int i = tid; i < ST * kAKT * kPieces; i += 64 * NW) {
+      const int row = i / kPieces, piece = i % kPieces;
+      if (piece * 8 >= a.d)
+        *(u32x4_t*)(sm + row * kRowB + ((piece ^ (D == 128 ? (row & 15) : ((row >> 1) & 7))) << 4)) =
+            u32x4_t{0u, 0u, 0u, 0u};
+    }
   }
   const unsigned smb = lds_address(sm);
   // byte offsets from the tile's first key (64 rows of less than 2^24 elements)
@@ -253,7 +260,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
     if (i < kLd) {
       if (in_k) lds_dma1(vk[i], gk, dk + i * NW * 1024);
     } else {
-      if (in_v) lds_dma1(vv[i - kLd], gv, dk + ST * kTile + (i - kLd) * NW * 1024);
+      lds_dma1(vv[i - kLd], gv, dk + ST * kTile + (i - kLd) * NW * 1024);
     }
   };
 
@@ -589,17 +596,23 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
   // Loader: load i fills rows kRowsPer i .. of the wave's own tile, pieces swizzled as
   // above.
   unsigned char* own = sm + wave * 4 * kTile;  // K0 V0 K1 V1
+  auto k_swizzle = [](int row) { return D == 128 ? (row & 15) : ((row >> 1) & 7); };
   if constexpr (PAD) {
-    for (int i = lane; i < 4 * kTile / 16; i += 64) *(u32x4_t*)(own + i * 16) = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      for (int i = lane; i < kKeys * kPieces; i += 64) {
+        const int row = i / kPieces, piece = i % kPieces;
+        if (piece * 8 >= a.d)
+          *(u32x4_t*)(own + 2 * b * kTile + row * kRowB + ((piece ^ k_swizzle(row)) << 4)) =
+              u32x4_t{0u, 0u, 0u, 0u};
+      }
     wave_sync();
   }
   const int lr = lane / kPieces, lpp = lane % kPieces;
-  auto k_piece = [&](int i) {
-    const int row = i * kRowsPer + lr;
-    return (lpp ^ (D == 128 ? (row & 15) : ((row >> 1) & 7))) * 8;
-  };
-  const int cv = (lpp ^ (D == 128 ? ((lr & 3) << 2) : (((lr >> 1) & 1) << 2))) * 8;
+  auto k_piece = [&](int i) { return (lpp ^ k_swizzle(i * kRowsPer + lr)) * 8; };
+  int cv = (lpp ^ (D == 128 ? ((lr & 3) << 2) : (((lr >> 1) & 1) << 2))) * 8;
   const unsigned short* kb = a.k + k0 * a.k_token + head * a.k_head;
+  if (PAD && cv >= a.d) cv = 0;
   const unsigned short* vb = a.v + k0 * a.v_token + head * a.v_head;
   const unsigned ob = lds_address(sm) + wave * 4 * kTile;
   auto issue = [&](int kt, int buf) {
@@ -616,8 +629,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < kLd; ++i) {
       const unsigned row = min(i * kRowsPer + lr, last);
-      if (!PAD || cv < a.d)
-        lds_dma1((row * (unsigned)a.v_token + cv) * 2, gv, ob + (2 * buf + 1) * kTile + i * 1024);
+      lds_dma1((row * (unsigned)a.v_token + cv) * 2, gv, ob + (2 * buf + 1) * kTile + i * 1024);
     }
   };
   const int krow = lane & 31;
