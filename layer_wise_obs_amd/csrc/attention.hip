@@ -15,10 +15,11 @@
 // A workgroup takes 128 rows of one sequence and key head, a row being a (token,
 // query head of the group) pair, so K and V are read once for all g heads and
 // single tokens fill g rows. Each of the four waves owns 32 rows. The products are
-// formed transposed, S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_32x32x16_bf16:
-// a lane then holds scores of one query only (its softmax needs one exchange with
-// the other half wave), and its P values already are the operand of the second
-// product -- the contraction order over keys is free, so V's transposing LDS reads
+// formed transposed, S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_16x16x32_bf16 (at
+// this card's power limit 5% ahead of the 32x32x16 form): a lane then holds scores of
+// two queries only (their softmax needs two exchanges with the other quarters of the
+// wave), and its P values already are the operand of the second product -- the
+// contraction order over keys is free, so V's transposing LDS reads
 // (ds_read_b64_tr_b16, 4 keys each) follow the order P has in the registers.
 // Tiles of 64 keys are copied into LDS by direct loads, double-buffered; the 16-byte
 // pieces of a row are XOR-swizzled so that both kinds of operand reads use all banks.
@@ -135,10 +136,11 @@ __device__ __forceinline__ bf16x2_t pack2(float a, float b) {
   return bf16x2_t{(__bf16)a, (__bf16)b};  // v_cvt_pk_bf16_f32, round to nearest even
 }
 
-// D elements per row in LDS, of which the first DC enter the products (d <= DC); NW
-// waves of 32 rows; ST tiles of keys in LDS; PAD: the head is shorter than D.
-template <int D, int DC, int NW, int ST, bool PAD>
-__global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
+// D elements per row in LDS, of which the first DC (the head rounded up to 16) make
+// channels of O; PAD: the head is shorter than D.
+template <int D, int DC, bool PAD>
+__global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
+  constexpr int NW = 4, ST = 2;              // waves of 32 rows; tiles of keys in LDS
   constexpr int kBM = 32 * NW;
   constexpr int kPieces = D / 8;             // 16-byte pieces per row
   constexpr int kRowB = D * 2;
@@ -445,29 +447,20 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(AttnArgs a) {
       for (int cb = 0; cb < kCB; ++cb) o[cb][rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     offsets(kAKT - 1);
+    if (kbeg < kend) {
+      next_tile(kbeg, 0);
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i)
-      if (kbeg + i * kAKT < kend) {
-        next_tile(kbeg + i * kAKT, i);
-#pragma unroll
-        for (int x = 0; x < 2 * kLd; ++x) load(x);
-      }
+      for (int x = 0; x < 2 * kLd; ++x) load(x);
+    }
     int buf = 0;
     for (int kt = kbeg; kt < kend; kt += kAKT) {
-      // this tile has landed (at most ST - 2 later ones are in flight)
-      static_assert(ST == 2 || ST == 3 && kLd <= 2, "vmcnt immediates");
-      if (ST == 2 || kt + kAKT >= kend)
-        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      else if (kLd == 2)
-        __asm__ volatile("s_waitcnt vmcnt(4)" ::: "memory");
-      else
-        __asm__ volatile("s_waitcnt vmcnt(2)" ::: "memory");
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this tile has landed
       __syncthreads();  // the buffer filled next was last read before this barrier
-      const bool more = kt + (ST - 1) * kAKT < kend;
-      if (more) next_tile(kt + (ST - 1) * kAKT, buf == 0 ? ST - 1 : buf - 1);
+      const bool more = kt + kAKT < kend;
+      if (more) next_tile(kt + kAKT, buf ^ 1);
       ks = sm + buf * kTile;
       vs = sm + (ST + buf) * kTile;
-      buf = buf == ST - 1 ? 0 : buf + 1;
+      buf ^= 1;
       if (kt < lim_last) {
         tile(kt, more, CAREFUL);
       } else if (more) {  // no row of this wave sees the tile
@@ -827,16 +820,22 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
   }
 }
 
-// Joins the splits of a (token, query head): eight groups of 32 lanes (4 elements
-// each) take every eighth split, group 0 adds the groups in order.
+// Joins the splits of the (token, query head) rows, groups of 32 lanes (4 elements
+// each): a group per row for many rows of few splits, else eight groups to a row, each
+// taking every eighth split; their sums are added in order. (512 queries of 32 heads in
+// two splits 19.4 us with a group per row, 29.6 with eight; 16 of 64 heads in eight, the
+// other way round, 278 and 272.)
+constexpr int kAJoinSplits = 8, kAJoinRows = 2048;
+
+template <bool FEW>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
-  __shared__ float part[8][132];  // 128 elements, l, any
-  const int64_t row = blockIdx.x;
+  __shared__ float part[FEW ? 1 : 8][132];  // 128 elements, l, any
+  const int grp = threadIdx.x / 32, lane = threadIdx.x & 31, e = lane * 4;
   const int hq = a.hk * a.g;
+  const int64_t row = FEW ? (int64_t)blockIdx.x * 8 + grp : blockIdx.x;
   const int64_t tok = row / hq;
   const int qh = (int)(row - tok * hq);
   if (tok < start_at(a.q_start, 0, a.nq) || tok >= start_at(a.q_start, a.nseq, a.nq)) return;
-  const int grp = threadIdx.x / 32, lane = threadIdx.x & 31, e = lane * 4;
   const int64_t step = a.nq * hq;
   float m = -INFINITY;
   for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.part_ml[s * step + row].x);
@@ -845,7 +844,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   const float ref = m == -INFINITY ? 0.f : m;
   f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
   float l = 0.f, any = 0.f;
-  for (int s = grp; s < a.splits; s += 8) {
+  for (int s = FEW ? 0 : grp; s < a.splits; s += FEW ? 1 : 8) {
     const float2 ml = a.part_ml[s * step + row];
     if (ml.y != 0.f) any = 1.f;  // 0: the piece saw no key
     if (ml.y <= 0.f) continue;   // -1: only scores of -inf
@@ -853,24 +852,27 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     l += ml.y * f;
     if (e < a.d) o += *(const f32x4_t*)(a.part_o + (s * step + row) * a.d + e) * f;
   }
+  if constexpr (!FEW) {
 #pragma unroll
-  for (int y = 0; y < 4; ++y) part[grp][e + y] = o[y];
-  if (lane == 0) {
-    part[grp][128] = l;
-    part[grp][129] = any;
-  }
-  __syncthreads();
-  if (grp || e >= a.d) return;
-  for (int s = 1; s < 8; ++s) {
+    for (int y = 0; y < 4; ++y) part[grp][e + y] = o[y];
+    if (lane == 0) {
+      part[grp][128] = l;
+      part[grp][129] = any;
+    }
+    __syncthreads();
+    if (grp) return;
+    for (int s = 1; s < 8; ++s) {
 #pragma unroll
-    for (int y = 0; y < 4; ++y) o[y] += part[s][e + y];
+      for (int y = 0; y < 4; ++y) o[y] += part[s][e + y];
+    }
+    l = 0.f;
+    any = 0.f;
+    for (int s = 0; s < 8; ++s) {
+      l += part[s][128];
+      any += part[s][129];
+    }
   }
-  l = 0.f;
-  any = 0.f;
-  for (int s = 0; s < 8; ++s) {
-    l += part[s][128];
-    any += part[s][129];
-  }
+  if (e >= a.d) return;
   // keys seen, but every score -inf: l is 0 and there is no softmax (NaN)
   u16x4_t w;
 #pragma unroll
@@ -878,11 +880,11 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   *(u16x4_t*)(a.o + tok * a.o_token + qh * a.o_head + e) = w;
 }
 
-template <int D, int DC, int NW, int ST, bool PAD>
+template <int D, int DC, bool PAD>
 void launch_kernel(const AttnArgs& a, hipStream_t s) {
-  const int64_t slots = a.nq * a.g / (32 * NW) + a.nseq;
-  hipLaunchKernelGGL((attention_kernel<D, DC, NW, ST, PAD>),
-                     dim3((unsigned)(slots * a.hk), (unsigned)a.splits), dim3(64 * NW), 0, s, a);
+  const int64_t slots = a.nq * a.g / 128 + a.nseq;
+  hipLaunchKernelGGL((attention_kernel<D, DC, PAD>),
+                     dim3((unsigned)(slots * a.hk), (unsigned)a.splits), dim3(256), 0, s, a);
 }
 
 template <int D, int DC, bool PAD>
@@ -901,29 +903,51 @@ struct AttnPlan {
 
 // By the sequences' average lengths, all that the host knows. Up to 32 rows a sequence
 // the call is bound by reading the keys: the few-rows kernel (one workgroup per compute
-// unit at a time), its keys in pieces of 192 or more while those do not fill the units,
+// unit at a time), its keys in pieces of 320 or more while those do not fill the units,
 // else of 512 or more up to four rounds, which even out the sequences' lengths. (16
 // sequences over 300001 keys, 8 key heads: 287, 272, 292, 330 us with two, four, eight,
-// sixteen rounds; one over 4096 keys, 32 heads: 22 us in 8 pieces, 28 in 16; four over
-// 4000 keys, 8 heads: 19, 15, 13 us in pieces of 512, 256, 128; one over 32768 keys, one
-// head: 22 us in 64 pieces, 27 in 128.) With more rows the products bound it and partial
-// results cost: two workgroups per unit, pieces of four tiles of 64 or more.
+// sixteen rounds; one over 512 keys, 32 heads: 10.9 us whole, 12.1 in two; over 1024: 15.6
+// whole, 13.8 in three; one over 32768 keys, one head: 22 us in 64 pieces, 27 in 128.)
+// With more rows the products bound it, and the pieces' results cost: the number of pieces
+// with the least modelled time. A workgroup takes 7 us and 1.25 a tile of 64 keys where it
+// has a compute unit for itself, 1.6 where two share it; more than two take turns, the
+// longest or the average one (causal: half of the newest keys) setting the time; pieces are
+// joined in 3 us and at 4 TB/s. (One sequence, whole and in pieces: 512 tokens, 32 heads of
+// 64, 14.3 us and 19.4 in two; 1024, 32 of 128, 29 and 39; 2048, 8 of 128 on 2, 46 and 37;
+// 4096, 8 of 96 on 1, 77 and 62 in four; 300 over 20000 keys, 16 of 128 on 4, 383 and 81 in
+// six, 78 in twelve. Of 18 shapes, 16 were within 11% of the best of eight numbers.)
 AttnPlan plan_of(const th_attention_params* p) {
   const int64_t g = p->hq / p->hk;
   const int64_t seqs = p->nseq < p->nq ? p->nseq : p->nq;
-  const int64_t rows = cdiv(p->nq, seqs) * g, keys = cdiv(p->nk, seqs);
+  const int64_t tokens = cdiv(p->nq, seqs), rows = tokens * g, keys = cdiv(p->nk, seqs);
   AttnPlan r;
   r.few = rows <= 32;
   const int64_t groups = seqs * cdiv(rows, r.few ? 32 : 128) * p->hk;
-  auto pieces = [&](int64_t workgroups, int64_t least) {
-    const int64_t s = workgroups / groups < keys / least ? workgroups / groups : keys / least;
-    return s < 1 ? (int64_t)1 : (s > 64 ? (int64_t)64 : s);
-  };
   if (r.few) {
-    const int64_t one = pieces(kAUnits, 192), more = pieces(4 * kAUnits, 512);
+    auto pieces = [&](int64_t workgroups, int64_t least) {
+      const int64_t s = workgroups / groups < keys / least ? workgroups / groups : keys / least;
+      return s < 1 ? (int64_t)1 : (s > 64 ? (int64_t)64 : s);
+    };
+    const int64_t one = pieces(kAUnits, 320), more = pieces(4 * kAUnits, 512);
     r.splits = (int)(one > more ? one : more);
-  } else {
-    r.splits = (int)pieces(2 * kAUnits, 4 * 64);
+    return r;
+  }
+  const int64_t tiles = cdiv(keys, kAKT);
+  const double seen = p->causal ? (double)keys - 0.5 * (double)(tokens < keys ? tokens : keys)
+                                : (double)keys;
+  r.splits = 1;
+  double least = 1e300;
+  for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+    if (s > 1 && 3 * s > tiles) break;  // three tiles at least
+    const double workgroups = (double)groups * s;
+    const double longest = (double)cdiv(tiles, s);
+    const double turns = seen / kAKT / s * workgroups / (2 * kAUnits);
+    double us = 7.0 + (longest > turns ? longest : turns) * (workgroups <= kAUnits ? 1.25 : 1.6);
+    if (s > 1) us += 3.0 + (double)s * (double)(p->nq * p->hq) * (double)(p->d + 2) * 8.0 / 4e6;
+    if (us < least) {
+      least = us;
+      r.splits = s;
+    }
   }
   return r;
 }
@@ -984,27 +1008,31 @@ hipError_t launch_attention(const void* Q, const void* K, const void* V, const i
   } else {
     switch (cdiv(p->d, 16)) {
       case 1:
-      case 2: launch_kernel<64, 32, 4, 2, true>(a, s); break;
-      case 3: launch_kernel<64, 48, 4, 2, true>(a, s); break;
+      case 2: launch_kernel<64, 32, true>(a, s); break;
+      case 3: launch_kernel<64, 48, true>(a, s); break;
       case 4:
         if (p->d < 64)
-          launch_kernel<64, 64, 4, 2, true>(a, s);
+          launch_kernel<64, 64, true>(a, s);
         else
-          launch_kernel<64, 64, 4, 2, false>(a, s);
+          launch_kernel<64, 64, false>(a, s);
         break;
-      case 5: launch_kernel<128, 80, 4, 2, true>(a, s); break;
-      case 6: launch_kernel<128, 96, 4, 2, true>(a, s); break;
-      case 7: launch_kernel<128, 112, 4, 2, true>(a, s); break;
+      case 5: launch_kernel<128, 80, true>(a, s); break;
+      case 6: launch_kernel<128, 96, true>(a, s); break;
+      case 7: launch_kernel<128, 112, true>(a, s); break;
       default:
         if (p->d < 128)
-          launch_kernel<128, 128, 4, 2, true>(a, s);
+          launch_kernel<128, 128, true>(a, s);
         else
-          launch_kernel<128, 128, 4, 2, false>(a, s);
+          launch_kernel<128, 128, false>(a, s);
     }
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)(p->nq * p->hq)), dim3(256), 0, s, a);
+  const int64_t rows = p->nq * p->hq;
+  if (a.splits <= kAJoinSplits && rows > kAJoinRows)
+    hipLaunchKernelGGL(attention_join_kernel<true>, dim3((unsigned)cdiv(rows, 8)), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(attention_join_kernel<false>, dim3((unsigned)rows), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
