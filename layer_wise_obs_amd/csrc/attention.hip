@@ -24,6 +24,11 @@
 // Tiles of 64 keys are copied into LDS by direct loads, double-buffered; the 16-byte
 // pieces of a row are XOR-swizzled so that both kinds of operand reads use all banks.
 //
+// Bound by two waves per SIMD (their registers: 64 of O, 32 each of Q, scores, V and K
+// operands) whose products and softmax overlap only in part: 16 sequences of 2048
+// tokens, 32 heads of 128, 650-690 us (800-845 TFLOP/s of the visible half), 38% of the
+// cycles in products; one sequence of 16384, 8 heads on 2, 535-570 (965-1030).
+//
 // Where there are few workgroups, the keys of each are split over several; the
 // partial (m, l, O) are joined by a second kernel in a fixed order.
 #include "common.h"
@@ -531,7 +536,9 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
 // key head, and its four waves every fourth tile of 32 keys, each with two tiles of its
 // own in LDS and no barrier in the loop; their (m, l, O) meet in LDS at the end. Bound
 // by reading K and V; against 128-row workgroups, whose other three waves had no rows,
-// a token over 300 keys of 32 heads went from 12.5 to 10.8 us. Everything else is as above.
+// a token over 300 keys of 32 heads went from 12.5 to 10.8 us. 16 tokens over 300001 keys,
+// 64 heads on 8: 252 us (4.9 TB/s) and 6 for the join. Products of 32x32x16 (their lanes
+// hold one query, so the softmax exchanges once); everything else is as above.
 template <int D, int DC, bool PAD>
 __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
   constexpr int kBM = 32, kKeys = 32, kWaves = 4;
