@@ -147,3 +147,32 @@ def test_prune_block_whole_composes_the_steps():
 def test_prune_block_whole_refuses_partial_workloads():
     with pytest.raises(ValueError):
         sequential.prune_block_whole(synth.config(3), L.make_params(pattern=(2, 4)))
+
+
+def test_two_streams_at_once_give_the_serial_results():
+    g = torch.Generator().manual_seed(9)
+    draw = lambda *s: torch.randn(s, generator=g).to(BF).to(DEV)
+    sets = []
+    for i in range(2):
+        W = draw(1032, 4096)
+        X = draw(70 + i, 4096)  # pieces of the contraction, joined through a workspace
+        q, k, v = draw(1 + i, 8, 128), draw(9000, 2, 128), draw(9000, 2, 128)  # pieces of the keys
+        assert L.linear_workspace_size(*X.shape, W.shape[0]) > 0
+        sets.append((X, W, q, k, v))
+
+    def run(X, W, q, k, v):
+        starts = [torch.tensor([0, t.shape[0]], dtype=torch.int32).to(DEV) for t in (q, k)]
+        return [(L.linear(X, W, act="silu"), L.attention(q, k, v, starts[0], k_start=starts[1]),
+                 L.rms_norm(X, W[0])) for _ in range(10)]
+
+    serial = [run(*s)[0] for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = []
+    for s, stream in zip(sets, streams):
+        with torch.cuda.stream(stream):
+            got.append(run(*s))
+    torch.cuda.synchronize()
+    for results, want in zip(got, serial):
+        for r in results:
+            assert all(torch.equal(a, b) for a, b in zip(r, want))
