@@ -203,9 +203,10 @@ def _require(index, name, t, shape, dtype):
     raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
-def _fresh(torch, t):
-    """A new dense tensor of t's shape, dtype and GPU."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+def _fresh(torch, t, dtype=None):
+    """A new dense tensor of t's shape, dtype (or this one) and GPU; less host time than
+    torch.empty with a shape."""
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def _row_pitch(strides, n, dense):
@@ -447,7 +448,8 @@ def linear(X, W, bias=None, act="none", residual=None, Y=None, out_dtype=None, w
     if residual is not None:
         ldr = _row_pitch(_require(index, "residual", residual, (n, c), out_dtype), n, c)
     if Y is None:
-        Y = torch.empty((n, c), dtype=out_dtype, device=X.device)
+        Y = (torch.empty((n, c), dtype=out_dtype, device=X.device) if residual is None
+             else _fresh(torch, residual))
     else:
         ldy = _row_pitch(_require(index, "Y", Y, (n, c), out_dtype), n, c)
     if ws is None:
@@ -470,7 +472,7 @@ def rms_norm(X, weight, eps=1e-5, Y=None, out_dtype=None):
     _require(index, "weight", weight, (b,), X.dtype)
     ldy = b
     if Y is None:
-        Y = torch.empty((n, b), dtype=out_dtype or X.dtype, device=X.device)
+        Y = _fresh(torch, X, out_dtype)
     else:
         ldy = _row_pitch(_require(index, "Y", Y, (n, b), out_dtype or Y.dtype), n, b)
     _call_on(index, lib().th_rms_norm, X.data_ptr(), _dtype_code(X), n, b, ldx, weight.data_ptr(),
