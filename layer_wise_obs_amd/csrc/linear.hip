@@ -29,6 +29,14 @@ constexpr int kLK = 64;  // contraction per stage
 constexpr int kLGroup = 4;  // token tiles per group in the walk order
 constexpr int kLRow = kLK * 2;
 
+// 16 bytes of a row of Y or the residual, aligned like its elements only: the memory
+// system takes such accesses at any of their addresses, so that odd widths and pitches
+// need no code of their own but for a row's last channels. (15485 tokens 2216 -> 9418, gelu
+// and residual, bf16: 694 us; element by element, a lane per eight channels 1022, a lane
+// per channel 1190.)
+typedef u32x4_t bf16_row_t __attribute__((aligned(2)));
+typedef f32x4_t f32_row_t __attribute__((aligned(4)));
+
 struct LinEpilogue {
   const unsigned short* bias;
   const void* residual;
@@ -36,7 +44,6 @@ struct LinEpilogue {
   int64_t ldr, ldy;
   int act;       // th_activation
   int y_f32;     // Y and residual are fp32 (else bf16)
-  int vec;       // 8 consecutive channels move as one or two 16-byte accesses
 };
 
 __device__ __forceinline__ float activate(float z, int act) {
@@ -48,10 +55,22 @@ __device__ __forceinline__ float activate(float z, int act) {
   }
 }
 
-// Channel q of token t.
-__device__ __forceinline__ void finish1(float v, int64_t t, int64_t q, const LinEpilogue& ep) {
-  if (ep.bias) v += bf16_to_f32(ep.bias[q]);
-  v = activate(v, ep.act);
+// All of v, one decision for them.
+__device__ __forceinline__ void activate8(float (&v)[8], int act) {
+  if (act == TH_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_RELU);
+  } else if (act == TH_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_SILU);
+  } else if (act == TH_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_GELU);
+  }
+}
+
+// Residual and store of channel q of token t, its activation v.
+__device__ __forceinline__ void put1(float v, int64_t t, int64_t q, const LinEpilogue& ep) {
   if (ep.y_f32) {
     if (ep.residual) v += ((const float*)ep.residual)[t * ep.ldr + q];
     ((float*)ep.y)[t * ep.ldy + q] = v;
@@ -60,63 +79,57 @@ __device__ __forceinline__ void finish1(float v, int64_t t, int64_t q, const Lin
     ((unsigned short*)ep.y)[t * ep.ldy + q] = f32_to_bf16_rne(v);
   }
 }
-
-// Eight consecutive channels q .. q+7 of token t (q + i < c and t < n hold where
-// the caller passes `count` of them).
-__device__ __forceinline__ void finish8(float (&v)[8], int64_t t, int64_t q, int count,
-                                        const LinEpilogue& ep) {
-  if (ep.bias) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < count) v[i] += bf16_to_f32(ep.bias[q + i]);
-  }
-  if (ep.act != TH_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], ep.act);
-  }
-  if (ep.vec) {  // then count is 8
-    if (ep.y_f32) {
-      if (ep.residual) {
-        const f32x4_t* r = (const f32x4_t*)((const float*)ep.residual + t * ep.ldr + q);
-        const f32x4_t a = r[0], b = r[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] += a[i];
-          v[4 + i] += b[i];
-        }
-      }
-      f32x4_t* y = (f32x4_t*)((float*)ep.y + t * ep.ldy + q);
-      y[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-      y[1] = f32x4_t{v[4], v[5], v[6], v[7]};
-    } else {
-      if (ep.residual) {
-        const u32x4_t r = *(const u32x4_t*)((const unsigned short*)ep.residual + t * ep.ldr + q);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[2 * i] += __uint_as_float(r[i] << 16);
-          v[2 * i + 1] += __uint_as_float(r[i] & 0xffff0000u);
-        }
-      }
-      u32x4_t o;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o[i] = (unsigned)f32_to_bf16_rne(v[2 * i]) | ((unsigned)f32_to_bf16_rne(v[2 * i + 1]) << 16);
-      *(u32x4_t*)((unsigned short*)ep.y + t * ep.ldy + q) = o;
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i >= count) break;
-    if (ep.y_f32) {
-      if (ep.residual) v[i] += ((const float*)ep.residual)[t * ep.ldr + q + i];
-      ((float*)ep.y)[t * ep.ldy + q + i] = v[i];
-    } else {
-      if (ep.residual) v[i] += bf16_to_f32(((const unsigned short*)ep.residual)[t * ep.ldr + q + i]);
-      ((unsigned short*)ep.y)[t * ep.ldy + q + i] = f32_to_bf16_rne(v[i]);
-    }
-  }
+// Channel q of token t.
+__device__ __forceinline__ void finish1(float v, int64_t t, int64_t q, const LinEpilogue& ep) {
+  if (ep.bias) v += bf16_to_f32(ep.bias[q]);
+  put1(activate(v, ep.act), t, q, ep);
 }
+
+// Residuals of eight consecutive channels as they are in memory, and their sum with v
+// stored.
+template <bool F32>
+struct Row8;
+template <>
+struct Row8<false> {
+  bf16_row_t r;
+  __device__ __forceinline__ void load(const LinEpilogue& ep, int64_t t, int64_t q) {
+    r = *(const bf16_row_t*)((const unsigned short*)ep.residual + t * ep.ldr + q);
+  }
+  __device__ __forceinline__ void put(float (&v)[8], const LinEpilogue& ep, int64_t t, int64_t q) const {
+    if (ep.residual) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] += __uint_as_float(r[i] << 16);
+        v[2 * i + 1] += __uint_as_float(r[i] & 0xffff0000u);
+      }
+    }
+    bf16x8_t y;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) y[x] = (__bf16)v[x];
+    *(bf16_row_t*)((unsigned short*)ep.y + t * ep.ldy + q) = __builtin_bit_cast(u32x4_t, y);
+  }
+};
+template <>
+struct Row8<true> {
+  f32_row_t a, b;
+  __device__ __forceinline__ void load(const LinEpilogue& ep, int64_t t, int64_t q) {
+    const float* r = (const float*)ep.residual + t * ep.ldr + q;
+    a = *(const f32_row_t*)r;
+    b = *(const f32_row_t*)(r + 4);
+  }
+  __device__ __forceinline__ void put(float (&v)[8], const LinEpilogue& ep, int64_t t, int64_t q) const {
+    if (ep.residual) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] += a[i];
+        v[4 + i] += b[i];
+      }
+    }
+    float* y = (float*)ep.y + t * ep.ldy + q;
+    *(f32_row_t*)y = f32x4_t{v[0], v[1], v[2], v[3]};
+    *(f32_row_t*)(y + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+  }
+};
 
 // Workgroup (x, split): tile x of the walk order, stages [split per, split per + per)
 // of the contraction. With part set, the tile's raw sums go to part[split][n][cp], cp
@@ -338,7 +351,7 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
   const int64_t cp = (c + 7) & ~(int64_t)7;
   const int tl = lane / kLanes, ql = (lane % kLanes) * 8;
   const int64_t q = N0 + wn * kCols + ql;
-  const int count = c - q < 8 ? (int)(c - q) : 8;
+  const bool whole = q + 8 <= c;  // else fewer than eight channels, or none
   auto token = [&](int i, int p) { return M0 + wm * 32 * WM + i * 32 + p * kTok + tl; };
   auto values = [&](int p) { return strip + (p * kTok + tl) * kPitch + ql; };
   auto write_strip = [&](int i) {
@@ -357,28 +370,11 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
       write_strip(i);
 #pragma unroll 1
       for (int p = 0; p < kPass; ++p) {
-        if (token(i, p) < n && count > 0) {
+        if (token(i, p) < n && q < c) {
           const f32x4_t* v = (const f32x4_t*)values(p);
           f32x4_t* o = (f32x4_t*)(part + ((int64_t)blockIdx.y * n + token(i, p)) * cp + q);
           o[0] = v[0];
           o[1] = v[1];
-        }
-      }
-      wave_sync();
-    }
-    return;
-  }
-  if (!ep.vec) {
-#pragma unroll
-    for (int i = 0; i < WM; ++i) {
-      write_strip(i);
-#pragma unroll 1
-      for (int p = 0; p < kPass; ++p) {
-        if (token(i, p) < n && count > 0) {
-          float v[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) v[x] = values(p)[x];
-          finish8(v, token(i, p), q, count, ep);
         }
       }
       wave_sync();
@@ -390,7 +386,7 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
   auto finish = [&](auto F32) __attribute__((always_inline)) {
     constexpr bool f32 = decltype(F32)::value;
     constexpr int kHeld = f32 && WM > 2 ? 2 : WM;
-    u32x4_t res[kHeld][kPass][f32 ? 2 : 1];
+    Row8<f32> res[kHeld][kPass];
 #pragma unroll
     for (int i0 = 0; i0 < WM; i0 += kHeld) {
       if (ep.residual) {
@@ -398,15 +394,7 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
         for (int i = 0; i < kHeld; ++i)
 #pragma unroll
           for (int p = 0; p < kPass; ++p)
-            if (token(i0 + i, p) < n && count > 0) {
-              const int64_t at = token(i0 + i, p) * ep.ldr + q;
-              if constexpr (f32) {
-                res[i][p][0] = ((const u32x4_t*)((const float*)ep.residual + at))[0];
-                res[i][p][1] = ((const u32x4_t*)((const float*)ep.residual + at))[1];
-              } else {
-                res[i][p][0] = *(const u32x4_t*)((const unsigned short*)ep.residual + at);
-              }
-            }
+            if (token(i0 + i, p) < n && whole) res[i][p].load(ep, token(i0 + i, p), q);
       }
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
@@ -414,41 +402,32 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
         if (ep.bias || ep.act != TH_ACT_NONE) {  // in place, by the lane that reads it next
 #pragma unroll 1
           for (int p = 0; p < kPass; ++p) {
-            float* v = values(p);
+            float *at = values(p), v[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const float b8 = ep.bias && count > 0 ? bf16_to_f32(ep.bias[q + x]) : 0.f;
-              v[x] = activate(v[x] + b8, ep.act);
+            for (int x = 0; x < 8; ++x) v[x] = at[x];
+            if (ep.bias) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) v[x] += q + x < c ? bf16_to_f32(ep.bias[q + x]) : 0.f;
             }
+            activate8(v, ep.act);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) at[x] = v[x];
           }
         }
 #pragma unroll
         for (int p = 0; p < kPass; ++p) {
-          if (token(i0 + i, p) >= n || count <= 0) continue;
+          if (token(i0 + i, p) >= n || !whole) continue;
           const f32x4_t* vp = (const f32x4_t*)values(p);
           const f32x4_t lo = vp[0], hi = vp[1];
           float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          const int64_t at = token(i0 + i, p) * ep.ldy + q;
-          if constexpr (f32) {
-            if (ep.residual) {
-#pragma unroll
-              for (int x = 0; x < 8; ++x) v[x] += __uint_as_float(res[i][p][x >> 2][x & 3]);
-            }
-            f32x4_t* y = (f32x4_t*)((float*)ep.y + at);
-            y[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-            y[1] = f32x4_t{v[4], v[5], v[6], v[7]};
-          } else {
-            if (ep.residual) {
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                v[2 * x] += __uint_as_float(res[i][p][0][x] << 16);
-                v[2 * x + 1] += __uint_as_float(res[i][p][0][x] & 0xffff0000u);
-              }
-            }
-            bf16x8_t y;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) y[x] = (__bf16)v[x];
-            *(bf16x8_t*)((unsigned short*)ep.y + at) = y;
+          res[i][p].put(v, ep, token(i0 + i, p), q);
+        }
+        if (!whole) {  // the last channels of a row
+#pragma unroll 1
+          for (int p = 0; p < kPass; ++p) {
+            if (token(i0 + i, p) >= n) break;
+#pragma unroll 1
+            for (int x = 0; q + x < c; ++x) put1(values(p)[x], token(i0 + i, p), q + x, ep);
           }
         }
         wave_sync();
@@ -461,7 +440,8 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
     finish(std::integral_constant<bool, false>{});
 }
 
-// Sum of the splits' raw products in order, then the epilogue: 8 channels per thread.
+// Sum of the splits' raw products in order, then the epilogue: 8 channels per thread,
+// those of a row's end one by one.
 __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restrict__ part, int splits,
                                                           int64_t n, int64_t c, LinEpilogue ep) {
   const int64_t per_row = cdiv(c, 8), cp = per_row * 8;
@@ -479,7 +459,26 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restric
       v[4 + x] += hi[x];
     }
   }
-  finish8(v, t, q, c - q < 8 ? (int)(c - q) : 8, ep);
+  if (ep.bias) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] += q + x < c ? bf16_to_f32(ep.bias[q + x]) : 0.f;
+  }
+  activate8(v, ep.act);
+  if (q + 8 > c) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      if (q + x < c) put1(v[x], t, q + x, ep);
+    return;
+  }
+  auto put = [&](auto F32) {
+    Row8<decltype(F32)::value> r;
+    if (ep.residual) r.load(ep, t, q);
+    r.put(v, ep, t, q);
+  };
+  if (ep.y_f32)
+    put(std::integral_constant<bool, true>{});
+  else
+    put(std::integral_constant<bool, false>{});
 }
 
 // Skinny products, up to 16 tokens: bound by reading W once. A workgroup takes 16
@@ -617,9 +616,6 @@ hipError_t launch_linear(const unsigned short* X, int64_t ldx, const unsigned sh
   ep.ldy = ldy;
   ep.act = act;
   ep.y_f32 = ydt == TH_F32;
-  const int64_t el = ep.y_f32 ? 4 : 8;
-  ep.vec = c % 8 == 0 && ldy % el == 0 && (!residual || ldr % el == 0) &&
-           (((uintptr_t)Y | (uintptr_t)residual) & 15) == 0;
   const LinPlan p = plan_of(n, b, c, part != nullptr);
   float* raw = p.splits > 1 ? part : nullptr;
   hipError_t e;

@@ -152,3 +152,19 @@ def test_linear_full_size_sampled():
     Y = L.linear(X, W, residual=R)
     rows = torch.tensor([0, 1, 255, 256, 65535, 65536, 100001, 131070, 131071])
     _check(Y[rows].cpu(), X[rows].cpu(), W.cpu(), None, "none", R[rows].cpu())
+
+
+@pytest.mark.parametrize("n,b,c", [(3, 64, 19), (70, 4096, 75), (150, 72, 331), (700, 136, 523)])
+@pytest.mark.parametrize("ydt", [BF, F32])
+@pytest.mark.parametrize("at", [0, 1, 3])
+def test_linear_rows_of_any_alignment(n, b, c, ydt, at):
+    print(f"[case] linear n={n} b={b} c={c} {ydt} at={at}", flush=True)
+    X, W, bias = _randn((n, b), n), _randn((c, b), c, scale=b ** -0.5), _randn((c,), 5)
+    wide = _randn((n, c + 4), 6, ydt)
+    R = wide[:, 4 - at:c + 4 - at]
+    buf = torch.full((n, c + 5), 7.0, dtype=ydt, device=DEV)  # odd pitches for odd and even c
+    Y = buf[:, at:at + c]
+    L.linear(X.to(DEV), W.to(DEV), bias=bias.to(DEV), act="silu", residual=_dev(wide)[:, 4 - at:c + 4 - at],
+             Y=Y)
+    _check(Y, X, W, bias, "silu", R)
+    assert bool((buf[:, :at] == 7).all()) and bool((buf[:, at + c:] == 7).all())
