@@ -255,9 +255,8 @@ th_status th_linear(const void* X, int64_t ldx, const void* W, th_dtype dt, int6
  * layers"]: Y_tq = X_tq / sqrt(mean_q X_tq^2 + eps) * weight_q. X [n,b] (row pitch
  * ldx, dtype xdt), weight [b] in xdt, Y [n,b] (row pitch ldy, dtype ydt); sums and
  * products in fp32, Y rounded once. Y may be X (same dtype and pitch); otherwise
- * they must not overlap. n = 0 is allowed; n < 2^31, eps >= 0. 16-byte accesses
- * where b % 8 == 0 and pointers and row pitches are 16-byte multiples, elementwise
- * otherwise. Asynchronous on the stream. */
+ * they must not overlap. n = 0 is allowed; n < 2^31, eps >= 0. Any width, row pitch
+ * and alignment of whole elements. Asynchronous on the stream. */
 th_status th_rms_norm(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t ldx,
                       const void* weight, double eps, void* Y, th_dtype ydt, int64_t ldy,
                       th_stream_t stream);

@@ -16,12 +16,19 @@ namespace {
 
 constexpr int kNChunks = 4;  // register-held chunks of 8 elements per thread
 
+// Eight elements, 16 bytes at a time, aligned like an element only: the memory system
+// takes such accesses at any of their addresses, so that odd widths and pitches need no
+// code of their own but for a row's last elements (65536 rows of 4095 in bf16: 331 us;
+// element by element 587).
+typedef u32x4_t bf16_row_t __attribute__((aligned(2)));
+typedef f32x4_t f32_row_t __attribute__((aligned(4)));
+
 struct Row8 {
   float v[8];
 };
 
 __device__ __forceinline__ Row8 load8(const unsigned short* p) {
-  const u32x4_t u = *(const u32x4_t*)p;
+  const u32x4_t u = *(const bf16_row_t*)p;
   Row8 r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -31,7 +38,7 @@ __device__ __forceinline__ Row8 load8(const unsigned short* p) {
   return r;
 }
 __device__ __forceinline__ Row8 load8(const float* p) {
-  const f32x4_t a = ((const f32x4_t*)p)[0], b = ((const f32x4_t*)p)[1];
+  const f32x4_t a = *(const f32_row_t*)p, b = *(const f32_row_t*)(p + 4);
   return Row8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
 }
 __device__ __forceinline__ void store8(unsigned short* p, const Row8& r) {
@@ -39,16 +46,34 @@ __device__ __forceinline__ void store8(unsigned short* p, const Row8& r) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     u[i] = (unsigned)f32_to_bf16_rne(r.v[2 * i]) | ((unsigned)f32_to_bf16_rne(r.v[2 * i + 1]) << 16);
-  *(u32x4_t*)p = u;
+  *(bf16_row_t*)p = u;
 }
 __device__ __forceinline__ void store8(float* p, const Row8& r) {
-  ((f32x4_t*)p)[0] = f32x4_t{r.v[0], r.v[1], r.v[2], r.v[3]};
-  ((f32x4_t*)p)[1] = f32x4_t{r.v[4], r.v[5], r.v[6], r.v[7]};
+  *(f32_row_t*)p = f32x4_t{r.v[0], r.v[1], r.v[2], r.v[3]};
+  *(f32_row_t*)(p + 4) = f32x4_t{r.v[4], r.v[5], r.v[6], r.v[7]};
 }
 __device__ __forceinline__ float load1(const unsigned short* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ void store1(unsigned short* p, float v) { *p = f32_to_bf16_rne(v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+
+// Elements q .. q+7 of a row of b: with a TAIL (b is no multiple of 8) those past its end
+// are 0, and not stored.
+template <bool TAIL, class T>
+__device__ __forceinline__ Row8 row_load(const T* row, int64_t q, int64_t b) {
+  if (!TAIL || q + 8 <= b) return load8(row + q);
+  Row8 r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r.v[e] = q + e < b ? load1(row + q + e) : 0.f;
+  return r;
+}
+template <bool TAIL, class T>
+__device__ __forceinline__ void row_store(T* row, int64_t q, int64_t b, const Row8& r) {
+  if (!TAIL || q + 8 <= b) return store8(row + q, r);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (q + e < b) store1(row + q + e, r.v[e]);
+}
 
 // Sum over the T threads of a workgroup, the same value in every thread.
 template <int T>
@@ -65,7 +90,7 @@ __device__ __forceinline__ float group_sum(float s, float* red) {
   return s;
 }
 
-template <class TI, class TO, int T>
+template <class TI, class TO, int T, bool TAIL>
 __global__ __launch_bounds__(T) void rms_norm_kernel(const TI* X, int64_t ldx, const TI* w, TO* Y,
                                                      int64_t ldy, int64_t b, float eps) {
   __shared__ float red[T / 64];
@@ -76,7 +101,7 @@ __global__ __launch_bounds__(T) void rms_norm_kernel(const TI* X, int64_t ldx, c
 #pragma unroll
   for (int i = 0; i < kNChunks; ++i) {
     const int64_t q = ((int64_t)i * T + threadIdx.x) * 8;
-    if (q < b) kept[i] = load8(x + q);
+    if (q < b) kept[i] = row_load<TAIL>(x, q, b);
   }
 #pragma unroll
   for (int i = 0; i < kNChunks; ++i) {
@@ -87,63 +112,45 @@ __global__ __launch_bounds__(T) void rms_norm_kernel(const TI* X, int64_t ldx, c
   }
   // columns past the register-held part are read again for the product
   for (int64_t q = ((int64_t)kNChunks * T + threadIdx.x) * 8; q < b; q += T * 8) {
-    const Row8 r = load8(x + q);
+    const Row8 r = row_load<TAIL>(x, q, b);
 #pragma unroll
     for (int e = 0; e < 8; ++e) s += r.v[e] * r.v[e];
   }
   const float scale = 1.0f / sqrtf(group_sum<T>(s, red) / (float)b + eps);
   auto put = [&](Row8 r, int64_t q) {
-    const Row8 g = load8(w + q);
+    const Row8 g = row_load<TAIL>(w, q, b);
 #pragma unroll
     for (int e = 0; e < 8; ++e) r.v[e] = r.v[e] * scale * g.v[e];
-    store8(y + q, r);
+    row_store<TAIL>(y, q, b, r);
   };
 #pragma unroll
   for (int i = 0; i < kNChunks; ++i) {
     const int64_t q = ((int64_t)i * T + threadIdx.x) * 8;
     if (q < b) put(kept[i], q);
   }
-  for (int64_t q = ((int64_t)kNChunks * T + threadIdx.x) * 8; q < b; q += T * 8) put(load8(x + q), q);
+  for (int64_t q = ((int64_t)kNChunks * T + threadIdx.x) * 8; q < b; q += T * 8) put(row_load<TAIL>(x, q, b), q);
 }
 
-// Any width, pitch and alignment: one element per thread and step.
-template <class TI, class TO>
-__global__ __launch_bounds__(256) void rms_norm_any_kernel(const TI* X, int64_t ldx, const TI* w,
-                                                           TO* Y, int64_t ldy, int64_t b,
-                                                           float eps) {
-  __shared__ float red[4];
-  const TI* x = X + (int64_t)blockIdx.x * ldx;
-  TO* y = Y + (int64_t)blockIdx.x * ldy;
-  float s = 0.f;
-  for (int64_t q = threadIdx.x; q < b; q += 256) {
-    const float v = load1(x + q);
-    s += v * v;
-  }
-  const float scale = 1.0f / sqrtf(group_sum<256>(s, red) / (float)b + eps);
-  for (int64_t q = threadIdx.x; q < b; q += 256) store1(y + q, load1(x + q) * scale * load1(w + q));
+template <class TI, class TO, int T, bool TAIL>
+hipError_t launch_rows(const void* X, int64_t ldx, const void* w, void* Y, int64_t ldy, int64_t n,
+                       int64_t b, float eps, hipStream_t s) {
+  const TI* x = (const TI*)X;
+  TO* y = (TO*)Y;
+  for (; n > 0; n -= kMaxGroups, x += kMaxGroups * ldx, y += kMaxGroups * ldy)
+    hipLaunchKernelGGL((rms_norm_kernel<TI, TO, T, TAIL>),
+                       dim3((unsigned)(n < kMaxGroups ? n : kMaxGroups)), dim3(T), 0, s, x, ldx,
+                       (const TI*)w, y, ldy, b, eps);
+  return hipGetLastError();
 }
 
 template <class TI, class TO>
 hipError_t launch_typed(const void* X, int64_t ldx, const void* w, void* Y, int64_t ldy, int64_t n,
                         int64_t b, float eps, hipStream_t s) {
-  // 16-byte accesses: 8 bf16 or 4 fp32 elements
-  const bool vec = b % 8 == 0 && ldx % (16 / sizeof(TI)) == 0 && ldy % (16 / sizeof(TO)) == 0 &&
-                   (((uintptr_t)X | (uintptr_t)w | (uintptr_t)Y) & 15) == 0;
-  const TI* x = (const TI*)X;
-  TO* y = (TO*)Y;
-  for (; n > 0; n -= kMaxGroups, x += kMaxGroups * ldx, y += kMaxGroups * ldy) {
-    const dim3 grid((unsigned)(n < kMaxGroups ? n : kMaxGroups));
-    if (!vec)
-      hipLaunchKernelGGL((rms_norm_any_kernel<TI, TO>), grid, dim3(256), 0, s, x, ldx,
-                         (const TI*)w, y, ldy, b, eps);
-    else if (b <= 1024)
-      hipLaunchKernelGGL((rms_norm_kernel<TI, TO, 64>), grid, dim3(64), 0, s, x, ldx, (const TI*)w,
-                         y, ldy, b, eps);
-    else
-      hipLaunchKernelGGL((rms_norm_kernel<TI, TO, 256>), grid, dim3(256), 0, s, x, ldx,
-                         (const TI*)w, y, ldy, b, eps);
-  }
-  return hipGetLastError();
+  if (b % 8)  // the whole rows' kernel needs fewer registers: 379 us against 405 with tails
+    return b <= 1024 ? launch_rows<TI, TO, 64, true>(X, ldx, w, Y, ldy, n, b, eps, s)
+                     : launch_rows<TI, TO, 256, true>(X, ldx, w, Y, ldy, n, b, eps, s);
+  return b <= 1024 ? launch_rows<TI, TO, 64, false>(X, ldx, w, Y, ldy, n, b, eps, s)
+                   : launch_rows<TI, TO, 256, false>(X, ldx, w, Y, ldy, n, b, eps, s);
 }
 
 }  // namespace
