@@ -13,7 +13,8 @@
 // workgroup computes them once per token into LDS for all its heads of q and k, while
 // its first heads are on their way.
 // A head is held by a group of lanes with 8 consecutive elements each (16 bytes of
-// bf16); a half-layout partner sits in another lane of the group.
+// bf16); a half-layout partner sits in another lane of the group, at the same place where
+// rot / 2 is a multiple of 8, and is fetched through LDS where it is not.
 #include "common.h"
 
 namespace th {
@@ -52,13 +53,16 @@ __device__ __forceinline__ float2 turn_of(double p, double f, float amplitude) {
   return make_float2(c * amplitude, s * amplitude);
 }
 
-// Eight elements as they are in memory, and as floats.
+// Eight elements as they are in memory, and as floats; aligned like an element only, which
+// the memory system takes.
+typedef u32x4_t bf16_row_t __attribute__((aligned(2)));
+typedef f32x4_t f32_row_t __attribute__((aligned(4)));
 template <class T>
 struct Raw8;
 template <>
 struct Raw8<unsigned short> {
   u32x4_t u;
-  __device__ __forceinline__ void load(const unsigned short* p) { u = *(const u32x4_t*)p; }
+  __device__ __forceinline__ void load(const unsigned short* p) { u = *(const bf16_row_t*)p; }
   __device__ __forceinline__ void to(float (&v)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -71,8 +75,8 @@ template <>
 struct Raw8<float> {
   f32x4_t a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = ((const f32x4_t*)p)[0];
-    b = ((const f32x4_t*)p)[1];
+    a = *(const f32_row_t*)p;
+    b = *(const f32_row_t*)(p + 4);
   }
   __device__ __forceinline__ void to(float (&v)[8]) const {
 #pragma unroll
@@ -87,22 +91,32 @@ __device__ __forceinline__ void put8(unsigned short* p, const float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     u[i] = (unsigned)f32_to_bf16_rne(v[2 * i]) | ((unsigned)f32_to_bf16_rne(v[2 * i + 1]) << 16);
-  *(u32x4_t*)p = u;
+  *(bf16_row_t*)p = u;
 }
 __device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
-  ((f32x4_t*)p)[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-  ((f32x4_t*)p)[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+  *(f32_row_t*)p = f32x4_t{v[0], v[1], v[2], v[3]};
+  *(f32_row_t*)(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
 }
 __device__ __forceinline__ float get1(const unsigned short* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ float get1(const float* p) { return *p; }
 __device__ __forceinline__ void put1(unsigned short* p, float v) { *p = f32_to_bf16_rne(v); }
 __device__ __forceinline__ void put1(float* p, float v) { *p = v; }
 
-// 16-byte accesses. G lanes (a power of two >= d / 8) hold a head; the workgroup's
-// 256 / G groups are `tokens` tokens x `phases` heads at a time.
-template <class T, int G, bool INTERLEAVED>
+// Where the other element of a pair is. (29807 tokens, 64 heads of 88, half, normed: 244 us
+// with 16-byte accesses and partners through LDS, 817 with a lane per pair; 11625 tokens, 64
+// heads of 64, 62 elements interleaved: 42 and 197.)
+enum Partner {
+  kNext,    // interleaved: the pair is in one lane
+  kLane,    // half, rot % 16 == 0: the same element of another lane
+  kAnyLane  // half: any element of another lane
+};
+
+// 16-byte accesses (d % 8 == 0). G lanes (a power of two >= d / 8) hold a head; the
+// workgroup's 256 / G groups are `tokens` tokens x `phases` heads at a time.
+template <class T, int G, int PARTNER>
 __global__ __launch_bounds__(kRThreads) void rotary_kernel(RotArgs a) {
   __shared__ float2 cs[kRMaxTokens * kRMaxPairs];
+  __shared__ __attribute__((aligned(16))) float xs[PARTNER == kAnyLane ? kRThreads * 8 : 4];
   const int pairs = a.rot >> 1;
   const int64_t token0 = a.from + (int64_t)blockIdx.x * a.tokens;
   constexpr int groups = kRThreads / G;
@@ -137,18 +151,29 @@ __global__ __launch_bounds__(kRThreads) void rotary_kernel(RotArgs a) {
   }
   __syncthreads();
   if (!works) return;
-  // this lane's pairs: 8 of them (half) or 4 (interleaved), the same for every head
-  float cosv[INTERLEAVED ? 4 : 8], sinv[INTERLEAVED ? 4 : 8];
-  const bool upper = !INTERLEAVED && e0 >= pairs;  // second element of its pairs
+  // this lane's pairs: 8 of them (half) or 4 (interleaved), the same for every head; an
+  // upper element's turn is v cos + partner sin, a lower one's v cos - partner sin
+  constexpr int kCs = PARTNER == kNext ? 4 : 8;
+  float cosv[kCs], sinv[kCs];
+  const bool upper = PARTNER == kLane && e0 >= pairs;  // second element of its pairs
   if (turned) {
-    const float2* c = cs + t * pairs + (INTERLEAVED ? e0 / 2 : (upper ? e0 - pairs : e0));
+    const float2* c = cs + t * pairs;
+    if constexpr (PARTNER == kNext) {
+      c += e0 / 2;
+    } else if constexpr (PARTNER == kLane) {
+      c += upper ? e0 - pairs : e0;
+    }
 #pragma unroll
-    for (int i = 0; i < (INTERLEAVED ? 4 : 8); ++i) {
-      cosv[i] = c[i].x;
-      sinv[i] = c[i].y;
+    for (int i = 0; i < kCs; ++i) {
+      const int e = e0 + (PARTNER == kNext ? 2 * i : i);
+      if (PARTNER != kLane && e >= a.rot) break;  // kLane: a lane is turned whole or not
+      const bool up = PARTNER == kLane ? upper : e >= pairs;
+      const float2 w = c[PARTNER != kAnyLane ? i : (up ? e - pairs : e)];
+      cosv[i] = w.x;
+      sinv[i] = PARTNER == kNext || up ? w.y : -w.y;
     }
   }
-  const int hops = pairs / 8;  // half: the partner's distance in lanes
+  const int hops = pairs / 8;  // kLane: the partner's distance in lanes
   const int partner = (threadIdx.x & 63) + (upper ? -hops : hops);
   for (int h0 = phase; h0 < all; h0 += phases * kRBatch) {
     if (h0 != phase) fetch(h0);
@@ -176,10 +201,11 @@ __global__ __launch_bounds__(kRThreads) void rotary_kernel(RotArgs a) {
           for (int i = 0; i < 8; ++i) v[i] = v[i] * scale * w[i];
         }
       }
-      if constexpr (INTERLEAVED) {
+      if constexpr (PARTNER == kNext) {
         if (turned) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
+            if (e0 + 2 * i >= a.rot) break;
             const float x = v[2 * i], y = v[2 * i + 1];
             v[2 * i] = x * cosv[i] - y * sinv[i];
             v[2 * i + 1] = y * cosv[i] + x * sinv[i];
@@ -187,12 +213,27 @@ __global__ __launch_bounds__(kRThreads) void rotary_kernel(RotArgs a) {
         }
       } else {
         float o[8];
+        if constexpr (PARTNER == kLane) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = __shfl(v[i], partner);
+          for (int i = 0; i < 8; ++i) o[i] = __shfl(v[i], partner);
+        } else {
+          float* head = xs + grp * G * 8;
+          wave_sync();  // the head before has been read
+          if (turned) {
+            *(f32x4_t*)(head + e0) = f32x4_t{v[0], v[1], v[2], v[3]};
+            *(f32x4_t*)(head + e0 + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+          }
+          wave_sync();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = e0 + i;
+            if (e < a.rot) o[i] = head[e < pairs ? e + pairs : e - pairs];
+          }
+        }
         if (turned) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            v[i] = upper ? v[i] * cosv[i] + o[i] * sinv[i] : v[i] * cosv[i] - o[i] * sinv[i];
+            if (PARTNER == kLane || e0 + i < a.rot) v[i] = v[i] * cosv[i] + o[i] * sinv[i];
         }
       }
       if (mine)
@@ -201,7 +242,7 @@ __global__ __launch_bounds__(kRThreads) void rotary_kernel(RotArgs a) {
   }
 }
 
-// Any head size, pitch and alignment: a workgroup per token, a wave per head at a
+// Heads of any size: a workgroup per token, a wave per head at a
 // time, one pair per lane and step.
 template <class T>
 __global__ __launch_bounds__(kRThreads) void rotary_any_kernel(RotArgs a) {
@@ -253,24 +294,18 @@ hipError_t launch_group(RotArgs a, hipStream_t s) {
     const int64_t left = cdiv(a.n - a.from, a.tokens);
     const dim3 grid((unsigned)(left < kMaxGroups ? left : kMaxGroups));
     if (a.interleaved)
-      hipLaunchKernelGGL((rotary_kernel<T, G, true>), grid, dim3(kRThreads), 0, s, a);
+      hipLaunchKernelGGL((rotary_kernel<T, G, kNext>), grid, dim3(kRThreads), 0, s, a);
+    else if (a.rot % 16 == 0)
+      hipLaunchKernelGGL((rotary_kernel<T, G, kLane>), grid, dim3(kRThreads), 0, s, a);
     else
-      hipLaunchKernelGGL((rotary_kernel<T, G, false>), grid, dim3(kRThreads), 0, s, a);
+      hipLaunchKernelGGL((rotary_kernel<T, G, kAnyLane>), grid, dim3(kRThreads), 0, s, a);
   }
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_typed(RotArgs a, hipStream_t s) {
-  // 16-byte accesses need whole chunks of 8 elements on either side of a pair
-  const int64_t el = 16 / sizeof(T);
-  bool vec = a.d % 8 == 0 && a.rot % 8 == 0 && (a.interleaved || a.rot % 16 == 0);
-  for (const RotSide& sd : a.side) {
-    if (!sd.heads) continue;
-    vec = vec && sd.xt % el == 0 && sd.xh % el == 0 && sd.yt % el == 0 && sd.yh % el == 0 &&
-          (((uintptr_t)sd.x | (uintptr_t)sd.y | (uintptr_t)sd.w) & 15) == 0;
-  }
-  if (!vec) {
+  if (a.d % 8) {
     for (; a.from < a.n; a.from += kMaxGroups) {
       const int64_t left = a.n - a.from;
       hipLaunchKernelGGL((rotary_any_kernel<T>),

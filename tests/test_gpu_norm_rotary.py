@@ -225,3 +225,35 @@ def test_rotary_more_tokens_than_a_launch_takes(d, n):
         # the two products by three roundings, the output by half a step
         assert ((got[:, :2] - want).abs() <= 2.0 ** -8 * want.abs() + 3 * 2.0 ** -20).all()
         assert torch.equal(got[:, 2:], torch.arange(3, d + 1, dtype=torch.float64).expand(4, -1))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("n,hq,hk,d,rot,normed", [
+    (7, 9, 2, 88, 88, True), (5, 3, 1, 32, 28, True), (33, 2, 2, 64, 62, False),
+    (4, 2, 1, 40, 40, False), (12, 3, 1, 256, 250, True), (300, 1, 1, 8, 6, True),
+    (9, 5, 5, 104, 2, False), (3, 65, 3, 128, 126, True), (40, 4, 2, 136, 136, False)])
+def test_rotary_pairs_and_rows_of_any_alignment(n, hq, hk, d, rot, normed, layout, dtype):
+    print(f"[case] rotary n={n} hq={hq} hk={hk} d={d} rot={rot} {layout} {dtype}", flush=True)
+    h = hq + hk
+    x = _randn((n, h * d + 3), n + d, dtype)  # odd token pitch, first element at 1
+    heads = lambda t: t[:, 1:1 + h * d].unflatten(1, (h, d))
+    dev = x.to(DEV)
+    q, k = heads(dev)[:, :hq], heads(dev)[:, hq:]
+    out = torch.full((n, h * d + 5), 7.0, dtype=dtype, device=DEV)
+    at = out[:, 3:3 + h * d].unflatten(1, (h, d))
+    pos = torch.randint(0, 100000, (n,), generator=torch.Generator().manual_seed(n),
+                        dtype=torch.int32)
+    freqs = L.rotary_freqs(rot, base=500000.0)
+    w = _randn((d,), 8, dtype) if normed else None
+    dw = None if w is None else w.to(DEV)
+    L.rotary(q, k, freqs.to(DEV), positions=pos.to(DEV), layout=layout, amplitude=0.75, q_norm=dw,
+             k_norm=dw, eps=1e-6, q_out=at[:, :hq], k_out=at[:, hq:])
+    _rot_check(at[:, :hq], heads(x)[:, :hq], pos.numpy(), freqs.numpy(), layout, 0.75, w, 1e-6)
+    _rot_check(at[:, hq:], heads(x)[:, hq:], pos.numpy(), freqs.numpy(), layout, 0.75, w, 1e-6)
+    assert bool((out[:, :3] == 7).all()) and bool((out[:, 3 + h * d:] == 7).all())
+    same = dev.clone()  # in place
+    L.rotary(heads(same)[:, :hq], heads(same)[:, hq:], freqs.to(DEV), positions=pos.to(DEV),
+             layout=layout, amplitude=0.75, q_norm=dw, k_norm=dw, eps=1e-6,
+             q_out=heads(same)[:, :hq], k_out=heads(same)[:, hq:])
+    assert torch.equal(heads(same), at)
