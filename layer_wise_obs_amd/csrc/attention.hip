@@ -475,7 +475,10 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
     }
   };
   pass(std::integral_constant<bool, false>{});
-  if (__syncthreads_or((bad & 0x80008000u) != 0)) pass(std::integral_constant<bool, true>{});
+  if (__syncthreads_or((bad & 0x80008000u) != 0)) {
+    pass(std::integral_constant<bool, true>{});
+    __syncthreads();  // a wave that is done puts its rows over tiles that others still read
+  }
 
 #pragma unroll
   for (int rb = 0; rb < 2; ++rb) {
@@ -500,8 +503,8 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
     }
     return;
   }
-  // Through LDS (free after the last barrier), so that a store instruction writes whole
-  // rows: 4 elements per lane of 32 rows each took 4.5 us per round of workgroups.
+  // Through LDS (free: every pass ends at a barrier), so that a store instruction writes
+  // whole rows: 4 elements per lane of 32 rows each took 4.5 us per round of workgroups.
   constexpr int kOutB = kRowB + 16;  // row pitch: rows 4 banks apart
   static_assert(NW * 32 * kOutB <= 2 * ST * kTile, "rows fit the tiles");
   unsigned char* ob = sm + wave * 32 * kOutB;

@@ -256,3 +256,24 @@ def test_attention_offsets_past_32_bits():
     K.copy_(k.to(DEV))
     V.copy_(v.to(DEV))
     _check(L.attention(q.to(DEV), K, V), q, k, v, [0, 5], [0, n])
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("n", [168, 300, 450])
+def test_attention_second_pass_with_waves_that_end_early(n, d, causal, value):
+    """The last value row is not finite, so the row blocks that meet it (hidden, or behind the
+    sequence's end) take a second pass. In the last block some waves have no rows, or none that
+    see the last tile (of an odd number, so that it lies in the first buffer): they write their
+    rows while the others may still be at it, and none of those may notice."""
+    print(f"[case] attention second pass n={n} d={d} causal={causal} {value}", flush=True)
+    Q, K, V = _randn((n, 2, d), 40), _randn((n, 2, d), 41), _randn((n, 2, d), 42)
+    V[n - 1] = value
+    V[n - 1, :, 8:] = 1.0  # the other channels stay finite in every row
+    dev = [t.to(DEV) for t in (Q, K, V)]
+    first = L.attention(*dev, causal=causal)
+    _check(first, Q, K, V, [0, n], [0, n], causal)
+    assert torch.all(first[:, :, 8:].isfinite())
+    for _ in range(4):
+        assert torch.equal(L.attention(*dev, causal=causal).nan_to_num(9.0), first.nan_to_num(9.0))
