@@ -44,7 +44,10 @@ namespace th {
 // g0 for the even loads and g1 for the odd ones. Load m = 2k + o takes vo[k]
 // from g_o and writes the 1 KB chunk at lds + 4096 m. No result registers;
 // completion is tracked by the callers' vmcnt waits. The s_add_u32 that step M0
-// write SCC, which the clobber list declares.
+// write SCC, which the clobber list declares. A vector instruction's write of an SGPR
+// (the compiler's readfirstlane of a base) and a load that reads it need five wait
+// states between them; the compiler does not see the loads, so the block begins with
+// five of its own (two moves and s_nop 2).
 __device__ __forceinline__ uint64_t uniform_u64(uint64_t x) {
   // readfirstlane returns int: go through unsigned so the low half is not sign-extended
   return ((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((unsigned)(x >> 32)) << 32) |
@@ -59,7 +62,7 @@ __device__ __forceinline__ void lds_dma10s(const unsigned (&vo)[5], const void* 
   unsigned saved;
   __asm__ volatile(
       "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %7\n\t"
+      "s_mov_b32 m0, %1\n\ts_nop 2\n\tglobal_load_lds_dwordx4 %2, %7\n\t"
       "s_add_u32 m0, %1, 4096\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %8\n\t"
       "s_add_u32 m0, %1, 8192\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %7\n\t"
       "s_add_u32 m0, %1, 12288\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %8\n\t"
@@ -83,15 +86,19 @@ __device__ __forceinline__ unsigned lds_address(const void* p) {
 // One load of 16 bytes per lane straight into LDS, in the saddr form: byte offset vo
 // (< 2^31) from the wave-uniform base g, into the 1 KB at LDS byte address lds
 // (wave-uniform). Lanes that are off write nothing, the others keep their places. No
-// result registers; completion is tracked by the callers' vmcnt waits.
+// result registers; completion is tracked by the callers' vmcnt waits. The load reads a
+// scalar copy of its base, which needs none of the wait states above and is the one that
+// M0 needs (linear layer of 131072 tokens 4096 -> 4096 in a graph: 3394 us, 3396 with the
+// waits, 3368 with neither; 8192 tokens 11008 -> 4096: 523, 527, 520).
 __device__ __forceinline__ void lds_dma1(unsigned vo, const void* g, unsigned lds) {
   const unsigned base = __builtin_amdgcn_readfirstlane(lds);
   const uint64_t gb = uniform_u64((uint64_t)(uintptr_t)g);
   unsigned saved;
+  uint64_t copy;
   __asm__ volatile(
-      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-      "global_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
-      : "=&s"(saved)
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_mov_b64 %1, %4\n\t"
+      "global_load_lds_dwordx4 %3, %1\n\ts_mov_b32 m0, %0"
+      : "=&s"(saved), "=&s"(copy)
       : "s"(base), "v"(vo), "s"(gb));
 }
 

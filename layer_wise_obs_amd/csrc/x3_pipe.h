@@ -78,7 +78,8 @@ __device__ __forceinline__ void dma12(const void* const (&g)[12], const void* ld
 
 // The same twelve loads with a wave-uniform global base (SGPR pair) and one
 // 32-bit byte offset per load and lane (saddr form): the offsets stay fixed for
-// a tile, and a stage only moves the base.
+// a tile, and a stage only moves the base. Five wait states before the first load: the
+// compiler may have written the base by a vector instruction (readfirstlane) just before.
 __device__ __forceinline__ void dma12s(const unsigned (&vo)[12], const void* gbase, const void* lds) {
   const unsigned base = __builtin_amdgcn_readfirstlane(
       (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
@@ -90,7 +91,7 @@ __device__ __forceinline__ void dma12s(const unsigned (&vo)[12], const void* gba
   unsigned saved;
   __asm__ volatile(
       "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %14\n\t"
+      "s_mov_b32 m0, %1\n\ts_nop 2\n\tglobal_load_lds_dwordx4 %2, %14\n\t"
       "s_add_u32 m0, %1, 4096\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %14\n\t"
       "s_add_u32 m0, %1, 8192\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %14\n\t"
       "s_add_u32 m0, %1, 12288\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %5, %14\n\t"
