@@ -826,7 +826,7 @@ th_status check_linear_sizes(int64_t n, int64_t b, int64_t c) {
     return fail(TH_ERR_INVALID_ARG, "needs n >= 0, c >= 1, b >= 8 and b % 8 == 0");
   if (b >= ((int64_t)1 << 22)) return fail(TH_ERR_INVALID_ARG, "b must be < 2^22");
   // a launch has less than 2^32 threads: at most 256 for 64 x 64 outputs, in ranges of a
-  // multiple of 8 workgroups; 512 for 16 outputs of few tokens
+  // multiple of 8 workgroups (few tokens take a launch per 2^26 channels)
   if (n >= ((int64_t)1 << 31) || c >= ((int64_t)1 << 27) ||
       cdiv(n, 64) * cdiv(c, 64) > ((int64_t)1 << 24) - 16)
     return fail(TH_ERR_INVALID_ARG, "n * c too large for one launch");

@@ -486,18 +486,18 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restric
 // memory into the operands of v_mfma_f32_16x16x32_bf16 (W as the first one: lane l
 // holds channel l % 16, k = 8 (l / 16) .. + 7), kSkSteps steps of 1 KB in flight per
 // wave, X comes from L2. The waves' sums meet in LDS and are added in the order of the
-// waves. 8.6 us for one token 4096 -> 4096 (3.9 TB/s, the launch included), 93 us for
+// waves. Workgroup x takes the channels from 16 (first + x). 8.6 us for one token 4096 -> 4096 (3.9 TB/s, the launch included), 93 us for
 // four 8192 -> 28672 (5.06 TB/s); nontemporal loads of W 9.5 and 111.
 constexpr int kSkWaves = 8;
 constexpr int kSkSteps = 8;
 
 __global__ __launch_bounds__(64 * kSkWaves) void linear_skinny_kernel(
     const unsigned short* __restrict__ X, int64_t ldx, const unsigned short* __restrict__ W, int n,
-    int64_t b, int64_t c, LinEpilogue ep) {
+    int64_t b, int64_t c, int64_t first, LinEpilogue ep) {
   __shared__ float red[kSkWaves][16][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r16 = lane & 15, kq = (lane >> 4) * 8;
-  const int64_t f0 = (int64_t)blockIdx.x * 16;
+  const int64_t f0 = (first + blockIdx.x) * 16;
   const int64_t fr = f0 + r16 < c ? f0 + r16 : c - 1;  // fills outputs that are not stored
   const unsigned short* wp = W + fr * b + kq;
   const unsigned short* xp = X + (r16 < n ? r16 : n - 1) * ldx + kq;
@@ -620,11 +620,16 @@ hipError_t launch_linear(const unsigned short* X, int64_t ldx, const unsigned sh
   float* raw = p.splits > 1 ? part : nullptr;
   hipError_t e;
   switch (p.tile) {
-    case kLinSkinny:
-      hipLaunchKernelGGL(linear_skinny_kernel, dim3((unsigned)cdiv(c, 16)), dim3(64 * kSkWaves), 0, s,
-                         X, ldx, W, (int)n, b, c, ep);
+    case kLinSkinny: {
+      // a launch has less than 2^32 threads, 512 to a workgroup
+      const int64_t groups = cdiv(c, 16), most = (int64_t)1 << 22;
+      for (int64_t first = 0; first < groups; first += most)
+        hipLaunchKernelGGL(linear_skinny_kernel,
+                           dim3((unsigned)(groups - first < most ? groups - first : most)),
+                           dim3(64 * kSkWaves), 0, s, X, ldx, W, (int)n, b, c, first, ep);
       e = hipGetLastError();
       break;
+    }
     case kLin64: e = launch_tiles<1, 1, 2, 4, 4>(X, ldx, W, n, b, c, p, raw, ep, s); break;
     case kLin128: e = launch_tiles<2, 1, 4, 4, 4>(X, ldx, W, n, b, c, p, raw, ep, s); break;
     case kLin128x256: e = launch_tiles<2, 2, 4, 3, 3>(X, ldx, W, n, b, c, p, raw, ep, s); break;

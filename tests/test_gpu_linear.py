@@ -168,3 +168,21 @@ def test_linear_rows_of_any_alignment(n, b, c, ydt, at):
              Y=Y)
     _check(Y, X, W, bias, "silu", R)
     assert bool((buf[:, :at] == 7).all()) and bool((buf[:, at + c:] == 7).all())
+
+
+@pytest.mark.parametrize("n", [1, 12])
+def test_linear_most_channels_of_few_tokens(n):
+    """The widest accepted layer: a workgroup per 16 channels is 2^32 threads in all, more than
+    one launch takes. Small whole numbers, so every output is exact."""
+    print(f"[case] linear {n} x 8 -> 2^27 - 1", flush=True)
+    b, c = 8, (1 << 27) - 1
+    W = torch.empty(c, b, dtype=BF, device=DEV)
+    q = torch.arange(c, dtype=torch.int32, device=DEV)
+    for j in range(b):
+        W[:, j] = (q + j) % 5
+    X = torch.zeros(n, b, dtype=BF, device=DEV)
+    X[:, 0], X[:, 1], X[:, 7] = 1, 2, torch.arange(n, device=DEV) % 3
+    Y = torch.full((n, c), 99.0, dtype=BF, device=DEV)
+    L.linear(X, W, Y=Y)
+    for t in range(n):
+        assert torch.equal(Y[t], (q % 5 + 2 * ((q + 1) % 5) + (t % 3) * ((q + 7) % 5)).to(BF))
