@@ -962,6 +962,10 @@ AttnPlan plan_of(const th_attention_params* p) {
   return r;
 }
 
+// The pieces' (m, l) of `rows` rows, then their O, which is read and written 16 bytes at a
+// time: an odd number of pairs is followed by 8 bytes of nothing.
+size_t part_ml_bytes(int64_t rows) { return ((size_t)rows * sizeof(float2) + 15) & ~(size_t)15; }
+
 }  // namespace
 
 int64_t attention_workgroups(const th_attention_params* p) {
@@ -973,7 +977,8 @@ size_t attention_workspace_bytes(const th_attention_params* p) {
   if (p->nq == 0) return 0;
   const int s = plan_of(p).splits;
   if (s == 1) return 0;
-  return (size_t)s * p->nq * p->hq * ((size_t)p->d * sizeof(float) + sizeof(float2));
+  const int64_t rows = s * p->nq * p->hq;
+  return part_ml_bytes(rows) + (size_t)rows * p->d * sizeof(float);
 }
 
 hipError_t launch_attention(const void* Q, const void* K, const void* V, const int32_t* q_start,
@@ -1005,7 +1010,9 @@ hipError_t launch_attention(const void* Q, const void* K, const void* V, const i
   const AttnPlan plan = plan_of(p);
   a.splits = workspace ? plan.splits : 1;
   a.part_ml = (float2*)workspace;
-  a.part_o = workspace ? (float*)(a.part_ml + (size_t)a.splits * p->nq * p->hq) : nullptr;
+  a.part_o = workspace
+                 ? (float*)((char*)workspace + part_ml_bytes(a.splits * p->nq * p->hq))
+                 : nullptr;
   if (plan.few) {
     if (p->d < 64)
       launch_few<64, 64, true>(a, s);

@@ -223,3 +223,14 @@ def test_binding_refuses_cpu_tensors():
         L.rms_norm(x, w)
     with pytest.raises(ValueError):
         L.rotary(torch.zeros(2, 1, 8), None, torch.zeros(4, dtype=torch.float64))
+
+
+@pytest.mark.parametrize("nq,hq,hk,nk", [(1, 1, 1, 1000), (1, 3, 3, 1000), (5, 1, 1, 3000), (2, 8, 2, 9000)])
+def test_attention_partial_rows_are_16_byte_aligned(nq, hq, hk, nk):
+    """The pieces' (maximum, sum) pairs are followed by their rows of d floats, moved 16 bytes at
+    a time: where the pairs are odd in number, their block is rounded up."""
+    d = 64
+    need = L.attention_workspace_size(_attention_params(nq=nq, nk=nk, hq=hq, hk=hk, nseq=1, o_token=hq * d))
+    pieces = need // (nq * hq * (d * 4 + 8))
+    assert pieces > 1 and need % 16 == 0
+    assert need == -(-pieces * nq * hq * 8 // 16) * 16 + pieces * nq * hq * d * 4

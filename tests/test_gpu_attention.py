@@ -277,3 +277,10 @@ def test_attention_second_pass_with_waves_that_end_early(n, d, causal, value):
     assert torch.all(first[:, :, 8:].isfinite())
     for _ in range(4):
         assert torch.equal(L.attention(*dev, causal=causal).nan_to_num(9.0), first.nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("nq,h,nk", [(1, 1, 1000), (1, 3, 1100), (3, 5, 3000), (101, 1, 2000)])
+def test_attention_odd_numbers_of_partial_rows(nq, h, nk):
+    print(f"[case] attention odd partial rows nq={nq} h={h} nk={nk}", flush=True)
+    Q, K, V = _randn((nq, h, 128), 50), _randn((nk, h, 128), 51), _randn((nk, h, 128), 52)
+    _check(L.attention(*(t.to(DEV) for t in (Q, K, V)), causal=False), Q, K, V, [0, nq], [0, nk], False)
