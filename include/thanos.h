@@ -327,7 +327,7 @@ typedef struct {
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
   int64_t nseq;
   int32_t causal;
-  double scale;       /* > 0, typically 1 / sqrt(d) */
+  double scale;       /* > 0, typically 1 / sqrt(d); scale log2(e) a normal fp32 number */
 } th_attention_params;
 
 /* dt must be TH_BF16; 8 <= d <= 128, d % 8 == 0; hk divides hq; strides are multiples

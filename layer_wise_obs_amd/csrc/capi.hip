@@ -15,6 +15,7 @@
 // recurrence, and the same update GEMM with U in place of the slices.
 // The budget, the threshold and every count stay on the device; the host
 // synchronises once, at the end, to read the status flags.
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -972,6 +973,11 @@ th_status th_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n
 }
 
 namespace {
+// Whether v is within the range of normal fp32 numbers.
+bool fp32_normal(double v) {
+  return std::fabs(v) >= (double)FLT_MIN && std::fabs(v) <= (double)FLT_MAX;
+}
+
 th_status check_attention(const th_attention_params* p) {
   const int64_t rows = ((int64_t)1 << 31) - ((int64_t)1 << 16);
   if (!p) return fail(TH_ERR_INVALID_ARG, "params is NULL");
@@ -996,8 +1002,10 @@ th_status check_attention(const th_attention_params* p) {
     return fail(TH_ERR_INVALID_ARG, "k_token and v_token must be < 2^24");
   if (heads_overlap(p->nq, p->hq, p->d, p->o_token, p->o_head))
     return fail(TH_ERR_INVALID_ARG, "the heads of O overlap");
-  if (!(p->scale > 0.0) || !std::isfinite(p->scale))
-    return fail(TH_ERR_INVALID_ARG, "scale must be finite and > 0");
+  // the kernels take scale log2(e) in fp32: 0 or infinite, it would make NaN of a score of
+  // -inf (every hidden key's) or 0
+  if (!(p->scale > 0.0) || !fp32_normal(p->scale * 1.4426950408889634))
+    return fail(TH_ERR_INVALID_ARG, "scale must be > 0 and scale * log2(e) a normal fp32 number");
   return TH_OK;
 }
 }  // namespace

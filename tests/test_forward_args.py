@@ -234,3 +234,17 @@ def test_attention_partial_rows_are_16_byte_aligned(nq, hq, hk, nk):
     pieces = need // (nq * hq * (d * 4 + 8))
     assert pieces > 1 and need % 16 == 0
     assert need == -(-pieces * nq * hq * 8 // 16) * 16 + pieces * nq * hq * d * 4
+
+
+@pytest.mark.parametrize("scale", [1e-300, 1e-46, 8e-39, 2.4e38, 1e300])
+def test_attention_refuses_scales_that_fp32_does_not_hold(scale):
+    """Times log2(e) they are 0, short of bits or infinite in fp32, where a hidden key's score
+    of -inf or a score of 0 would become NaN."""
+    assert _attention(scale=scale) == L.TH_ERR_INVALID_ARG
+    p, out = _attention_params(scale=scale), ctypes.c_size_t(0)
+    assert L.lib().th_attention_workspace_size(ctypes.byref(p), ctypes.byref(out)) == L.TH_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("scale", [8.2e-39, 1e-30, 1e30, 2.35e38])
+def test_attention_takes_scales_that_fp32_holds(scale):
+    assert L.attention_workspace_size(_attention_params(scale=scale)) == 0

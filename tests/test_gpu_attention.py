@@ -284,3 +284,12 @@ def test_attention_odd_numbers_of_partial_rows(nq, h, nk):
     print(f"[case] attention odd partial rows nq={nq} h={h} nk={nk}", flush=True)
     Q, K, V = _randn((nq, h, 128), 50), _randn((nk, h, 128), 51), _randn((nk, h, 128), 52)
     _check(L.attention(*(t.to(DEV) for t in (Q, K, V)), causal=False), Q, K, V, [0, nq], [0, nk], False)
+
+
+@pytest.mark.parametrize("lens", [[(70, 70), (3, 1)], [(1, 900), (2, 1)]])
+def test_attention_smallest_scale_weighs_all_visible_keys_alike(lens):
+    print(f"[case] attention smallest scale {lens}", flush=True)
+    qs, ks = _starts([a for a, _ in lens]), _starts([b for _, b in lens])
+    Q, K, V = _randn((qs[-1], 2, 64), 60), _randn((ks[-1], 1, 64), 61), _randn((ks[-1], 1, 64), 62)
+    got = L.attention(Q.to(DEV), K.to(DEV), V.to(DEV), _i32(qs), k_start=_i32(ks), scale=8.2e-39)
+    _check(got, Q, K, V, qs, ks, scale=8.2e-39)
