@@ -255,8 +255,9 @@ th_status th_linear(const void* X, int64_t ldx, const void* W, th_dtype dt, int6
  * layers"]: Y_tq = X_tq / sqrt(mean_q X_tq^2 + eps) * weight_q. X [n,b] (row pitch
  * ldx, dtype xdt), weight [b] in xdt, Y [n,b] (row pitch ldy, dtype ydt); sums and
  * products in fp32, Y rounded once. Y may be X (same dtype and pitch); otherwise
- * they must not overlap. n = 0 is allowed; n < 2^31, eps >= 0. Any width, row pitch
- * and alignment of whole elements. Asynchronous on the stream. */
+ * they must not overlap. n = 0 is allowed; n < 2^31; eps 0 or a positive normal
+ * fp32 number. A row whose sum of squares passes fp32's range gives zeros. Any width,
+ * row pitch and alignment of whole elements. Asynchronous on the stream. */
 th_status th_rms_norm(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t ldx,
                       const void* weight, double eps, void* Y, th_dtype ydt, int64_t ldy,
                       th_stream_t stream);
@@ -276,7 +277,8 @@ typedef struct {
 typedef enum { TH_ROTARY_HALF = 0, TH_ROTARY_INTERLEAVED = 1 } th_rotary_layout;
 
 /* q and k (host structs; k may be NULL): heads of d elements, 1 <= d <= 256, dtype
- * dt. A head with a norm becomes x / sqrt(mean x^2 + eps) * norm first. Then the
+ * dt. A head with a norm becomes x / sqrt(mean x^2 + eps) * norm first (eps as in
+ * th_rms_norm, norms alike in fp32). Then the
  * pairs of its first rot elements (even, 0 <= rot <= d), (x_i, x_{i+rot/2}) for
  * TH_ROTARY_HALF or (x_2i, x_2i+1) for TH_ROTARY_INTERLEAVED, i < rot/2, turn by
  * the angle positions[t] * freqs[i]: (a, b) -> amplitude (a cos - b sin,

@@ -822,6 +822,14 @@ th_status th_gated_ffn_input(const void* X, const void* W_gate, const void* W_up
 // ------------------------------------------------- the block's other forward steps
 
 namespace {
+// Whether v is within the range of normal fp32 numbers.
+bool fp32_normal(double v) {
+  return std::fabs(v) >= (double)FLT_MIN && std::fabs(v) <= (double)FLT_MAX;
+}
+// The norms add eps in fp32, where a smaller one is 0 (a row of zeros would become NaN) or
+// short of bits, a larger one infinite.
+bool eps_ok(double eps) { return eps == 0.0 || (eps > 0.0 && fp32_normal(eps)); }
+
 th_status check_linear_sizes(int64_t n, int64_t b, int64_t c) {
   if (n < 0 || c < 1 || b < 8 || b % 8)
     return fail(TH_ERR_INVALID_ARG, "needs n >= 0, c >= 1, b >= 8 and b % 8 == 0");
@@ -882,8 +890,7 @@ th_status th_rms_norm(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t
   if (n < 0 || n >= ((int64_t)1 << 31) || b < 1)
     return fail(TH_ERR_INVALID_ARG, "needs 0 <= n < 2^31 and b >= 1");
   if (ldx < b || ldy < b) return fail(TH_ERR_INVALID_ARG, "a row pitch is smaller than b");
-  if (!(eps >= 0.0) || !std::isfinite(eps))
-    return fail(TH_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!eps_ok(eps)) return fail(TH_ERR_INVALID_ARG, "eps must be 0 or a normal fp32 number > 0");
   if (!weight || (n > 0 && (!X || !Y))) return fail(TH_ERR_INVALID_ARG, "NULL argument");
   if (X && X == Y && (xdt != ydt || ldx != ldy))
     return fail(TH_ERR_INVALID_ARG, "in place needs one dtype and pitch");
@@ -956,8 +963,8 @@ th_status th_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n
   if (layout != TH_ROTARY_HALF && layout != TH_ROTARY_INTERLEAVED)
     return fail(TH_ERR_INVALID_ARG, "unknown layout");
   if (rot > 0 && !freqs) return fail(TH_ERR_INVALID_ARG, "freqs is NULL");
-  if (!std::isfinite(amplitude) || !(eps >= 0.0) || !std::isfinite(eps))
-    return fail(TH_ERR_INVALID_ARG, "amplitude must be finite, eps finite and >= 0");
+  if (!std::isfinite(amplitude)) return fail(TH_ERR_INVALID_ARG, "amplitude must be finite");
+  if (!eps_ok(eps)) return fail(TH_ERR_INVALID_ARG, "eps must be 0 or a normal fp32 number > 0");
   bool work = false;
   th_status st = check_heads(q, n, d, &work);
   if (st == TH_OK && k) st = check_heads(k, n, d, &work);
@@ -973,11 +980,6 @@ th_status th_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n
 }
 
 namespace {
-// Whether v is within the range of normal fp32 numbers.
-bool fp32_normal(double v) {
-  return std::fabs(v) >= (double)FLT_MIN && std::fabs(v) <= (double)FLT_MAX;
-}
-
 th_status check_attention(const th_attention_params* p) {
   const int64_t rows = ((int64_t)1 << 31) - ((int64_t)1 << 16);
   if (!p) return fail(TH_ERR_INVALID_ARG, "params is NULL");

@@ -248,3 +248,16 @@ def test_attention_refuses_scales_that_fp32_does_not_hold(scale):
 @pytest.mark.parametrize("scale", [8.2e-39, 1e-30, 1e30, 2.35e38])
 def test_attention_takes_scales_that_fp32_holds(scale):
     assert L.attention_workspace_size(_attention_params(scale=scale)) == 0
+
+
+@pytest.mark.parametrize("eps", [1e-300, 1e-46, 1.1e-38, 3.5e38, 1e300])
+def test_norms_refuse_eps_that_fp32_does_not_hold(eps):
+    """Added in fp32 it would be 0 (a row of zeros: 0 / 0), short of bits or infinite."""
+    assert L.lib().th_rms_norm(*_norm_args(eps=eps)) == L.TH_ERR_INVALID_ARG
+    assert L.lib().th_rotary(*_rotary_args(eps=eps)) == L.TH_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("eps", [0.0, 1.2e-38, 3.4e38])
+def test_norms_take_eps_that_fp32_holds(eps):
+    assert L.lib().th_rms_norm(*_norm_args(eps=eps, n=0)) == L.TH_OK
+    assert L.lib().th_rotary(*_rotary_args(eps=eps, n=0)) == L.TH_OK

@@ -257,3 +257,12 @@ def test_rotary_pairs_and_rows_of_any_alignment(n, hq, hk, d, rot, normed, layou
              layout=layout, amplitude=0.75, q_norm=dw, k_norm=dw, eps=1e-6,
              q_out=heads(same)[:, :hq], k_out=heads(same)[:, hq:])
     assert torch.equal(heads(same), at)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norms_of_zeros_at_the_smallest_eps(dtype):
+    print(f"[case] norms of zeros, smallest eps {dtype}", flush=True)
+    x, w = torch.zeros(3, 2, 64, dtype=dtype, device=DEV), torch.ones(64, dtype=dtype, device=DEV)
+    assert torch.all(L.rms_norm(x[:, 0], w, eps=1.2e-38) == 0)
+    y, _ = L.rotary(x, None, L.rotary_freqs(64, device=DEV), q_norm=w, eps=1.2e-38)
+    assert torch.all(y == 0)
