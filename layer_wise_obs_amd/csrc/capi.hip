@@ -963,7 +963,8 @@ th_status th_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n
   if (layout != TH_ROTARY_HALF && layout != TH_ROTARY_INTERLEAVED)
     return fail(TH_ERR_INVALID_ARG, "unknown layout");
   if (rot > 0 && !freqs) return fail(TH_ERR_INVALID_ARG, "freqs is NULL");
-  if (!std::isfinite(amplitude)) return fail(TH_ERR_INVALID_ARG, "amplitude must be finite");
+  if (amplitude != 0.0 && !fp32_normal(amplitude))  // infinite, it would make NaN of a 0
+    return fail(TH_ERR_INVALID_ARG, "amplitude must be 0 or a normal fp32 number");
   if (!eps_ok(eps)) return fail(TH_ERR_INVALID_ARG, "eps must be 0 or a normal fp32 number > 0");
   bool work = false;
   th_status st = check_heads(q, n, d, &work);

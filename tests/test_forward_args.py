@@ -261,3 +261,11 @@ def test_norms_refuse_eps_that_fp32_does_not_hold(eps):
 def test_norms_take_eps_that_fp32_holds(eps):
     assert L.lib().th_rms_norm(*_norm_args(eps=eps, n=0)) == L.TH_OK
     assert L.lib().th_rotary(*_rotary_args(eps=eps, n=0)) == L.TH_OK
+
+
+@pytest.mark.parametrize("amp,ok", [(1e39, False), (-1e300, False), (1e-39, False), (INF, False),
+                                    (0.0, True), (-3.4e38, True), (1.2e-38, True)])
+def test_rotary_amplitude_is_one_that_fp32_holds(amp, ok):
+    """Infinite in fp32, it would make NaN of an element of 0."""
+    got = L.lib().th_rotary(*_rotary_args(amp=amp, n=0))
+    assert got == (L.TH_OK if ok else L.TH_ERR_INVALID_ARG)
