@@ -284,9 +284,10 @@ typedef enum { TH_ROTARY_HALF = 0, TH_ROTARY_INTERLEAVED = 1 } th_rotary_layout;
  * the angle positions[t] * freqs[i]: (a, b) -> amplitude (a cos - b sin,
  * b cos + a sin). The elements past rot keep their (normed) value. positions [n]
  * int32 (device; any order and sign), or NULL for 0 .. n-1; freqs [rot/2] double
- * (device), see th_rotary_freqs. Angles are reduced in fp64, the rest is fp32,
- * outputs rounded once. amplitude: 0 or a normal fp32 number. Neither side's y may
- * overlap the other side's x or y. n = 0 is allowed; n * heads < 2^31. Asynchronous. */
+ * (device), see th_rotary_freqs. Angles, their sines and cosines are fp64,
+ * rounded once; the rest is fp32, outputs rounded once. amplitude: 0 or a normal
+ * fp32 number. Neither side's y may overlap the other side's x or y. n = 0 is
+ * allowed; n * heads < 2^31. Asynchronous. */
 th_status th_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n, int64_t d,
                     int64_t rot, th_rotary_layout layout, const int32_t* positions,
                     const double* freqs, double amplitude, double eps, th_stream_t stream);

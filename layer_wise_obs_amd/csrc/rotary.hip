@@ -9,9 +9,9 @@
 //
 // Bound by memory: one read and one write of the heads. p f_i is formed and
 // reduced to turns in fp64 (p f_i reaches 10^6 radians, where fp32 is off by 0.06),
-// then sine and cosine are fp32. They depend on the token and the pair only, so a
-// workgroup computes them once per token into LDS for all its heads of q and k, while
-// its first heads are on their way.
+// and its sine and cosine are rounded to fp32 once. They depend on the token and the
+// pair only, so a workgroup computes them once per token into LDS for all its heads of
+// q and k, while its first heads are on their way.
 // A head is held by a group of lanes with 8 consecutive elements each (16 bytes of
 // bf16); a half-layout partner sits in another lane of the group, at the same place where
 // rot / 2 is a multiple of 8, and is fetched through LDS where it is not.
@@ -44,13 +44,15 @@ struct RotArgs {
   float amplitude, eps, inv_d;
 };
 
-// (cos, sin) of position p at frequency f, in fp32 from an angle reduced in fp64.
+// (cos, sin) of position p at frequency f times the amplitude, formed in fp64 and rounded
+// once. (In fp32 from an angle rounded to fp32, a sine or cosine is off by up to 2^-23.4
+// however small it is: fp32 heads come out a tenth less exact, 5001 tokens of 28 heads of
+// 96 take 20.95 us instead of 21.07.)
 __device__ __forceinline__ float2 turn_of(double p, double f, float amplitude) {
-  double t = p * f * 0.15915494309189533577;  // turns
-  t -= rint(t);
-  float s, c;
-  sincospif((float)(2.0 * t), &s, &c);
-  return make_float2(c * amplitude, s * amplitude);
+  const double t = p * f * 0.15915494309189533577;  // turns
+  double s, c;
+  sincospi(2.0 * (t - rint(t)), &s, &c);
+  return make_float2((float)(c * amplitude), (float)(s * amplitude));
 }
 
 // Eight elements as they are in memory, and as floats; aligned like an element only, which

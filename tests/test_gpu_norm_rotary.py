@@ -266,3 +266,29 @@ def test_norms_of_zeros_at_the_smallest_eps(dtype):
     assert torch.all(L.rms_norm(x[:, 0], w, eps=1.2e-38) == 0)
     y, _ = L.rotary(x, None, L.rotary_freqs(64, device=DEV), q_norm=w, eps=1.2e-38)
     assert torch.all(y == 0)
+
+
+@pytest.mark.parametrize("d", [16, 10])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_small_sines_and_cosines_keep_their_bits(d, layout):
+    """Pairs of (1, 0) become (cos, sin) themselves: each is formed in fp64 (good to a few units
+    there) from an angle that is off by 3 roundings of itself, and rounded once."""
+    print(f"[case] rotary sines and cosines d={d} {layout}", flush=True)
+    n, pairs = 5000, d // 2
+    x = torch.zeros(n, 1, d, dtype=F32)
+    first = slice(0, pairs) if layout == "half" else slice(0, d, 2)
+    second = slice(pairs, d) if layout == "half" else slice(1, d, 2)
+    x[:, :, first] = 1.0
+    pos = torch.randint(-100000, 100000, (n,), generator=torch.Generator().manual_seed(3),
+                        dtype=torch.int32)
+    freqs = torch.tensor(([1.0, 0.37, np.pi / 64, 1e-4, 2.0, 1e-6, 0.05, 1.5])[:pairs],
+                         dtype=torch.float64)
+    y, _ = L.rotary(x.to(DEV), None, freqs.to(DEV), positions=pos.to(DEV), layout=layout)
+    angle = pos.numpy().astype(np.longdouble)[:, None] * freqs.numpy().astype(np.longdouble)
+    got = y[:, 0].double().cpu().numpy()
+    far = 3 * 2.0 ** -53 * np.abs(angle).astype(np.float64) + 2.0 ** -50
+    for part, ref in ((first, np.cos(angle)), (second, np.sin(angle))):
+        ref = ref.astype(np.float64)
+        tol = U * np.abs(ref) + 1.01 * far
+        err = np.abs(got[:, part] - ref)
+        assert np.all(err <= tol), np.max(err / tol)
