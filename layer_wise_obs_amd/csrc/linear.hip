@@ -46,11 +46,33 @@ struct LinEpilogue {
   int y_f32;     // Y and residual are fp32 (else bf16)
 };
 
+// z Phi(z), Phi(-|z|) = erfc(|z| / sqrt 2) / 2 = e^(-z^2/2) t Q(t), t = 1 / (1 + |z| / 2), Q
+// of degree 10 fitted here to erfcx by weighted least squares (2.2e-8 of itself at most, for
+// |z| <= 13.8, past which the result is below fp32's range). Every |z| keeps its relative
+// accuracy, (16 + 1.5 z^2) 2^-24 counted in roundings; 1 + erff(z / sqrt 2) has none left
+// at z = -5. (16384 tokens 4096 -> 4096: 435 us, with erff 446, with erfcf 471.)
+__device__ __forceinline__ float gelu(float z) {
+  const float a = fabsf(z), t = __builtin_amdgcn_rcpf(fmaf(a, 0.5f, 1.0f));
+  float q = -0.0370472595f;
+  q = fmaf(q, t, 0.175881296f);
+  q = fmaf(q, t, -0.28242594f);
+  q = fmaf(q, t, 0.0463377908f);
+  q = fmaf(q, t, 0.393810064f);
+  q = fmaf(q, t, -0.43306008f);
+  q = fmaf(q, t, 0.0639118254f);
+  q = fmaf(q, t, 0.0201857612f);
+  q = fmaf(q, t, 0.153776303f);
+  q = fmaf(q, t, 0.19914858f);
+  q = fmaf(q, t, 0.199481636f);
+  const float h = q * t * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+  return z > 0.0f ? z * (1.0f - h) : z * h;
+}
+
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
     case TH_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
     case TH_ACT_SILU: return z / (1.0f + expf(-z));
-    case TH_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case TH_ACT_GELU: return gelu(z);
     default: return z;
   }
 }

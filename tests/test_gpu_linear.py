@@ -186,3 +186,35 @@ def test_linear_most_channels_of_few_tokens(n):
     L.linear(X, W, Y=Y)
     for t in range(n):
         assert torch.equal(Y[t], (q % 5 + 2 * ((q + 1) % 5) + (t % 3) * ((q + 7) % 5)).to(BF))
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_linear_gelu_keeps_its_bits_in_the_tails(n):
+    """Arguments that are exact in fp32 (one weight of 8 bits, another of 8 bits 2^-9 below it):
+    the result is off by at most (16 + 1.5 z^2) roundings of itself. Counted: the exponent's
+    product of three rounded factors, 3 U z^2 / 2; the hardware's exponential and reciprocal,
+    2 U each, the latter met up to 1.6 times with the 2 U of its argument and of itself; 4 U of
+    the polynomial and its fit; 4 U of the last products."""
+    print(f"[case] linear gelu tails n={n}", flush=True)
+    z = torch.linspace(-12.5, 12.5, 9001)
+    hi = z.to(BF)
+    W = torch.zeros(z.numel(), 8, dtype=BF)
+    W[:, 0], W[:, 3] = hi, ((z - hi.float())).to(BF)
+    X = torch.zeros(n, 8, dtype=BF)
+    X[:, 0] = X[:, 3] = 1.0
+    zz = W[:, 0].double().numpy() + W[:, 3].double().numpy()
+    assert np.array_equal(zz, zz.astype(np.float32))
+    ref = O.forward_linear(X[:1], W, None, "gelu")[0]
+    Y = L.linear(X.to(DEV), W.to(DEV), act="gelu", out_dtype=F32).cpu().double().numpy()
+    tol = (16 + 1.5 * zz * zz) * U * np.abs(ref)
+    assert np.all(np.abs(Y - ref) <= tol), np.max(np.abs(Y - ref) / tol)
+
+
+def test_linear_gelu_of_infinities_and_zero():
+    print("[case] linear gelu infinities", flush=True)
+    W = torch.zeros(4, 8, dtype=BF)
+    W[:, 0] = torch.tensor([float("inf"), 1e30, -1e30, 0.0])
+    X = torch.zeros(1, 8, dtype=BF)
+    X[0, 0] = 1.0
+    Y = L.linear(X.to(DEV), W.to(DEV), act="gelu", out_dtype=F32).cpu()[0]
+    assert Y[0] == float("inf") and Y[1] == W[1, 0].float() and Y[2] == 0 and Y[3] == 0
