@@ -336,11 +336,13 @@ typedef struct {
 /* dt must be TH_BF16; 8 <= d <= 128, d % 8 == 0; hk divides hq; strides are multiples
  * of 8 (k_token, v_token < 2^24) and Q, K, V, O 16-byte aligned; nq * hq / hk,
  * nk < 2^31 - 2^16; hk times the row blocks (of 32 rows where the sequences average
- * no more, else of 128), plus hk nseq, < 2^24. O must not overlap the inputs. Scores, maxima, sums and O accumulate in fp32; the weights
- * enter the second product rounded to bf16. workspace (optional, may be NULL with
- * workspace_bytes 0; 16-byte aligned) lets launches of few queries split the keys;
- * size from th_attention_workspace_size (0 where it does not help). The order of all
- * sums is fixed, so repeated calls give identical bits. Asynchronous. */
+ * no more, else of 128), plus hk nseq, < 2^24. O must not overlap the inputs. Scores,
+ * maxima, sums and O accumulate in fp32. The weights enter the second product rounded to
+ * bf16; where the sequences average no more than 32 rows (tokens times hq / hk), as a
+ * bf16 value and its rest. workspace (optional, may be NULL with workspace_bytes 0;
+ * 16-byte aligned) lets launches of few queries split the keys; size from
+ * th_attention_workspace_size (0 where it does not help). The order of all sums is
+ * fixed, so repeated calls give identical bits. Asynchronous. */
 th_status th_attention_workspace_size(const th_attention_params* p, size_t* bytes /* host */);
 th_status th_attention(const void* Q, const void* K, const void* V, th_dtype dt,
                        const int32_t* q_start, const int32_t* k_start,

@@ -9,8 +9,10 @@
 // rescaled by 2^(m_old - m_new) when m moves. m only has to be near the maximum:
 // it moves when a score passes it by more than 8 (p <= 2^8 then), so most tiles
 // need no rescaling. m, l and O are fp32; p is rounded to bf16 for the matrix cores
-// (off by at most 2^-8 of itself, like the output's own rounding; fp32 weights would
-// need three times the matrix work).
+// (off by at most 2^-8 of itself, like the output's own rounding: against 64 bits 2.0e-3
+// rms instead of 1.65e-3). Products of what that rounding leaves, 2^-16 of p, too would
+// take 673 -> 1079 us for 16 sequences of 2048 tokens, 32 heads of 128 (92 registers
+// spill), 90 -> 104 for 24 prompts, heads of 80. The kernel for few rows below has them.
 //
 // A workgroup takes 128 rows of one sequence and key head, a row being a (token,
 // query head of the group) pair, so K and V are read once for all g heads and
@@ -540,8 +542,11 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
 // own in LDS and no barrier in the loop; their (m, l, O) meet in LDS at the end. Bound
 // by reading K and V; against 128-row workgroups, whose other three waves had no rows,
 // a token over 300 keys of 32 heads went from 12.5 to 10.8 us. 16 tokens over 300001 keys,
-// 64 heads on 8: 252 us (4.9 TB/s) and 6 for the join. Products of 32x32x16 (their lanes
-// hold one query, so the softmax exchanges once); everything else is as above.
+// 64 heads on 8: 262 us (4.7 TB/s) and 6 for the join. Products of 32x32x16 (their lanes
+// hold one query, so the softmax exchanges once). The weights enter the second product as
+// a bf16 value and its rest, so 2^-16 of each is lost and not 2^-8 (error against 64 bits
+// 1.65e-3 rms, the output's own rounding, instead of 2.14e-3; 3% more time, as the matrix
+// cores are 6% busy). Everything else is as above.
 template <int D, int DC, bool PAD>
 __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
   constexpr int kBM = 32, kKeys = 32, kWaves = 4;
@@ -699,17 +704,22 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
       m = mn;
     }
     const float ref = m == -INFINITY ? 0.f : -m;
-    bf16x8_t pf[2];
+    bf16x8_t pf[2], pr[2];  // the weights and what their rounding left
 #pragma unroll
-    for (int ks16 = 0; ks16 < 2; ++ks16)
+    for (int ks16 = 0; ks16 < 2; ++ks16) {
+      u32x4_t wf, wr;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int e = ks16 * 8 + 2 * x;
-        const bf16x2_t p = pack2(exp2_fast(fmaf(s[e], a.c, ref)), exp2_fast(fmaf(s[e + 1], a.c, ref)));
-        l = __builtin_amdgcn_fdot2_f32_bf16(p, bf16x2_t{(__bf16)1.0f, (__bf16)1.0f}, l, false);
-        pf[ks16][2 * x] = p[0];
-        pf[ks16][2 * x + 1] = p[1];
+        const float p0 = exp2_fast(fmaf(s[e], a.c, ref)), p1 = exp2_fast(fmaf(s[e + 1], a.c, ref));
+        l += p0 + p1;
+        wf[x] = __builtin_bit_cast(unsigned, pack2(p0, p1));
+        wr[x] = __builtin_bit_cast(unsigned, pack2(p0 - __uint_as_float(wf[x] << 16),
+                                                   p1 - __uint_as_float(wf[x] & 0xffff0000u)));
       }
+      pf[ks16] = __builtin_bit_cast(bf16x8_t, wf);
+      pr[ks16] = __builtin_bit_cast(bf16x8_t, wr);
+    }
     if constexpr (careful) {
       if (masked) {
 #pragma unroll
@@ -726,9 +736,11 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
               const f32x16_t zero = {};
               const f32x16_t z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                   __builtin_bit_cast(bf16x8_t, one), pf[ks16], zero, 0, 0, 0);
+              const f32x16_t y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  __builtin_bit_cast(bf16x8_t, one), pr[ks16], zero, 0, 0, 0);
               if (kt + 16 * ks16 + j < lim) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[db][e] += z[e];
+                for (int e = 0; e < 16; ++e) o[db][e] += z[e] + (isfinite(y[e]) ? y[e] : 0.f);
               }
             }
           }
@@ -739,8 +751,18 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
     for (int ks16 = 0; ks16 < 2; ++ks16)
 #pragma unroll
       for (int db = 0; db < kDB; ++db)
-        o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            __builtin_bit_cast(bf16x8_t, v_frag(ks16, db)), pf[ks16], o[db], 0, 0, 0);
+        {
+          const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, v_frag(ks16, db));
+          o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[ks16], o[db], 0, 0, 0);
+          if constexpr (careful) {
+            const f32x16_t zero = {};
+            const f32x16_t y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pr[ks16], zero, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[db][e] += isfinite(y[e]) ? y[e] : 0.f;
+          } else {
+            o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pr[ks16], o[db], 0, 0, 0);
+          }
+        }
   };
   auto pass = [&](auto CAREFUL) __attribute__((always_inline)) {
     m = -INFINITY;
@@ -769,7 +791,16 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
   };
   static_assert(kLd == 8 || kLd == 4, "vmcnt immediates");
   pass(std::integral_constant<bool, false>{});
-  if (__syncthreads_or((bad & 0x80008000u) != 0)) {
+  // An infinity that a row sees stays one times p, but is NaN times p's rest (0, or of the
+  // other sign): where anything is not finite, the second pass leaves such products of the
+  // rests out.
+  float zeros[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kDB; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) zeros[e & 3] = fmaf(o[i][e], 0.f, zeros[e & 3]);
+  const float zero = (zeros[0] + zeros[1]) + (zeros[2] + zeros[3]);
+  if (__syncthreads_or((bad & 0x80008000u) != 0 || zero != 0.f)) {
     pass(std::integral_constant<bool, true>{});
     __syncthreads();
   }

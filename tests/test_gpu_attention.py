@@ -293,3 +293,45 @@ def test_attention_smallest_scale_weighs_all_visible_keys_alike(lens):
     Q, K, V = _randn((qs[-1], 2, 64), 60), _randn((ks[-1], 1, 64), 61), _randn((ks[-1], 1, 64), 62)
     got = L.attention(Q.to(DEV), K.to(DEV), V.to(DEV), _i32(qs), k_start=_i32(ks), scale=8.2e-39)
     _check(got, Q, K, V, qs, ks, scale=8.2e-39)
+
+
+@pytest.mark.parametrize("nk", [5, 40, 700])
+@pytest.mark.parametrize("d", [64, 72, 128])
+def test_attention_single_tokens_weigh_in_more_than_16_bits(nk, d):
+    """Single tokens' weights enter the second product as a bf16 value and its rest, 2^-16 of
+    themselves at most being left (half a step of half a step). Values of +-1 that mostly
+    cancel, so that the output's own rounding hides nothing of it. Small scores: the same
+    bound of a weight's fp32 error as everywhere is then about 2^-13."""
+    print(f"[case] attention weights nk={nk} d={d}", flush=True)
+    nseq, h = 60, 4
+    qs, ks = list(range(nseq + 1)), [nk * i for i in range(nseq + 1)]
+    Q, K = _randn((nseq, h, d), 70, 0.5), _randn((nk * nseq, h, d), 71, 0.25)
+    V = torch.ones(nk * nseq, h, d, dtype=BF)
+    V[1::2] = -1.0
+    V[:, :, 1::2] *= -1.0
+    got = L.attention(Q.to(DEV), K.to(DEV), V.to(DEV), _i32(qs), k_start=_i32(ks)).double().cpu().numpy()
+    ref = O.attention(Q, K, V, qs, ks)
+    size = float(Q.float().norm(dim=2).max() * K.float().norm(dim=2).max()) * d ** -0.5
+    e = size * (2 * (d + 4) + 5) * U + (2 + nk / 2 + 70) * U
+    tol = 2.0 ** -16 + 2 * e + 2.0 ** -8 * np.abs(ref)  # sum p |v| / sum p is 1
+    assert e < 2.0 ** -13
+    assert np.all(np.abs(got - ref) <= tol), np.max(np.abs(got - ref) / tol)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("d", [64, 72, 128])
+@pytest.mark.parametrize("lens", [[(1, 100), (2, 31)], [(1, 6000), (3, 5000)]])
+def test_attention_single_tokens_over_values_that_are_not_finite(lens, d, value):
+    """A visible infinity stays one (times a weight, whose rest may be 0 or negative), in its
+    channel alone; hidden ones enter nowhere."""
+    print(f"[case] attention visible non-finite {lens} d={d} {value}", flush=True)
+    qs, ks = _starts([a for a, _ in lens]), _starts([b for _, b in lens])
+    Q, K, V = _randn((qs[-1], 4, d), 73), _randn((ks[-1], 2, d), 74), _randn((ks[-1], 2, d), 75)
+    V[10, 0, 3] = value           # seen by the first sequence
+    V[ks[-1] - 1, 1, 9] = value   # by the second one's last token only
+    got = L.attention(Q.to(DEV), K.to(DEV), V.to(DEV), _i32(qs), k_start=_i32(ks))
+    _check(got, Q, K, V, qs, ks)
+    fin = got.isfinite().cpu()
+    want = torch.ones_like(fin)
+    want[0, :2, 3] = want[-1, 2:, 9] = False
+    assert torch.equal(fin, want)
