@@ -342,7 +342,10 @@ typedef struct {
  * bf16 value and its rest. workspace (optional, may be NULL with workspace_bytes 0;
  * 16-byte aligned) lets launches of few queries split the keys; size from
  * th_attention_workspace_size (0 where it does not help). The order of all sums is
- * fixed, so repeated calls give identical bits. Asynchronous. */
+ * fixed, so repeated calls give identical bits. How the work is cut follows the average
+ * lengths, all that the host knows: sequences that differ by more than a factor of about
+ * ten, or a prompt among many single tokens, are faster in a call of their own.
+ * Asynchronous. */
 th_status th_attention_workspace_size(const th_attention_params* p, size_t* bytes /* host */);
 th_status th_attention(const void* Q, const void* K, const void* V, th_dtype dt,
                        const int32_t* q_start, const int32_t* k_start,

@@ -957,6 +957,11 @@ struct AttnPlan {
 // 64, 14.3 us and 19.4 in two; 1024, 32 of 128, 29 and 39; 2048, 8 of 128 on 2, 46 and 37;
 // 4096, 8 of 96 on 1, 77 and 62 in four; 300 over 20000 keys, 16 of 128 on 4, 383 and 81 in
 // six, 78 in twelve. Of 18 shapes, 16 were within 11% of the best of eight numbers.)
+// Batches that the averages misjudge take as long as their worst sequence, and are better
+// called in parts: one token over 100000 keys among 63 over 100, 64 heads on 8: 662 us, 95
+// and 17 in two calls; over 20000 among 63 over 2000: 207, 37 and 118; a prompt of 4000
+// tokens among 255 single ones over 1000 keys, 32 heads: 1228, 148 and 784 (on 8 key heads
+// 349, 144 and 213).
 AttnPlan plan_of(const th_attention_params* p) {
   const int64_t g = p->hq / p->hk;
   const int64_t seqs = p->nseq < p->nq ? p->nseq : p->nq;

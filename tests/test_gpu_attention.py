@@ -335,3 +335,34 @@ def test_attention_single_tokens_over_values_that_are_not_finite(lens, d, value)
     want = torch.ones_like(fin)
     want[0, :2, 3] = want[-1, 2:, 9] = False
     assert torch.equal(fin, want)
+
+
+@pytest.mark.parametrize("lens,hq,hk,d", [
+    ([(1, 700)] * 20 + [(400, 400)] + [(1, 90)] * 43, 2, 2, 64),  # averages below 32 rows
+    ([(1, 33)] * 9 + [(3, 9000)] + [(0, 50)] * 3, 8, 2, 128),     # pieces by a short average
+    ([(1, 100)] * 31 + [(1, 20000)] + [(1, 1)] * 32, 16, 2, 128),
+    ([(600, 700), (1, 1), (1, 5000)], 4, 1, 80)])                 # averages above
+def test_attention_sequences_far_from_their_average(lens, hq, hk, d):
+    """A prompt among single tokens, and lengths a factor of 200 apart: the kernel and the number
+    of pieces follow the average lengths, the results must not."""
+    print(f"[case] attention uneven {len(lens)} sequences hq={hq} hk={hk} d={d}", flush=True)
+    qs, ks = _starts([a for a, _ in lens]), _starts([b for _, b in lens])
+    Q, K, V = _randn((qs[-1], hq, d), 80, 2.0), _randn((ks[-1], hk, d), 81), _randn((ks[-1], hk, d), 82)
+    _check(L.attention(Q.to(DEV), K.to(DEV), V.to(DEV), _i32(qs), k_start=_i32(ks)), Q, K, V, qs, ks)
+
+
+def test_attention_calibration_size():
+    """16 sequences of 2048 tokens, 32 heads of 128: several rounds of workgroups. Sampled rows
+    against fp64, each alone: its query over the keys that it sees."""
+    print("[case] attention 16 x 2048, 32 heads of 128", flush=True)
+    n, seqs, h, d = 2048, 16, 32, 128
+    g = torch.Generator(device=DEV).manual_seed(90)
+    Q, K, V = (torch.randn(seqs * n, h, d, generator=g, device=DEV).to(BF) for _ in range(3))
+    got = L.attention(Q, K, V, _i32([n * i for i in range(seqs + 1)]))
+    for s, i in ((0, 0), (0, 63), (3, 1000), (7, 127), (7, 128), (11, 2047), (15, 1), (15, 2047)):
+        a = s * n
+        k, v = K[a:a + i + 1].cpu(), V[a:a + i + 1].cpu()
+        _check(got[a + i:a + i + 1], Q[a + i:a + i + 1].cpu(), k, v, [0, 1], [0, i + 1])
+    assert torch.all(got.isfinite())
+    again = L.attention(Q, K, V, _i32([n * i for i in range(seqs + 1)]))
+    assert torch.equal(got, again)

@@ -218,3 +218,12 @@ def test_linear_gelu_of_infinities_and_zero():
     X[0, 0] = 1.0
     Y = L.linear(X.to(DEV), W.to(DEV), act="gelu", out_dtype=F32).cpu()[0]
     assert Y[0] == float("inf") and Y[1] == W[1, 0].float() and Y[2] == 0 and Y[3] == 0
+
+
+@pytest.mark.parametrize("n,b,c", [(1, 8192, 1024), (12, 8192, 100), (13, 11008, 64), (1, 28672, 17),
+                                   (5, 11008, 512), (200, 28672, 40)])
+def test_linear_few_channels_of_a_long_contraction(n, b, c):
+    print(f"[case] linear n={n} b={b} c={c}", flush=True)
+    X, W = _randn((n, b), n), _randn((c, b), c, scale=b ** -0.5)
+    for ydt in (BF, F32):
+        _check(L.linear(X.to(DEV), W.to(DEV), out_dtype=ydt), X, W, None, "none", None)
