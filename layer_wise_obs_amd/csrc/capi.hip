@@ -971,6 +971,8 @@ th_status th_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n
   if (st == TH_OK && k) st = check_heads(k, n, d, &work);
   if (st != TH_OK) return st;
   if (!work) return TH_OK;
+  if (q->heads > 0 && k && k->heads > 0 && (q->y == k->x || q->y == k->y || k->y == q->x))
+    return fail(TH_ERR_INVALID_ARG, "y must not be the other side's x or y");
   const int64_t heads = q->heads + (k ? k->heads : 0);
   if (n >= (((int64_t)1 << 31) + heads - 1) / heads)
     return fail(TH_ERR_INVALID_ARG, "n * heads must be < 2^31");

@@ -269,3 +269,13 @@ def test_rotary_amplitude_is_one_that_fp32_holds(amp, ok):
     """Infinite in fp32, it would make NaN of an element of 0."""
     got = L.lib().th_rotary(*_rotary_args(amp=amp, n=0))
     assert got == (L.TH_OK if ok else L.TH_ERR_INVALID_ARG)
+
+
+@pytest.mark.parametrize("q,k", [
+    (dict(x=FAKE, y=FAKE), dict(x=FAKE, y=2 * FAKE)), (dict(x=FAKE, y=2 * FAKE), dict(x=FAKE, y=FAKE)),
+    (dict(x=FAKE, y=2 * FAKE), dict(x=3 * FAKE, y=2 * FAKE)),
+    (dict(x=FAKE, y=FAKE), dict(x=FAKE, y=FAKE))])
+def test_rotary_refuses_outputs_that_the_other_side_uses(q, k):
+    """One side would be written while the other is still read, in no fixed order."""
+    q, k = _heads(**q), _heads(**k, heads=2)
+    assert L.lib().th_rotary(*_rotary_args(q=q, k=k)) == L.TH_ERR_INVALID_ARG

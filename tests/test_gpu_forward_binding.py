@@ -83,3 +83,15 @@ def test_single_rows_of_any_stride():
     f = thanos.rotary_freqs(16, device="cuda")
     assert torch.equal(thanos.rotary(h, None, f)[0], thanos.rotary(x[:, None], None, f)[0])
     assert torch.equal(thanos.attention(h, h, h), x[:, None])
+
+
+def test_no_rows():
+    f = thanos.rotary_freqs(16, device="cuda")
+    assert thanos.linear(_t(0, 16), _t(8, 16), bias=_t(8), act="gelu").shape == (0, 8)
+    assert thanos.linear(_t(0, 16), _t(8, 16), residual=_t(0, 8)).shape == (0, 8)
+    assert thanos.rms_norm(_t(0, 16), _t(16), out_dtype=torch.float32).dtype == torch.float32
+    q, k = thanos.rotary(_t(0, 2, 16), _t(0, 1, 16), f, q_norm=_t(16))
+    assert q.shape == (0, 2, 16) and k.shape == (0, 1, 16)
+    starts = torch.zeros(4, dtype=torch.int32, device="cuda")  # three sequences, all empty
+    assert thanos.attention(_t(0, 2, 16), _t(0, 1, 16), _t(0, 1, 16), starts).shape == (0, 2, 16)
+    torch.cuda.synchronize()
