@@ -292,3 +292,19 @@ def test_rotary_small_sines_and_cosines_keep_their_bits(d, layout):
         tol = U * np.abs(ref) + 1.01 * far
         err = np.abs(got[:, part] - ref)
         assert np.all(err <= tol), np.max(err / tol)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rms_norm_scale_is_rounded_once(dtype):
+    """Rows (1, k, 0 ..): their sum of squares and its mean (of 2^m columns) are exact in fp32, so
+    the output of the 1 is the scale itself, within half a step of fp32 (and what the last
+    correction leaves, 2^-45)."""
+    print(f"[case] rms norm scale {dtype}", flush=True)
+    for b in (2, 64, 2048):
+        k = torch.arange(1, 257 if dtype == BF else 4096, dtype=torch.float32)
+        X = torch.zeros(k.numel(), b, dtype=dtype)
+        X[:, 0], X[:, 1] = 1.0, k.to(dtype)
+        Y = L.rms_norm(X.to(DEV), torch.ones(b, dtype=dtype, device=DEV), eps=0.0, out_dtype=F32)
+        ref = 1.0 / np.sqrt((1.0 + k.double().numpy() ** 2) / b)
+        err = np.abs(Y[:, 0].double().cpu().numpy() - ref)
+        assert np.all(err <= (U + 2.0 ** -44) * ref), np.max(err / ref) / U
