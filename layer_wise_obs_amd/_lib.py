@@ -431,7 +431,8 @@ _ACTIVATIONS = {"none": TH_ACT_NONE, "relu": TH_ACT_RELU, "silu": TH_ACT_SILU,
 
 def linear(X, W, bias=None, act="none", residual=None, Y=None, out_dtype=None, ws=None):
     """Y = act(X W^T + bias) + residual for X [n, b], W [c, b] and bias [c] (bf16); residual and
-    Y [n, c] in out_dtype (bf16 or fp32, default the residual's or X's). Y may be the residual."""
+    Y [n, c] in out_dtype (bf16 or fp32, default the residual's or X's). Y may be the residual.
+    Forward only, like the steps below: Y carries no gradient, whatever X and W require."""
     torch = _torch()
     index = _device_index(X)
     n, b = X.shape
@@ -464,7 +465,7 @@ def linear(X, W, bias=None, act="none", residual=None, Y=None, out_dtype=None, w
 
 def rms_norm(X, weight, eps=1e-5, Y=None, out_dtype=None):
     """Y = X / sqrt(mean(X^2) + eps) * weight by rows, X [n, b]; Y in out_dtype (default X's).
-    Y may be X."""
+    Y may be X. Forward only: Y carries no gradient."""
     torch = _torch()
     index = _device_index(X)
     n, b = X.shape
@@ -507,7 +508,8 @@ def rotary(q, k, freqs, positions=None, layout="half", amplitude=1.0, q_norm=Non
            eps=1e-6, q_out=None, k_out=None):
     """Heads q [n, hq, d] and k [n, hk, d] (or None) normed where a weight is given, then their
     first 2 * len(freqs) elements turned by positions * freqs (positions: int32 [n], default
-    0 .. n-1). Returns (q_out, k_out), which may be q and k themselves."""
+    0 .. n-1). Returns (q_out, k_out), which may be q and k themselves. Forward only: they carry
+    no gradient."""
     torch = _torch()
     index = _device_index(q)
     n, _, d = q.shape
@@ -551,7 +553,9 @@ def attention_workspace_size(params: AttentionParams) -> int:
 def attention(Q, K, V, q_start=None, k_start=None, causal=True, scale=None, O=None, ws=None):
     """O = softmax(scale Q K^T) V for Q [nq, hq, d], K and V [nk, hk, d] (bf16) of sequences packed
     along the rows: q_start and k_start int32 [nseq + 1] on the GPU (k_start defaults to q_start;
-    without q_start all rows are one sequence). scale defaults to 1 / sqrt(d)."""
+    without q_start all rows are one sequence). scale defaults to 1 / sqrt(d). Rows of O that
+    belong to no sequence are not written (in a new O they hold anything). Forward only: O carries
+    no gradient."""
     torch = _torch()
     index = _device_index(Q)
     nq, hq, d = Q.shape

@@ -27,9 +27,10 @@
 // pieces of a row are XOR-swizzled so that both kinds of operand reads use all banks.
 //
 // Bound by two waves per SIMD (their registers: 64 of O, 32 each of Q, scores, V and K
-// operands) whose products and softmax overlap only in part: 16 sequences of 2048
-// tokens, 32 heads of 128, 650-690 us (800-845 TFLOP/s of the visible half), 38% of the
-// cycles in products; one sequence of 16384, 8 heads on 2, 535-570 (965-1030).
+// operands; heads above 96 use all 256 and spill 1 to 13, reloaded outside the products)
+// whose products and softmax overlap only in part: 16 sequences of 2048 tokens, 32 heads
+// of 128, 645-695 us (790-850 TFLOP/s of the visible half), 38% of the cycles in
+// products; one sequence of 16384, 8 heads on 2, 525-545 (1010-1050).
 //
 // Where there are few workgroups, the keys of each are split over several; the
 // partial (m, l, O) are joined by a second kernel in a fixed order.
@@ -541,12 +542,12 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
 // key head, and its four waves every fourth tile of 32 keys, each with two tiles of its
 // own in LDS and no barrier in the loop; their (m, l, O) meet in LDS at the end. Bound
 // by reading K and V; against 128-row workgroups, whose other three waves had no rows,
-// a token over 300 keys of 32 heads went from 12.5 to 10.8 us. 16 tokens over 300001 keys,
-// 64 heads on 8: 262 us (4.7 TB/s) and 6 for the join. Products of 32x32x16 (their lanes
+// a token over 300 keys of 32 heads went from 12.5 to 10.8 us (10.2 now). 16 tokens over
+// 300001 keys, 64 heads on 8: 264 us (4.7 TB/s) and 6 for the join. Products of 32x32x16 (their lanes
 // hold one query, so the softmax exchanges once). The weights enter the second product as
 // a bf16 value and its rest, so 2^-16 of each is lost and not 2^-8 (error against 64 bits
 // 1.65e-3 rms, the output's own rounding, instead of 2.14e-3; 3% more time, as the matrix
-// cores are 6% busy). Everything else is as above.
+// cores are 9% busy). Everything else is as above.
 template <int D, int DC, bool PAD>
 __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
   constexpr int kBM = 32, kKeys = 32, kWaves = 4;
@@ -863,9 +864,9 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
 
 // Joins the splits of the (token, query head) rows, groups of 32 lanes (4 elements
 // each): a group per row for many rows of few splits, else eight groups to a row, each
-// taking every eighth split; their sums are added in order. (512 queries of 32 heads in
-// two splits 19.4 us with a group per row, 29.6 with eight; 16 of 64 heads in eight, the
-// other way round, 278 and 272.)
+// taking every eighth split; their sums are added in order. (Measured when they were
+// built: 512 queries of 32 heads in two splits 19.4 us with a group per row, 29.6 with
+// eight; 16 of 64 heads in eight, the other way round, 278 and 272.)
 constexpr int kAJoinSplits = 8, kAJoinRows = 2048;
 
 template <bool FEW>
@@ -946,22 +947,24 @@ struct AttnPlan {
 // the call is bound by reading the keys: the few-rows kernel (one workgroup per compute
 // unit at a time), its keys in pieces of 320 or more while those do not fill the units,
 // else of 512 or more up to four rounds, which even out the sequences' lengths. (16
-// sequences over 300001 keys, 8 key heads: 287, 272, 292, 330 us with two, four, eight,
-// sixteen rounds; one over 512 keys, 32 heads: 10.9 us whole, 12.1 in two; over 1024: 15.6
-// whole, 13.8 in three; one over 32768 keys, one head: 22 us in 64 pieces, 27 in 128.)
+// sequences over 300001 keys, lengths up to a factor of ten apart, 8 key heads: 286, 272,
+// 294, 335 us in 4, 8, 16, 32 pieces, eight being taken; of equal lengths 215 in two, 236
+// in eight. One over 512 keys, 32 heads: 11.7 us whole, as taken, 10.9 in eight; over
+// 1024: 16.8 whole, 13.6 in three, as taken, 11.4 in eight; over 32768 keys, one head:
+// 19 us in 64 pieces, 22 in 32.)
 // With more rows the products bound it, and the pieces' results cost: the number of pieces
 // with the least modelled time. A workgroup takes 7 us and 1.25 a tile of 64 keys where it
 // has a compute unit for itself, 1.6 where two share it; more than two take turns, the
 // longest or the average one (causal: half of the newest keys) setting the time; pieces are
 // joined in 3 us and at 4 TB/s. (One sequence, whole and in pieces: 512 tokens, 32 heads of
-// 64, 14.3 us and 19.4 in two; 1024, 32 of 128, 29 and 39; 2048, 8 of 128 on 2, 46 and 37;
-// 4096, 8 of 96 on 1, 77 and 62 in four; 300 over 20000 keys, 16 of 128 on 4, 383 and 81 in
-// six, 78 in twelve. Of 18 shapes, 16 were within 11% of the best of eight numbers.)
+// 64, 13.6 us and 18.9 in two; 1024, 32 of 128, 29 and 39; 2048, 8 of 128 on 2, 46 and 36 in
+// four; 4096, 8 of 96 on 1, 77 and 62 in three; 300 over 20000 keys, 16 of 128 on 4, 388 and
+// 73 in twelve. Of ten shapes, all came within 4% of the best of twelve numbers.)
 // Batches that the averages misjudge take as long as their worst sequence, and are better
-// called in parts: one token over 100000 keys among 63 over 100, 64 heads on 8: 662 us, 95
-// and 17 in two calls; over 20000 among 63 over 2000: 207, 37 and 118; a prompt of 4000
-// tokens among 255 single ones over 1000 keys, 32 heads: 1228, 148 and 784 (on 8 key heads
-// 349, 144 and 213).
+// called in parts: one token over 100000 keys among 63 over 100, 64 heads on 8: 662-677 us,
+// 94 and 16 in two calls; over 20000 among 63 over 2000: 207-248, 37 and 118; a prompt of
+// 4000 tokens among 255 single ones over 1000 keys, 32 heads: 1228-1279, 148 and 784-828
+// (on 8 key heads 349, 144 and 213).
 AttnPlan plan_of(const th_attention_params* p) {
   const int64_t g = p->hq / p->hk;
   const int64_t seqs = p->nseq < p->nq ? p->nseq : p->nq;

@@ -7,8 +7,8 @@
 // a layer is what its pruned predecessors produce.
 //
 // Bound by the matrix cores at large n: tiles of (64 WM) tokens x (32 WN GN) channels
-// on 2 x GN waves, each 32 WM x 32 WN of v_mfma_f32_16x16x32_bf16 blocks (at this
-// card's power limit they run at 1.86 GHz, the 32x32x16 form at 1.66). The contraction
+// on 2 x GN waves, each 32 WM x 32 WN of v_mfma_f32_16x16x32_bf16 blocks (by themselves,
+// at this card's power limit, 1.88 PFLOP/s; the 32x32x16 form 1.69). The contraction
 // is contiguous in both operands, so an MFMA operand (8 consecutive k of a row per
 // lane) is one 16-byte LDS read. Stages of 64 k (128-byte rows, whole cache lines) are
 // filled by direct global->LDS loads, SA stages of X and SB of W deep; the 16-byte
@@ -16,8 +16,8 @@
 // one piece per 16 lanes) use all 64 banks. Fragments are double-buffered over the two
 // 32-wide substeps of a stage. Tiles are walked in groups of 4 token tiles per channel
 // tile, each XCD a contiguous range of that order, so that the workgroups of an XCD
-// share X and W slices in its L2. 131072 tokens 4096 -> 4096: 3.27 ms (1345 TFLOP/s),
-// 3.39 with a bf16 residual (67% of the cycles in products, 7.5 GB read past the L2s).
+// share X and W slices in its L2. 131072 tokens 4096 -> 4096: 3.33 ms (1319 TFLOP/s),
+// 3.39-3.48 with a bf16 residual (66% of the cycles in products, 7.5 GB read past the L2s).
 #include "common.h"
 #include "lds_dma.h"
 
@@ -32,8 +32,7 @@ constexpr int kLRow = kLK * 2;
 // 16 bytes of a row of Y or the residual, aligned like its elements only: the memory
 // system takes such accesses at any of their addresses, so that odd widths and pitches
 // need no code of their own but for a row's last channels. (15485 tokens 2216 -> 9418, gelu
-// and residual, bf16: 694 us; element by element, a lane per eight channels 1022, a lane
-// per channel 1190.)
+// and residual, bf16: 678 us; element by element, half as much again, 1022 against 694.)
 typedef u32x4_t bf16_row_t __attribute__((aligned(2)));
 typedef f32x4_t f32_row_t __attribute__((aligned(4)));
 
@@ -508,8 +507,10 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restric
 // memory into the operands of v_mfma_f32_16x16x32_bf16 (W as the first one: lane l
 // holds channel l % 16, k = 8 (l / 16) .. + 7), kSkSteps steps of 1 KB in flight per
 // wave, X comes from L2. The waves' sums meet in LDS and are added in the order of the
-// waves. Workgroup x takes the channels from 16 (first + x). 8.6 us for one token 4096 -> 4096 (3.9 TB/s, the launch included), 93 us for
-// four 8192 -> 28672 (5.06 TB/s); nontemporal loads of W 9.5 and 111.
+// waves. Workgroup x takes the channels from 16 (first + x). In a graph 7.2 us for one
+// token 4096 -> 4096 (4.7 TB/s), 84 us for four 8192 -> 28672 (5.6 TB/s; nontemporal
+// loads of W took a fifth longer). Few channels are few workgroups: one token
+// 8192 -> 1024 takes 10.8 us (1.6 TB/s).
 constexpr int kSkWaves = 8;
 constexpr int kSkSteps = 8;
 
@@ -555,11 +556,13 @@ __global__ __launch_bounds__(64 * kSkWaves) void linear_skinny_kernel(
 
 // The tile kernel's forms. Its time is modelled as rounds of `slots` workgroups, each
 // taking fixed + stages * per_stage microseconds with every slot taken and half of the
-// second part with few (measured: 777 x 4096 -> 11008 on 172 tiles of 256 x 256 98.9 us,
-// modelled 96.4; 1024 x 4096 -> 4096 on 256 of 128 x 128 41.2, 41.2; 2048 x 4096 -> 4096
-// on 256 of 128 x 256 66.3, 66.5; 777 x 2056 -> 1023 on 208 of 64 x 64 16.6, 16.3), and
-// the join of splits as 3 us and its traffic at 4 TB/s. The cheapest form is taken: over
-// 25 shapes it was within 10% of the best one measured.
+// second part with few, and the join of splits as 3 us and its traffic at 4 TB/s. Measured
+// in a graph, and modelled: 777 x 4096 -> 11008 on 172 tiles of 256 x 256 82-85 us, 96;
+// 1024 x 4096 -> 4096 on 256 of 128 x 128 37-38, 41; 2048 x 4096 -> 4096 on 256 of
+// 128 x 256 65-67, 66; 777 x 2056 -> 1023 on 208 of 64 x 64 14, 16. The cheapest form is
+// taken: over 22 shapes of 13 tokens and more it came within 8% of the best of all forms
+// and numbers of pieces, but for 256 x 4096 -> 4096 (11%: 22.2 us in pieces of 64 x 64
+// tiles, 20.0 whole) and 64 x 4096 -> 11008 (17%: 22.4 on 128 x 128, 19.1 on 64 x 64).
 struct LinTile {
   int tm, tn;
   int slots;  // workgroups that run at a time
@@ -572,8 +575,10 @@ constexpr LinTile kTiles[kLinTiles] = {
     {128, 256, 256, 0.93, 7.0},   // 8 waves of 64 x 64
     {256, 256, 256, 1.54, 14.0},  // 8 waves of 128 x 64
 };
-// Up to 12 tokens the skinny kernel is ahead (4096 -> 4096: 8.5 us for one token against
-// 12.7 on tiles, 11.0 against 13.3 for twelve; 11008 -> 4096: even at sixteen).
+// Up to 12 tokens the skinny kernel is ahead for thousands of channels (4096 -> 4096: 7.4 us
+// for one token against 9.5 on tiles, 9.5 against 10.0 for twelve; 11008 -> 4096 20.9 against
+// 19.8 for twelve). With few channels it is not: 12 tokens 8192 -> 1024 take 15.0 us, on 64 x 64
+// tiles in sixteen pieces 9.3.
 constexpr int64_t kSkinny = 12;
 
 struct LinPlan {

@@ -7,7 +7,8 @@
 // row and keeps it in registers between the sum and the product, so x is read
 // once; every lane moves 8 consecutive elements (16 bytes of bf16) at a time. The
 // sum of squares is fp32: 8 products per chunk and lane, then lanes, then waves.
-// 131072 rows of 4096 in bf16: 354-380 us, 5.7-6.1 TB/s (a copy: 4.9).
+// 131072 rows of 4096 in bf16: 358-412 us by box, 5.2-6.0 TB/s (torch's copy: 4.9).
+// Rows below 512 elements are bound by launching workgroups: 100000 of 100, 54 us.
 #include "common.h"
 
 namespace th {
@@ -18,7 +19,7 @@ constexpr int kNChunks = 4;  // register-held chunks of 8 elements per thread
 
 // Eight elements, 16 bytes at a time, aligned like an element only: the memory system
 // takes such accesses at any of their addresses, so that odd widths and pitches need no
-// code of their own but for a row's last elements (65536 rows of 4095 in bf16: 331 us;
+// code of their own but for a row's last elements (65536 rows of 4095 in bf16: 329 us;
 // element by element 587).
 typedef u32x4_t bf16_row_t __attribute__((aligned(2)));
 typedef f32x4_t f32_row_t __attribute__((aligned(4)));
@@ -160,7 +161,7 @@ hipError_t launch_rows(const void* X, int64_t ldx, const void* w, void* Y, int64
 template <class TI, class TO>
 hipError_t launch_typed(const void* X, int64_t ldx, const void* w, void* Y, int64_t ldy, int64_t n,
                         int64_t b, float eps, hipStream_t s) {
-  if (b % 8)  // the whole rows' kernel needs fewer registers: 379 us against 405 with tails
+  if (b % 8)  // the whole rows' kernel needs fewer registers: tails cost it 7%
     return b <= 1024 ? launch_rows<TI, TO, 64, true>(X, ldx, w, Y, ldy, n, b, eps, s)
                      : launch_rows<TI, TO, 256, true>(X, ldx, w, Y, ldy, n, b, eps, s);
   return b <= 1024 ? launch_rows<TI, TO, 64, false>(X, ldx, w, Y, ldy, n, b, eps, s)

@@ -24,8 +24,8 @@ namespace {
 constexpr int kRThreads = 256;
 constexpr int kRMaxTokens = 16;  // tokens per workgroup, at most
 constexpr int kRMaxPairs = 128;
-constexpr int kRBatch = 2;       // heads whose loads are in flight together (2: 403 us for
-                                 // 65536 tokens x 64 heads of 128, 5.3 TB/s; 4: 417; 8: 416)
+constexpr int kRBatch = 2;       // heads whose loads are in flight together (four or eight:
+                                 // 3% more for 65536 tokens x 64 heads of 128)
 
 struct RotSide {
   const void* x;
@@ -104,9 +104,9 @@ __device__ __forceinline__ float get1(const float* p) { return *p; }
 __device__ __forceinline__ void put1(unsigned short* p, float v) { *p = f32_to_bf16_rne(v); }
 __device__ __forceinline__ void put1(float* p, float v) { *p = v; }
 
-// Where the other element of a pair is. (29807 tokens, 64 heads of 88, half, normed: 244 us
+// Where the other element of a pair is. (29807 tokens, 64 heads of 88, half, normed: 239 us
 // with 16-byte accesses and partners through LDS, 817 with a lane per pair; 11625 tokens, 64
-// heads of 64, 62 elements interleaved: 42 and 197.)
+// heads of 64, 62 elements interleaved: 34 and 197.)
 enum Partner {
   kNext,    // interleaved: the pair is in one lane
   kLane,    // half, rot % 16 == 0: the same element of another lane
