@@ -250,6 +250,54 @@ th_status th_linear(const void* X, int64_t ldx, const void* W, th_dtype dt, int6
                     int64_t ldr, void* Y, th_dtype ydt, int64_t ldy, void* workspace,
                     size_t workspace_bytes, th_stream_t stream);
 
+/* Microscaled matrices, the form in which the pruned layers of a block are served [BLOG,
+ * "The compression target: linear layers"]: [n, b] in blocks of 32 consecutive elements of
+ * a row; a value is its element times 2^(scale - 127) of its block. Elements are e4m3 (a
+ * byte: sign, 4 bits of exponent, 3 of mantissa, up to 448) or e2m1 (4 bits, up to 6;
+ * element 2i of a row in the low half of byte i). Scales are a byte a block; 255: none of
+ * the block's values is a number. */
+typedef enum { TH_MX_E4M3 = 0, TH_MX_E2M1 = 1 } th_mx_type;
+typedef struct {
+  void* elements; /* element bytes of row t from elements + t * ld */
+  void* scales;   /* scales of row t from scales + t * lds, b / 32 bytes */
+  int64_t ld, lds; /* row pitches in BYTES */
+  int32_t type;   /* th_mx_type */
+} th_mx;
+
+/* X [n,b] (row pitch ldx elements, dtype xdt) in the form of Y (host struct; its buffers are
+ * written): a block's scale is the smallest power at which none of its elements, rounded to
+ * nearest even, passes the type's largest number, so an element is off by at most half a
+ * step; below 2^-127 elements become 0 or what is left of them, past 2^119 (e4m3) and 2^125
+ * (e2m1) they saturate. A block that holds a NaN or an infinity gets scale 255 and
+ * elements 0. b % 32 == 0; any row pitch and alignment; n = 0 is allowed, n < 2^31. Buffers
+ * must not overlap. Asynchronous. */
+th_status th_mx_quantize(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t ldx,
+                         const th_mx* Y, th_stream_t stream);
+/* The values of X [n,b] as Y (row pitch ldy elements, dtype ydt), rounded once. Arguments as
+ * above. Asynchronous. */
+th_status th_mx_dequantize(const th_mx* X, int64_t n, int64_t b, void* Y, th_dtype ydt,
+                           int64_t ldy, th_stream_t stream);
+
+/* th_linear on microscaled operands, Y = act(X W^T + bias) + residual: X [n,b] in either
+ * type, W [c,b] of TH_MX_E2M1. Elements 16-byte aligned with row pitches that are multiples
+ * of 16; scales likewise, and the bytes up to lds of every row, the last one's included, may
+ * be read (they are never used). bias [c] bf16 or NULL, act, residual and Y (bf16 or fp32:
+ * ydt) as in th_linear, any pitch and alignment. Products are exact and sums fp32 where X
+ * is e2m1, where Y is fp32 and where n <= 16; with an e4m3 X and a bf16 Y the matrix cores
+ * align the products of eight consecutive elements to the largest and drop what lies 13
+ * binary places below it (5e-6 of Y in root mean square, 1/300 of Y's own rounding).
+ * n >= 0, c >= 1, 32 <= b < 2^22, b % 32 == 0, pitches < 2^22 bytes. workspace (optional, may
+ * be NULL with workspace_bytes 0; 16-byte aligned) lets launches with few tiles split the
+ * contraction; size from th_mx_linear_workspace_size (xtype: th_mx_type of X; 0 where it does
+ * not help). The order of all sums is fixed, so repeated calls give identical bits.
+ * Asynchronous. */
+th_status th_mx_linear_workspace_size(int32_t xtype, int64_t n, int64_t b, int64_t c, th_dtype ydt,
+                                      size_t* bytes /* host */);
+th_status th_mx_linear(const th_mx* X, const th_mx* W, int64_t n, int64_t b, int64_t c,
+                       const void* bias, th_activation act, const void* residual, int64_t ldr,
+                       void* Y, th_dtype ydt, int64_t ldy, void* workspace, size_t workspace_bytes,
+                       th_stream_t stream);
+
 /* Root-mean-square norm of the rows of a residual stream, what the q/k/v and the
  * gate/up projections of a block read [BLOG, "The compression target: linear
  * layers"]: Y_tq = X_tq / sqrt(mean_q X_tq^2 + eps) * weight_q. X [n,b] (row pitch
@@ -261,6 +309,19 @@ th_status th_linear(const void* X, int64_t ldx, const void* W, th_dtype dt, int6
 th_status th_rms_norm(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t ldx,
                       const void* weight, double eps, void* Y, th_dtype ydt, int64_t ldy,
                       th_stream_t stream);
+
+/* The norm behind an addition to the residual stream: h = X + R rounded to xdt, stored in sum
+ * (optional), and h / sqrt(mean h^2 + eps) * weight in Y (dtype ydt) or, with Y NULL,
+ * microscaled in Y_mx (host struct), what th_mx_linear reads. R NULL: h = X, and sum has to be
+ * NULL. X, R, sum [n,b] in xdt with their own row pitches in elements, weight [b] in xdt.
+ * Sums, root and products in fp64, every output rounded once (Y_mx: scales and roundings as
+ * in th_mx_quantize of the unrounded values; b % 32 == 0). sum may be X or R (same pitch); Y
+ * and Y_mx must not overlap other buffers. n, eps, widths, pitches and alignments as in
+ * th_rms_norm. Asynchronous. */
+th_status th_add_rms_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, th_dtype xdt,
+                          int64_t n, int64_t b, const void* weight, double eps, void* sum,
+                          int64_t ldsum, void* Y, th_dtype ydt, int64_t ldy, const th_mx* Y_mx,
+                          th_stream_t stream);
 
 /* Rotary positions of the queries and keys of n tokens, with an optional norm of
  * each head in the same pass. Element e of head h of token t is at
@@ -351,6 +412,66 @@ th_status th_attention(const void* Q, const void* K, const void* V, th_dtype dt,
                        const int32_t* q_start, const int32_t* k_start,
                        const th_attention_params* p, void* O, void* workspace,
                        size_t workspace_bytes, th_stream_t stream);
+
+/* A paged cache of the keys and values of nseq sequences (host struct; pointers to the
+ * device). Element e of head h of token j of page p is at k[p * k_page + j * k_token +
+ * h * k_head + e] (strides in elements); v likewise. Key x of sequence s is token
+ * x % page_tokens of page pages[s * pages_row + x / page_tokens]; the sequence has k_len[s]
+ * keys, the newest tokens' included. Lengths outside [0, width * page_tokens] are taken as
+ * the nearest end of it. Sequences may share pages. */
+typedef struct {
+  void *k, *v;
+  int64_t npages, page_tokens; /* page_tokens: a power of two, 16 .. 65536 */
+  int64_t hk, d;               /* key heads; elements per head */
+  int64_t k_page, k_token, k_head, v_page, v_token, v_head;
+  const int32_t* pages;        /* [nseq][width], row pitch pages_row */
+  const int32_t* k_len;        /* [nseq] */
+  int64_t nseq, width, pages_row;
+} th_paged_cache;
+
+/* The keys and values of nq new tokens, K and V [nq, hk, d] (strides in elements), into the
+ * cache's pages. q_start as in th_attention (nseq + 1 ascending int32, device): rows
+ * q_start[s] .. q_start[s+1]-1 are the last keys of sequence s, the last row its key
+ * k_len[s]-1. q_start NULL: every sequence has nq / nseq rows. A row whose key is before the
+ * sequence's first, or whose page is not in [0, npages), is not stored, nor are rows before
+ * q_start[0] and from q_start[nseq] on; start values outside [0, nq] are moved to its ends.
+ * Where two rows have one place, either is left there. dt must be TH_BF16; d and alignment as in
+ * th_paged_attention, also of K and V. Asynchronous. */
+th_status th_cache_store(const void* K, int64_t k_token, int64_t k_head, const void* V,
+                         int64_t v_token, int64_t v_head, th_dtype dt, int64_t nq,
+                         const int32_t* q_start, const th_paged_cache* cache,
+                         th_stream_t stream);
+
+/* th_attention of nq new tokens over a paged cache that holds their keys already: rows
+ * q_start[s] .. q_start[s+1]-1 of Q and O (NULL: nq / nseq rows each) over the k_len[s] keys
+ * of sequence s. With causal != 0 the last row sees the sequence's last key, the one before
+ * it one key fewer, and so on. A row that sees no key gets zeros; what hidden keys and
+ * values, and page places past k_len, hold never enters; rows of no sequence are left as they
+ * are. Pages outside [0, npages) are read as the nearest end of it. */
+typedef struct {
+  int64_t nq, hq;  /* rows and heads of Q and O */
+  int64_t q_token, q_head, o_token, o_head;
+  int32_t causal;
+  int32_t even;    /* != 0: q_start is NULL */
+  double scale;    /* as in th_attention */
+} th_paged_params;
+
+/* dt must be TH_BF16; 8 <= d <= 128, d % 8 == 0; hk divides hq; strides are multiples of 8
+ * (k_token, v_token < 2^24), all >= 0, and Q, O, k, v 16-byte aligned; nq * hq / hk and
+ * width * page_tokens < 2^31 - 2^16, npages < 2^31, nseq < 2^24; row blocks and pieces of
+ * keys in one launch < 2^24. O must not overlap the inputs. Precision as in th_attention.
+ * The host needs no lengths: how the keys are cut into pieces is found on the device from
+ * the real ones, sequences of up to 32 rows (tokens times hq / hk) apart from longer ones,
+ * so that batches of unlike sequences keep every compute unit busy, and a captured call
+ * follows the lengths of each replay. workspace (optional, may be NULL with
+ * workspace_bytes 0; 16-byte aligned) lets the keys be cut; size from
+ * th_paged_attention_workspace_size. The order of all sums is fixed by the lengths, so
+ * repeated calls give identical bits. Asynchronous. */
+th_status th_paged_attention_workspace_size(const th_paged_cache* cache, const th_paged_params* p,
+                                            size_t* bytes /* host */);
+th_status th_paged_attention(const void* Q, th_dtype dt, const int32_t* q_start,
+                             const th_paged_cache* cache, const th_paged_params* p, void* O,
+                             void* workspace, size_t workspace_bytes, th_stream_t stream);
 
 /* Comparator: the column-sequential schedule of SparseGPT on the same Hessian and
  * factor [BLOG, "The scaling problem, and what SparseGPT changes": left to right,

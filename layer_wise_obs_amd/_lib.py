@@ -19,6 +19,7 @@ TH_SCORE_OBS, TH_SCORE_WANDA = 0, 1
 TH_BASE_MAGNITUDE, TH_BASE_WANDA = 0, 1
 TH_ACT_NONE, TH_ACT_RELU, TH_ACT_SILU, TH_ACT_GELU = range(4)
 TH_ROTARY_HALF, TH_ROTARY_INTERLEAVED = 0, 1
+TH_MX_E4M3, TH_MX_E2M1 = 0, 1
 STATUS_NAMES = {0: "TH_OK", 1: "TH_ERR_INVALID_ARG", 2: "TH_ERR_NOT_SPD", 3: "TH_ERR_NONFINITE",
                 4: "TH_ERR_WORKSPACE", 5: "TH_ERR_HIP"}
 
@@ -62,6 +63,23 @@ class AttentionParams(ctypes.Structure):
         "o_token", "o_head", "nseq")] + [("causal", ctypes.c_int32), ("scale", ctypes.c_double)]
 
 
+class Mx(ctypes.Structure):
+    _fields_ = [("elements", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("lds", ctypes.c_int64), ("type", ctypes.c_int32)]
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [(x, ctypes.c_int64) for x in (
+        "npages", "page_tokens", "hk", "d", "k_page", "k_token", "k_head", "v_page", "v_token",
+        "v_head")] + [("pages", ctypes.c_void_p), ("k_len", ctypes.c_void_p)] + [
+        (x, ctypes.c_int64) for x in ("nseq", "width", "pages_row")]
+
+
+class PagedParams(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("nq", "hq", "q_token", "q_head", "o_token", "o_head")] + [
+        ("causal", ctypes.c_int32), ("even", ctypes.c_int32), ("scale", ctypes.c_double)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -100,6 +118,19 @@ _SIG = {
                                     ctypes.POINTER(ctypes.c_size_t)],
     "th_attention": [_P, _P, _P, _I32, _P, _P, ctypes.POINTER(AttentionParams), _P, _P,
                      ctypes.c_size_t, _P],
+    "th_mx_quantize": [_P, _I32, _I64, _I64, _I64, ctypes.POINTER(Mx), _P],
+    "th_mx_dequantize": [ctypes.POINTER(Mx), _I64, _I64, _P, _I32, _I64, _P],
+    "th_mx_linear_workspace_size": [_I32, _I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_size_t)],
+    "th_mx_linear": [ctypes.POINTER(Mx), ctypes.POINTER(Mx), _I64, _I64, _I64, _P, _I32, _P, _I64, _P,
+                     _I32, _I64, _P, ctypes.c_size_t, _P],
+    "th_add_rms_norm": [_P, _I64, _P, _I64, _I32, _I64, _I64, _P, ctypes.c_double, _P, _I64, _P, _I32,
+                        _I64, ctypes.POINTER(Mx), _P],
+    "th_cache_store": [_P, _I64, _I64, _P, _I64, _I64, _I32, _I64, _P, ctypes.POINTER(PagedCache),
+                       _P],
+    "th_paged_attention_workspace_size": [ctypes.POINTER(PagedCache), ctypes.POINTER(PagedParams),
+                                          ctypes.POINTER(ctypes.c_size_t)],
+    "th_paged_attention": [_P, _I32, _P, ctypes.POINTER(PagedCache), ctypes.POINTER(PagedParams), _P,
+                           _P, ctypes.c_size_t, _P],
     "th_prune_sparsegpt": [_P, _I32, _I64, _I64, _P, _I32, _I64, _P, ctypes.POINTER(PruneParams),
                            _P, _P, _P, ctypes.c_size_t, ctypes.POINTER(Stats),
                            ctypes.POINTER(_I64), _P],
@@ -481,6 +512,167 @@ def rms_norm(X, weight, eps=1e-5, Y=None, out_dtype=None):
     return Y
 
 
+_MX_TYPES = {"e4m3": TH_MX_E4M3, "e2m1": TH_MX_E2M1}
+
+
+class MxMatrix:
+    """A microscaled matrix [n, b]: its type ("e4m3" or "e2m1"), elements (uint8 [n, b], or
+    [n, b / 2] with element 2i in the low half of byte i) and scales (uint8 [n, b / 32]); a value is
+    its element times 2^(scale - 127) of its 32. The scales' rows are a multiple of 16 bytes apart
+    where mx_linear is to read them."""
+    __slots__ = ("type", "elements", "scales")
+
+    def __init__(self, type, elements, scales):
+        if type not in _MX_TYPES:
+            raise ValueError(f"type must be one of {sorted(_MX_TYPES)}, not {type!r}")
+        self.type, self.elements, self.scales = type, elements, scales
+
+    @classmethod
+    def empty(cls, n, b, type, device):
+        torch = _torch()
+        if b % 32:
+            raise ValueError(f"b must be a multiple of 32, not {b}")
+        scales = torch.empty((n, -(-b // 512) * 16), dtype=torch.uint8, device=device)
+        return cls(type, torch.empty((n, b if type == "e4m3" else b // 2), dtype=torch.uint8,
+                                     device=device), scales[:, :b // 32])
+
+    @property
+    def shape(self):
+        n, width = self.elements.shape
+        return n, width if self.type == "e4m3" else 2 * width
+
+    @property
+    def device(self):
+        return self.elements.device
+
+
+def _mx(index, name, m):
+    """(n, b, host struct) of a microscaled matrix on GPU index."""
+    torch = _torch()
+    n, b = m.shape
+    blocks = b // 32
+    e = _row_pitch(_require(index, name + ".elements", m.elements, m.elements.shape, torch.uint8), n,
+                   m.elements.shape[1])
+    s = _require(index, name + ".scales", m.scales, (n, blocks), torch.uint8)
+    # a single row's pitch, which no access uses, is given as a multiple of 16 that holds it
+    s = s[0] if n > 1 else -(-blocks // 16) * 16
+    e = e if n > 1 else -(-e // 16) * 16
+    return n, b, Mx(m.elements.data_ptr(), m.scales.data_ptr(), e, s, _MX_TYPES[m.type])
+
+
+def mx_quantize(X, type="e2m1", out=None):
+    """X [n, b] (bf16 or fp32, b a multiple of 32) as a new microscaled matrix, or in out: a block's
+    scale is the smallest power at which none of its elements passes the type's largest number;
+    elements rounded to nearest even. A block with a NaN or an infinity holds no numbers."""
+    index = _device_index(X)
+    n, b = X.shape
+    ldx = _row_pitch(_require(index, "X", X, (n, b), X.dtype), n, b)
+    if out is None:
+        out = MxMatrix.empty(n, b, type, X.device)
+    no, bo, y = _mx(index, "out", out)
+    if (no, bo) != (n, b):
+        raise ValueError(f"out must have shape {(n, b)}, not {(no, bo)}")
+    _call_on(index, lib().th_mx_quantize, X.data_ptr(), _dtype_code(X), n, b, ldx, y)
+    return out
+
+
+def mx_dequantize(X, Y=None, out_dtype=None):
+    """The values of a microscaled matrix, Y [n, b] in out_dtype (default bf16)."""
+    torch = _torch()
+    index = _device_index(X.elements)
+    n, b, x = _mx(index, "X", X)
+    ldy = b
+    if Y is None:
+        Y = torch.empty((n, b), dtype=out_dtype or torch.bfloat16, device=X.device)
+    else:
+        ldy = _row_pitch(_require(index, "Y", Y, (n, b), out_dtype or Y.dtype), n, b)
+    _call_on(index, lib().th_mx_dequantize, x, n, b, Y.data_ptr(), _dtype_code(Y), ldy)
+    return Y
+
+
+def mx_linear_workspace_size(type: str, n: int, b: int, c: int, out_dtype) -> int:
+    torch = _torch()
+    out = ctypes.c_size_t(0)
+    _check(lib().th_mx_linear_workspace_size(_MX_TYPES[type], n, b, c,
+                                             TH_F32 if out_dtype == torch.float32 else TH_BF16,
+                                             ctypes.byref(out)))
+    return out.value
+
+
+def mx_linear(X, W, bias=None, act="none", residual=None, Y=None, out_dtype=None, ws=None):
+    """Y = act(X W^T + bias) + residual for microscaled X [n, b] (either type) and W [c, b]
+    ("e2m1"), bias [c] bf16; residual and Y [n, c] in out_dtype (bf16 or fp32, default the
+    residual's or bf16). Y may be the residual. Forward only."""
+    torch = _torch()
+    index = _device_index(X.elements)
+    n, b, x = _mx(index, "X", X)
+    c, bw, w = _mx(index, "W", W)
+    if bw != b:
+        raise ValueError(f"W must have {b} columns, not {bw}")
+    if out_dtype is None:
+        out_dtype = next((t.dtype for t in (Y, residual) if t is not None), torch.bfloat16)
+    if bias is not None:
+        _require(index, "bias", bias, (c,), torch.bfloat16)
+    ldr = ldy = c
+    if residual is not None:
+        ldr = _row_pitch(_require(index, "residual", residual, (n, c), out_dtype), n, c)
+    if Y is None:
+        Y = (torch.empty((n, c), dtype=out_dtype, device=X.device) if residual is None
+             else _fresh(torch, residual))
+    else:
+        ldy = _row_pitch(_require(index, "Y", Y, (n, c), out_dtype), n, c)
+    if ws is None:
+        nbytes = mx_linear_workspace_size(X.type, n, b, c, out_dtype)
+        ws = workspace(nbytes, X.device) if nbytes else None
+    at, nbytes = (None, 0) if ws is None else _workspace_on(index, ws)
+    _call_on(index, lib().th_mx_linear, x, w, n, b, c, _addr(bias), _ACTIVATIONS[act],
+             _addr(residual), ldr, Y.data_ptr(), _dtype_code(Y), ldy, at, nbytes)
+    return Y
+
+
+def add_rms_norm(X, weight, residual=None, eps=1e-5, out=None, sum_out=None):
+    """(h, Y): h = X + residual in X's dtype (a new tensor, or sum_out, which may be X or the
+    residual; X itself without a residual) and Y = h / sqrt(mean(h^2) + eps) * weight by rows.
+    out: "e4m3", "e2m1" or a MxMatrix for a microscaled Y; a dtype or a tensor for a plain one
+    (default X's dtype). Forward only."""
+    torch = _torch()
+    index = _device_index(X)
+    n, b = X.shape
+    dtype = X.dtype
+    ldx = _row_pitch(_require(index, "X", X, (n, b), dtype), n, b)
+    _require(index, "weight", weight, (b,), dtype)
+    ldr = ldsum = ldy = b
+    h = X
+    if residual is not None:
+        ldr = _row_pitch(_require(index, "residual", residual, (n, b), dtype), n, b)
+        if sum_out is None:
+            h = _fresh(torch, X)
+        else:
+            h = sum_out
+            ldsum = _row_pitch(_require(index, "sum_out", h, (n, b), dtype), n, b)
+    elif sum_out is not None:
+        raise ValueError("sum_out goes with residual")
+    Y, y, mx, code = None, None, None, TH_BF16
+    if isinstance(out, str):
+        out = MxMatrix.empty(n, b, out, X.device)
+    if isinstance(out, MxMatrix):
+        Y = out
+        no, bo, mx = _mx(index, "out", out)
+        if (no, bo) != (n, b):
+            raise ValueError(f"out must have shape {(n, b)}, not {(no, bo)}")
+    else:
+        if out is None or isinstance(out, torch.dtype):
+            Y = _fresh(torch, X, out)
+        else:
+            Y = out
+            ldy = _row_pitch(_require(index, "out", Y, (n, b), Y.dtype), n, b)
+        y, code = Y.data_ptr(), _dtype_code(Y)
+    _call_on(index, lib().th_add_rms_norm, X.data_ptr(), ldx, _addr(residual), ldr, _dtype_code(X), n,
+             b, weight.data_ptr(), float(eps), None if residual is None else h.data_ptr(), ldsum, y,
+             code, ldy, mx)
+    return h, Y
+
+
 def rotary_freqs(rot: int, base=10000.0, divide=1.0, bands=None, device=None):
     """Frequencies of the rot/2 pairs (float64, rot/2 values, on device) for rotary().
 
@@ -585,6 +777,87 @@ def attention(Q, K, V, q_start=None, k_start=None, causal=True, scale=None, O=No
     at, nbytes = (None, 0) if ws is None else _workspace_on(index, ws)
     _call_on(index, lib().th_attention, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _dtype_code(Q),
              _addr(q_start), _addr(k_start), p, O.data_ptr(), at, nbytes)
+    return O
+
+
+def _paged_cache(index, k_cache, v_cache, pages, k_len):
+    """Host struct of a paged cache, and its dtype."""
+    torch = _torch()
+    npages, page, hk, d = k_cache.shape
+    dtype = k_cache.dtype
+    k_s = _require(index, "k_cache", k_cache, (npages, page, hk, d), dtype)
+    v_s = _require(index, "v_cache", v_cache, (npages, page, hk, d), dtype)
+    nseq, width = pages.shape
+    row = _row_pitch(_require(index, "pages", pages, (nseq, width), torch.int32), nseq, width)
+    if k_len.shape != (nseq,) or (nseq > 1 and k_len.stride(0) != 1):
+        raise ValueError(f"k_len must be contiguous with shape {(nseq,)}")
+    _require(index, "k_len", k_len, (nseq,), torch.int32)
+    # strides of a dimension of one element, which no access uses, are given as the dense ones
+    k_s, v_s = ((s[0] if npages > 1 else page * hk * d, s[1], s[2] if hk > 1 else d)
+                for s in (k_s, v_s))
+    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), npages, page, hk, d, *k_s, *v_s,
+                      pages.data_ptr(), k_len.data_ptr(), nseq, width, row)
+
+
+def cache_store(K, V, k_cache, v_cache, pages, k_len, q_start=None):
+    """New keys and values K and V [nq, hk, d] (bf16) into the pages of k_cache and v_cache
+    [pages, page_tokens, hk, d] (any strides of whole heads): rows q_start[s] .. q_start[s+1]-1 are the
+    last keys of sequence s, whose key x is row x % page_tokens of page pages[s, x // page_tokens];
+    pages int32 [nseq, width], k_len int32 [nseq] with the new ones counted, q_start int32
+    [nseq + 1] (default: nq / nseq rows each). Rows whose key or page is out of range are not
+    stored."""
+    torch = _torch()
+    index = _device_index(K)
+    nq, hk, d = K.shape
+    dtype = K.dtype
+    k_s = _pitches(_require(index, "K", K, (nq, hk, d), dtype), nq, hk, d)
+    v_s = _pitches(_require(index, "V", V, (nq, hk, d), dtype), nq, hk, d)
+    cache = _paged_cache(index, k_cache, v_cache, pages, k_len)
+    if (cache.hk, cache.d) != (hk, d) or k_cache.dtype != dtype:
+        raise ValueError("K, V and the cache must have the same heads and dtype")
+    if q_start is not None:
+        _require(index, "q_start", q_start, (cache.nseq + 1,), torch.int32)
+    _call_on(index, lib().th_cache_store, K.data_ptr(), *k_s, V.data_ptr(), *v_s, _dtype_code(K), nq,
+             _addr(q_start), cache)
+
+
+def paged_attention_workspace_size(cache: PagedCache, params: PagedParams) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().th_paged_attention_workspace_size(ctypes.byref(cache), ctypes.byref(params),
+                                                   ctypes.byref(out)))
+    return out.value
+
+
+def paged_attention(Q, k_cache, v_cache, pages, k_len, q_start=None, causal=True, scale=None, O=None,
+                    ws=None):
+    """attention() of new tokens Q [nq, hq, d] (bf16) over a paged cache that holds their keys (see
+    cache_store): rows q_start[s] .. q_start[s+1]-1 (default nq / nseq each) over the k_len[s] keys of
+    sequence s, causal to its last key. The lengths stay on the GPU; a narrower view of pages than the
+    longest sequence cuts it off. Rows of O that belong to no sequence are not written (in a new O
+    they hold anything). Forward only."""
+    torch = _torch()
+    index = _device_index(Q)
+    nq, hq, d = Q.shape
+    dtype = Q.dtype
+    q_s = _pitches(_require(index, "Q", Q, (nq, hq, d), dtype), nq, hq, d)
+    cache = _paged_cache(index, k_cache, v_cache, pages, k_len)
+    if cache.d != d or k_cache.dtype != dtype:
+        raise ValueError("Q and the cache must have the same elements per head and dtype")
+    if O is None:  # rows that belong to no sequence are not written
+        O = _fresh(torch, Q)
+        o_s = hq * d, d
+    else:
+        o_s = _pitches(_require(index, "O", O, (nq, hq, d), dtype), nq, hq, d)
+    if q_start is not None:
+        _require(index, "q_start", q_start, (cache.nseq + 1,), torch.int32)
+    p = PagedParams(nq, hq, *q_s, *o_s, 1 if causal else 0, 1 if q_start is None else 0,
+                    d ** -0.5 if scale is None else float(scale))
+    if ws is None:
+        nbytes = paged_attention_workspace_size(cache, p)
+        ws = workspace(nbytes, Q.device) if nbytes else None
+    at, nbytes = (None, 0) if ws is None else _workspace_on(index, ws)
+    _call_on(index, lib().th_paged_attention, Q.data_ptr(), _dtype_code(Q), _addr(q_start), cache, p,
+             O.data_ptr(), at, nbytes)
     return O
 
 

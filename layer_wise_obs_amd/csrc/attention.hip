@@ -37,12 +37,15 @@
 #include "common.h"
 #include "lds_dma.h"
 
+#include <algorithm>
+
 namespace th {
 
 namespace {
 
 constexpr int kAKT = 64;   // keys per tile
 constexpr float kAMove = 8.0f;  // log2 of how far p may pass 1 before m moves
+constexpr int kAUnits = 256;  // compute units
 
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
 typedef short v8i16_t __attribute__((ext_vector_type(8)));
@@ -59,6 +62,17 @@ struct AttnArgs {
   float c;        // scale * log2(e)
   float* part_o;  // [splits][nq][hq][d]
   float2* part_ml;
+};
+
+// A paged cache: K and V are its pages, a key is found through its sequence's row of page
+// numbers; k_start has lengths in the place of starts.
+struct PagedArgs : AttnArgs {
+  const int32_t* pages;
+  int64_t pages_row, k_page, v_page, npages;
+  int64_t keys_most;  // a sequence's pages hold as many keys
+  int64_t each;       // rows of a sequence without q_start
+  int shift;          // log2 of a page's keys
+  int slots;          // bound of the pieces' partial results per key head; 0: no keys are cut
 };
 
 // Entry i of a start array, kept inside [0, n]: whatever it holds, no access leaves
@@ -116,6 +130,135 @@ __device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, int64_t slot,
   return r;
 }
 
+// ---------------------------------------------------------------- paged: the work
+
+// Keys of a piece are whole tiles of kTileKeys; what the few-rows kernel and the other one take:
+// sequences of up to kAFewRows rows (tokens times the group), and longer ones.
+constexpr int kAFewRows = 32;
+
+struct PagedWork {
+  int sequence;            // -1: none
+  int64_t q0, q1;          // its rows of Q
+  int lk;                  // its keys
+  int64_t row0;            // first row of the block
+  int per, piece, pieces;  // keys of a piece, this one and how many there are
+  int slot;                // of this piece's partial result, where there are several
+};
+
+// Rows, keys, row blocks of sequence s, as the kernel takes them (0 blocks: not its own).
+template <int BM, bool FEW>
+__device__ __forceinline__ void paged_sequence(const PagedArgs& a, int64_t s, int64_t& q0, int64_t& q1,
+                                               int& lk, int& blocks) {
+  if (a.q_start) {
+    q0 = start_at(a.q_start, (int)s, a.nq);
+    q1 = start_at(a.q_start, (int)s + 1, a.nq);
+  } else {
+    q0 = s * a.each;
+    q1 = q0 + a.each;
+  }
+  const int64_t l = a.k_start[s];
+  lk = (int)(l < 0 ? 0 : (l > a.keys_most ? a.keys_most : l));
+  const int64_t rows = q1 > q0 ? (q1 - q0) * a.g : 0;
+  blocks = (rows <= kAFewRows) == FEW ? (int)cdiv(rows, BM) : 0;
+}
+
+// Keys of a piece, from all sequences' real lengths: sum over the row blocks of their keys, T
+// tiles, is shared out over the workgroups that are wanted, so that pieces are alike whatever
+// the sequences are. Few rows: 256 workgroups (one per compute unit) with 320 keys at least, or
+// four rounds of them with 512. Others: two workgroups per compute unit, where there are not
+// as many already.
+template <int TILE, bool FEW>
+__device__ __forceinline__ int paged_per(const PagedArgs& a, int64_t tiles, int64_t blocks) {
+  if (a.slots == 0) return 0x7fffffff;
+  int64_t per;
+  if constexpr (FEW) {
+    const int64_t one = cdiv(tiles * a.hk, kAUnits), four = cdiv(tiles * a.hk, 4 * kAUnits);
+    per = min(max(one, (int64_t)(320 / TILE)), max(four, (int64_t)(512 / TILE)));
+  } else {
+    per = max(cdiv(tiles * a.hk, 2 * kAUnits) * (blocks * a.hk >= kAUnits ? 2 : 1), (int64_t)3);
+  }
+  return (int)min(per, (int64_t)(1 << 24)) * TILE;
+}
+
+// Inclusive sum over the lanes up to this one.
+__device__ __forceinline__ unsigned lanes_scan(unsigned v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const unsigned u = __shfl_up(v, d);
+    v += lane >= d ? u : 0u;
+  }
+  return v;
+}
+
+// Item `item` of the work: sequences in order, their row blocks, their pieces.
+// item < 0: the piece 0 of row `row` (of one key head) of sequence `sequence` is looked for.
+template <int BM, int TILE, bool FEW>
+__device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, int64_t item, int lane,
+                                                int64_t sequence = 0, int64_t row = 0) {
+  PagedWork r;
+  r.sequence = -1;
+  int64_t tiles = 0, all = 0;
+  for (int64_t s0 = 0; s0 < a.nseq; s0 += 64) {
+    int64_t q0, q1;
+    int lk, blocks = 0;
+    if (s0 + lane < a.nseq) paged_sequence<BM, FEW>(a, s0 + lane, q0, q1, lk, blocks);
+    if (blocks) {
+      tiles += (int64_t)blocks * ((lk + TILE - 1) / TILE);
+      all += blocks;
+    }
+  }
+  if (a.slots) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+      tiles += __shfl_xor(tiles, d);
+      all += __shfl_xor(all, d);
+    }
+  }
+  r.per = paged_per<TILE, FEW>(a, tiles, all);
+  int64_t before = 0;  // items of the sequences before
+  int64_t cut = 0;     // and those among them that leave partial results
+  for (int64_t s0 = 0; s0 < a.nseq; s0 += 64) {
+    int64_t q0 = 0, q1 = 0;
+    int lk = 0, blocks = 0;
+    if (s0 + lane < a.nseq) paged_sequence<BM, FEW>(a, s0 + lane, q0, q1, lk, blocks);
+    const int pieces = blocks ? max(1, (int)cdiv(lk, r.per)) : 0;
+    const unsigned count = (unsigned)blocks * (unsigned)pieces, part = pieces > 1 ? count : 0u;
+    const unsigned upto = lanes_scan(count, lane), parts = lanes_scan(part, lane);
+    const bool here = item >= 0 ? before + upto > item : s0 + lane == sequence;
+    const unsigned long long found = __ballot(here);
+    if (found) {
+      const int f = __ffsll(found) - 1;
+      const int64_t first = before + __builtin_amdgcn_readlane((int)(upto - count), f);
+      const int64_t slot = cut + __builtin_amdgcn_readlane((int)(parts - part), f);
+      r.sequence = (int)s0 + f;
+      r.q0 = __builtin_amdgcn_readlane((int)q0, f);
+      r.q1 = __builtin_amdgcn_readlane((int)q1, f);
+      r.lk = __builtin_amdgcn_readlane(lk, f);
+      r.pieces = __builtin_amdgcn_readlane(pieces, f);
+      const int64_t local = item >= 0 ? item - first : row / BM * r.pieces;
+      const int64_t block = r.pieces ? local / r.pieces : 0;
+      r.piece = (int)(local - block * r.pieces);
+      r.row0 = block * BM;
+      r.slot = r.pieces > 1 ? (int)(slot + local) : -1;
+      // starts that do not ascend can ask for more than there is room for
+      if (r.pieces > 1 && slot + local - r.piece + r.pieces > a.slots) r.sequence = -1;
+      return r;
+    }
+    before += (unsigned)__builtin_amdgcn_readlane((int)upto, 63);
+    cut += (unsigned)__builtin_amdgcn_readlane((int)parts, 63);
+  }
+  return r;
+}
+
+// Page numbers of a sequence's keys, one per lane for 16 keys each: lane i those from `from` +
+// `step`(i). Places past the sequence's last key repeat its last page; pages outside the
+// cache are moved to its ends.
+__device__ __forceinline__ int paged_number(const PagedArgs& a, const int32_t* row, int64_t key, int lk) {
+  key = key < lk ? key : lk - 1;
+  const int64_t p = row[key >> a.shift];
+  return (int)(p < 0 ? 0 : (p >= a.npages ? a.npages - 1 : p));
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Maximum over the two lanes (l, l + 32) that share a query.
@@ -146,8 +289,9 @@ __device__ __forceinline__ bf16x2_t pack2(float a, float b) {
 
 // D elements per row in LDS, of which the first DC (the head rounded up to 16) make
 // channels of O; PAD: the head is shorter than D.
-template <int D, int DC, bool PAD>
-__global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
+template <int D, int DC, bool PAD, class Args>
+__global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
+  constexpr bool kPaged = std::is_same<Args, PagedArgs>::value;
   constexpr int NW = 4, ST = 2;              // waves of 32 rows; tiles of keys in LDS
   constexpr int kBM = 32 * NW;
   constexpr int kPieces = D / 8;             // 16-byte pieces per row
@@ -161,14 +305,28 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int head = blockIdx.x % a.hk;
-  // the last slots first: a causal sequence's longest rows are its last
-  const int64_t slot = (int64_t)(gridDim.x / a.hk) - 1 - blockIdx.x / a.hk;
-  const Sequence sq = sequence_of<kBM>(a, slot, lane);
-  if (sq.index < 0) return;
-  const int64_t q0 = sq.q0, q1 = sq.q1, k0 = sq.k0, k1 = sq.k1;
-  const int lk = k1 > k0 ? (int)(k1 - k0) : 0;
+  int64_t q0, q1, k0 = 0, row0;
+  int lk;
+  [[maybe_unused]] PagedWork work;
+  if constexpr (kPaged) {
+    work = paged_work<kBM, kAKT, false>(a, blockIdx.x / a.hk, lane);
+    if (work.sequence < 0) return;
+    q0 = work.q0;
+    q1 = work.q1;
+    lk = work.lk;
+    row0 = work.row0;
+  } else {
+    // the last slots first: a causal sequence's longest rows are its last
+    const int64_t slot = (int64_t)(gridDim.x / a.hk) - 1 - blockIdx.x / a.hk;
+    const Sequence sq = sequence_of<kBM>(a, slot, lane);
+    if (sq.index < 0) return;
+    q0 = sq.q0;
+    q1 = sq.q1;
+    k0 = sq.k0;
+    lk = sq.k1 > k0 ? (int)(sq.k1 - k0) : 0;
+    row0 = (slot - (q0 * a.g / kBM + sq.index)) * kBM;
+  }
   const int64_t rows = q1 > q0 ? (q1 - q0) * a.g : 0;
-  const int64_t row0 = (slot - (q0 * a.g / kBM + sq.index)) * kBM;
   if (row0 < 0 || row0 >= rows) return;
   const int off = lk - (int)(q1 - q0);  // key of the same age as query 0
 
@@ -180,8 +338,17 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
   };
   const int64_t row_end = row0 + kBM < rows ? row0 + kBM : rows;
   const int keys = limit_of(row_end - 1);
-  const int per = (int)cdiv(cdiv(keys, kAKT), a.splits) * kAKT;
-  const int kbeg = min(keys, (int)blockIdx.y * per), kend = min(keys, kbeg + per);
+  int kbeg, kend;
+  bool cut;
+  if constexpr (kPaged) {
+    kbeg = min(keys, work.piece * work.per);
+    kend = keys - kbeg < work.per ? keys : kbeg + work.per;
+    cut = work.pieces > 1;
+  } else {
+    const int per = (int)cdiv(cdiv(keys, kAKT), a.splits) * kAKT;
+    kbeg = min(keys, (int)blockIdx.y * per), kend = min(keys, kbeg + per);
+    cut = a.splits > 1;
+  }
 
   // this lane's rows: r16 of each block of 16
   const int64_t wrow = row0 + wave * 32;
@@ -232,8 +399,8 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
   static_assert(D == 64 || NW * kRowsPer % 16 == 0, "one K swizzle per lane");
   const int ck = (lpp ^ swk) * 8;
   int cv = (lpp ^ swv) * 8;
-  const unsigned short* kb = a.k + k0 * a.k_token + head * a.k_head;
-  const unsigned short* vb = a.v + k0 * a.v_token + head * a.v_head;
+  const unsigned short* kb = a.k + (kPaged ? 0 : k0 * a.k_token) + head * a.k_head;
+  const unsigned short* vb = a.v + (kPaged ? 0 : k0 * a.v_token) + head * a.v_head;
   // K's pieces past the head are zero in every tile and never loaded; V's repeat its
   // first piece: they make channels that are not stored
   const bool in_k = !PAD || ck < a.d;
@@ -252,7 +419,8 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
   auto offsets = [&](int last) {  // rows past `last` read that one: they are masked
 #pragma unroll
     for (int i = 0; i < kLd; ++i) {
-      const unsigned row = min(row_w + NW * i * kRowsPer, last);
+      unsigned row = min(row_w + NW * i * kRowsPer, last);
+      if constexpr (kPaged) row &= 15;  // of its 16 keys
       vk[i] = (row * (unsigned)a.k_token + ck) * 2;
       vv[i] = (row * (unsigned)a.v_token + cv) * 2;
     }
@@ -260,13 +428,42 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
   // The next tile's loads, one by one: i < kLd of K, then kLd of V.
   const unsigned short *gk = kb, *gv = vb;
   unsigned dk = 0;
+  // Paged: a load's rows lie in 16 consecutive keys, which are of one page. Lane x of `here`
+  // holds the page of keys 16 x .. of the 1024 at hand, of `coming` of the next 1024.
+  [[maybe_unused]] int here = 0, coming = 0, tile_key = 0, tile_last = 0;
+  [[maybe_unused]] const int32_t* page_row = nullptr;
+  if constexpr (kPaged) page_row = a.pages + work.sequence * a.pages_row;
   auto next_tile = [&](int kt, int buf) {
     if (kt + kAKT > lk) offsets(lk - 1 - kt);  // the sequence's last tile
-    gk = kb + (int64_t)kt * a.k_token;
-    gv = vb + (int64_t)kt * a.v_token;
+    if constexpr (kPaged) {
+      if ((kt & 1023) == 0 || kt == kbeg) {
+        const int64_t from = kt & ~1023;
+        here = kt == kbeg ? paged_number(a, page_row, from + 16 * lane, lk) : coming;
+        coming = paged_number(a, page_row, from + 1024 + 16 * lane, lk);
+      }
+      tile_key = kt;
+      tile_last = min(lk - 1 - kt, kAKT - 1);
+    } else {
+      gk = kb + (int64_t)kt * a.k_token;
+      gv = vb + (int64_t)kt * a.v_token;
+    }
     dk = smb + buf * kTile + wave * 1024;
   };
   auto load = [&](int i) {
+    if constexpr (kPaged) {
+      const int x = i < kLd ? i : i - kLd;
+      // the first key of the 16 that the load's rows are of, and its place in the page
+      const int key = tile_key + (min((wave + NW * x) * kRowsPer, tile_last) & ~15);
+      const int64_t page = __builtin_amdgcn_readlane(here, (key >> 4) & 63);
+      const int in = key & ((1 << a.shift) - 1);
+      if (i < kLd) {
+        if (in_k) lds_dma1(vk[x], kb + page * a.k_page + (int64_t)in * a.k_token, dk + x * NW * 1024);
+      } else {
+        lds_dma1(vv[x], vb + page * a.v_page + (int64_t)in * a.v_token,
+                 dk + ST * kTile + x * NW * 1024);
+      }
+      return;
+    }
     if (i < kLd) {
       if (in_k) lds_dma1(vk[i], gk, dk + i * NW * 1024);
     } else {
@@ -489,11 +686,15 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
     l[rb] += __shfl_xor(l[rb], 32);
   }
   // element 4 quad + e of each block of 16 is in register e
-  if (a.splits > 1) {
+  if (cut) {
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb) {
       if (!valid[rb]) continue;
-      const int64_t at = ((int64_t)blockIdx.y * a.nq + q0 + tok[rb]) * (a.hk * a.g) + qh[rb];
+      int64_t at;
+      if constexpr (kPaged)
+        at = ((int64_t)work.slot * a.hk + head) * kBM + wave * 32 + rb * 16 + r16;
+      else
+        at = ((int64_t)blockIdx.y * a.nq + q0 + tok[rb]) * (a.hk * a.g) + qh[rb];
       // l = -1 marks a piece that saw keys, all of them with scores of -inf
       if (quad == 0)
         a.part_ml[at] = make_float2(m[rb], lim[rb] > kbeg && l[rb] == 0.f ? -1.f : l[rb]);
@@ -548,8 +749,9 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
 // a bf16 value and its rest, so 2^-16 of each is lost and not 2^-8 (error against 64 bits
 // 1.65e-3 rms, the output's own rounding, instead of 2.14e-3; 3% more time, as the matrix
 // cores are 9% busy). Everything else is as above.
-template <int D, int DC, bool PAD>
-__global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
+template <int D, int DC, bool PAD, class Args>
+__global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
+  constexpr bool kPaged = std::is_same<Args, PagedArgs>::value;
   constexpr int kBM = 32, kKeys = 32, kWaves = 4;
   constexpr int kPieces = D / 8, kRowB = D * 2;
   constexpr int kTile = kKeys * kRowB;     // one operand's tile
@@ -564,13 +766,27 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int head = blockIdx.x % a.hk;
-  const int64_t slot = (int64_t)(gridDim.x / a.hk) - 1 - blockIdx.x / a.hk;
-  const Sequence sq = sequence_of<kBM>(a, slot, lane);
-  if (sq.index < 0) return;
-  const int64_t q0 = sq.q0, q1 = sq.q1, k0 = sq.k0, k1 = sq.k1;
-  const int lk = k1 > k0 ? (int)(k1 - k0) : 0;
+  int64_t q0, q1, k0 = 0, row0;
+  int lk;
+  [[maybe_unused]] PagedWork work;
+  if constexpr (kPaged) {
+    work = paged_work<kBM, kKeys, true>(a, blockIdx.x / a.hk, lane);
+    if (work.sequence < 0) return;
+    q0 = work.q0;
+    q1 = work.q1;
+    lk = work.lk;
+    row0 = work.row0;
+  } else {
+    const int64_t slot = (int64_t)(gridDim.x / a.hk) - 1 - blockIdx.x / a.hk;
+    const Sequence sq = sequence_of<kBM>(a, slot, lane);
+    if (sq.index < 0) return;
+    q0 = sq.q0;
+    q1 = sq.q1;
+    k0 = sq.k0;
+    lk = sq.k1 > k0 ? (int)(sq.k1 - k0) : 0;
+    row0 = (slot - (q0 * a.g / kBM + sq.index)) * kBM;
+  }
   const int64_t rows = q1 > q0 ? (q1 - q0) * a.g : 0;
-  const int64_t row0 = (slot - (q0 * a.g / kBM + sq.index)) * kBM;
   if (row0 < 0 || row0 >= rows) return;
   const int off = lk - (int)(q1 - q0);
   auto limit_of = [&](int64_t r) {
@@ -580,8 +796,17 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
   };
   const int64_t row_end = row0 + kBM < rows ? row0 + kBM : rows;
   const int keys = limit_of(row_end - 1);
-  const int per = (int)cdiv(cdiv(keys, kKeys), a.splits) * kKeys;
-  const int kbeg = min(keys, (int)blockIdx.y * per), kend = min(keys, kbeg + per);
+  int kbeg, kend;
+  bool cut;
+  if constexpr (kPaged) {
+    kbeg = min(keys, work.piece * work.per);
+    kend = keys - kbeg < work.per ? keys : kbeg + work.per;
+    cut = work.pieces > 1;
+  } else {
+    const int per = (int)cdiv(cdiv(keys, kKeys), a.splits) * kKeys;
+    kbeg = min(keys, (int)blockIdx.y * per), kend = min(keys, kbeg + per);
+    cut = a.splits > 1;
+  }
   const int64_t mine = row0 + (lane & 31);
   const int64_t r = mine < row_end ? mine : row_end - 1;
   const int64_t tok = (unsigned)r / (unsigned)a.g;
@@ -620,11 +845,50 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
   const int lr = lane / kPieces, lpp = lane % kPieces;
   auto k_piece = [&](int i) { return (lpp ^ k_swizzle(i * kRowsPer + lr)) * 8; };
   int cv = (lpp ^ (D == 128 ? ((lr & 3) << 2) : (((lr >> 1) & 1) << 2))) * 8;
-  const unsigned short* kb = a.k + k0 * a.k_token + head * a.k_head;
+  const unsigned short* kb = a.k + (kPaged ? 0 : k0 * a.k_token) + head * a.k_head;
   if (PAD && cv >= a.d) cv = 0;
-  const unsigned short* vb = a.v + k0 * a.v_token + head * a.v_head;
+  const unsigned short* vb = a.v + (kPaged ? 0 : k0 * a.v_token) + head * a.v_head;
   const unsigned ob = lds_address(sm) + wave * 4 * kTile;
+  // Paged: the wave's tiles are 128 keys apart and of two times 16 keys, each of one page. Lanes
+  // 2x and 2x + 1 of `here` hold the pages of the tile x of the 32 at hand, of `coming` of the
+  // next 32.
+  [[maybe_unused]] int here = 0, coming = 0;
+  [[maybe_unused]] const int32_t* page_row = nullptr;
+  if constexpr (kPaged) page_row = a.pages + work.sequence * a.pages_row;
   auto issue = [&](int kt, int buf) {
+    if constexpr (kPaged) {
+      const int x = (kt - kbeg) / (kWaves * kKeys);
+      if ((x & 31) == 0) {
+        const int64_t key = (int64_t)kt + (lane >> 1) * (kWaves * kKeys) + (lane & 1) * 16;
+        here = x == 0 ? paged_number(a, page_row, key, lk) : coming;
+        coming = paged_number(a, page_row, key + 32 * kWaves * kKeys, lk);
+      }
+      const int last = min(kKeys, lk - kt) - 1, in_page = (1 << a.shift) - 1;
+      const unsigned short *gk[2], *gv[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t page = __builtin_amdgcn_readlane(here, 2 * (x & 31) + h);
+        const int in = (kt + 16 * h) & in_page;
+        gk[h] = kb + page * a.k_page + (int64_t)in * a.k_token;
+        gv[h] = vb + page * a.v_page + (int64_t)in * a.v_token;
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * kLd; ++i) {
+        const int y = i < kLd ? i : i - kLd;
+        const int h = min(y * kRowsPer, last) >> 4;  // the 16 keys that the load's rows are of
+        const unsigned row = min(y * kRowsPer + lr, last) & 15;
+        if (i < kLd) {
+          const int ck = k_piece(y);
+          if (!PAD || ck < a.d)
+            lds_dma1((row * (unsigned)a.k_token + ck) * 2, h ? gk[1] : gk[0],
+                     ob + 2 * buf * kTile + y * 1024);
+        } else {
+          lds_dma1((row * (unsigned)a.v_token + cv) * 2, h ? gv[1] : gv[0],
+                   ob + (2 * buf + 1) * kTile + y * 1024);
+        }
+      }
+      return;
+    }
     const unsigned short* gk = kb + (int64_t)kt * a.k_token;
     const unsigned short* gv = vb + (int64_t)kt * a.v_token;
     const int last = min(kKeys, lk - kt) - 1;  // rows past the keys read the last: masked
@@ -838,8 +1102,12 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
     f[w] = lw == 0.f ? 0.f : exp2_fast(sm_m[w][rr] - rt);
     lt += lw * f[w];
   }
-  const int64_t at = ((int64_t)blockIdx.y * a.nq + q0 + ot) * (a.hk * a.g) + oh;
-  if (a.splits > 1 && (tid & 7) == 0)
+  int64_t at;
+  if constexpr (kPaged)
+    at = ((int64_t)work.slot * a.hk + head) * kBM + rr;
+  else
+    at = ((int64_t)blockIdx.y * a.nq + q0 + ot) * (a.hk * a.g) + oh;
+  if (cut && (tid & 7) == 0)
     a.part_ml[at] = make_float2(mt, min(vis, kend) > kbeg && lt == 0.f ? -1.f : lt);
   const float inv = vis > 0 ? 1.0f / lt : 0.f;
 #pragma unroll
@@ -851,7 +1119,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
     for (int w = 0; w < kWaves; ++w)
       if (f[w] != 0.f)
         v += *(const f32x4_t*)((const float*)(sm + w * 4 * kTile) + rr * kOutW + e) * f[w];
-    if (a.splits > 1) {
+    if (cut) {
       *(f32x4_t*)(a.part_o + at * a.d + e) = v;
     } else {
       const bf16x2_t w0 = vis > 0 ? pack2(v[0] * inv, v[1] * inv) : pack2(0.f, 0.f);
@@ -869,30 +1137,28 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttnArgs a) {
 // eight; 16 of 64 heads in eight, the other way round, 278 and 272.)
 constexpr int kAJoinSplits = 8, kAJoinRows = 2048;
 
+// Pieces 0 .. splits - 1 of one row, whose results are at ml + s * step and po + s * step * d,
+// joined into o (d elements) by `groups` groups of 32 lanes (1, or the workgroup's 8), grp and
+// lane being this thread's.
 template <bool FEW>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+__device__ __forceinline__ void join_row(const float2* ml, const float* po, int64_t step, int splits,
+                                         int d, int grp, int lane, unsigned short* out) {
   __shared__ float part[FEW ? 1 : 8][132];  // 128 elements, l, any
-  const int grp = threadIdx.x / 32, lane = threadIdx.x & 31, e = lane * 4;
-  const int hq = a.hk * a.g;
-  const int64_t row = FEW ? (int64_t)blockIdx.x * 8 + grp : blockIdx.x;
-  const int64_t tok = row / hq;
-  const int qh = (int)(row - tok * hq);
-  if (tok < start_at(a.q_start, 0, a.nq) || tok >= start_at(a.q_start, a.nseq, a.nq)) return;
-  const int64_t step = a.nq * hq;
+  const int e = lane * 4;
   float m = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.part_ml[s * step + row].x);
+  for (int s = lane; s < splits; s += 32) m = fmaxf(m, ml[s * step].x);
 #pragma unroll
   for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x, 32));
   const float ref = m == -INFINITY ? 0.f : m;
   f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
   float l = 0.f, any = 0.f;
-  for (int s = FEW ? 0 : grp; s < a.splits; s += FEW ? 1 : 8) {
-    const float2 ml = a.part_ml[s * step + row];
-    if (ml.y != 0.f) any = 1.f;  // 0: the piece saw no key
-    if (ml.y <= 0.f) continue;   // -1: only scores of -inf
-    const float f = exp2_fast(ml.x - ref);
-    l += ml.y * f;
-    if (e < a.d) o += *(const f32x4_t*)(a.part_o + (s * step + row) * a.d + e) * f;
+  for (int s = FEW ? 0 : grp; s < splits; s += FEW ? 1 : 8) {
+    const float2 y = ml[s * step];
+    if (y.y != 0.f) any = 1.f;  // 0: the piece saw no key
+    if (y.y <= 0.f) continue;   // -1: only scores of -inf
+    const float f = exp2_fast(y.x - ref);
+    l += y.y * f;
+    if (e < d) o += *(const f32x4_t*)(po + s * step * d + e) * f;
   }
   if constexpr (!FEW) {
 #pragma unroll
@@ -914,29 +1180,118 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
       any += part[s][129];
     }
   }
-  if (e >= a.d) return;
+  if (e >= d) return;
   // keys seen, but every score -inf: l is 0 and there is no softmax (NaN)
   u16x4_t w;
 #pragma unroll
   for (int y = 0; y < 4; ++y) w[y] = any > 0.f ? f32_to_bf16_rne(o[y] / l) : (unsigned short)0;
-  *(u16x4_t*)(a.o + tok * a.o_token + qh * a.o_head + e) = w;
+  *(u16x4_t*)(out + e) = w;
 }
 
-template <int D, int DC, bool PAD>
-void launch_kernel(const AttnArgs& a, hipStream_t s) {
-  const int64_t slots = a.nq * a.g / 128 + a.nseq;
-  hipLaunchKernelGGL((attention_kernel<D, DC, PAD>),
-                     dim3((unsigned)(slots * a.hk), (unsigned)a.splits), dim3(256), 0, s, a);
+template <bool FEW>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+  const int grp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int hq = a.hk * a.g;
+  const int64_t row = FEW ? (int64_t)blockIdx.x * 8 + grp : blockIdx.x;
+  const int64_t tok = row / hq;
+  const int qh = (int)(row - tok * hq);
+  if (tok < start_at(a.q_start, 0, a.nq) || tok >= start_at(a.q_start, a.nseq, a.nq)) return;
+  join_row<FEW>(a.part_ml + row, a.part_o + row * a.d, a.nq * hq, a.splits, a.d, grp, lane,
+                a.o + tok * a.o_token + qh * a.o_head);
 }
 
-template <int D, int DC, bool PAD>
-void launch_few(const AttnArgs& a, hipStream_t s) {
-  const int64_t slots = a.nq * a.g / 32 + a.nseq;
-  hipLaunchKernelGGL((attention_few_kernel<D, DC, PAD>),
-                     dim3((unsigned)(slots * a.hk), (unsigned)a.splits), dim3(256), 0, s, a);
+// The same for rows of a paged call, those whose keys were cut. Few rows: workgroup x has row
+// x % rows of key head (x / rows) % hk of a sequence; otherwise x is a (token, query head).
+template <int BM, int TILE, bool FEWROWS>
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int rows) {
+  const int lane = threadIdx.x & 63;
+  int64_t s, row;
+  int head;
+  if constexpr (FEWROWS) {
+    const int64_t x = blockIdx.x / rows;
+    row = blockIdx.x - x * rows;
+    s = x / a.hk;
+    head = (int)(x - s * a.hk);
+  } else {
+    const int hq = a.hk * a.g;
+    const int64_t tok = blockIdx.x / hq;
+    const int qh = (int)(blockIdx.x - tok * hq);
+    int64_t q0;
+    if (a.q_start) {
+      // the last sequence that begins at or before the token
+      int64_t lo = 0, len = a.nseq;
+      for (;;) {
+        const int64_t step = (len + 63) >> 6, at = lane * step;
+        const bool before = at < len && start_at(a.q_start, (int)(lo + at), a.nq) <= tok;
+        const int count = __popcll(__ballot(before));
+        if (count == 0) return;
+        lo += (count - 1) * step;
+        if (step == 1) break;
+        len = min(step, len - (count - 1) * step);
+      }
+      s = lo;
+      q0 = start_at(a.q_start, (int)s, a.nq);
+      if (tok >= start_at(a.q_start, (int)s + 1, a.nq)) return;
+    } else {
+      s = tok / a.each;
+      q0 = s * a.each;
+    }
+    head = qh / a.g;
+    row = (tok - q0) * a.g + qh - head * a.g;
+  }
+  const PagedWork w = paged_work<BM, TILE, FEWROWS>(a, -1, lane, s, row);
+  if (w.sequence < 0 || w.pieces < 2 || row >= (w.q1 - w.q0) * a.g) return;
+  const int64_t tok = w.q0 + row / a.g;
+  const int qh = head * a.g + (int)(row % a.g);
+  const int64_t at = ((int64_t)w.slot * a.hk + head) * BM + (row - w.row0);
+  join_row<false>(a.part_ml + at, a.part_o + at * a.d, (int64_t)a.hk * BM, w.pieces, a.d,
+                  threadIdx.x / 32, threadIdx.x & 31, a.o + tok * a.o_token + qh * a.o_head);
 }
 
-constexpr int kAUnits = 256;  // compute units
+template <int D, int DC, bool PAD, class Args>
+void launch_kernel(const Args& a, dim3 groups, hipStream_t s) {
+  hipLaunchKernelGGL((attention_kernel<D, DC, PAD, Args>), groups, dim3(256), 0, s, a);
+}
+
+template <int D, int DC, bool PAD, class Args>
+void launch_few(const Args& a, dim3 groups, hipStream_t s) {
+  hipLaunchKernelGGL((attention_few_kernel<D, DC, PAD, Args>), groups, dim3(256), 0, s, a);
+}
+
+// The kernel for heads of a.d elements.
+template <class Args>
+void launch_by_head(const Args& a, bool few, dim3 groups, hipStream_t s) {
+  if (few) {
+    if (a.d < 64)
+      launch_few<64, 64, true>(a, groups, s);
+    else if (a.d == 64)
+      launch_few<64, 64, false>(a, groups, s);
+    else if (a.d < 128)
+      launch_few<128, 128, true>(a, groups, s);
+    else
+      launch_few<128, 128, false>(a, groups, s);
+    return;
+  }
+  switch (cdiv(a.d, 16)) {
+    case 1:
+    case 2: launch_kernel<64, 32, true>(a, groups, s); break;
+    case 3: launch_kernel<64, 48, true>(a, groups, s); break;
+    case 4:
+      if (a.d < 64)
+        launch_kernel<64, 64, true>(a, groups, s);
+      else
+        launch_kernel<64, 64, false>(a, groups, s);
+      break;
+    case 5: launch_kernel<128, 80, true>(a, groups, s); break;
+    case 6: launch_kernel<128, 96, true>(a, groups, s); break;
+    case 7: launch_kernel<128, 112, true>(a, groups, s); break;
+    default:
+      if (a.d < 128)
+        launch_kernel<128, 128, true>(a, groups, s);
+      else
+        launch_kernel<128, 128, false>(a, groups, s);
+  }
+}
 
 struct AttnPlan {
   bool few;    // 32-row workgroups whose waves share the keys
@@ -1052,36 +1407,8 @@ hipError_t launch_attention(const void* Q, const void* K, const void* V, const i
   a.part_o = workspace
                  ? (float*)((char*)workspace + part_ml_bytes(a.splits * p->nq * p->hq))
                  : nullptr;
-  if (plan.few) {
-    if (p->d < 64)
-      launch_few<64, 64, true>(a, s);
-    else if (p->d == 64)
-      launch_few<64, 64, false>(a, s);
-    else if (p->d < 128)
-      launch_few<128, 128, true>(a, s);
-    else
-      launch_few<128, 128, false>(a, s);
-  } else {
-    switch (cdiv(p->d, 16)) {
-      case 1:
-      case 2: launch_kernel<64, 32, true>(a, s); break;
-      case 3: launch_kernel<64, 48, true>(a, s); break;
-      case 4:
-        if (p->d < 64)
-          launch_kernel<64, 64, true>(a, s);
-        else
-          launch_kernel<64, 64, false>(a, s);
-        break;
-      case 5: launch_kernel<128, 80, true>(a, s); break;
-      case 6: launch_kernel<128, 96, true>(a, s); break;
-      case 7: launch_kernel<128, 112, true>(a, s); break;
-      default:
-        if (p->d < 128)
-          launch_kernel<128, 128, true>(a, s);
-        else
-          launch_kernel<128, 128, false>(a, s);
-    }
-  }
+  const int64_t slots = a.nq * a.g / (plan.few ? 32 : 128) + a.nseq;
+  launch_by_head(a, plan.few, dim3((unsigned)(slots * a.hk), (unsigned)a.splits), s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t rows = p->nq * p->hq;
@@ -1089,6 +1416,126 @@ hipError_t launch_attention(const void* Q, const void* K, const void* V, const i
     hipLaunchKernelGGL(attention_join_kernel<true>, dim3((unsigned)cdiv(rows, 8)), dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL(attention_join_kernel<false>, dim3((unsigned)rows), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- paged: plan and launches
+
+namespace {
+
+struct PagedPlan {
+  bool few, many;               // whether either kernel has sequences to take
+  int64_t few_items, many_items;  // work items a key head, at most
+  int few_slots, many_slots;      // partial results a key head
+  int64_t few_rows;             // rows of a sequence of the first kind
+};
+
+// What the device can find there, from sizes alone: sequences of up to kAFewRows rows have one
+// row block, others one per 128 rows or part of them; pieces are cut from T tiles so that
+// T / per <= target / hk, and there are T / per + (row blocks) of them at most, those of cut
+// row blocks no more than 2 T / per.
+PagedPlan plan_of(const th_paged_cache* c, const th_paged_params* p) {
+  PagedPlan r = {};
+  const int64_t g = p->hq / c->hk, nseq = c->nseq, most = c->width * c->page_tokens;
+  const int64_t each = p->even ? p->nq / nseq * g : 0;
+  r.few = p->nq > 0 && (p->even ? each <= kAFewRows : g <= kAFewRows);
+  r.many = p->nq > 0 && (p->even ? each > kAFewRows : p->nq * g > kAFewRows);
+  r.few_rows = p->even ? each : kAFewRows;
+  auto bound = [&](int64_t blocks, int64_t target, int64_t least, int64_t& items, int& slots) {
+    const int64_t pieces = cdiv(most, least);
+    slots = pieces > 1 ? (int)(2 * target / c->hk) : 0;
+    items = slots ? target / c->hk + blocks : blocks;
+    if (slots && pieces < (1 << 20) && blocks * pieces < items) items = blocks * pieces;
+    if (slots > items) slots = (int)items;
+  };
+  if (r.few)
+    bound(nseq < p->nq ? nseq : p->nq, 4 * kAUnits, 320, r.few_items, r.few_slots);
+  if (r.many) {
+    const int64_t longer = p->nq * g / (kAFewRows + 1);
+    bound(p->nq * g / 128 + (nseq < longer ? nseq : longer), 2 * kAUnits, 3 * kAKT, r.many_items,
+          r.many_slots);
+  }
+  return r;
+}
+
+size_t paged_rows(const PagedPlan& r, const th_paged_cache* c) {
+  return ((size_t)r.few_slots * 32 + (size_t)r.many_slots * 128) * (size_t)c->hk;
+}
+
+}  // namespace
+
+int64_t paged_attention_workgroups(const th_paged_cache* c, const th_paged_params* p) {
+  if (p->nq == 0) return 0;
+  const PagedPlan r = plan_of(c, p);
+  int64_t most = (r.few_items > r.many_items ? r.few_items : r.many_items) * c->hk;
+  if (r.few_slots) most = std::max(most, c->nseq * c->hk * r.few_rows);  // of the join
+  if (r.many_slots) most = std::max(most, p->nq * p->hq);
+  return most;
+}
+
+size_t paged_attention_workspace_bytes(const th_paged_cache* c, const th_paged_params* p) {
+  if (p->nq == 0) return 0;
+  const size_t rows = paged_rows(plan_of(c, p), c);
+  return rows ? part_ml_bytes((int64_t)rows) + rows * (size_t)c->d * sizeof(float) : 0;
+}
+
+hipError_t launch_paged_attention(const void* Q, const int32_t* q_start, const th_paged_cache* c,
+                                  const th_paged_params* p, void* O, void* workspace, hipStream_t s) {
+  PagedArgs a = {};
+  a.q = (const unsigned short*)Q;
+  a.k = (const unsigned short*)c->k;
+  a.v = (const unsigned short*)c->v;
+  a.o = (unsigned short*)O;
+  a.q_token = p->q_token;
+  a.q_head = p->q_head;
+  a.k_token = c->k_token;
+  a.k_head = c->k_head;
+  a.v_token = c->v_token;
+  a.v_head = c->v_head;
+  a.o_token = p->o_token;
+  a.o_head = p->o_head;
+  a.q_start = q_start;
+  a.k_start = c->k_len;
+  a.nq = p->nq;
+  a.nseq = (int)c->nseq;
+  a.hk = (int)c->hk;
+  a.g = (int)(p->hq / c->hk);
+  a.d = (int)c->d;
+  a.causal = p->causal != 0;
+  a.c = (float)(p->scale * 1.4426950408889634);
+  a.pages = c->pages;
+  a.pages_row = c->pages_row;
+  a.k_page = c->k_page;
+  a.v_page = c->v_page;
+  a.npages = c->npages;
+  a.keys_most = c->npages > 0 ? c->width * c->page_tokens : 0;
+  a.each = p->nq / c->nseq;
+  a.shift = __builtin_ctzll((unsigned long long)c->page_tokens);
+  const PagedPlan plan = plan_of(c, p);
+  const size_t rows = workspace ? paged_rows(plan, c) : 0;
+  a.part_ml = (float2*)workspace;
+  a.part_o = workspace ? (float*)((char*)workspace + part_ml_bytes((int64_t)rows)) : nullptr;
+  if (plan.few) {
+    a.slots = workspace ? plan.few_slots : 0;
+    launch_by_head(a, true, dim3((unsigned)(plan.few_items * a.hk)), s);
+    if (a.slots)
+      hipLaunchKernelGGL((paged_join_kernel<32, 32, true>),
+                         dim3((unsigned)(c->nseq * a.hk * plan.few_rows)), dim3(256), 0, s, a,
+                         (int)plan.few_rows);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !plan.many) return e;
+  }
+  if (plan.many) {
+    if (workspace) {  // behind the results of the few rows
+      a.part_ml += (int64_t)plan.few_slots * 32 * a.hk;
+      a.part_o += (int64_t)plan.few_slots * 32 * a.hk * a.d;
+    }
+    a.slots = workspace ? plan.many_slots : 0;
+    launch_by_head(a, false, dim3((unsigned)(plan.many_items * a.hk)), s);
+    if (a.slots)
+      hipLaunchKernelGGL((paged_join_kernel<128, kAKT, false>), dim3((unsigned)(p->nq * p->hq)),
+                         dim3(256), 0, s, a, 0);
+  }
   return hipGetLastError();
 }
 

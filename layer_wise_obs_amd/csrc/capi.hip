@@ -901,6 +901,128 @@ th_status th_rms_norm(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t
   return TH_OK;
 }
 
+namespace {
+// A microscaled matrix [n, b]; for products its rows are read 16 bytes at a time.
+th_status check_mx(const th_mx* m, int64_t n, int64_t b, bool product) {
+  if (!m) return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (m->type != TH_MX_E4M3 && m->type != TH_MX_E2M1)
+    return fail(TH_ERR_INVALID_ARG, "unknown microscaled type");
+  if (n < 0 || n >= ((int64_t)1 << 31) || b < 32 || b % 32 || b >= ((int64_t)1 << 31))
+    return fail(TH_ERR_INVALID_ARG, "needs 0 <= n < 2^31, 32 <= b < 2^31 and b % 32 == 0");
+  if (m->ld < (m->type == TH_MX_E4M3 ? b : b / 2) || m->lds < b / 32)
+    return fail(TH_ERR_INVALID_ARG, "a row pitch is smaller than a row");
+  if (n > 0 && (!m->elements || !m->scales)) return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (n > 0 && m->elements == m->scales)
+    return fail(TH_ERR_INVALID_ARG, "elements and scales must not overlap");
+  if (product && ((m->ld | m->lds | (int64_t)(uintptr_t)m->elements | (int64_t)(uintptr_t)m->scales) & 15))
+    return fail(TH_ERR_INVALID_ARG, "elements and scales: 16-byte alignment and pitches of a multiple of 16");
+  if (product && (m->ld >= ((int64_t)1 << 22) || m->lds >= ((int64_t)1 << 22)))
+    return fail(TH_ERR_INVALID_ARG, "row pitches must be < 2^22 bytes");
+  return TH_OK;
+}
+}  // namespace
+
+th_status th_mx_quantize(const void* X, th_dtype xdt, int64_t n, int64_t b, int64_t ldx,
+                         const th_mx* Y, th_stream_t stream) {
+  if (!dtype_ok(xdt)) return fail(TH_ERR_INVALID_ARG, "unknown dtype");
+  th_status st = check_mx(Y, n, b, false);
+  if (st != TH_OK) return st;
+  if (ldx < b) return fail(TH_ERR_INVALID_ARG, "a row pitch is smaller than b");
+  if (n == 0) return TH_OK;
+  if (!X) return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (X == Y->elements || X == Y->scales)
+    return fail(TH_ERR_INVALID_ARG, "Y must not be the input");
+  TH_HIP(launch_mx_quantize(X, xdt, ldx, n, b, *Y, (hipStream_t)stream), "mx quantize");
+  return TH_OK;
+}
+
+th_status th_mx_dequantize(const th_mx* X, int64_t n, int64_t b, void* Y, th_dtype ydt,
+                           int64_t ldy, th_stream_t stream) {
+  if (!dtype_ok(ydt)) return fail(TH_ERR_INVALID_ARG, "unknown dtype");
+  th_status st = check_mx(X, n, b, false);
+  if (st != TH_OK) return st;
+  if (ldy < b) return fail(TH_ERR_INVALID_ARG, "a row pitch is smaller than b");
+  if (n == 0) return TH_OK;
+  if (!Y) return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (Y == X->elements || Y == X->scales)
+    return fail(TH_ERR_INVALID_ARG, "Y must not be the input");
+  TH_HIP(launch_mx_dequantize(*X, n, b, Y, ydt, ldy, (hipStream_t)stream), "mx dequantize");
+  return TH_OK;
+}
+
+th_status th_mx_linear_workspace_size(int32_t xtype, int64_t n, int64_t b, int64_t c, th_dtype ydt,
+                                      size_t* bytes) {
+  if (!bytes) return fail(TH_ERR_INVALID_ARG, "bytes is NULL");
+  if (xtype != TH_MX_E4M3 && xtype != TH_MX_E2M1)
+    return fail(TH_ERR_INVALID_ARG, "unknown microscaled type");
+  if (!dtype_ok(ydt)) return fail(TH_ERR_INVALID_ARG, "unknown dtype");
+  if (b % 32) return fail(TH_ERR_INVALID_ARG, "needs b % 32 == 0");
+  th_status st = check_linear_sizes(n, b, c);
+  if (st != TH_OK) return st;
+  *bytes = n == 0 ? 0 : mx_linear_workspace_floats(xtype, n, b, c, ydt) * sizeof(float);
+  return TH_OK;
+}
+
+th_status th_mx_linear(const th_mx* X, const th_mx* W, int64_t n, int64_t b, int64_t c,
+                       const void* bias, th_activation act, const void* residual, int64_t ldr,
+                       void* Y, th_dtype ydt, int64_t ldy, void* workspace, size_t workspace_bytes,
+                       th_stream_t stream) {
+  if (!dtype_ok(ydt)) return fail(TH_ERR_INVALID_ARG, "unknown dtype");
+  th_status st = check_linear_sizes(n, b, c);
+  if (st == TH_OK) st = check_mx(X, n, b, true);
+  if (st == TH_OK) st = check_mx(W, c, b, true);
+  if (st != TH_OK) return st;
+  if (W->type != TH_MX_E2M1) return fail(TH_ERR_INVALID_ARG, "W must be e2m1");
+  if (act < TH_ACT_NONE || act > TH_ACT_GELU) return fail(TH_ERR_INVALID_ARG, "unknown activation");
+  if (ldy < c || (residual && ldr < c))
+    return fail(TH_ERR_INVALID_ARG, "a row pitch is smaller than c");
+  if (n == 0) return TH_OK;
+  if (!Y) return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (Y == X->elements || Y == X->scales || Y == W->elements || Y == W->scales || Y == bias)
+    return fail(TH_ERR_INVALID_ARG, "Y must not be an input but the residual");
+  if (Y == residual && ldr != ldy)
+    return fail(TH_ERR_INVALID_ARG, "a residual in place needs Y's pitch");
+  if (workspace && ((uintptr_t)workspace & 15))
+    return fail(TH_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  const size_t need = mx_linear_workspace_floats(X->type, n, b, c, ydt) * sizeof(float);
+  if (workspace && workspace_bytes < need) return fail(TH_ERR_WORKSPACE, "workspace too small");
+  TH_HIP(launch_mx_linear(*X, *W, n, b, c, (const unsigned short*)bias, act, residual, ldr, Y, ydt,
+                          ldy, (float*)workspace, (hipStream_t)stream),
+         "mx linear");
+  return TH_OK;
+}
+
+th_status th_add_rms_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, th_dtype xdt,
+                          int64_t n, int64_t b, const void* weight, double eps, void* sum,
+                          int64_t ldsum, void* Y, th_dtype ydt, int64_t ldy, const th_mx* Y_mx,
+                          th_stream_t stream) {
+  if (!dtype_ok(xdt) || (!Y_mx && !dtype_ok(ydt))) return fail(TH_ERR_INVALID_ARG, "unknown dtype");
+  if (n < 0 || n >= ((int64_t)1 << 31) || b < 1)
+    return fail(TH_ERR_INVALID_ARG, "needs 0 <= n < 2^31 and b >= 1");
+  if (Y_mx) {
+    if (Y) return fail(TH_ERR_INVALID_ARG, "one of Y and Y_mx");
+    th_status st = check_mx(Y_mx, n, b, false);
+    if (st != TH_OK) return st;
+  }
+  if (ldx < b || (R && ldr < b) || (sum && ldsum < b) || (!Y_mx && ldy < b))
+    return fail(TH_ERR_INVALID_ARG, "a row pitch is smaller than b");
+  if (!eps_ok(eps)) return fail(TH_ERR_INVALID_ARG, "eps must be 0 or a normal fp32 number > 0");
+  if (!R && sum) return fail(TH_ERR_INVALID_ARG, "sum goes with R");
+  if (!weight || (n > 0 && (!X || (!Y && !Y_mx)))) return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (n == 0) return TH_OK;
+  if ((sum && sum == X && ldsum != ldx) || (sum && sum == R && ldsum != ldr))
+    return fail(TH_ERR_INVALID_ARG, "a sum in place needs the same pitch");
+  if (sum && sum == weight) return fail(TH_ERR_INVALID_ARG, "sum must not be the weight");
+  const void* out[2] = {Y_mx ? Y_mx->elements : Y, Y_mx ? Y_mx->scales : nullptr};
+  for (const void* o : out)
+    if (o && (o == X || o == R || o == sum || o == weight))
+      return fail(TH_ERR_INVALID_ARG, "Y must not be another argument");
+  TH_HIP(launch_add_rms_norm(X, xdt, ldx, R, ldr, weight, sum, ldsum, Y, ydt, ldy, Y_mx, n, b, eps,
+                             (hipStream_t)stream),
+         "add rms norm");
+  return TH_OK;
+}
+
 th_status th_rotary_freqs(int64_t rot, const th_rotary_scaling* scaling, double* freqs) {
   if (rot < 0 || rot % 2 || rot > 256)
     return fail(TH_ERR_INVALID_ARG, "rot must be even, 0 <= rot <= 256");
@@ -1043,6 +1165,113 @@ th_status th_attention(const void* Q, const void* K, const void* V, th_dtype dt,
   TH_HIP(launch_attention(Q, K, V, q_start, k_start ? k_start : q_start, p, O, workspace,
                           (hipStream_t)stream),
          "attention");
+  return TH_OK;
+}
+
+namespace {
+th_status check_cache(const th_paged_cache* c) {
+  const int64_t most = ((int64_t)1 << 31) - ((int64_t)1 << 16);
+  if (!c) return fail(TH_ERR_INVALID_ARG, "cache is NULL");
+  if (c->npages < 0 || c->npages >= ((int64_t)1 << 31))
+    return fail(TH_ERR_INVALID_ARG, "needs 0 <= npages < 2^31");
+  if (c->page_tokens < 16 || c->page_tokens > 65536 || (c->page_tokens & (c->page_tokens - 1)))
+    return fail(TH_ERR_INVALID_ARG, "page_tokens must be a power of two, 16 .. 65536");
+  if (c->hk < 1 || c->hk >= ((int64_t)1 << 16)) return fail(TH_ERR_INVALID_ARG, "needs 1 <= hk < 2^16");
+  if (c->d < 8 || c->d > 128 || c->d % 8)
+    return fail(TH_ERR_INVALID_ARG, "needs 8 <= d <= 128 and d % 8 == 0");
+  if (c->nseq < 1 || c->nseq >= ((int64_t)1 << 24))
+    return fail(TH_ERR_INVALID_ARG, "needs 1 <= nseq < 2^24");
+  if (c->width < 0 || c->pages_row < c->width || c->width >= most / c->page_tokens)
+    return fail(TH_ERR_INVALID_ARG, "needs 0 <= width <= pages_row, width * page_tokens < 2^31 - 2^16");
+  const int64_t strides[6] = {c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head};
+  for (int64_t v : strides)
+    if (v < 0 || v % 8) return fail(TH_ERR_INVALID_ARG, "strides must be multiples of 8, >= 0");
+  if (c->k_token >= ((int64_t)1 << 24) || c->v_token >= ((int64_t)1 << 24))
+    return fail(TH_ERR_INVALID_ARG, "k_token and v_token must be < 2^24");
+  if (((uintptr_t)c->k | (uintptr_t)c->v) & 15)
+    return fail(TH_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  if (!c->k_len || (c->width > 0 && !c->pages) || (c->npages > 0 && (!c->k || !c->v)))
+    return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  return TH_OK;
+}
+
+th_status check_paged(const th_paged_cache* c, const th_paged_params* p) {
+  const int64_t rows = ((int64_t)1 << 31) - ((int64_t)1 << 16);
+  th_status st = check_cache(c);
+  if (st != TH_OK) return st;
+  if (!p) return fail(TH_ERR_INVALID_ARG, "params is NULL");
+  if (p->hq < 1 || p->hq >= ((int64_t)1 << 16) || p->hq % c->hk)
+    return fail(TH_ERR_INVALID_ARG, "needs 1 <= hq < 2^16 and hk | hq");
+  if (p->nq < 0 || p->nq >= rows || p->nq * (p->hq / c->hk) >= rows)
+    return fail(TH_ERR_INVALID_ARG, "needs 0 <= nq, nq * hq / hk < 2^31 - 2^16");
+  if (p->even && p->nq % c->nseq)
+    return fail(TH_ERR_INVALID_ARG, "without q_start nq has to be a multiple of nseq");
+  const int64_t strides[4] = {p->q_token, p->q_head, p->o_token, p->o_head};
+  for (int64_t v : strides)
+    if (v < 0 || v % 8) return fail(TH_ERR_INVALID_ARG, "strides must be multiples of 8, >= 0");
+  if (heads_overlap(p->nq, p->hq, c->d, p->o_token, p->o_head))
+    return fail(TH_ERR_INVALID_ARG, "the heads of O overlap");
+  if (!(p->scale > 0.0) || !fp32_normal(p->scale * 1.4426950408889634))
+    return fail(TH_ERR_INVALID_ARG, "scale must be > 0 and scale * log2(e) a normal fp32 number");
+  // a launch has less than 2^32 threads, 256 to a workgroup
+  if (paged_attention_workgroups(c, p) >= ((int64_t)1 << 24))
+    return fail(TH_ERR_INVALID_ARG, "too many rows, heads and sequences for one launch");
+  return TH_OK;
+}
+}  // namespace
+
+th_status th_cache_store(const void* K, int64_t k_token, int64_t k_head, const void* V,
+                         int64_t v_token, int64_t v_head, th_dtype dt, int64_t nq,
+                         const int32_t* q_start, const th_paged_cache* cache,
+                         th_stream_t stream) {
+  if (dt != TH_BF16) return fail(TH_ERR_INVALID_ARG, "bf16 only");
+  th_status st = check_cache(cache);
+  if (st != TH_OK) return st;
+  if (nq < 0 || nq >= ((int64_t)1 << 31)) return fail(TH_ERR_INVALID_ARG, "needs 0 <= nq < 2^31");
+  if (!q_start && nq % cache->nseq)
+    return fail(TH_ERR_INVALID_ARG, "without q_start nq has to be a multiple of nseq");
+  const int64_t strides[4] = {k_token, k_head, v_token, v_head};
+  for (int64_t v : strides)
+    if (v < 0 || v % 8) return fail(TH_ERR_INVALID_ARG, "strides must be multiples of 8, >= 0");
+  if (((uintptr_t)K | (uintptr_t)V) & 15)
+    return fail(TH_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  if (nq == 0 || cache->npages == 0 || cache->width == 0) return TH_OK;
+  if (!K || !V) return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (K == cache->k || K == cache->v || V == cache->k || V == cache->v)
+    return fail(TH_ERR_INVALID_ARG, "the new tokens must not be the cache");
+  TH_HIP(launch_cache_store(K, k_token, k_head, V, v_token, v_head, nq, q_start, cache,
+                            (hipStream_t)stream),
+         "cache store");
+  return TH_OK;
+}
+
+th_status th_paged_attention_workspace_size(const th_paged_cache* cache, const th_paged_params* p,
+                                            size_t* bytes) {
+  if (!bytes) return fail(TH_ERR_INVALID_ARG, "bytes is NULL");
+  th_status st = check_paged(cache, p);
+  if (st != TH_OK) return st;
+  *bytes = paged_attention_workspace_bytes(cache, p);
+  return TH_OK;
+}
+
+th_status th_paged_attention(const void* Q, th_dtype dt, const int32_t* q_start,
+                             const th_paged_cache* cache, const th_paged_params* p, void* O,
+                             void* workspace, size_t workspace_bytes, th_stream_t stream) {
+  if (dt != TH_BF16) return fail(TH_ERR_INVALID_ARG, "bf16 only");
+  th_status st = check_paged(cache, p);
+  if (st != TH_OK) return st;
+  if ((p->even != 0) != (q_start == nullptr))
+    return fail(TH_ERR_INVALID_ARG, "even has to be set without q_start, and only then");
+  if (((uintptr_t)Q | (uintptr_t)O | (uintptr_t)workspace) & 15)
+    return fail(TH_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  if (p->nq == 0) return TH_OK;
+  if (!Q || !O) return fail(TH_ERR_INVALID_ARG, "NULL argument");
+  if (O == Q || O == cache->k || O == cache->v)
+    return fail(TH_ERR_INVALID_ARG, "O must not be an input");
+  if (workspace && workspace_bytes < paged_attention_workspace_bytes(cache, p))
+    return fail(TH_ERR_WORKSPACE, "workspace too small");
+  TH_HIP(launch_paged_attention(Q, q_start, cache, p, O, workspace, (hipStream_t)stream),
+         "paged attention");
   return TH_OK;
 }
 

@@ -245,6 +245,24 @@ hipError_t launch_linear(const unsigned short* X, int64_t ldx, const unsigned sh
 hipError_t launch_rms_norm(const void* X, th_dtype xdt, int64_t ldx, const void* w, void* Y,
                            th_dtype ydt, int64_t ldy, int64_t n, int64_t b, float eps,
                            hipStream_t s);
+// m, if not NULL, in the place of Y; R and sum may be NULL
+hipError_t launch_add_rms_norm(const void* X, th_dtype xdt, int64_t ldx, const void* R, int64_t ldr,
+                               const void* w, void* sum, int64_t ldsum, void* Y, th_dtype ydt,
+                               int64_t ldy, const th_mx* m, int64_t n, int64_t b, double eps,
+                               hipStream_t s);
+
+// mx.hip
+hipError_t launch_mx_quantize(const void* X, th_dtype xdt, int64_t ldx, int64_t n, int64_t b,
+                              const th_mx& y, hipStream_t s);
+hipError_t launch_mx_dequantize(const th_mx& x, int64_t n, int64_t b, void* Y, th_dtype ydt,
+                                int64_t ldy, hipStream_t s);
+
+// mx_linear.hip
+// workspace (floats) of the split contraction: 0 where it does not help
+size_t mx_linear_workspace_floats(int xtype, int64_t n, int64_t b, int64_t c, th_dtype ydt);
+hipError_t launch_mx_linear(const th_mx& X, const th_mx& W, int64_t n, int64_t b, int64_t c,
+                            const unsigned short* bias, int act, const void* residual, int64_t ldr,
+                            void* Y, th_dtype ydt, int64_t ldy, float* part, hipStream_t s);
 
 // rotary.hip
 hipError_t launch_rotary(const th_heads* q, const th_heads* k, th_dtype dt, int64_t n, int64_t d,
@@ -258,6 +276,17 @@ size_t attention_workspace_bytes(const th_attention_params* p);
 hipError_t launch_attention(const void* Q, const void* K, const void* V, const int32_t* q_start,
                             const int32_t* k_start, const th_attention_params* p, void* O,
                             void* workspace, hipStream_t s);
+
+// the same over a paged cache
+int64_t paged_attention_workgroups(const th_paged_cache* c, const th_paged_params* p);
+size_t paged_attention_workspace_bytes(const th_paged_cache* c, const th_paged_params* p);
+hipError_t launch_paged_attention(const void* Q, const int32_t* q_start, const th_paged_cache* c,
+                                  const th_paged_params* p, void* O, void* workspace, hipStream_t s);
+
+// cache.hip
+hipError_t launch_cache_store(const void* K, int64_t k_token, int64_t k_head, const void* V,
+                              int64_t v_token, int64_t v_head, int64_t nq, const int32_t* q_start,
+                              const th_paged_cache* c, hipStream_t s);
 
 // rows.hip
 hipError_t launch_row_energy(const void* W, th_dtype wdt, int64_t c, int64_t b, const float* g,

@@ -20,6 +20,7 @@
 // 3.39-3.48 with a bf16 residual (66% of the cycles in products, 7.5 GB read past the L2s).
 #include "common.h"
 #include "lds_dma.h"
+#include "linear_epilogue.h"
 
 namespace th {
 
@@ -28,129 +29,6 @@ namespace {
 constexpr int kLK = 64;  // contraction per stage
 constexpr int kLGroup = 4;  // token tiles per group in the walk order
 constexpr int kLRow = kLK * 2;
-
-// 16 bytes of a row of Y or the residual, aligned like its elements only: the memory
-// system takes such accesses at any of their addresses, so that odd widths and pitches
-// need no code of their own but for a row's last channels. (15485 tokens 2216 -> 9418, gelu
-// and residual, bf16: 678 us; element by element, half as much again, 1022 against 694.)
-typedef u32x4_t bf16_row_t __attribute__((aligned(2)));
-typedef f32x4_t f32_row_t __attribute__((aligned(4)));
-
-struct LinEpilogue {
-  const unsigned short* bias;
-  const void* residual;
-  void* y;
-  int64_t ldr, ldy;
-  int act;       // th_activation
-  int y_f32;     // Y and residual are fp32 (else bf16)
-};
-
-// z Phi(z), Phi(-|z|) = erfc(|z| / sqrt 2) / 2 = e^(-z^2/2) t Q(t), t = 1 / (1 + |z| / 2), Q
-// of degree 10 fitted here to erfcx by weighted least squares (2.2e-8 of itself at most, for
-// |z| <= 13.8, past which the result is below fp32's range). Every |z| keeps its relative
-// accuracy, (16 + 1.5 z^2) 2^-24 counted in roundings; 1 + erff(z / sqrt 2) has none left
-// at z = -5. (16384 tokens 4096 -> 4096: 435 us, with erff 446, with erfcf 471.)
-__device__ __forceinline__ float gelu(float z) {
-  const float a = fabsf(z), t = __builtin_amdgcn_rcpf(fmaf(a, 0.5f, 1.0f));
-  float q = -0.0370472595f;
-  q = fmaf(q, t, 0.175881296f);
-  q = fmaf(q, t, -0.28242594f);
-  q = fmaf(q, t, 0.0463377908f);
-  q = fmaf(q, t, 0.393810064f);
-  q = fmaf(q, t, -0.43306008f);
-  q = fmaf(q, t, 0.0639118254f);
-  q = fmaf(q, t, 0.0201857612f);
-  q = fmaf(q, t, 0.153776303f);
-  q = fmaf(q, t, 0.19914858f);
-  q = fmaf(q, t, 0.199481636f);
-  const float h = q * t * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
-  return z > 0.0f ? z * (1.0f - h) : z * h;
-}
-
-__device__ __forceinline__ float activate(float z, int act) {
-  switch (act) {
-    case TH_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
-    case TH_ACT_SILU: return z / (1.0f + expf(-z));
-    case TH_ACT_GELU: return gelu(z);
-    default: return z;
-  }
-}
-
-// All of v, one decision for them.
-__device__ __forceinline__ void activate8(float (&v)[8], int act) {
-  if (act == TH_ACT_RELU) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_RELU);
-  } else if (act == TH_ACT_SILU) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_SILU);
-  } else if (act == TH_ACT_GELU) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_GELU);
-  }
-}
-
-// Residual and store of channel q of token t, its activation v.
-__device__ __forceinline__ void put1(float v, int64_t t, int64_t q, const LinEpilogue& ep) {
-  if (ep.y_f32) {
-    if (ep.residual) v += ((const float*)ep.residual)[t * ep.ldr + q];
-    ((float*)ep.y)[t * ep.ldy + q] = v;
-  } else {
-    if (ep.residual) v += bf16_to_f32(((const unsigned short*)ep.residual)[t * ep.ldr + q]);
-    ((unsigned short*)ep.y)[t * ep.ldy + q] = f32_to_bf16_rne(v);
-  }
-}
-// Channel q of token t.
-__device__ __forceinline__ void finish1(float v, int64_t t, int64_t q, const LinEpilogue& ep) {
-  if (ep.bias) v += bf16_to_f32(ep.bias[q]);
-  put1(activate(v, ep.act), t, q, ep);
-}
-
-// Residuals of eight consecutive channels as they are in memory, and their sum with v
-// stored.
-template <bool F32>
-struct Row8;
-template <>
-struct Row8<false> {
-  bf16_row_t r;
-  __device__ __forceinline__ void load(const LinEpilogue& ep, int64_t t, int64_t q) {
-    r = *(const bf16_row_t*)((const unsigned short*)ep.residual + t * ep.ldr + q);
-  }
-  __device__ __forceinline__ void put(float (&v)[8], const LinEpilogue& ep, int64_t t, int64_t q) const {
-    if (ep.residual) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] += __uint_as_float(r[i] << 16);
-        v[2 * i + 1] += __uint_as_float(r[i] & 0xffff0000u);
-      }
-    }
-    bf16x8_t y;
-#pragma unroll
-    for (int x = 0; x < 8; ++x) y[x] = (__bf16)v[x];
-    *(bf16_row_t*)((unsigned short*)ep.y + t * ep.ldy + q) = __builtin_bit_cast(u32x4_t, y);
-  }
-};
-template <>
-struct Row8<true> {
-  f32_row_t a, b;
-  __device__ __forceinline__ void load(const LinEpilogue& ep, int64_t t, int64_t q) {
-    const float* r = (const float*)ep.residual + t * ep.ldr + q;
-    a = *(const f32_row_t*)r;
-    b = *(const f32_row_t*)(r + 4);
-  }
-  __device__ __forceinline__ void put(float (&v)[8], const LinEpilogue& ep, int64_t t, int64_t q) const {
-    if (ep.residual) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] += a[i];
-        v[4 + i] += b[i];
-      }
-    }
-    float* y = (float*)ep.y + t * ep.ldy + q;
-    *(f32_row_t*)y = f32x4_t{v[0], v[1], v[2], v[3]};
-    *(f32_row_t*)(y + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
-  }
-};
 
 // Workgroup (x, split): tile x of the walk order, stages [split per, split per + per)
 // of the contraction. With part set, the tile's raw sums go to part[split][n][cp], cp
@@ -372,7 +250,6 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
   const int64_t cp = (c + 7) & ~(int64_t)7;
   const int tl = lane / kLanes, ql = (lane % kLanes) * 8;
   const int64_t q = N0 + wn * kCols + ql;
-  const bool whole = q + 8 <= c;  // else fewer than eight channels, or none
   auto token = [&](int i, int p) { return M0 + wm * 32 * WM + i * 32 + p * kTok + tl; };
   auto values = [&](int p) { return strip + (p * kTok + tl) * kPitch + ql; };
   auto write_strip = [&](int i) {
@@ -402,104 +279,7 @@ __global__ __launch_bounds__(128 * GN) void linear_tile_kernel(
     }
     return;
   }
-  // The residuals of all strips (fp32: of two at a time) are on their way before the
-  // first one is used: read strip by strip they cost 16 round trips to memory a tile.
-  auto finish = [&](auto F32) __attribute__((always_inline)) {
-    constexpr bool f32 = decltype(F32)::value;
-    constexpr int kHeld = f32 && WM > 2 ? 2 : WM;
-    Row8<f32> res[kHeld][kPass];
-#pragma unroll
-    for (int i0 = 0; i0 < WM; i0 += kHeld) {
-      if (ep.residual) {
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-#pragma unroll
-          for (int p = 0; p < kPass; ++p)
-            if (token(i0 + i, p) < n && whole) res[i][p].load(ep, token(i0 + i, p), q);
-      }
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        write_strip(i0 + i);
-        if (ep.bias || ep.act != TH_ACT_NONE) {  // in place, by the lane that reads it next
-#pragma unroll 1
-          for (int p = 0; p < kPass; ++p) {
-            float *at = values(p), v[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = at[x];
-            if (ep.bias) {
-#pragma unroll
-              for (int x = 0; x < 8; ++x) v[x] += q + x < c ? bf16_to_f32(ep.bias[q + x]) : 0.f;
-            }
-            activate8(v, ep.act);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) at[x] = v[x];
-          }
-        }
-#pragma unroll
-        for (int p = 0; p < kPass; ++p) {
-          if (token(i0 + i, p) >= n || !whole) continue;
-          const f32x4_t* vp = (const f32x4_t*)values(p);
-          const f32x4_t lo = vp[0], hi = vp[1];
-          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          res[i][p].put(v, ep, token(i0 + i, p), q);
-        }
-        if (!whole) {  // the last channels of a row
-#pragma unroll 1
-          for (int p = 0; p < kPass; ++p) {
-            if (token(i0 + i, p) >= n) break;
-#pragma unroll 1
-            for (int x = 0; q + x < c; ++x) put1(values(p)[x], token(i0 + i, p), q + x, ep);
-          }
-        }
-        wave_sync();
-      }
-    }
-  };
-  if (ep.y_f32)
-    finish(std::integral_constant<bool, true>{});
-  else
-    finish(std::integral_constant<bool, false>{});
-}
-
-// Sum of the splits' raw products in order, then the epilogue: 8 channels per thread,
-// those of a row's end one by one.
-__global__ __launch_bounds__(256) void linear_join_kernel(const float* __restrict__ part, int splits,
-                                                          int64_t n, int64_t c, LinEpilogue ep) {
-  const int64_t per_row = cdiv(c, 8), cp = per_row * 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n * per_row) return;
-  const int64_t t = i / per_row, q = (i - t * per_row) * 8;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const f32x4_t* p = (const f32x4_t*)(part + t * cp + q);
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s, p += n * cp / 4) {
-    const f32x4_t lo = p[0], hi = p[1];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      v[x] += lo[x];
-      v[4 + x] += hi[x];
-    }
-  }
-  if (ep.bias) {
-#pragma unroll
-    for (int x = 0; x < 8; ++x) v[x] += q + x < c ? bf16_to_f32(ep.bias[q + x]) : 0.f;
-  }
-  activate8(v, ep.act);
-  if (q + 8 > c) {
-#pragma unroll
-    for (int x = 0; x < 8; ++x)
-      if (q + x < c) put1(v[x], t, q + x, ep);
-    return;
-  }
-  auto put = [&](auto F32) {
-    Row8<decltype(F32)::value> r;
-    if (ep.residual) r.load(ep, t, q);
-    r.put(v, ep, t, q);
-  };
-  if (ep.y_f32)
-    put(std::integral_constant<bool, true>{});
-  else
-    put(std::integral_constant<bool, false>{});
+  finish_tile<WM, kPass>(ep, n, c, q, token, values, write_strip);
 }
 
 // Skinny products, up to 16 tokens: bound by reading W once. A workgroup takes 16

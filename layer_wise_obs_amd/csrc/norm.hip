@@ -9,72 +9,23 @@
 // sum of squares is fp32: 8 products per chunk and lane, then lanes, then waves.
 // 131072 rows of 4096 in bf16: 358-412 us by box, 5.2-6.0 TB/s (torch's copy: 4.9).
 // Rows below 512 elements are bound by launching workgroups: 100000 of 100, 54 us.
+//
+// With the addition of the residual before it, h = x + r rounded to the stream's type, and an
+// output that may be microscaled (mx.h), what a product of 8- or 4-bit operands reads: the
+// second kernel. There sums, root and products are in 64 bits, so that y is rounded once, from
+// a value off by less than 2^-48 of itself: where it lies next to a border between two
+// elements, or the block's largest next to one between two scales, fp32's error of 2^-23
+// decides for a step of 2^-4. The vector units have the rate (five 64-bit operations an element
+// against 7 bytes).
 #include "common.h"
+#include "mx.h"
+#include "row8.h"
 
 namespace th {
 
 namespace {
 
 constexpr int kNChunks = 4;  // register-held chunks of 8 elements per thread
-
-// Eight elements, 16 bytes at a time, aligned like an element only: the memory system
-// takes such accesses at any of their addresses, so that odd widths and pitches need no
-// code of their own but for a row's last elements (65536 rows of 4095 in bf16: 329 us;
-// element by element 587).
-typedef u32x4_t bf16_row_t __attribute__((aligned(2)));
-typedef f32x4_t f32_row_t __attribute__((aligned(4)));
-
-struct Row8 {
-  float v[8];
-};
-
-__device__ __forceinline__ Row8 load8(const unsigned short* p) {
-  const u32x4_t u = *(const bf16_row_t*)p;
-  Row8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = __uint_as_float(u[i] << 16);
-    r.v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
-  return r;
-}
-__device__ __forceinline__ Row8 load8(const float* p) {
-  const f32x4_t a = *(const f32_row_t*)p, b = *(const f32_row_t*)(p + 4);
-  return Row8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
-}
-__device__ __forceinline__ void store8(unsigned short* p, const Row8& r) {
-  u32x4_t u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    u[i] = (unsigned)f32_to_bf16_rne(r.v[2 * i]) | ((unsigned)f32_to_bf16_rne(r.v[2 * i + 1]) << 16);
-  *(bf16_row_t*)p = u;
-}
-__device__ __forceinline__ void store8(float* p, const Row8& r) {
-  *(f32_row_t*)p = f32x4_t{r.v[0], r.v[1], r.v[2], r.v[3]};
-  *(f32_row_t*)(p + 4) = f32x4_t{r.v[4], r.v[5], r.v[6], r.v[7]};
-}
-__device__ __forceinline__ float load1(const unsigned short* p) { return bf16_to_f32(*p); }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ void store1(unsigned short* p, float v) { *p = f32_to_bf16_rne(v); }
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-
-// Elements q .. q+7 of a row of b: with a TAIL (b is no multiple of 8) those past its end
-// are 0, and not stored.
-template <bool TAIL, class T>
-__device__ __forceinline__ Row8 row_load(const T* row, int64_t q, int64_t b) {
-  if (!TAIL || q + 8 <= b) return load8(row + q);
-  Row8 r;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) r.v[e] = q + e < b ? load1(row + q + e) : 0.f;
-  return r;
-}
-template <bool TAIL, class T>
-__device__ __forceinline__ void row_store(T* row, int64_t q, int64_t b, const Row8& r) {
-  if (!TAIL || q + 8 <= b) return store8(row + q, r);
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (q + e < b) store1(row + q + e, r.v[e]);
-}
 
 // Sum over the T threads of a workgroup, the same value in every thread.
 template <int T>
@@ -168,6 +119,167 @@ hipError_t launch_typed(const void* X, int64_t ldx, const void* w, void* Y, int6
                    : launch_rows<TI, TO, 256, false>(X, ldx, w, Y, ldy, n, b, eps, s);
 }
 
+// ---------------------------------------------------------------- residual and norm
+
+template <int W>
+__device__ __forceinline__ double row_sum(double s, double* red) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) s += __shfl_xor(s, m);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0.0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) s += red[w];
+  }
+  return s;
+}
+
+// fp64 to fp32, rounded to odd: where bits are lost, towards zero with the last bit set. A
+// rounding of the result to fewer bits, or its comparison with a number of fewer bits, is then
+// that of the value itself.
+__device__ __forceinline__ float to_odd(double y) {
+  const float f = (float)y;
+  const double t = (double)f;
+  unsigned u = __float_as_uint(f);
+  if (t != y) u = (u - (fabs(t) > fabs(y) ? 1u : 0u)) | 1u;
+  return __uint_as_float(u);
+}
+
+struct NormOut {  // Y, or the elements and scales of a microscaled one
+  void* y;
+  unsigned char* scales;
+  int64_t ldy, lds;  // Y: elements; microscaled: bytes
+};
+
+// OUT: -1 bf16, -2 fp32, else a th_mx_type. W waves to a row of b elements.
+template <class TI, int OUT, int W, bool TAIL>
+__global__ __launch_bounds__(256) void add_rms_norm_kernel(const TI* X, int64_t ldx, const TI* R,
+                                                           int64_t ldr, const TI* w, TI* S, int64_t ldsum,
+                                                           NormOut out, int64_t n, int64_t b, double eps) {
+  constexpr int kRows = 4 / W, T = 64 * W;
+  __shared__ double red[4];
+  const int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? threadIdx.x / 64 : 0);
+  if (row >= n) return;
+  const int t = threadIdx.x % T;
+  const TI* x = X + row * ldx;
+  const TI* r = R ? R + row * ldr : nullptr;
+  TI* sum = S ? S + row * ldsum : nullptr;
+  // h as it is held: the sum in the stream's type
+  auto stream = [&](int64_t q) {
+    Row8 h = row_load<TAIL>(x, q, b);
+    if (r) {
+      const Row8 a = row_load<TAIL>(r, q, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h.v[e] += a.v[e];
+        if constexpr (std::is_same<TI, unsigned short>::value)
+          h.v[e] = bf16_to_f32(f32_to_bf16_rne(h.v[e]));
+      }
+    }
+    return h;
+  };
+  double s = 0.0;
+  auto add = [&](const Row8& h) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fma((double)h.v[e], (double)h.v[e], s);
+  };
+  Row8 kept[kNChunks];
+#pragma unroll
+  for (int i = 0; i < kNChunks; ++i) {
+    const int64_t q = ((int64_t)i * T + t) * 8;
+    if (q < b) kept[i] = stream(q);
+  }
+#pragma unroll
+  for (int i = 0; i < kNChunks; ++i) {
+    const int64_t q = ((int64_t)i * T + t) * 8;
+    if (q < b) {
+      add(kept[i]);
+      if (sum) row_store<TAIL>(sum, q, b, kept[i]);
+    }
+  }
+  // columns past the register-held part: formed and added here, read again for the product
+  // (from the sum, which may have taken the place of x or r)
+  for (int64_t q = ((int64_t)kNChunks * T + t) * 8; q < b; q += T * 8) {
+    const Row8 h = stream(q);
+    add(h);
+    if (sum) row_store<TAIL>(sum, q, b, h);
+  }
+  const double scale = 1.0 / sqrt(row_sum<W>(s, red) / (double)b + eps);
+  auto put = [&](const Row8& h, int64_t q) {
+    const Row8 g = row_load<TAIL>(w, q, b);
+    Row8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double y = (double)h.v[e] * scale * (double)g.v[e];
+      v.v[e] = OUT == -2 ? (float)y : to_odd(y);
+    }
+    if constexpr (OUT == -1)
+      row_store<TAIL>((unsigned short*)out.y + row * out.ldy, q, b, v);
+    else if constexpr (OUT == -2)
+      row_store<TAIL>((float*)out.y + row * out.ldy, q, b, v);
+    else
+      mx_put8<OUT>(v.v, (unsigned char*)out.y + row * out.ldy, out.scales + row * out.lds, q);
+  };
+#pragma unroll
+  for (int i = 0; i < kNChunks; ++i) {
+    const int64_t q = ((int64_t)i * T + t) * 8;
+    if (q < b) put(kept[i], q);
+  }
+  for (int64_t q = ((int64_t)kNChunks * T + t) * 8; q < b; q += T * 8)
+    put(sum ? row_load<TAIL>((const TI*)sum, q, b) : stream(q), q);
+}
+
+template <class TI, int OUT, int W, bool TAIL>
+hipError_t launch_add_rows(const TI* x, int64_t ldx, const TI* r, int64_t ldr, const TI* w, TI* sum,
+                           int64_t ldsum, NormOut o, int64_t n, int64_t b, double eps, hipStream_t s) {
+  constexpr int64_t kMost = kMaxGroups * (4 / W);
+  const int64_t unit = OUT == -1 ? 2 : (OUT == -2 ? 4 : 1);
+  for (; n > 0; n -= kMost) {
+    const int64_t m = n < kMost ? n : kMost;
+    hipLaunchKernelGGL((add_rms_norm_kernel<TI, OUT, W, TAIL>), dim3((unsigned)cdiv(m, 4 / W)),
+                       dim3(256), 0, s, x, ldx, r, ldr, w, sum, ldsum, o, m, b, eps);
+    x += kMost * ldx;
+    if (r) r += kMost * ldr;
+    if (sum) sum += kMost * ldsum;
+    o.y = (char*)o.y + kMost * o.ldy * unit;
+    if (o.scales) o.scales += kMost * o.lds;
+  }
+  return hipGetLastError();
+}
+
+template <class TI, int OUT>
+hipError_t launch_add_typed(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* w,
+                            void* sum, int64_t ldsum, const NormOut& o, int64_t n, int64_t b,
+                            double eps, hipStream_t s) {
+  const TI *x = (const TI*)X, *r = (const TI*)R, *g = (const TI*)w;
+  TI* h = (TI*)sum;
+  // a wave to a row up to what its registers hold
+  const bool one = b <= 64 * 8 * kNChunks;
+  if constexpr (OUT < 0) {
+    if (b % 8)
+      return one ? launch_add_rows<TI, OUT, 1, true>(x, ldx, r, ldr, g, h, ldsum, o, n, b, eps, s)
+                 : launch_add_rows<TI, OUT, 4, true>(x, ldx, r, ldr, g, h, ldsum, o, n, b, eps, s);
+  }
+  return one ? launch_add_rows<TI, OUT, 1, false>(x, ldx, r, ldr, g, h, ldsum, o, n, b, eps, s)
+             : launch_add_rows<TI, OUT, 4, false>(x, ldx, r, ldr, g, h, ldsum, o, n, b, eps, s);
+}
+
+template <class TI>
+hipError_t launch_add_out(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* w,
+                          void* sum, int64_t ldsum, void* Y, th_dtype ydt, int64_t ldy, const th_mx* m,
+                          int64_t n, int64_t b, double eps, hipStream_t s) {
+  if (m) {
+    const NormOut o = {m->elements, (unsigned char*)m->scales, m->ld, m->lds};
+    return m->type == TH_MX_E4M3
+               ? launch_add_typed<TI, TH_MX_E4M3>(X, ldx, R, ldr, w, sum, ldsum, o, n, b, eps, s)
+               : launch_add_typed<TI, TH_MX_E2M1>(X, ldx, R, ldr, w, sum, ldsum, o, n, b, eps, s);
+  }
+  const NormOut o = {Y, nullptr, ldy, 0};
+  return ydt == TH_BF16 ? launch_add_typed<TI, -1>(X, ldx, R, ldr, w, sum, ldsum, o, n, b, eps, s)
+                        : launch_add_typed<TI, -2>(X, ldx, R, ldr, w, sum, ldsum, o, n, b, eps, s);
+}
+
 }  // namespace
 
 hipError_t launch_rms_norm(const void* X, th_dtype xdt, int64_t ldx, const void* w, void* Y,
@@ -179,6 +291,16 @@ hipError_t launch_rms_norm(const void* X, th_dtype xdt, int64_t ldx, const void*
                           : launch_typed<h, float>(X, ldx, w, Y, ldy, n, b, eps, s);
   return ydt == TH_BF16 ? launch_typed<float, h>(X, ldx, w, Y, ldy, n, b, eps, s)
                         : launch_typed<float, float>(X, ldx, w, Y, ldy, n, b, eps, s);
+}
+
+hipError_t launch_add_rms_norm(const void* X, th_dtype xdt, int64_t ldx, const void* R, int64_t ldr,
+                               const void* w, void* sum, int64_t ldsum, void* Y, th_dtype ydt,
+                               int64_t ldy, const th_mx* m, int64_t n, int64_t b, double eps,
+                               hipStream_t s) {
+  return xdt == TH_BF16 ? launch_add_out<unsigned short>(X, ldx, R, ldr, w, sum, ldsum, Y, ydt, ldy, m,
+                                                         n, b, eps, s)
+                        : launch_add_out<float>(X, ldx, R, ldr, w, sum, ldsum, Y, ydt, ldy, m, n, b,
+                                                eps, s);
 }
 
 }  // namespace th

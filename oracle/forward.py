@@ -8,7 +8,8 @@ import math
 
 import numpy as np
 
-__all__ = ["forward_linear", "rms_norm", "rotary_freqs", "rotary", "attention"]
+__all__ = ["forward_linear", "rms_norm", "rotary_freqs", "rotary", "attention", "mx_numbers",
+           "mx_quantize", "mx_values", "paged_keys", "paged_store"]
 
 
 def _f64(x) -> np.ndarray:
@@ -94,4 +95,86 @@ def attention(Q, K, V, q_start, k_start, causal=True, scale=None) -> np.ndarray:
                     z = K[k0:end, h // g] @ Q[i, h] * scale
                     p = np.exp(z - np.max(z))
                     out[i, h] = (p / np.sum(p)) @ V[k0:end, h // g]
+    return out
+
+
+def mx_numbers(form) -> list:
+    """The form's numbers from 0 up, in the order of their codes, and the one that would follow."""
+    bits, bias, last = {"e4m3": (3, 7, 126), "e2m1": (1, 1, 7)}[form]
+    out = []
+    for code in range(last + 2):
+        e, m = code >> bits, code & ((1 << bits) - 1)
+        out.append(math.ldexp(m, 1 - bias - bits) if e == 0
+                   else math.ldexp((1 << bits) + m, e - bias - bits))
+    return out
+
+
+def _mx_nearest(v, numbers):
+    """Code of the number nearest to each of v >= 0 (a tie: the even code)."""
+    n = np.array(numbers)
+    i = np.clip(np.searchsorted(n, v, side="right") - 1, 0, len(n) - 2)
+    up, down = n[i + 1] - v, v - n[i]
+    return i + ((up < down) | ((up == down) & (i % 2 == 1)))
+
+
+def mx_quantize(X, form):
+    """(codes [n, b], scales [n, b / 32]) of X: exponents are tried from the lowest that can be
+    until the block's largest number is rounded to one of the form's."""
+    X = _f64(X)
+    n, b = X.shape
+    numbers = mx_numbers(form)
+    last = len(numbers) - 2
+    top = int(math.log2(numbers[last]))
+    x = X.reshape(n, b // 32, 32)
+    codes = np.zeros(x.shape, dtype=np.int64)
+    scales = np.zeros((n, b // 32), dtype=np.int64)
+    for t in range(n):
+        for j in range(b // 32):
+            v = np.abs(x[t, j])
+            if not np.isfinite(v).all():
+                scales[t, j] = 255
+                continue
+            big = float(v.max())
+            e = -127 if big == 0 else max(-127, math.frexp(big)[1] - 1 - top - 1)
+            while e < 127 - top and _mx_nearest(math.ldexp(big, -e), numbers) > last:
+                e += 1
+            codes[t, j] = np.minimum(_mx_nearest(np.ldexp(v, -e), numbers), last)
+            codes[t, j] += np.signbit(x[t, j]) * (last + (2 if form == "e4m3" else 1))
+            scales[t, j] = e + 127
+    return codes.reshape(n, b), scales
+
+
+def mx_values(codes, scales, form) -> np.ndarray:
+    """The numbers that codes [n, b] stand for with their blocks' scales."""
+    numbers = mx_numbers(form)
+    half = 128 if form == "e4m3" else 8
+    table = np.array(numbers[:half - 1] + [np.nan] if form == "e4m3" else numbers[:8])
+    codes, scales = np.asarray(codes), np.asarray(scales)
+    v = np.where(codes >= half, -1.0, 1.0) * table[codes % half]
+    power = np.where(scales == 255, np.nan, np.ldexp(1.0, scales.astype(np.int64) - 127))
+    return v * np.repeat(power, 32, axis=1)
+
+
+def paged_keys(cache, pages, k_len):
+    """Keys (or values) of every sequence of a paged cache [pages, page, hk, d], packed, and
+    their starts."""
+    cache = _f64(cache)
+    page = cache.shape[1]
+    rows, starts = [], [0]
+    for row, n in zip(np.asarray(pages), k_len):
+        rows += [cache[row[x // page], x % page] for x in range(n)]
+        starts.append(starts[-1] + n)
+    return np.array(rows).reshape(starts[-1], *cache.shape[2:]), starts
+
+
+def paged_store(cache, new, pages, k_len, q_start):
+    """The cache with the new rows as the last keys of their sequences."""
+    out = _f64(cache).copy()
+    new, page = _f64(new), out.shape[1]
+    for s in range(len(q_start) - 1):
+        for t in range(q_start[s], q_start[s + 1]):
+            key = k_len[s] - (q_start[s + 1] - t)
+            p = pages[s][key // page] if 0 <= key < page * len(pages[s]) else -1
+            if 0 <= p < out.shape[0]:
+                out[p, key % page] = new[t]
     return out
