@@ -72,6 +72,7 @@ struct PagedArgs : AttnArgs {
   int64_t keys_most;  // a sequence's pages hold as many keys
   int64_t each;       // rows of a sequence without q_start
   int shift;          // log2 of a page's keys
+  int rows_from, rows_to;  // the kernel takes sequences of so many rows (tokens times the group)
   int slots;          // bound of the pieces' partial results per key head; 0: no keys are cut
 };
 
@@ -132,9 +133,7 @@ __device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, int64_t slot,
 
 // ---------------------------------------------------------------- paged: the work
 
-// Keys of a piece are whole tiles of kTileKeys; what the few-rows kernel and the other one take:
-// sequences of up to kAFewRows rows (tokens times the group), and longer ones.
-constexpr int kAFewRows = 32;
+constexpr int kAFewRows = 32;  // rows of a sequence that the few-rows kernel takes in one block
 
 struct PagedWork {
   int sequence;            // -1: none
@@ -146,7 +145,7 @@ struct PagedWork {
 };
 
 // Rows, keys, row blocks of sequence s, as the kernel takes them (0 blocks: not its own).
-template <int BM, bool FEW>
+template <int BM>
 __device__ __forceinline__ void paged_sequence(const PagedArgs& a, int64_t s, int64_t& q0, int64_t& q1,
                                                int& lk, int& blocks) {
   if (a.q_start) {
@@ -159,25 +158,25 @@ __device__ __forceinline__ void paged_sequence(const PagedArgs& a, int64_t s, in
   const int64_t l = a.k_start[s];
   lk = (int)(l < 0 ? 0 : (l > a.keys_most ? a.keys_most : l));
   const int64_t rows = q1 > q0 ? (q1 - q0) * a.g : 0;
-  blocks = (rows <= kAFewRows) == FEW ? (int)cdiv(rows, BM) : 0;
+  blocks = rows >= a.rows_from && rows <= a.rows_to ? (int)cdiv(rows, BM) : 0;
 }
 
-// Keys of a piece, from all sequences' real lengths: sum over the row blocks of their keys, T
-// tiles, is shared out over the workgroups that are wanted, so that pieces are alike whatever
-// the sequences are. Few rows: 256 workgroups (one per compute unit) with 320 keys at least, or
-// four rounds of them with 512. Others: two workgroups per compute unit, where there are not
-// as many already.
+// Tiles of a piece, from all sequences' real lengths: the tiles of all row blocks are shared out
+// over the workgroups that are wanted, so that pieces are alike whatever the sequences are. (fp32
+// is off by less than 2^-17 of the sum; the bounds of the pieces' number want no fewer.) Few
+// rows: 256 workgroups (one per compute unit) with 320 keys at least, or four rounds of them with
+// 512. Others: two workgroups per compute unit, where there are not as many already.
 template <int TILE, bool FEW>
-__device__ __forceinline__ int paged_per(const PagedArgs& a, int64_t tiles, int64_t blocks) {
-  if (a.slots == 0) return 0x7fffffff;
-  int64_t per;
-  if constexpr (FEW) {
-    const int64_t one = cdiv(tiles * a.hk, kAUnits), four = cdiv(tiles * a.hk, 4 * kAUnits);
-    per = min(max(one, (int64_t)(320 / TILE)), max(four, (int64_t)(512 / TILE)));
-  } else {
-    per = max(cdiv(tiles * a.hk, 2 * kAUnits) * (blocks * a.hk >= kAUnits ? 2 : 1), (int64_t)3);
-  }
-  return (int)min(per, (int64_t)(1 << 24)) * TILE;
+__device__ __forceinline__ int paged_per(const PagedArgs& a, float tiles, float blocks) {
+  if (a.slots == 0) return 1 << 26;  // more than any sequence has
+  const float work = ceilf(tiles * (float)a.hk * (1.0f + 0x1p-16f));
+  float per;
+  if constexpr (FEW)
+    per = fminf(fmaxf(ceilf(work * (1.0f / kAUnits)), 320 / TILE),
+                fmaxf(ceilf(work * (0.25f / kAUnits)), 512 / TILE));
+  else
+    per = fmaxf(ceilf(work * (blocks * (float)a.hk >= kAUnits ? 1.0f : 0.5f) / kAUnits), 3.0f);
+  return (int)fminf(per, 0x1p26f);
 }
 
 // Inclusive sum over the lanes up to this one.
@@ -190,21 +189,24 @@ __device__ __forceinline__ unsigned lanes_scan(unsigned v, int lane) {
   return v;
 }
 
-// Item `item` of the work: sequences in order, their row blocks, their pieces.
-// item < 0: the piece 0 of row `row` (of one key head) of sequence `sequence` is looked for.
-template <int BM, int TILE, bool FEW>
-__device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, int64_t item, int lane,
-                                                int64_t sequence = 0, int64_t row = 0) {
+// Piece `at` of the work: sequences in order, their row blocks, the blocks' pieces; BY_SLOT: of
+// those only that leave partial results. A lane looks at a sequence.
+template <int BM, int TILE, bool FEW, bool BY_SLOT>
+__device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, unsigned at, int lane) {
   PagedWork r;
   r.sequence = -1;
-  int64_t tiles = 0, all = 0;
-  for (int64_t s0 = 0; s0 < a.nseq; s0 += 64) {
-    int64_t q0, q1;
-    int lk, blocks = 0;
-    if (s0 + lane < a.nseq) paged_sequence<BM, FEW>(a, s0 + lane, q0, q1, lk, blocks);
-    if (blocks) {
-      tiles += (int64_t)blocks * ((lk + TILE - 1) / TILE);
-      all += blocks;
+  int64_t q0 = 0, q1 = 0;
+  int lk = 0, blocks = 0;
+  auto look = [&](int s0) {
+    blocks = 0;
+    if (s0 + lane < a.nseq) paged_sequence<BM>(a, s0 + lane, q0, q1, lk, blocks);
+  };
+  float tiles = 0.f, all = 0.f;
+  if (a.slots || a.nseq <= 64) {
+    for (int s0 = 0; s0 < a.nseq; s0 += 64) {
+      look(s0);
+      tiles += (float)blocks * (float)((unsigned)(lk + TILE - 1) / TILE);
+      all += (float)blocks;
     }
   }
   if (a.slots) {
@@ -214,34 +216,33 @@ __device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, int64_t item
       all += __shfl_xor(all, d);
     }
   }
-  r.per = paged_per<TILE, FEW>(a, tiles, all);
-  int64_t before = 0;  // items of the sequences before
-  int64_t cut = 0;     // and those among them that leave partial results
-  for (int64_t s0 = 0; s0 < a.nseq; s0 += 64) {
-    int64_t q0 = 0, q1 = 0;
-    int lk = 0, blocks = 0;
-    if (s0 + lane < a.nseq) paged_sequence<BM, FEW>(a, s0 + lane, q0, q1, lk, blocks);
-    const int pieces = blocks ? max(1, (int)cdiv(lk, r.per)) : 0;
-    const unsigned count = (unsigned)blocks * (unsigned)pieces, part = pieces > 1 ? count : 0u;
-    const unsigned upto = lanes_scan(count, lane), parts = lanes_scan(part, lane);
-    const bool here = item >= 0 ? before + upto > item : s0 + lane == sequence;
-    const unsigned long long found = __ballot(here);
+  const int per = paged_per<TILE, FEW>(a, tiles, all);
+  unsigned before = 0, cut = 0;  // pieces of the sequences before, and those among them with results
+  for (int s0 = 0; s0 < a.nseq; s0 += 64) {
+    if (a.nseq > 64) look(s0);
+    const unsigned of = (unsigned)(lk + TILE - 1) / TILE;
+    const unsigned pieces = blocks ? (of ? (of - 1) / (unsigned)per + 1 : 1u) : 0u;
+    const unsigned count = (unsigned)blocks * pieces, part = pieces > 1 ? count : 0u;
+    const unsigned upto = lanes_scan(count, lane), parts = a.slots ? lanes_scan(part, lane) : 0u;
+    const unsigned long long found = __ballot(BY_SLOT ? cut + parts > at : before + upto > at);
     if (found) {
       const int f = __ffsll(found) - 1;
-      const int64_t first = before + __builtin_amdgcn_readlane((int)(upto - count), f);
-      const int64_t slot = cut + __builtin_amdgcn_readlane((int)(parts - part), f);
-      r.sequence = (int)s0 + f;
+      const unsigned first = before + __builtin_amdgcn_readlane((int)(upto - count), f);
+      const unsigned slot = cut + __builtin_amdgcn_readlane((int)(parts - part), f);
+      r.sequence = s0 + f;
       r.q0 = __builtin_amdgcn_readlane((int)q0, f);
       r.q1 = __builtin_amdgcn_readlane((int)q1, f);
       r.lk = __builtin_amdgcn_readlane(lk, f);
-      r.pieces = __builtin_amdgcn_readlane(pieces, f);
-      const int64_t local = item >= 0 ? item - first : row / BM * r.pieces;
-      const int64_t block = r.pieces ? local / r.pieces : 0;
-      r.piece = (int)(local - block * r.pieces);
-      r.row0 = block * BM;
-      r.slot = r.pieces > 1 ? (int)(slot + local) : -1;
+      const unsigned np = (unsigned)__builtin_amdgcn_readlane((int)pieces, f);
+      const unsigned local = at - (BY_SLOT ? slot : first), block = local / np;
+      r.pieces = (int)np;
+      r.piece = (int)(local - block * np);
+      r.row0 = (int64_t)block * BM;
+      // a sequence's pieces are alike: 2^31 keys at most
+      r.per = (int)(((unsigned)(r.lk + TILE - 1) / TILE + np - 1) / np) * TILE;
+      r.slot = np > 1 ? (int)(slot + local) : -1;
       // starts that do not ascend can ask for more than there is room for
-      if (r.pieces > 1 && slot + local - r.piece + r.pieces > a.slots) r.sequence = -1;
+      if (np > 1 && slot + block * np + np > (unsigned)a.slots) r.sequence = -1;
       return r;
     }
     before += (unsigned)__builtin_amdgcn_readlane((int)upto, 63);
@@ -250,13 +251,26 @@ __device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, int64_t item
   return r;
 }
 
-// Page numbers of a sequence's keys, one per lane for 16 keys each: lane i those from `from` +
-// `step`(i). Places past the sequence's last key repeat its last page; pages outside the
-// cache are moved to its ends.
+// Page of key `key` of a sequence (keys behind its last: of that one), inside the cache.
 __device__ __forceinline__ int paged_number(const PagedArgs& a, const int32_t* row, int64_t key, int lk) {
   key = key < lk ? key : lk - 1;
   const int64_t p = row[key >> a.shift];
   return (int)(p < 0 ? 0 : (p >= a.npages ? a.npages - 1 : p));
+}
+// Where the 16 keys of `key` (a multiple of 16; behind the last: the last key's 16) begin in their
+// page, in elements of K and V.
+struct PagedPlace {
+  int64_t k, v;
+  __device__ __forceinline__ void set(const PagedArgs& a, int64_t page, int64_t key, int lk) {
+    key = (key < lk ? key : lk - 1) & ~15;
+    const int in = (int)key & ((1 << a.shift) - 1);
+    k = page * a.k_page + (int64_t)in * a.k_token;
+    v = page * a.v_page + (int64_t)in * a.v_token;
+  }
+};
+__device__ __forceinline__ int64_t readlane64(int64_t v, int lane) {
+  return (int64_t)((uint64_t)(unsigned)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+                   (unsigned)__builtin_amdgcn_readlane((int)v, lane));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -309,7 +323,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
   int lk;
   [[maybe_unused]] PagedWork work;
   if constexpr (kPaged) {
-    work = paged_work<kBM, kAKT, false>(a, blockIdx.x / a.hk, lane);
+    work = paged_work<kBM, kAKT, false, false>(a, blockIdx.x / a.hk, lane);
     if (work.sequence < 0) return;
     q0 = work.q0;
     q1 = work.q1;
@@ -341,7 +355,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
   int kbeg, kend;
   bool cut;
   if constexpr (kPaged) {
-    kbeg = min(keys, work.piece * work.per);
+    kbeg = (int)min((int64_t)keys, (int64_t)work.piece * work.per);
     kend = keys - kbeg < work.per ? keys : kbeg + work.per;
     cut = work.pieces > 1;
   } else {
@@ -428,21 +442,21 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
   // The next tile's loads, one by one: i < kLd of K, then kLd of V.
   const unsigned short *gk = kb, *gv = vb;
   unsigned dk = 0;
-  // Paged: a load's rows lie in 16 consecutive keys, which are of one page. Lane x of `here`
-  // holds the page of keys 16 x .. of the 1024 at hand, of `coming` of the next 1024.
-  [[maybe_unused]] int here = 0, coming = 0, tile_key = 0, tile_last = 0;
+  // Paged: a load's rows lie in 16 consecutive keys, which are of one page. Lane x of `place` holds
+  // where keys 16 x .. of the 1024 at hand are, `coming` the page of those of the next 1024.
+  [[maybe_unused]] PagedPlace place = {0, 0};
+  [[maybe_unused]] int coming = 0, first16 = 0;
   [[maybe_unused]] const int32_t* page_row = nullptr;
   if constexpr (kPaged) page_row = a.pages + work.sequence * a.pages_row;
   auto next_tile = [&](int kt, int buf) {
     if (kt + kAKT > lk) offsets(lk - 1 - kt);  // the sequence's last tile
     if constexpr (kPaged) {
       if ((kt & 1023) == 0 || kt == kbeg) {
-        const int64_t from = kt & ~1023;
-        here = kt == kbeg ? paged_number(a, page_row, from + 16 * lane, lk) : coming;
-        coming = paged_number(a, page_row, from + 1024 + 16 * lane, lk);
+        const int64_t from = (kt & ~1023) + 16 * lane;
+        place.set(a, kt == kbeg ? paged_number(a, page_row, from, lk) : coming, from, lk);
+        coming = paged_number(a, page_row, from + 1024, lk);
       }
-      tile_key = kt;
-      tile_last = min(lk - 1 - kt, kAKT - 1);
+      first16 = (kt >> 4) & 63;
     } else {
       gk = kb + (int64_t)kt * a.k_token;
       gv = vb + (int64_t)kt * a.v_token;
@@ -452,15 +466,11 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
   auto load = [&](int i) {
     if constexpr (kPaged) {
       const int x = i < kLd ? i : i - kLd;
-      // the first key of the 16 that the load's rows are of, and its place in the page
-      const int key = tile_key + (min((wave + NW * x) * kRowsPer, tile_last) & ~15);
-      const int64_t page = __builtin_amdgcn_readlane(here, (key >> 4) & 63);
-      const int in = key & ((1 << a.shift) - 1);
+      const int at = first16 + ((wave + NW * x) * kRowsPer >> 4);
       if (i < kLd) {
-        if (in_k) lds_dma1(vk[x], kb + page * a.k_page + (int64_t)in * a.k_token, dk + x * NW * 1024);
+        if (in_k) lds_dma1(vk[x], kb + readlane64(place.k, at), dk + x * NW * 1024);
       } else {
-        lds_dma1(vv[x], vb + page * a.v_page + (int64_t)in * a.v_token,
-                 dk + ST * kTile + x * NW * 1024);
+        lds_dma1(vv[x], vb + readlane64(place.v, at), dk + ST * kTile + x * NW * 1024);
       }
       return;
     }
@@ -770,7 +780,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
   int lk;
   [[maybe_unused]] PagedWork work;
   if constexpr (kPaged) {
-    work = paged_work<kBM, kKeys, true>(a, blockIdx.x / a.hk, lane);
+    work = paged_work<kBM, kKeys, true, false>(a, blockIdx.x / a.hk, lane);
     if (work.sequence < 0) return;
     q0 = work.q0;
     q1 = work.q1;
@@ -799,7 +809,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
   int kbeg, kend;
   bool cut;
   if constexpr (kPaged) {
-    kbeg = min(keys, work.piece * work.per);
+    kbeg = (int)min((int64_t)keys, (int64_t)work.piece * work.per);
     kend = keys - kbeg < work.per ? keys : kbeg + work.per;
     cut = work.pieces > 1;
   } else {
@@ -850,59 +860,46 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
   const unsigned short* vb = a.v + (kPaged ? 0 : k0 * a.v_token) + head * a.v_head;
   const unsigned ob = lds_address(sm) + wave * 4 * kTile;
   // Paged: the wave's tiles are 128 keys apart and of two times 16 keys, each of one page. Lanes
-  // 2x and 2x + 1 of `here` hold the pages of the tile x of the 32 at hand, of `coming` of the
-  // next 32.
-  [[maybe_unused]] int here = 0, coming = 0;
+  // 2x and 2x + 1 of `place` hold where those of tile x of the 32 at hand are, of `coming` the
+  // pages of the next 32.
+  [[maybe_unused]] PagedPlace place = {0, 0};
+  [[maybe_unused]] int coming = 0;
   [[maybe_unused]] const int32_t* page_row = nullptr;
   if constexpr (kPaged) page_row = a.pages + work.sequence * a.pages_row;
-  auto issue = [&](int kt, int buf) {
-    if constexpr (kPaged) {
-      const int x = (kt - kbeg) / (kWaves * kKeys);
-      if ((x & 31) == 0) {
-        const int64_t key = (int64_t)kt + (lane >> 1) * (kWaves * kKeys) + (lane & 1) * 16;
-        here = x == 0 ? paged_number(a, page_row, key, lk) : coming;
-        coming = paged_number(a, page_row, key + 32 * kWaves * kKeys, lk);
-      }
-      const int last = min(kKeys, lk - kt) - 1, in_page = (1 << a.shift) - 1;
-      const unsigned short *gk[2], *gv[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t page = __builtin_amdgcn_readlane(here, 2 * (x & 31) + h);
-        const int in = (kt + 16 * h) & in_page;
-        gk[h] = kb + page * a.k_page + (int64_t)in * a.k_token;
-        gv[h] = vb + page * a.v_page + (int64_t)in * a.v_token;
-      }
-#pragma unroll
-      for (int i = 0; i < 2 * kLd; ++i) {
-        const int y = i < kLd ? i : i - kLd;
-        const int h = min(y * kRowsPer, last) >> 4;  // the 16 keys that the load's rows are of
-        const unsigned row = min(y * kRowsPer + lr, last) & 15;
-        if (i < kLd) {
-          const int ck = k_piece(y);
-          if (!PAD || ck < a.d)
-            lds_dma1((row * (unsigned)a.k_token + ck) * 2, h ? gk[1] : gk[0],
-                     ob + 2 * buf * kTile + y * 1024);
-        } else {
-          lds_dma1((row * (unsigned)a.v_token + cv) * 2, h ? gv[1] : gv[0],
-                   ob + (2 * buf + 1) * kTile + y * 1024);
-        }
-      }
-      return;
+  // One operand of a tile. K goes first: it finds the places of either.
+  int64_t gk[2] = {0, 0}, gv[2] = {0, 0};  // of the last tile whose K was issued
+  [[maybe_unused]] auto find_places = [&](int kt, const auto& a) __attribute__((always_inline)) {
+    const int x = (kt - kbeg) / (kWaves * kKeys);
+    if ((x & 31) == 0) {
+      const int64_t key = (int64_t)kt + (lane >> 1) * (kWaves * kKeys) + (lane & 1) * 16;
+      place.set(a, x == 0 ? paged_number(a, page_row, key, lk) : coming, key, lk);
+      coming = paged_number(a, page_row, key + 32 * kWaves * kKeys, lk);
     }
-    const unsigned short* gk = kb + (int64_t)kt * a.k_token;
-    const unsigned short* gv = vb + (int64_t)kt * a.v_token;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      gk[h] = readlane64(place.k, 2 * (x & 31) + h);
+      gv[h] = readlane64(place.v, 2 * (x & 31) + h);
+    }
+  };
+  auto issue = [&](int kt, int buf, bool of_k) __attribute__((always_inline)) {
+    if constexpr (kPaged) {
+      if (of_k) find_places(kt, a);
+    } else {
+      gk[0] = (int64_t)kt * a.k_token;
+      gv[0] = (int64_t)kt * a.v_token;
+    }
     const int last = min(kKeys, lk - kt) - 1;  // rows past the keys read the last: masked
 #pragma unroll
     for (int i = 0; i < kLd; ++i) {
-      const unsigned row = min(i * kRowsPer + lr, last);
-      const int ck = k_piece(i);
-      if (!PAD || ck < a.d)
-        lds_dma1((row * (unsigned)a.k_token + ck) * 2, gk, ob + 2 * buf * kTile + i * 1024);
-    }
-#pragma unroll
-    for (int i = 0; i < kLd; ++i) {
-      const unsigned row = min(i * kRowsPer + lr, last);
-      lds_dma1((row * (unsigned)a.v_token + cv) * 2, gv, ob + (2 * buf + 1) * kTile + i * 1024);
+      const unsigned row = min(i * kRowsPer + lr, last) & (kPaged ? 15 : 31);
+      const int h = kPaged ? i * kRowsPer >> 4 : 0;  // the 16 keys that the load's rows are of
+      if (of_k) {
+        const int ck = k_piece(i);
+        if (!PAD || ck < a.d)
+          lds_dma1((row * (unsigned)a.k_token + ck) * 2, kb + gk[h], ob + 2 * buf * kTile + i * 1024);
+      } else {
+        lds_dma1((row * (unsigned)a.v_token + cv) * 2, vb + gv[h], ob + (2 * buf + 1) * kTile + i * 1024);
+      }
     }
   };
   const int krow = lane & 31;
@@ -917,6 +914,32 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
   f32x16_t o[kDB];
   float m, l;
   unsigned bad = 0;
+  // Two tiles are in flight, and the keys of a third as soon as this one's are read: at a tile's
+  // beginning its K has landed and its V may not have. Loads that are newer than the ones waited
+  // for, in units of an operand's; the pages' own loads among them only make the waits stricter.
+  constexpr int kStep = kWaves * kKeys;
+  auto wait_newer = [&](int units) __attribute__((always_inline)) {
+    static_assert(kLd == 8 || kLd == 4, "vmcnt immediates");
+    if (units == 3)
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * kLd) : "memory");
+    else if (units == 2)
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLd) : "memory");
+    else if (units == 1)
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kLd) : "memory");
+    else
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  };
+  auto keys_landed = [&](int kt) __attribute__((always_inline)) { wait_newer(kt + kStep < kend ? 3 : 1); };
+  auto values_landed = [&](int kt) __attribute__((always_inline)) {
+    wait_newer(kt + 2 * kStep < kend ? 3 : (kt + kStep < kend ? 2 : 0));
+  };
+  auto refill = [&](int kt, int buf, bool of_k) __attribute__((always_inline)) {
+    if (kt + 2 * kStep < kend) {
+      // the operand's reads are done before it is filled again
+      __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      issue(kt + 2 * kStep, buf, of_k);
+    }
+  };
   auto tile = [&](int kt, int buf, auto CAREFUL) __attribute__((always_inline)) {
     constexpr bool careful = decltype(CAREFUL)::value;
     const unsigned char* ks = own + 2 * buf * kTile;
@@ -938,12 +961,14 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
     f32x16_t s;
 #pragma unroll
     for (int e = 0; e < 16; ++e) s[e] = s2[0][e] + s2[1][e];
+    refill(kt, buf, true);
     const bool masked = kt + kKeys > lim_first;
     if (masked) {
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         s[e] = kt + 8 * (e >> 2) + 4 * half + (e & 3) < lim ? s[e] : -INFINITY;
       if constexpr (!careful) {
+        values_landed(kt);
 #pragma unroll
         for (int ks16 = 0; ks16 < 2; ++ks16)
 #pragma unroll
@@ -985,6 +1010,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
       pf[ks16] = __builtin_bit_cast(bf16x8_t, wf);
       pr[ks16] = __builtin_bit_cast(bf16x8_t, wr);
     }
+    values_landed(kt);
     if constexpr (careful) {
       if (masked) {
 #pragma unroll
@@ -1036,25 +1062,19 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
     for (int i = 0; i < kDB; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
-    constexpr int step = kWaves * kKeys;
     int kt = kbeg + wave * kKeys, buf = 0;
-    if (kt < kend) issue(kt, 0);
-    for (; kt < kend; kt += step, buf ^= 1) {
-      if (kt + step < kend) {
-        // the other buffer's reads are done before it is filled again
-        __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        issue(kt + step, buf ^ 1);
-        if constexpr (kLd == 8)
-          __asm__ volatile("s_waitcnt vmcnt(16)" ::: "memory");
-        else
-          __asm__ volatile("s_waitcnt vmcnt(8)" ::: "memory");
-      } else {
-        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (kt + x * kStep < kend) {
+        issue(kt + x * kStep, x, true);
+        issue(kt + x * kStep, x, false);
       }
+    for (; kt < kend; kt += kStep, buf ^= 1) {
+      keys_landed(kt);
       tile(kt, buf, CAREFUL);
+      refill(kt, buf, false);
     }
   };
-  static_assert(kLd == 8 || kLd == 4, "vmcnt immediates");
   pass(std::integral_constant<bool, false>{});
   // An infinity that a row sees stays one times p, but is NaN times p's rest (0, or of the
   // other sign): where anything is not finite, the second pass leaves such products of the
@@ -1200,52 +1220,33 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
                 a.o + tok * a.o_token + qh * a.o_head);
 }
 
-// The same for rows of a paged call, those whose keys were cut. Few rows: workgroup x has row
-// x % rows of key head (x / rows) % hk of a sequence; otherwise x is a (token, query head).
-template <int BM, int TILE, bool FEWROWS>
-__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a, int rows) {
-  const int lane = threadIdx.x & 63;
-  int64_t s, row;
-  int head;
-  if constexpr (FEWROWS) {
-    const int64_t x = blockIdx.x / rows;
-    row = blockIdx.x - x * rows;
-    s = x / a.hk;
-    head = (int)(x - s * a.hk);
-  } else {
-    const int hq = a.hk * a.g;
-    const int64_t tok = blockIdx.x / hq;
-    const int qh = (int)(blockIdx.x - tok * hq);
-    int64_t q0;
-    if (a.q_start) {
-      // the last sequence that begins at or before the token
-      int64_t lo = 0, len = a.nseq;
-      for (;;) {
-        const int64_t step = (len + 63) >> 6, at = lane * step;
-        const bool before = at < len && start_at(a.q_start, (int)(lo + at), a.nq) <= tok;
-        const int count = __popcll(__ballot(before));
-        if (count == 0) return;
-        lo += (count - 1) * step;
-        if (step == 1) break;
-        len = min(step, len - (count - 1) * step);
-      }
-      s = lo;
-      q0 = start_at(a.q_start, (int)s, a.nq);
-      if (tok >= start_at(a.q_start, (int)s + 1, a.nq)) return;
-    } else {
-      s = tok / a.each;
-      q0 = s * a.each;
-    }
-    head = qh / a.g;
-    row = (tok - q0) * a.g + qh - head * a.g;
+// The same for a paged call: workgroup (slot, key head) joins a share of the rows of the row block
+// that left a partial result there, each of its pieces another one. Up to eight pieces a group
+// of 32 lanes per row, else the eight groups to a row.
+template <int BM, int TILE, bool FEW>
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
+  const int grp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int head = blockIdx.x % a.hk;
+  const PagedWork w = paged_work<BM, TILE, FEW, true>(a, blockIdx.x / a.hk, threadIdx.x & 63);
+  if (w.sequence < 0) return;
+  const int64_t rows = (w.q1 - w.q0) * a.g - w.row0;
+  const int block = (int)(rows < BM ? rows : BM), share = (int)cdiv(block, w.pieces);
+  const int end = min(block, (w.piece + 1) * share);
+  const int64_t first = ((int64_t)(w.slot - w.piece) * a.hk + head) * BM, step = (int64_t)a.hk * BM;
+  auto join = [&](int r, auto ALONE) {
+    const int64_t row = w.row0 + r, tok = w.q0 + (unsigned)row / (unsigned)a.g;
+    const int qh = head * a.g + (int)((unsigned)row % (unsigned)a.g);
+    join_row<decltype(ALONE)::value>(a.part_ml + first + r, a.part_o + (first + r) * a.d, step, w.pieces,
+                                     a.d, grp, lane, a.o + tok * a.o_token + qh * a.o_head);
+  };
+  if (w.pieces <= 8) {
+    for (int r = w.piece * share + grp; r < end; r += 8) join(r, std::integral_constant<bool, true>{});
+    return;
   }
-  const PagedWork w = paged_work<BM, TILE, FEWROWS>(a, -1, lane, s, row);
-  if (w.sequence < 0 || w.pieces < 2 || row >= (w.q1 - w.q0) * a.g) return;
-  const int64_t tok = w.q0 + row / a.g;
-  const int qh = head * a.g + (int)(row % a.g);
-  const int64_t at = ((int64_t)w.slot * a.hk + head) * BM + (row - w.row0);
-  join_row<false>(a.part_ml + at, a.part_o + at * a.d, (int64_t)a.hk * BM, w.pieces, a.d,
-                  threadIdx.x / 32, threadIdx.x & 31, a.o + tok * a.o_token + qh * a.o_head);
+  for (int r = w.piece * share; r < end; ++r) {
+    join(r, std::integral_constant<bool, false>{});
+    __syncthreads();  // the groups' sums have been read
+  }
 }
 
 template <int D, int DC, bool PAD, class Args>
@@ -1424,23 +1425,27 @@ hipError_t launch_attention(const void* Q, const void* K, const void* V, const i
 namespace {
 
 struct PagedPlan {
-  bool few, many;               // whether either kernel has sequences to take
-  int64_t few_items, many_items;  // work items a key head, at most
+  bool few, many;  // which of the two kernels run
+  int few_to;      // rows of a sequence that the first takes; the second those above
+  int64_t few_items, many_items;  // pieces a key head, at most
   int few_slots, many_slots;      // partial results a key head
-  int64_t few_rows;             // rows of a sequence of the first kind
 };
 
-// What the device can find there, from sizes alone: sequences of up to kAFewRows rows have one
-// row block, others one per 128 rows or part of them; pieces are cut from T tiles so that
-// T / per <= target / hk, and there are T / per + (row blocks) of them at most, those of cut
-// row blocks no more than 2 T / per.
+// Which kernels: by the average rows, as in th_attention; but where they are few and some
+// sequences may be longer all the same, either kernel takes its own. (A launch that finds nothing
+// to do takes 3 to 10 us; a chunk of 1000 tokens in 32-row blocks takes twice as long as in
+// 128-row ones.) The rest is what the device can find there, from sizes alone: sequences of r rows
+// have r / BM row blocks, or part of one more; pieces are cut from T tiles so that
+// T / per <= target / hk, and there are T / per + (row blocks) of them at most, those of cut row
+// blocks no more than 2 T / per.
 PagedPlan plan_of(const th_paged_cache* c, const th_paged_params* p) {
   PagedPlan r = {};
+  if (p->nq == 0) return r;
   const int64_t g = p->hq / c->hk, nseq = c->nseq, most = c->width * c->page_tokens;
-  const int64_t each = p->even ? p->nq / nseq * g : 0;
-  r.few = p->nq > 0 && (p->even ? each <= kAFewRows : g <= kAFewRows);
-  r.many = p->nq > 0 && (p->even ? each > kAFewRows : p->nq * g > kAFewRows);
-  r.few_rows = p->even ? each : kAFewRows;
+  const int64_t rows = p->nq * g, seqs = nseq < p->nq ? nseq : p->nq;
+  r.few = rows <= kAFewRows * nseq;
+  r.many = !r.few || (!p->even && p->nq > 2 * nseq && rows > kAFewRows);
+  r.few_to = r.many ? kAFewRows : 0x7fffffff;
   auto bound = [&](int64_t blocks, int64_t target, int64_t least, int64_t& items, int& slots) {
     const int64_t pieces = cdiv(most, least);
     slots = pieces > 1 ? (int)(2 * target / c->hk) : 0;
@@ -1448,12 +1453,10 @@ PagedPlan plan_of(const th_paged_cache* c, const th_paged_params* p) {
     if (slots && pieces < (1 << 20) && blocks * pieces < items) items = blocks * pieces;
     if (slots > items) slots = (int)items;
   };
-  if (r.few)
-    bound(nseq < p->nq ? nseq : p->nq, 4 * kAUnits, 320, r.few_items, r.few_slots);
+  if (r.few) bound(r.many ? seqs : rows / 32 + seqs, 4 * kAUnits, 320, r.few_items, r.few_slots);
   if (r.many) {
-    const int64_t longer = p->nq * g / (kAFewRows + 1);
-    bound(p->nq * g / 128 + (nseq < longer ? nseq : longer), 2 * kAUnits, 3 * kAKT, r.many_items,
-          r.many_slots);
+    const int64_t longer = r.few ? std::min(seqs, rows / (kAFewRows + 1)) : seqs;
+    bound(rows / 128 + longer, 2 * kAUnits, 3 * kAKT, r.many_items, r.many_slots);
   }
   return r;
 }
@@ -1467,10 +1470,8 @@ size_t paged_rows(const PagedPlan& r, const th_paged_cache* c) {
 int64_t paged_attention_workgroups(const th_paged_cache* c, const th_paged_params* p) {
   if (p->nq == 0) return 0;
   const PagedPlan r = plan_of(c, p);
-  int64_t most = (r.few_items > r.many_items ? r.few_items : r.many_items) * c->hk;
-  if (r.few_slots) most = std::max(most, c->nseq * c->hk * r.few_rows);  // of the join
-  if (r.many_slots) most = std::max(most, p->nq * p->hq);
-  return most;
+  return std::max(std::max(r.few_items, r.many_items), (int64_t)std::max(r.few_slots, r.many_slots)) *
+         c->hk;
 }
 
 size_t paged_attention_workspace_bytes(const th_paged_cache* c, const th_paged_params* p) {
@@ -1516,25 +1517,26 @@ hipError_t launch_paged_attention(const void* Q, const int32_t* q_start, const t
   a.part_ml = (float2*)workspace;
   a.part_o = workspace ? (float*)((char*)workspace + part_ml_bytes((int64_t)rows)) : nullptr;
   if (plan.few) {
+    a.rows_from = 1;
+    a.rows_to = plan.few_to;
     a.slots = workspace ? plan.few_slots : 0;
     launch_by_head(a, true, dim3((unsigned)(plan.few_items * a.hk)), s);
     if (a.slots)
-      hipLaunchKernelGGL((paged_join_kernel<32, 32, true>),
-                         dim3((unsigned)(c->nseq * a.hk * plan.few_rows)), dim3(256), 0, s, a,
-                         (int)plan.few_rows);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !plan.many) return e;
+      hipLaunchKernelGGL((paged_join_kernel<32, 32, true>), dim3((unsigned)(a.slots * a.hk)), dim3(256),
+                         0, s, a);
   }
   if (plan.many) {
     if (workspace) {  // behind the results of the few rows
       a.part_ml += (int64_t)plan.few_slots * 32 * a.hk;
       a.part_o += (int64_t)plan.few_slots * 32 * a.hk * a.d;
     }
+    a.rows_from = plan.few ? plan.few_to + 1 : 1;
+    a.rows_to = 0x7fffffff;
     a.slots = workspace ? plan.many_slots : 0;
     launch_by_head(a, false, dim3((unsigned)(plan.many_items * a.hk)), s);
     if (a.slots)
-      hipLaunchKernelGGL((paged_join_kernel<128, kAKT, false>), dim3((unsigned)(p->nq * p->hq)),
-                         dim3(256), 0, s, a, 0);
+      hipLaunchKernelGGL((paged_join_kernel<128, kAKT, false>), dim3((unsigned)(a.slots * a.hk)),
+                         dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }

@@ -53,14 +53,21 @@ __device__ __forceinline__ float activate(float z, int act) {
   }
 }
 
+// z / (1 + e^-z) to 2 units and |z| 2^-23 of itself, for outputs that are rounded to bf16: a
+// division and expf would take five times as long.
+__device__ __forceinline__ float silu_near(float z) {
+  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+}
+
 // All of v, one decision for them.
+template <bool NEAR = false>
 __device__ __forceinline__ void activate8(float (&v)[8], int act) {
   if (act == TH_ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_RELU);
   } else if (act == TH_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_SILU);
+    for (int i = 0; i < 8; ++i) v[i] = NEAR ? silu_near(v[i]) : activate(v[i], TH_ACT_SILU);
   } else if (act == TH_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_GELU);
@@ -132,15 +139,15 @@ struct Out8<true> {
 // Epilogue of a wave's WM strips of 32 tokens, each kPass passes of the lanes' tokens:
 // write_strip(i) puts strip i into LDS, values(p) is then the lane's eight channels from q of
 // its token(i, p).
-template <int WM, int kPass, class Token, class Values, class Write>
+template <int WM, int kPass, bool NEAR = false, class Token, class Values, class Write>
 __device__ __forceinline__ void finish_tile(const LinEpilogue& ep, int64_t n, int64_t c, int64_t q,
                                             Token&& token, Values&& values, Write&& write_strip) {
   const bool whole = q + 8 <= c;  // else fewer than eight channels, or none
-  // The residuals of all strips (fp32: of two at a time) are on their way before the
+  // The residuals of all strips, or as many as 64 registers hold, are on their way before the
   // first one is used: read strip by strip they cost 16 round trips to memory a tile.
   auto finish = [&](auto F32) __attribute__((always_inline)) {
     constexpr bool f32 = decltype(F32)::value;
-    constexpr int kHeld = f32 && WM > 2 ? 2 : WM;
+    constexpr int kRoom = 16 / (kPass * (f32 ? 2 : 1)), kHeld = WM < kRoom ? WM : kRoom;
     Out8<f32> res[kHeld][kPass];
 #pragma unroll
     for (int i0 = 0; i0 < WM; i0 += kHeld) {
@@ -164,7 +171,7 @@ __device__ __forceinline__ void finish_tile(const LinEpilogue& ep, int64_t n, in
 #pragma unroll
               for (int x = 0; x < 8; ++x) v[x] += q + x < c ? bf16_to_f32(ep.bias[q + x]) : 0.f;
             }
-            activate8(v, ep.act);
+            activate8<NEAR && !f32>(v, ep.act);
 #pragma unroll
             for (int x = 0; x < 8; ++x) at[x] = v[x];
           }

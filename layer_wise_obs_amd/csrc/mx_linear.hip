@@ -32,8 +32,8 @@ namespace th {
 
 namespace {
 
-constexpr int kMK = 128;      // contraction per stage
-constexpr int kMSuper = 4;    // stages per 16 bytes of scales
+constexpr int kMK = 256;         // contraction per step: whole cache lines of 4-bit rows
+constexpr int kMScaleSlots = 4;  // buffers of 16 bytes (512 k) of scales a row
 constexpr int kMGroup = 4;    // token tiles per group in the walk order
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
@@ -67,24 +67,29 @@ constexpr int kMxCode = TYPE == TH_MX_E4M3 ? 0 : 4;
 __device__ __forceinline__ void mx_part(const i32x8_t& v, i32x8_t& high, i32x8_t& low) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const unsigned u = (unsigned)v[i], one = (u >> 6) & 0x01010101u;
-    const unsigned mask = (one << 8) - one;  // bytes of ones: a byte's borrow is the next one's carry
+    const unsigned u = (unsigned)v[i];
+    // selectors 12 and 13 stand for bytes of zeros and of ones
+    const unsigned mask = __builtin_amdgcn_perm(0u, 0u, ((u >> 6) & 0x01010101u) | 0x0c0c0c0cu);
     high[i] = (int)(u & mask);
     low[i] = (int)(u & ~mask);
   }
 }
 
-template <int XT, int FM, int FN, int GN, int S, bool EXACT>
-__global__ __launch_bounds__(128 * GN) void mx_tile_kernel(MxOperand X, MxOperand W, int64_t n, int64_t b,
-                                                           int64_t c, int ntm, int ntn, int per_xcd,
-                                                           int stages_per_split,
-                                                           float* __restrict__ part, LinEpilogue ep) {
-  constexpr int TM = 64 * FM, TN = 32 * FN * GN;
-  constexpr int kWaves = 2 * GN;
-  constexpr int kXRow = XT == TH_MX_E4M3 ? kMK : kMK / 2, kWRow = kMK / 2;  // bytes of a stage's row
-  constexpr int kA = TM * kXRow, kB = TN * kWRow;
-  constexpr int LA = kA / 1024 / kWaves, LB = kB / 1024 / kWaves;  // 1 KB loads per wave and stage
-  constexpr int kScales = (TM + TN) * 16;  // of 512 k
+template <int XT, int FM, int FN, int GM, int GN, int RX, int RW, bool EXACT>
+__global__ __launch_bounds__(64 * GM * GN, 1) void mx_tile_kernel(MxOperand X, MxOperand W, int64_t n,
+                                                                  int64_t b, int64_t c, int ntm, int ntn,
+                                                                  int per_xcd, int steps_per_split,
+                                                                  float* __restrict__ part,
+                                                                  LinEpilogue ep) {
+  constexpr bool kWide = XT == TH_MX_E4M3;  // X's rows of a step are two stages of 128 bytes
+  constexpr int TM = 32 * FM * GM, TN = 32 * FN * GN;
+  constexpr int kWaves = GM * GN;
+  constexpr int kXStage = TM * 128, kWStage = TN * 128;
+  constexpr int kHalves = kWide ? 2 : 1;
+  constexpr int kWAt = RX * kHalves * kXStage, kSAt = kWAt + RW * kWStage;  // in LDS
+  constexpr int LX = TM / 8 / kWaves, LW = TN / 8 / kWaves;  // 1 KB loads per wave and stage
+  constexpr int kScales = (TM + TN) * 16;                    // of 512 k
+  constexpr int kLds = kSAt + kMScaleSlots * kScales;
   const int wg = blockIdx.x;
   const int lin = (wg % 8) * per_xcd + wg / 8;
   if (lin >= ntm * ntn) return;
@@ -97,278 +102,297 @@ __global__ __launch_bounds__(128 * GN) void mx_tile_kernel(MxOperand X, MxOperan
     tn = in / gs;
   }
   const int64_t M0 = (int64_t)tm * TM, N0 = (int64_t)tn * TN;
-  const int nk_all = (int)cdiv(b, kMK);
-  const int s_begin = blockIdx.y * stages_per_split;  // a multiple of kMSuper
-  const int nk = min(stages_per_split, nk_all - s_begin);
+  const int steps = (int)cdiv(b, kMK);
+  const int s_begin = blockIdx.y * steps_per_split;  // even
+  const int nk = min(steps_per_split, steps - s_begin);
   if (nk <= 0) return;  // no split of the launch is empty
 
-  __shared__ __attribute__((aligned(1024))) unsigned char sm[S * (kA + kB) + 2 * kScales];
+  __shared__ __attribute__((aligned(1024))) unsigned char sm[kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / GN, wn = wave % GN;
   const unsigned smb = lds_address(sm);
 
-  // Loader: chunks of 1 KB, wave w those w + kWaves m of either operand. Rows of 64 bytes: lane l
-  // fills row 16 chunk + l / 4 at physical piece l % 4, swizzled by (row / 4) & 3; of 128 bytes:
-  // row 8 chunk + l / 8 at piece l % 8, by (row / 2) & 7. Either is the same in a lane's chunks.
-  auto piece_of = [&](int row_bytes) {
-    return row_bytes == 64 ? (lane & 3) ^ ((lane >> 4) & 3)
-                           : (lane & 7) ^ (((wave & 1) << 2) + (lane >> 4));
-  };
-  const int la = piece_of(kXRow), lb = piece_of(kWRow);
-  unsigned va[LA], vb[LB];
+  // Loader: chunks of 1 KB (8 rows of 128 bytes), wave w those w + kWaves m of either operand. Lane
+  // l fills row 8 chunk + l / 8 at physical piece l % 8; (row / 2) & 7 is the same in each of its
+  // chunks.
+  const int lp = (lane & 7) ^ (((wave & 1) << 2) + (lane >> 4));
+  unsigned vx[LX], vw[LW];
 #pragma unroll
-  for (int m = 0; m < LA; ++m) {
-    int64_t r = M0 + (wave + kWaves * m) * (1024 / kXRow) + lane / (kXRow / 16);
+  for (int m = 0; m < LX; ++m) {
+    int64_t r = M0 + (wave + kWaves * m) * 8 + (lane >> 3);
     r = r < n ? r : n - 1;  // rows past the end feed outputs that are never stored
-    va[m] = (unsigned)((r - M0) * X.ld + la * 16);
+    vx[m] = (unsigned)((r - M0) * X.ld + lp * 16);
   }
 #pragma unroll
-  for (int m = 0; m < LB; ++m) {
-    int64_t r = N0 + (wave + kWaves * m) * (1024 / kWRow) + lane / (kWRow / 16);
+  for (int m = 0; m < LW; ++m) {
+    int64_t r = N0 + (wave + kWaves * m) * 8 + (lane >> 3);
     r = r < c ? r : c - 1;
-    vb[m] = (unsigned)((r - N0) * W.ld + lb * 16);
+    vw[m] = (unsigned)((r - N0) * W.ld + lp * 16);
   }
-  // Scales: 64 rows a load, X's rows first; the first waves have one each.
-  constexpr int kScaleLoads = (TM + TN) / 64;
-  static_assert(kScaleLoads <= kWaves, "one load of scales per wave");
-  const bool scale_x = wave * 64 < TM;
-  unsigned vs;
-  {
-    const int64_t first = scale_x ? M0 + wave * 64 : N0 + wave * 64 - TM;
-    int64_t r = first + lane;
-    const int64_t last = (scale_x ? n : c) - 1;
+  // Scales: 64 rows a load, X's rows first; a wave has those w + kWaves m, of X all or none.
+  constexpr int kScaleLoads = (TM + TN) / 64, LS = (kScaleLoads + kWaves - 1) / kWaves;
+  static_assert(LS == 1 || TM / 64 % kWaves == 0, "a load's rows are of one operand");
+  unsigned vs[LS];
+  const unsigned char* scale_base[LS];
+#pragma unroll
+  for (int m = 0; m < LS; ++m) {
+    const int at = (wave + kWaves * m) * 64;
+    const bool of_x = at < TM;
+    int64_t r = of_x ? M0 + at + lane : N0 + at - TM + lane;
+    const int64_t last = (of_x ? n : c) - 1;
     r = r < last ? r : last;
-    vs = (unsigned)(scale_x ? (r - M0) * X.lds : (r - N0) * W.lds);
+    vs[m] = (unsigned)(of_x ? (r - M0) * X.lds : (r - N0) * W.lds);
+    scale_base[m] = of_x ? X.scales + M0 * X.lds : W.scales + N0 * W.lds;
   }
-  const unsigned char* scale_base = scale_x ? X.scales + M0 * X.lds : W.scales + N0 * W.lds;
-  const unsigned scale_lds = smb + S * (kA + kB) + wave * 1024;
-  const int st_last = nk_all - 1, super_last = st_last / kMSuper;
-  auto load_scales = [&](int it) {  // those of the stages from it on, a multiple of kMSuper
-    if (wave >= kScaleLoads) return;
-    const int u = (s_begin + it) / kMSuper;
-    lds_dma1(vs, scale_base + (int64_t)min(u, super_last) * 16,
-             scale_lds + (it / kMSuper % 2) * kScales);
+  const int super_last = (int)((b - 1) / 512);
+  auto scale_slot = [&](int u) { return kSAt + u % kMScaleSlots * kScales; };
+  auto load_scales = [&](int u) {  // those of steps 2 u and 2 u + 1
+    const int64_t from = (int64_t)min(s_begin / 2 + u, super_last) * 16;
+#pragma unroll
+    for (int m = 0; m < LS; ++m)
+      if (kWaves * (m + 1) <= kScaleLoads || wave + kWaves * m < kScaleLoads)
+        lds_dma1(vs[m], scale_base[m] + from, smb + scale_slot(u) + (wave + kWaves * m) * 1024);
   };
-  // Stages past the last are loaded too (never read), so that every stage has the same number
-  // of loads for the vmcnt waits; they re-read the last. Pieces of the last stage past b
-  // re-read its piece 0; zero_tail clears them. Loads of scales among them only make the
-  // waits stricter.
-  const int64_t k_last = (int64_t)st_last * kMK;
-  const bool a_past = k_last + la * (kMK / (kXRow / 16)) >= b;
-  const bool b_past = k_last + lb * (kMK / (kWRow / 16)) >= b;
+  // Stages past the last are loaded too (never read), so that every step has the same number of
+  // loads for the vmcnt waits; they re-read the last. Pieces of the last stage past b re-read
+  // its piece 0. Loads of scales among them only make the waits stricter.
+  const int x_last = (int)((b - 1) / (kMK / kHalves)), w_last = steps - 1;
+  const unsigned x_back = (int64_t)x_last * (kMK / kHalves) + lp * (kWide ? 16 : 32) >= b ? lp * 16 : 0;
+  const unsigned w_back = (int64_t)w_last * kMK + lp * 32 >= b ? lp * 16 : 0;
   const unsigned char *xs = X.elements, *ws = W.elements;
-  unsigned abase = 0, bbase = 0;
-  bool a_last = false, b_last = false;
-  auto stage_a = [&](int it) {
-    const int st = s_begin + it;
-    xs = X.elements + M0 * X.ld + (int64_t)min(st, st_last) * kXRow;
-    abase = smb + (it % S) * kA + wave * 1024;
-    if (st >= st_last && !a_last) {  // from here on every stage issued is the last one
-      a_last = true;
-      if (a_past) {
-#pragma unroll
-        for (int m = 0; m < LA; ++m) va[m] -= la * 16;
-      }
-    }
+  unsigned xbase = 0, wbase = 0, x_cut = 0, w_cut = 0;
+  auto stage_x = [&](int it, int half) {
+    const int st = (s_begin + it) * kHalves + half;
+    xs = X.elements + M0 * X.ld + (int64_t)min(st, x_last) * 128;
+    xbase = smb + (it % RX * kHalves + half) * kXStage + wave * 1024;
+    x_cut = st >= x_last ? x_back : 0;
   };
-  auto stage_b = [&](int it) {
+  auto stage_w = [&](int it) {
     const int st = s_begin + it;
-    ws = W.elements + N0 * W.ld + (int64_t)min(st, st_last) * kWRow;
-    bbase = smb + S * kA + (it % S) * kB + wave * 1024;
-    if (st >= st_last && !b_last) {
-      b_last = true;
-      if (b_past) {
-#pragma unroll
-        for (int m = 0; m < LB; ++m) vb[m] -= lb * 16;
-      }
-    }
+    ws = W.elements + N0 * W.ld + (int64_t)min(st, w_last) * 128;
+    wbase = smb + kWAt + it % RW * kWStage + wave * 1024;
+    w_cut = st >= w_last ? w_back : 0;
   };
-  auto issue_a = [&](int m) { lds_dma1(va[m], xs, abase + m * kWaves * 1024); };
-  auto issue_b = [&](int m) { lds_dma1(vb[m], ws, bbase + m * kWaves * 1024); };
-  // Zero this wave's pieces of stage it that lie past b, and, where the stage is the first of
-  // the last scales, the scales of blocks past it (255 there would make NaN of 0). Its own loads
-  // have landed.
-  auto zero_tail = [&](int it) {
-    const int st = s_begin + it;
-    if (it % kMSuper == 0 && st / kMSuper == super_last && wave < kScaleLoads) {
-      const int blocks = (int)(b / kMxBlock) - super_last * 16;
-      if (blocks < 16) {
-        unsigned* z = (unsigned*)(sm + S * (kA + kB) + (it / kMSuper % 2) * kScales + wave * 1024 +
-                                  lane * 16);
+  auto issue_x = [&](int m) { lds_dma1(vx[m] - x_cut, xs, xbase + m * kWaves * 1024); };
+  auto issue_w = [&](int m) { lds_dma1(vw[m] - w_cut, ws, wbase + m * kWaves * 1024); };
+  // Scales of blocks past b become 0 on either side: whatever numbers the pieces re-read, their
+  // products are below 2^-242 and count nothing. (A NaN among them is in its row already; as it is,
+  // such a scale might be 255.) By the wave that loaded them, once they have landed.
+  auto clear_past = [&](int u) {
+    if (s_begin / 2 + u != super_last) return;
+    const int blocks = (int)(b / kMxBlock) - super_last * 16;
+    for (int at = wave; at < kScaleLoads && blocks < 16; at += kWaves) {
+      unsigned* z = (unsigned*)(sm + scale_slot(u) + at * 1024 + lane * 16);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int left = blocks - 4 * x;  // of this word's four
-          if (left < 4) z[x] = left <= 0 ? 0u : z[x] & (0xffffffffu >> (32 - 8 * left));
-        }
+      for (int x = 0; x < 4; ++x) {
+        const int left = blocks - 4 * x;  // of this word's four
+        if (left < 4) z[x] = left <= 0 ? 0u : z[x] & (0xffffffffu >> (32 - 8 * left));
       }
-    }
-    if (st != st_last) return;
-    const u32x4_t zero = u32x4_t{0u, 0u, 0u, 0u};
-    if (a_past) {
-#pragma unroll
-      for (int m = 0; m < LA; ++m)
-        *(u32x4_t*)(sm + (it % S) * kA + (wave + m * kWaves) * 1024 + lane * 16) = zero;
-    }
-    if (b_past) {
-#pragma unroll
-      for (int m = 0; m < LB; ++m)
-        *(u32x4_t*)(sm + S * kA + (it % S) * kB + (wave + m * kWaves) * 1024 + lane * 16) = zero;
     }
   };
 
-  f32x16_t acc[FM][FN];
+  // the products of X's two parts have sums of their own where there are registers for them:
+  // fewer wait for the one before
+  constexpr bool kTwo = EXACT && kWide && FM * FN <= 2;
+  f32x16_t acc[FM][FN], acc_low[kTwo ? FM : 1][kTwo ? FN : 1];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = acc_low[kTwo ? i : 0][kTwo ? j : 0][e] = 0.f;
 
   const int r32 = lane & 31, half = lane >> 5;
-  const int waddr = r32 * 64 + ((half ^ ((r32 >> 2) & 3)) << 4);   // rows of 64 bytes
-  const int xaddr = XT == TH_MX_E4M3 ? r32 * 128 + ((half ^ ((r32 >> 1) & 7)) << 4) : waddr;
+  const int faddr = r32 * 128 + ((half ^ ((r32 >> 1) & 7)) << 4);
   struct Frags {
     MxFrag<XT> a[FM];
     MxFrag<TH_MX_E2M1> b[FN];
   };
   Frags f0, f1;
-  int sa[FM], sb[FN], sa2[FM], sb2[FN];
+  int sa[2][FM], sb[2][FN];  // scales of the first and the second 128 k of a step
   // operand y of substep sub (64 k): the FN blocks of W, then the FM of X
   auto read_one = [&](int it, int sub, int y, Frags& f) {
     if (y < FN) {
-      f.b[y].v = *(const i32x4_t*)(sm + S * kA + (it % S) * kB + (wn * FN + y) * 32 * kWRow +
-                                   (waddr ^ (sub << 5)));
+      f.b[y].v = *(const i32x4_t*)(sm + kWAt + it % RW * kWStage + (wn * FN + y) * 4096 + (faddr ^ (sub << 5)));
+    } else if constexpr (kWide) {
+      const unsigned char* p = sm + (it % RX * 2 + sub / 2) * kXStage + (wm * FM + y - FN) * 4096;
+      const i32x4_t lo = *(const i32x4_t*)(p + (faddr ^ (sub % 2 << 6)));
+      const i32x4_t hi = *(const i32x4_t*)(p + (faddr ^ (sub % 2 << 6) ^ 32));
+      f.a[y - FN].v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
-      const unsigned char* p = sm + (it % S) * kA + (wm * FM + y - FN) * 32 * kXRow;
-      if constexpr (XT == TH_MX_E4M3) {
-        const i32x4_t lo = *(const i32x4_t*)(p + (xaddr ^ (sub << 6)));
-        const i32x4_t hi = *(const i32x4_t*)(p + (xaddr ^ (sub << 6) ^ 32));
-        f.a[y - FN].v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      } else {
-        f.a[y - FN].v = *(const i32x4_t*)(p + (xaddr ^ (sub << 5)));
-      }
+      f.a[y - FN].v =
+          *(const i32x4_t*)(sm + it % RX * kXStage + (wm * FM + y - FN) * 4096 + (faddr ^ (sub << 5)));
     }
   };
-  // Scales of a stage's four blocks of 32 k, shifted so that substep sub's is byte 2 sub.
-  auto read_scale = [&](int it, int y, int (&a)[FM], int (&bb)[FN]) {
-    const unsigned char* p = sm + S * (kA + kB) + (it / kMSuper % 2) * kScales + (it % kMSuper) * 4;
+  // Scales of four blocks of 32 k, as they are; shifted, byte 2 (sub % 2) is substep sub's.
+  auto read_scale = [&](int it, int h, int y) {
+    const unsigned char* p = sm + scale_slot(it / 2) + (it % 2 * 2 + h) * 4;
     if (y < FN)
-      bb[y] = *(const int*)(p + (TM + (wn * FN + y) * 32 + r32) * 16);
+      sb[h][y] = *(const int*)(p + (TM + (wn * FN + y) * 32 + r32) * 16);
     else
-      a[y - FN] = *(const int*)(p + ((wm * FM + y - FN) * 32 + r32) * 16);
+      sa[h][y - FN] = *(const int*)(p + ((wm * FM + y - FN) * 32 + r32) * 16);
   };
-  auto shift_scales = [&](int (&a)[FM], int (&bb)[FN]) {
+  auto shift_scales = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) a[i] = (int)((unsigned)a[i] >> (8 * half));
+    for (int i = 0; i < FM; ++i) sa[h][i] = (int)((unsigned)sa[h][i] >> (8 * half));
 #pragma unroll
-    for (int j = 0; j < FN; ++j) bb[j] = (int)((unsigned)bb[j] >> (8 * half));
+    for (int j = 0; j < FN; ++j) sb[h][j] = (int)((unsigned)sb[h][j] >> (8 * half));
   };
   // One substep's products, with reads and loads between them; the order is pinned.
-  auto mfmas = [&](const Frags& f, auto SUB, auto&& between) __attribute__((always_inline)) {
-    constexpr int sub = decltype(SUB)::value;
+  auto products = [&](const Frags& f, auto SUB, auto&& between) __attribute__((always_inline)) {
+    constexpr int h = decltype(SUB)::value / 2, byte = decltype(SUB)::value % 2 * 2;
+    auto product = [&](const i32x8_t& x, f32x16_t& to, int i, int j) __attribute__((always_inline)) {
+      to = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          x, f.b[j].wide(), to, kMxCode<XT>, kMxCode<TH_MX_E2M1>, byte, sa[h][i], byte, sb[h][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      [[maybe_unused]] i32x8_t high, low;
-      if constexpr (EXACT && XT == TH_MX_E4M3) mx_part(f.a[i].v, high, low);
+      if constexpr (EXACT && kWide) {
+        i32x8_t high, low;
+        mx_part(f.a[i].v, high, low);
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        if constexpr (EXACT && XT == TH_MX_E4M3) {
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              low, f.b[j].wide(), acc[i][j], kMxCode<XT>, kMxCode<TH_MX_E2M1>, 2 * sub, sa[i], 2 * sub,
-              sb[j]);
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              high, f.b[j].wide(), acc[i][j], kMxCode<XT>, kMxCode<TH_MX_E2M1>, 2 * sub, sa[i],
-              2 * sub, sb[j]);
-        } else {
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              f.a[i].wide(), f.b[j].wide(), acc[i][j], kMxCode<XT>, kMxCode<TH_MX_E2M1>, 2 * sub,
-              sa[i], 2 * sub, sb[j]);
+        for (int j = 0; j < FN; ++j) product(low, kTwo ? acc_low[kTwo ? i : 0][kTwo ? j : 0] : acc[i][j], i, j);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          product(high, acc[i][j], i, j);
+          between(i * FN + j);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        between(i * FN + j);
-        __builtin_amdgcn_sched_barrier(0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          product(f.a[i].wide(), acc[i][j], i, j);
+          between(i * FN + j);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   };
   constexpr int kProducts = FM * FN, kReads = (FM + FN + kProducts - 1) / kProducts;
-  constexpr int kLoadsA = (LA + kProducts - 1) / kProducts, kLoadsB = (LB + kProducts - 1) / kProducts;
-  constexpr int kGapA = kProducts / LA > 0 ? kProducts / LA : 1;
-  constexpr int kGapB = kProducts / LB > 0 ? kProducts / LB : 1;
+  constexpr int kLoadsX = (LX + kProducts - 1) / kProducts, kLoadsW = (LW + kProducts - 1) / kProducts;
+  constexpr int kGapX = kProducts / LX > 0 ? kProducts / LX : 1;
+  constexpr int kGapW = kProducts / LW > 0 ? kProducts / LW : 1;
+  auto reads = [&](int x, int it, int sub, Frags& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int y = 0; y < kReads; ++y)
+      if (x * kReads + y < FM + FN) read_one(it, sub, x * kReads + y, f);
+  };
+  auto scales = [&](int x, int it, int h) __attribute__((always_inline)) {
+#pragma unroll
+    for (int y = 0; y < kReads; ++y)
+      if (x * kReads + y < FM + FN) read_scale(it, h, x * kReads + y);
+  };
+  auto loads_x = [&](int x) __attribute__((always_inline)) {
+    if (x % kGapX == 0) {
+#pragma unroll
+      for (int m = 0; m < kLoadsX; ++m)
+        if (x / kGapX * kLoadsX + m < LX) issue_x(x / kGapX * kLoadsX + m);
+    }
+  };
+  auto loads_w = [&](int x) __attribute__((always_inline)) {
+    if (x % kGapW == 0) {
+#pragma unroll
+      for (int m = 0; m < kLoadsW; ++m)
+        if (x / kGapW * kLoadsW + m < LW) issue_w(x / kGapW * kLoadsW + m);
+    }
+  };
+  // Loads not waited for before substep 3, where the next step's X (its first half) and W have to
+  // have landed, and before substep 1, where this step's second half of X has to. They are issued
+  // in the order: X (of 8 bits: its second half) of step it + RX in substep 3, W of it + RW in
+  // the next step's substep 0, the first half of X of it + 1 + RX in its substep 1.
+  constexpr int kStep = LX * kHalves + LW;
+  constexpr int kLeft3 = kWide ? (RX == 1 ? 0 : LX + (RW - 2) * kStep) : (RW - 2) * kStep;
+  constexpr int kLeft1 = LW + (RX - 1) * kStep;
+  static_assert(RX == RW || (kWide && RX == 1 && RW == 2), "the order of the loads");
+  static_assert(kLeft3 < 64 && kLeft1 < 64, "vmcnt immediates");
 
-  // prologue: the first two scales, W's and X's stages 0 .. S-2, waited for; then W's S-1
+  // prologue: the first scales, then steps 0 .. R-1 but for the last W, step 0 waited for
   load_scales(0);
-  load_scales(kMSuper);
+  load_scales(1);
 #pragma unroll
-  for (int it = 0; it < S - 1; ++it) {
-    stage_b(it);
+  for (int it = 0; it < RW; ++it) {
+    if (it < RX) {
 #pragma unroll
-    for (int m = 0; m < LB; ++m) issue_b(m);
-    stage_a(it);
+      for (int h = 0; h < kHalves; ++h) {
+        stage_x(it, h);
 #pragma unroll
-    for (int m = 0; m < LA; ++m) issue_a(m);
+        for (int m = 0; m < LX; ++m) issue_x(m);
+      }
+    }
+    if (it < RW - 1) {
+      stage_w(it);
+#pragma unroll
+      for (int m = 0; m < LW; ++m) issue_w(m);
+    }
   }
-  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  zero_tail(0);
+  __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((RW - 2) * LW + (RX - 1) * LX * kHalves) : "memory");
+  clear_past(0);
+  clear_past(1);
   __syncthreads();
-  stage_b(S - 1);
-#pragma unroll
-  for (int m = 0; m < LB; ++m) issue_b(m);
 #pragma unroll
   for (int y = 0; y < FM + FN; ++y) {
     read_one(0, 0, y, f0);
-    read_scale(0, y, sa, sb);
+    read_scale(0, 0, y);
   }
-  shift_scales(sa, sb);
-  // A stage: half its products, then (its last operands read, the next stage landed, the
-  // barrier) the other half. X's stage it + S - 1 goes into the buffer freed by the barrier of
-  // stage it - 1 during the first half, W's stage it + S into the one freed by this stage's
-  // during the second, every fourth stage's scales likewise.
+  // A step of 256 k: four substeps, each reading the next one's operands. Before the last one the
+  // next step has landed, and the barrier frees this step's buffers (with 8 bits, another one
+  // before the second frees the first half of X). But for the scales' at its beginning a step
+  // has no branch: behind one the compiler puts the products before it, whose results nothing
+  // needs yet.
   for (int it = 0; it < nk; ++it) {
-    stage_a(it + S - 1);
-    mfmas(f0, std::integral_constant<int, 0>{}, [&](int x) __attribute__((always_inline)) {
-#pragma unroll
-      for (int y = 0; y < kReads; ++y)
-        if (x * kReads + y < FM + FN) read_one(it, 1, x * kReads + y, f1);
-      if (x % kGapA == 0) {
-#pragma unroll
-        for (int m = 0; m < kLoadsA; ++m)
-          if (x / kGapA * kLoadsA + m < LA) issue_a(x / kGapA * kLoadsA + m);
-      }
+    if (it % 4 == 0) {  // into the buffers whose last reads lie before the last barrier
+      load_scales(it / 2 + 2);
+      load_scales(it / 2 + 3);
+    } else if (it % 4 == 3) {  // they have landed, and are read from this step's end on
+      clear_past(it / 2 + 1);
+      clear_past(it / 2 + 2);
+    }
+    shift_scales(0);
+    stage_w(it - 1 + RW);
+    products(f0, std::integral_constant<int, 0>{}, [&](int x) __attribute__((always_inline)) {
+      reads(x, it, 1, f1);
+      loads_w(x);
     });
-    __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 2) * (LA + LB)) : "memory");
-    zero_tail(it + 1);
+    if constexpr (kWide) {
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft1) : "memory");
+      __syncthreads();
+      stage_x(it + RX, 0);
+    }
+    products(f1, std::integral_constant<int, 1>{}, [&](int x) __attribute__((always_inline)) {
+      reads(x, it, 2, f0);
+      scales(x, it, 1);
+      if constexpr (kWide) loads_x(x);
+    });
+    shift_scales(1);
+    products(f0, std::integral_constant<int, 2>{}, [&](int x) __attribute__((always_inline)) {
+      reads(x, it, 3, f1);
+    });
+    __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft3) : "memory");
     __syncthreads();
-    stage_b(it + S);
-    if (it % kMSuper == kMSuper - 1) load_scales(it + 1 + kMSuper);
-    mfmas(f1, std::integral_constant<int, 1>{}, [&](int x) __attribute__((always_inline)) {
-#pragma unroll
-      for (int y = 0; y < kReads; ++y)
-        if (x * kReads + y < FM + FN) {
-          read_one(it + 1, 0, x * kReads + y, f0);
-          read_scale(it + 1, x * kReads + y, sa2, sb2);
-        }
-      if (x % kGapB == 0) {
-#pragma unroll
-        for (int m = 0; m < kLoadsB; ++m)
-          if (x / kGapB * kLoadsB + m < LB) issue_b(x / kGapB * kLoadsB + m);
-      }
+    stage_x(it + RX, kHalves - 1);
+    products(f1, std::integral_constant<int, 3>{}, [&](int x) __attribute__((always_inline)) {
+      reads(x, it + 1, 0, f0);
+      scales(x, it + 1, 0);
+      loads_x(x);
     });
-#pragma unroll
-    for (int i = 0; i < FM; ++i) sa[i] = sa2[i];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) sb[j] = sb2[j];
-    shift_scales(sa, sb);
   }
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();  // every wave's loads have landed: the stages may be reused
 
+  if constexpr (kTwo) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] += acc_low[i][j];
+  }
   // Epilogue through LDS, one 32-token strip of the wave's block at a time: the lane holds
   // channel l % 32 of each block and tokens 8 (e / 4) + 4 (l / 32) + e % 4; read back, a lane has
   // 8 consecutive channels of one token.
   constexpr int kCols = 32 * FN, kPitch = kCols + 4;
-  static_assert(kWaves * 32 * kPitch * 4 <= S * (kA + kB), "strips fit the stages");
+  static_assert(kWaves * 32 * kPitch * 4 <= kLds, "strips fit the stages");
   float* strip = (float*)sm + wave * 32 * kPitch;
   constexpr int kLanes = kCols / 8;   // lanes per token
   constexpr int kTok = 64 / kLanes;   // tokens per pass
@@ -403,7 +427,7 @@ __global__ __launch_bounds__(128 * GN) void mx_tile_kernel(MxOperand X, MxOperan
     }
     return;
   }
-  finish_tile<FM, kPass>(ep, n, c, q, token, values, write_strip);
+  finish_tile<FM, kPass, true>(ep, n, c, q, token, values, write_strip);
 }
 
 // Up to 16 tokens: bound by reading W once. A workgroup takes 16 channels, its eight waves a
@@ -478,32 +502,35 @@ __global__ __launch_bounds__(64 * kMsWaves) void mx_skinny_kernel(MxOperand X, M
   }
 }
 
-// The tile kernel's forms, their time modelled as in linear.hip: rounds of `slots` workgroups,
-// each fixed + stages * per_stage microseconds with every slot taken and half of the second
-// part with few, and the join of splits as 3 us and its traffic at 4 TB/s.
+// The tile kernel's forms. Its time is modelled as rounds of `slots` workgroups, each fixed +
+// steps * (microseconds a step, by kind: e2m1, e4m3, e4m3 in two parts): `full` with all slots
+// taken, and of forms with two workgroups per compute unit as soon as units are shared; between
+// `lone` and that, by their number, in the other forms. The join of splits takes 3 us and its
+// traffic at 4 TB/s. @@MODEL
 struct MxTile {
   int tm, tn;
   int slots;
-  double per_stage[3], fixed;  // per stage: e2m1, e4m3, e4m3 in two parts
+  double lone[3], full[3], fixed;
 };
 enum { kMx64 = 0, kMx128 = 1, kMx128x256 = 2, kMx256 = 3, kMxTiles = 4, kMxSkinny = 4 };
+constexpr int kMxUnits = 256;  // compute units
 constexpr MxTile kMxForms[kMxTiles] = {
-    {64, 64, 512, {0.4, 0.5, 0.6}, 4.0},
-    {128, 128, 512, {0.5, 0.7, 0.9}, 6.0},
-    {128, 256, 256, {0.6, 0.85, 1.1}, 7.0},
-    {256, 256, 256, {1.0, 1.45, 2.2}, 12.0},
+    {64, 64, 2 * kMxUnits, {0.27, 0.42, 0.95}, {0.44, 0.62, 1.17}, 5.0},   // 4 waves of 32 x 32
+    {128, 128, 2 * kMxUnits, {0.52, 0.68, 1.48}, {1.15, 1.5, 2.7}, 5.0},   // 8 waves of 32 x 64
+    {128, 256, kMxUnits, {0.70, 1.05, 2.6}, {1.1, 1.35, 2.8}, 6.0},        // 8 waves of 64 x 64
+    {256, 256, kMxUnits, {1.1, 1.87, 4.3}, {2.1, 2.95, 5.7}, 6.0},         // 8 waves of 64 x 128
 };
 constexpr int64_t kMxSkinnyTokens = 16;
 
 struct MxPlan {
   int tile;
   int splits;  // pieces of the contraction
-  int per;     // stages per piece, a multiple of kMSuper
+  int per;     // steps per piece, even where there are several
 };
 
 MxPlan plan_of(int xtype, int64_t n, int64_t b, int64_t c, bool exact, bool can_split) {
-  const int64_t stages = cdiv(b, kMK);
-  MxPlan best = {kMxSkinny, 1, (int)stages};
+  const int64_t steps = cdiv(b, kMK);
+  MxPlan best = {kMxSkinny, 1, (int)steps};
   if (n <= kMxSkinnyTokens) return best;
   const int kind = xtype == TH_MX_E2M1 ? 0 : (exact ? 2 : 1);
   double least = 1e300;
@@ -511,13 +538,15 @@ MxPlan plan_of(int xtype, int64_t n, int64_t b, int64_t c, bool exact, bool can_
     const MxTile& k = kMxForms[t];
     const int64_t tiles = cdiv(n, k.tm) * cdiv(c, k.tn);
     for (int64_t want : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (want > 1 && (!can_split || stages < kMSuper * want || tiles * want > 4 * k.slots)) break;
-      const int64_t per = want == 1 ? stages : cdiv(cdiv(stages, kMSuper), want) * kMSuper;
-      const int64_t splits = cdiv(stages, per);
+      if (want > 1 && (!can_split || steps < 2 * want || tiles * want > 4 * k.slots)) break;
+      const int64_t per = want == 1 ? steps : cdiv(cdiv(steps, 2), want) * 2;
+      const int64_t splits = cdiv(steps, per);
       const int64_t full = tiles * splits / k.slots, rest = tiles * splits % k.slots;
-      double us = (double)full * (k.fixed + (double)per * k.per_stage[kind]);
-      if (rest)
-        us += k.fixed + (double)per * k.per_stage[kind] * (0.5 + 0.5 * (double)rest / k.slots);
+      double us = (double)full * (k.fixed + (double)per * k.full[kind]);
+      if (rest) {
+        const double share = k.slots > kMxUnits ? (rest > kMxUnits ? 1.0 : 0.0) : (double)rest / k.slots;
+        us += k.fixed + (double)per * (k.lone[kind] + (k.full[kind] - k.lone[kind]) * share);
+      }
       if (splits > 1) us += 3.0 + 8.0 * (double)splits * (double)n * (double)c / 4e6;
       if (us < least) {
         least = us;
@@ -528,13 +557,13 @@ MxPlan plan_of(int xtype, int64_t n, int64_t b, int64_t c, bool exact, bool can_
   return best;
 }
 
-template <int XT, int FM, int FN, int GN, int S, bool EXACT>
+template <int XT, int FM, int FN, int GM, int GN, int RX, int RW, bool EXACT>
 hipError_t launch_tiles(const MxOperand& X, const MxOperand& W, int64_t n, int64_t b, int64_t c,
                         const MxPlan& p, float* part, const LinEpilogue& ep, hipStream_t s) {
-  const int ntm = (int)cdiv(n, 64 * FM), ntn = (int)cdiv(c, 32 * FN * GN);
+  const int ntm = (int)cdiv(n, 32 * FM * GM), ntn = (int)cdiv(c, 32 * FN * GN);
   const int per_xcd = (int)cdiv((int64_t)ntm * ntn, 8);
-  hipLaunchKernelGGL((mx_tile_kernel<XT, FM, FN, GN, S, EXACT>),
-                     dim3((unsigned)(8 * per_xcd), (unsigned)p.splits), dim3(128 * GN), 0, s, X, W, n, b,
+  hipLaunchKernelGGL((mx_tile_kernel<XT, FM, FN, GM, GN, RX, RW, EXACT>),
+                     dim3((unsigned)(8 * per_xcd), (unsigned)p.splits), dim3(64 * GM * GN), 0, s, X, W, n, b,
                      c, ntm, ntn, per_xcd, p.per, part, ep);
   return hipGetLastError();
 }
@@ -544,10 +573,10 @@ hipError_t launch_form(const MxOperand& X, const MxOperand& W, int64_t n, int64_
                        const MxPlan& p, float* part, const LinEpilogue& ep, hipStream_t s) {
   constexpr bool wide = XT == TH_MX_E4M3;
   switch (p.tile) {
-    case kMx64: return launch_tiles<XT, 1, 1, 2, 4, EXACT>(X, W, n, b, c, p, part, ep, s);
-    case kMx128: return launch_tiles<XT, 2, 1, 4, wide ? 3 : 4, EXACT>(X, W, n, b, c, p, part, ep, s);
-    case kMx128x256: return launch_tiles<XT, 2, 2, 4, 4, EXACT>(X, W, n, b, c, p, part, ep, s);
-    default: return launch_tiles<XT, 4, 2, 4, wide ? 3 : 4, EXACT>(X, W, n, b, c, p, part, ep, s);
+    case kMx64: return launch_tiles<XT, 1, 1, 2, 2, wide ? 3 : 4, wide ? 3 : 4, EXACT>(X, W, n, b, c, p, part, ep, s);
+    case kMx128: return launch_tiles<XT, 1, 2, 4, 2, wide ? 1 : 2, 2, EXACT>(X, W, n, b, c, p, part, ep, s);
+    case kMx128x256: return launch_tiles<XT, 2, 2, 2, 4, 2, 2, EXACT>(X, W, n, b, c, p, part, ep, s);
+    default: return launch_tiles<XT, 2, 4, 4, 2, wide ? 1 : 2, 2, EXACT>(X, W, n, b, c, p, part, ep, s);
   }
 }
 

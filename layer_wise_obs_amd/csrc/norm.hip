@@ -146,6 +146,61 @@ __device__ __forceinline__ float to_odd(double y) {
   return __uint_as_float(u);
 }
 
+// Eight elements of the residual stream as they are held.
+template <class T>
+struct Held;
+template <>
+struct Held<unsigned short> {
+  u32x4_t u;
+  __device__ __forceinline__ float at(int e) const {
+    return __uint_as_float(e & 1 ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+      u[i] = __builtin_bit_cast(unsigned, pair_t{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
+    }
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void load(const unsigned short* p, int64_t q, int64_t b) {
+    if (!TAIL || q + 8 <= b) {
+      u = *(const bf16_row_t*)(p + q);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u[i] = (q + 2 * i < b ? p[q + 2 * i] : 0u) | (q + 2 * i + 1 < b ? (unsigned)p[q + 2 * i + 1] << 16 : 0u);
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void store(unsigned short* p, int64_t q, int64_t b) const {
+    if (!TAIL || q + 8 <= b) {
+      *(bf16_row_t*)(p + q) = u;
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (q + e < b) p[q + e] = (unsigned short)(u[e >> 1] >> (16 * (e & 1)));
+  }
+};
+template <>
+struct Held<float> {
+  Row8 r;
+  __device__ __forceinline__ float at(int e) const { return r.v[e]; }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = v[e];
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void load(const float* p, int64_t q, int64_t b) {
+    r = row_load<TAIL>(p, q, b);
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void store(float* p, int64_t q, int64_t b) const {
+    row_store<TAIL>(p, q, b, r);
+  }
+};
+
 struct NormOut {  // Y, or the elements and scales of a microscaled one
   void* y;
   unsigned char* scales;
@@ -165,69 +220,114 @@ __global__ __launch_bounds__(256) void add_rms_norm_kernel(const TI* X, int64_t 
   const TI* x = X + row * ldx;
   const TI* r = R ? R + row * ldr : nullptr;
   TI* sum = S ? S + row * ldsum : nullptr;
-  // h as it is held: the sum in the stream's type
-  auto stream = [&](int64_t q) {
-    Row8 h = row_load<TAIL>(x, q, b);
-    if (r) {
-      const Row8 a = row_load<TAIL>(r, q, b);
+  typedef Held<TI> H;
+  // the sum in the stream's type
+  auto added = [&](const H& h, const H& a) {
+    float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h.v[e] += a.v[e];
-        if constexpr (std::is_same<TI, unsigned short>::value)
-          h.v[e] = bf16_to_f32(f32_to_bf16_rne(h.v[e]));
-      }
+    for (int e = 0; e < 8; ++e) v[e] = h.at(e) + a.at(e);
+    H z;
+    z.set(v);
+    return z;
+  };
+  auto stream = [&](int64_t q) {
+    H h;
+    h.template load<TAIL>(x, q, b);
+    if (r) {
+      H a;
+      a.template load<TAIL>(r, q, b);
+      h = added(h, a);
     }
     return h;
   };
   double s = 0.0;
-  auto add = [&](const Row8& h) {
+  auto add = [&](const H& h) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = fma((double)h.v[e], (double)h.v[e], s);
+    for (int e = 0; e < 8; ++e) s = fma((double)h.at(e), (double)h.at(e), s);
   };
-  Row8 kept[kNChunks];
+  H kept[kNChunks];
+  if (r) {  // all loads on their way before the first sum
+    H other[kNChunks];
 #pragma unroll
-  for (int i = 0; i < kNChunks; ++i) {
-    const int64_t q = ((int64_t)i * T + t) * 8;
-    if (q < b) kept[i] = stream(q);
-  }
+    for (int i = 0; i < kNChunks; ++i) {
+      const int64_t q = ((int64_t)i * T + t) * 8;
+      if (q < b) {
+        kept[i].template load<TAIL>(x, q, b);
+        other[i].template load<TAIL>(r, q, b);
+      }
+    }
 #pragma unroll
-  for (int i = 0; i < kNChunks; ++i) {
-    const int64_t q = ((int64_t)i * T + t) * 8;
-    if (q < b) {
-      add(kept[i]);
-      if (sum) row_store<TAIL>(sum, q, b, kept[i]);
+    for (int i = 0; i < kNChunks; ++i) {
+      const int64_t q = ((int64_t)i * T + t) * 8;
+      if (q < b) {
+        kept[i] = added(kept[i], other[i]);
+        if (sum) kept[i].template store<TAIL>(sum, q, b);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kNChunks; ++i) {
+      const int64_t q = ((int64_t)i * T + t) * 8;
+      if (q < b) kept[i].template load<TAIL>(x, q, b);
     }
   }
+#pragma unroll
+  for (int i = 0; i < kNChunks; ++i)
+    if (((int64_t)i * T + t) * 8 < b) add(kept[i]);
   // columns past the register-held part: formed and added here, read again for the product
   // (from the sum, which may have taken the place of x or r)
   for (int64_t q = ((int64_t)kNChunks * T + t) * 8; q < b; q += T * 8) {
-    const Row8 h = stream(q);
+    const H h = stream(q);
     add(h);
-    if (sum) row_store<TAIL>(sum, q, b, h);
+    if (sum) h.template store<TAIL>(sum, q, b);
   }
   const double scale = 1.0 / sqrt(row_sum<W>(s, red) / (double)b + eps);
-  auto put = [&](const Row8& h, int64_t q) {
-    const Row8 g = row_load<TAIL>(w, q, b);
+  // The products in fp32 are off by less than four units of their last place. Only where one
+  // lies that near to a place where roundings to the output's type meet, or scales do (its last
+  // 16 bits tell: 1 in 7000), does fp64 have to decide: the wave then forms its eight again.
+  const float near = (float)scale;
+  const bool far = !(near > 0x1p-100f && near < 0x1p100f);
+  auto put = [&](const H& h, int64_t q) {
+    H g;
+    g.template load<TAIL>(w, q, b);
     Row8 v;
+    if constexpr (OUT == -2) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v.v[e] = (float)((double)h.at(e) * scale * (double)g.at(e));
+      row_store<TAIL>((float*)out.y + row * out.ldy, q, b, v);
+      return;
+    }
+    unsigned least = 0xffffffffu;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const double y = (double)h.v[e] * scale * (double)g.v[e];
-      v.v[e] = OUT == -2 ? (float)y : to_odd(y);
+      v.v[e] = h.at(e) * near * g.at(e);
+      least = min(least, (__float_as_uint(v.v[e]) + (OUT == -1 ? 0x8004u : 4u)) << 16);
     }
-    if constexpr (OUT == -1)
-      row_store<TAIL>((unsigned short*)out.y + row * out.ldy, q, b, v);
-    else if constexpr (OUT == -2)
-      row_store<TAIL>((float*)out.y + row * out.ldy, q, b, v);
-    else
+    if (__any(least <= 8u << 16 || far)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v.v[e] = to_odd((double)h.at(e) * scale * (double)g.at(e));
+    }
+    if constexpr (OUT == -1) {
+      Held<unsigned short> y;
+      y.set(v.v);
+      y.template store<TAIL>((unsigned short*)out.y + row * out.ldy, q, b);
+    } else if constexpr (OUT >= 0) {
       mx_put8<OUT>(v.v, (unsigned char*)out.y + row * out.ldy, out.scales + row * out.lds, q);
+    }
   };
 #pragma unroll
   for (int i = 0; i < kNChunks; ++i) {
     const int64_t q = ((int64_t)i * T + t) * 8;
     if (q < b) put(kept[i], q);
   }
-  for (int64_t q = ((int64_t)kNChunks * T + t) * 8; q < b; q += T * 8)
-    put(sum ? row_load<TAIL>((const TI*)sum, q, b) : stream(q), q);
+  for (int64_t q = ((int64_t)kNChunks * T + t) * 8; q < b; q += T * 8) {
+    H h;
+    if (sum)
+      h.template load<TAIL>(sum, q, b);
+    else
+      h = stream(q);
+    put(h, q);
+  }
 }
 
 template <class TI, int OUT, int W, bool TAIL>
