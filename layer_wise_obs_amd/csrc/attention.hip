@@ -133,6 +133,7 @@ __device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, int64_t slot,
 
 // ---------------------------------------------------------------- paged: the work
 
+constexpr float kAShare = 1.0f, kALeast = 10.0f;
 constexpr int kAFewRows = 32;  // rows of a sequence that the few-rows kernel takes in one block
 
 struct PagedWork {
@@ -162,20 +163,25 @@ __device__ __forceinline__ void paged_sequence(const PagedArgs& a, int64_t s, in
 }
 
 // Tiles of a piece, from all sequences' real lengths: the tiles of all row blocks are shared out
-// over the workgroups that are wanted, so that pieces are alike whatever the sequences are. (fp32
-// is off by less than 2^-17 of the sum; the bounds of the pieces' number want no fewer.) Few
-// rows: 256 workgroups (one per compute unit) with 320 keys at least, or four rounds of them with
-// 512. Others: two workgroups per compute unit, where there are not as many already.
+// over the workgroups that run at a time, two to a compute unit, so that pieces are alike whatever
+// the sequences are. (fp32 is off by less than 2^-17 of the sum; the bounds of the pieces' number
+// want no fewer.) Few rows: pieces of 320 keys at least; (row block, key head) pairs that leave
+// room are cut into as many pieces as run at a time, one short piece each counted; more pairs into
+// twice as many, which evens out their lengths; so many that they even out by themselves, where
+// one is longer than a workgroup's share. Others: pieces of a share, or two where the row blocks
+// fill the units. @@
 template <int TILE, bool FEW>
 __device__ __forceinline__ int paged_per(const PagedArgs& a, float tiles, float blocks) {
   if (a.slots == 0) return 1 << 26;  // more than any sequence has
-  const float work = ceilf(tiles * (float)a.hk * (1.0f + 0x1p-16f));
+  const float work = ceilf(tiles * (float)a.hk * (1.0f + 0x1p-16f)), pairs = blocks * (float)a.hk;
   float per;
-  if constexpr (FEW)
-    per = fminf(fmaxf(ceilf(work * (1.0f / kAUnits)), 320 / TILE),
-                fmaxf(ceilf(work * (0.25f / kAUnits)), 512 / TILE));
-  else
-    per = fmaxf(ceilf(work * (blocks * (float)a.hk >= kAUnits ? 1.0f : 0.5f) / kAUnits), 3.0f);
+  if constexpr (FEW) {
+    const float at_once = pairs <= kAUnits ? 2 * kAUnits - pairs : (pairs < 6 * kAUnits ? 4 * kAUnits : 2 * kAUnits);
+    per = fmaxf(ceilf(work / at_once * (1.0f + 0x1p-20f)), 320 / TILE);
+  } else {
+    const float share = work * (0.5f / kAUnits);
+    per = fmaxf(ceilf(fmaxf(share * kAShare, fminf(share, kALeast))), 3.0f);
+  }
   return (int)fminf(per, 0x1p26f);
 }
 
@@ -197,9 +203,27 @@ __device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, unsigned at,
   r.sequence = -1;
   int64_t q0 = 0, q1 = 0;
   int lk = 0, blocks = 0;
+  int who = lane;  // the lane's sequence, from s0
   auto look = [&](int s0) {
     blocks = 0;
     if (s0 + lane < a.nseq) paged_sequence<BM>(a, s0 + lane, q0, q1, lk, blocks);
+    who = lane;
+    if (!FEW && a.nseq > 1 && a.nseq <= 64) {
+      // the ones with most keys first: a long piece that begins last keeps the others waiting (@@)
+      const int all = a.nseq;
+      int rank = 0;
+      for (int j = 0; j < all; ++j) {
+        const int other = __builtin_amdgcn_readlane(lk, j);
+        rank += other > lk || (other == lk && j < lane) ? 1 : 0;
+      }
+      rank = lane < all ? rank : lane;
+      auto move = [&](int v) { return __builtin_amdgcn_ds_permute(rank * 4, v); };
+      q0 = move((int)q0);
+      q1 = move((int)q1);
+      lk = move(lk);
+      blocks = move(blocks);
+      who = move(lane);
+    }
   };
   float tiles = 0.f, all = 0.f;
   if (a.slots || a.nseq <= 64) {
@@ -229,7 +253,7 @@ __device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, unsigned at,
       const int f = __ffsll(found) - 1;
       const unsigned first = before + __builtin_amdgcn_readlane((int)(upto - count), f);
       const unsigned slot = cut + __builtin_amdgcn_readlane((int)(parts - part), f);
-      r.sequence = s0 + f;
+      r.sequence = s0 + __builtin_amdgcn_readlane(who, f);
       r.q0 = __builtin_amdgcn_readlane((int)q0, f);
       r.q1 = __builtin_amdgcn_readlane((int)q1, f);
       r.lk = __builtin_amdgcn_readlane(lk, f);
@@ -237,7 +261,8 @@ __device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, unsigned at,
       const unsigned local = at - (BY_SLOT ? slot : first), block = local / np;
       r.pieces = (int)np;
       r.piece = (int)(local - block * np);
-      r.row0 = (int64_t)block * BM;
+      // the last rows first: causal ones see most keys
+      r.row0 = (int64_t)((unsigned)__builtin_amdgcn_readlane(blocks, f) - 1 - block) * BM;
       // a sequence's pieces are alike: 2^31 keys at most
       r.per = (int)(((unsigned)(r.lk + TILE - 1) / TILE + np - 1) / np) * TILE;
       r.slot = np > 1 ? (int)(slot + local) : -1;
@@ -759,10 +784,13 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
 // a bf16 value and its rest, so 2^-16 of each is lost and not 2^-8 (error against 64 bits
 // 1.65e-3 rms, the output's own rounding, instead of 2.14e-3; 3% more time, as the matrix
 // cores are 9% busy). Everything else is as above.
-template <int D, int DC, bool PAD, class Args>
-__global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
+// Paged, a workgroup has two waves where there are more than compute units, so that a unit holds
+// two: the work before a workgroup's first and after its last tile (7 us and more) is beside the
+// other's loads. @@
+template <int D, int DC, bool PAD, int WAVES, class Args>
+__global__ __launch_bounds__(64 * WAVES, 1) void attention_few_kernel(Args a) {
   constexpr bool kPaged = std::is_same<Args, PagedArgs>::value;
-  constexpr int kBM = 32, kKeys = 32, kWaves = 4;
+  constexpr int kBM = 32, kKeys = 32, kWaves = WAVES;
   constexpr int kPieces = D / 8, kRowB = D * 2;
   constexpr int kTile = kKeys * kRowB;     // one operand's tile
   constexpr int kLd = kTile / 1024;        // 1 KB loads per operand
@@ -859,7 +887,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
   if (PAD && cv >= a.d) cv = 0;
   const unsigned short* vb = a.v + (kPaged ? 0 : k0 * a.v_token) + head * a.v_head;
   const unsigned ob = lds_address(sm) + wave * 4 * kTile;
-  // Paged: the wave's tiles are 128 keys apart and of two times 16 keys, each of one page. Lanes
+  // Paged: the wave's tiles are 32 kWaves keys apart and of two times 16 keys, each of one page. Lanes
   // 2x and 2x + 1 of `place` hold where those of tile x of the 32 at hand are, of `coming` the
   // pages of the next 32.
   [[maybe_unused]] PagedPlace place = {0, 0};
@@ -1104,7 +1132,8 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
     sm_l[wave][lane] = l;
   }
   __syncthreads();
-  const int rr = tid >> 3;  // eight threads per row
+  constexpr int kRowThreads = 64 * kWaves / 32;
+  const int rr = tid / kRowThreads;
   if (row0 + rr >= row_end) return;
   const int64_t rg = row0 + rr;
   const int64_t ot = (unsigned)rg / (unsigned)a.g;
@@ -1127,12 +1156,12 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(Args a) {
     at = ((int64_t)work.slot * a.hk + head) * kBM + rr;
   else
     at = ((int64_t)blockIdx.y * a.nq + q0 + ot) * (a.hk * a.g) + oh;
-  if (cut && (tid & 7) == 0)
+  if (cut && tid % kRowThreads == 0)
     a.part_ml[at] = make_float2(mt, min(vis, kend) > kbeg && lt == 0.f ? -1.f : lt);
   const float inv = vis > 0 ? 1.0f / lt : 0.f;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {  // elements 4 (tid % 8) + 32 i
-    const int e = (tid & 7) * 4 + 32 * i;
+  for (int i = 0; i < D / (4 * kRowThreads); ++i) {
+    const int e = (tid % kRowThreads) * 4 + 4 * kRowThreads * i;
     if (e >= a.d) break;
     f32x4_t v = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1172,13 +1201,28 @@ __device__ __forceinline__ void join_row(const float2* ml, const float* po, int6
   const float ref = m == -INFINITY ? 0.f : m;
   f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
   float l = 0.f, any = 0.f;
-  for (int s = FEW ? 0 : grp; s < splits; s += FEW ? 1 : 8) {
-    const float2 y = ml[s * step];
-    if (y.y != 0.f) any = 1.f;  // 0: the piece saw no key
-    if (y.y <= 0.f) continue;   // -1: only scores of -inf
-    const float f = exp2_fast(y.x - ref);
-    l += y.y * f;
-    if (e < d) o += *(const f32x4_t*)(po + s * step * d + e) * f;
+  constexpr int kApart = FEW ? 1 : 8, kAtOnce = 4;  // pieces whose results are on their way together
+  for (int s0 = FEW ? 0 : grp; s0 < splits; s0 += kApart * kAtOnce) {
+    float2 y[kAtOnce];
+    f32x4_t v[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int64_t s = s0 + u * kApart;
+      y[u] = make_float2(0.f, 0.f);
+      v[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (s < splits) {
+        y[u] = ml[s * step];
+        if (e < d) v[u] = *(const f32x4_t*)(po + s * step * d + e);  // anything, where no key was seen
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (y[u].y != 0.f) any = 1.f;  // 0: the piece saw no key
+      if (y[u].y <= 0.f) continue;   // -1: only scores of -inf
+      const float f = exp2_fast(y[u].x - ref);
+      l += y[u].y * f;
+      o += v[u] * f;
+    }
   }
   if constexpr (!FEW) {
 #pragma unroll
@@ -1221,8 +1265,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 }
 
 // The same for a paged call: workgroup (slot, key head) joins a share of the rows of the row block
-// that left a partial result there, each of its pieces another one. Up to eight pieces a group
-// of 32 lanes per row, else the eight groups to a row.
+// that left a partial result there, each of its pieces another one: a group of 32 lanes per row,
+// or, for few rows of many pieces, the eight groups to a row.
 template <int BM, int TILE, bool FEW>
 __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
   const int grp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -1239,7 +1283,7 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
     join_row<decltype(ALONE)::value>(a.part_ml + first + r, a.part_o + (first + r) * a.d, step, w.pieces,
                                      a.d, grp, lane, a.o + tok * a.o_token + qh * a.o_head);
   };
-  if (w.pieces <= 8) {
+  if (w.pieces <= 8 || share > 2) {
     for (int r = w.piece * share + grp; r < end; r += 8) join(r, std::integral_constant<bool, true>{});
     return;
   }
@@ -1256,7 +1300,13 @@ void launch_kernel(const Args& a, dim3 groups, hipStream_t s) {
 
 template <int D, int DC, bool PAD, class Args>
 void launch_few(const Args& a, dim3 groups, hipStream_t s) {
-  hipLaunchKernelGGL((attention_few_kernel<D, DC, PAD, Args>), groups, dim3(256), 0, s, a);
+  if constexpr (std::is_same<Args, PagedArgs>::value) {
+    if (groups.x > kAUnits) {
+      hipLaunchKernelGGL((attention_few_kernel<D, DC, PAD, 2, Args>), groups, dim3(128), 0, s, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((attention_few_kernel<D, DC, PAD, 4, Args>), groups, dim3(256), 0, s, a);
 }
 
 // The kernel for heads of a.d elements.
@@ -1456,7 +1506,7 @@ PagedPlan plan_of(const th_paged_cache* c, const th_paged_params* p) {
   if (r.few) bound(r.many ? seqs : rows / 32 + seqs, 4 * kAUnits, 320, r.few_items, r.few_slots);
   if (r.many) {
     const int64_t longer = r.few ? std::min(seqs, rows / (kAFewRows + 1)) : seqs;
-    bound(rows / 128 + longer, 2 * kAUnits, 3 * kAKT, r.many_items, r.many_slots);
+    bound(rows / 128 + longer, (int64_t)(2 * kAUnits / kAShare), 3 * kAKT, r.many_items, r.many_slots);
   }
   return r;
 }
