@@ -7,6 +7,7 @@ has not been built, loading raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -520,44 +521,76 @@ class MxMatrix:
     [n, b / 2] with element 2i in the low half of byte i) and scales (uint8 [n, b / 32]); a value is
     its element times 2^(scale - 127) of its 32. The scales' rows are a multiple of 16 bytes apart
     where mx_linear is to read them."""
-    __slots__ = ("type", "elements", "scales")
+    __slots__ = ("type", "_elements", "_scales", "_new")
 
     def __init__(self, type, elements, scales):
         if type not in _MX_TYPES:
             raise ValueError(f"type must be one of {sorted(_MX_TYPES)}, not {type!r}")
-        self.type, self.elements, self.scales = type, elements, scales
+        self.type, self._elements, self._scales, self._new = type, elements, scales, None
 
     @classmethod
     def empty(cls, n, b, type, device):
+        """A new one, both parts in one allocation; the tensors are made when they are asked for
+        (2 us less on the way to a kernel)."""
         torch = _torch()
+        if type not in _MX_TYPES:
+            raise ValueError(f"type must be one of {sorted(_MX_TYPES)}, not {type!r}")
         if b % 32:
             raise ValueError(f"b must be a multiple of 32, not {b}")
-        scales = torch.empty((n, -(-b // 512) * 16), dtype=torch.uint8, device=device)
-        return cls(type, torch.empty((n, b if type == "e4m3" else b // 2), dtype=torch.uint8,
-                                     device=device), scales[:, :b // 32])
+        width = b if type == "e4m3" else b // 2
+        pitch = -(-b // 512) * 16
+        m = cls.__new__(cls)
+        m.type, m._elements, m._scales = type, None, None
+        m._new = torch.empty(n * (width + pitch), dtype=torch.uint8, device=device), n, b, width, pitch
+        return m
+
+    @property
+    def elements(self):
+        if self._elements is None:
+            buf, n, _, width, _ = self._new
+            self._elements = buf.as_strided((n, width), (width, 1))
+        return self._elements
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            buf, n, b, width, pitch = self._new
+            self._scales = buf.as_strided((n, b // 32), (pitch, 1), n * width)
+        return self._scales
 
     @property
     def shape(self):
-        n, width = self.elements.shape
+        if self._new is not None:
+            return self._new[1:3]
+        n, width = self._elements.shape
         return n, width if self.type == "e4m3" else 2 * width
 
     @property
     def device(self):
-        return self.elements.device
+        return (self._elements if self._new is None else self._new[0]).device
+
+
+def _mx_index(m) -> int:
+    return _device_index(m._elements if m._new is None else m._new[0])
 
 
 def _mx(index, name, m):
     """(n, b, host struct) of a microscaled matrix on GPU index."""
+    if m._new is not None:
+        buf, n, b, width, pitch = m._new
+        if buf.get_device() != index:
+            raise ValueError(f"{name} must live on GPU {index}")
+        at = buf.data_ptr()
+        # its scales begin 16-byte aligned: rows of 16 bytes and more before them
+        return n, b, Mx(at, at + n * width, width, pitch, _MX_TYPES[m.type])
     torch = _torch()
-    n, b = m.shape
-    blocks = b // 32
-    e = _row_pitch(_require(index, name + ".elements", m.elements, m.elements.shape, torch.uint8), n,
-                   m.elements.shape[1])
-    s = _require(index, name + ".scales", m.scales, (n, blocks), torch.uint8)
-    # a single row's pitch, which no access uses, is given as a multiple of 16 that holds it
-    s = s[0] if n > 1 else -(-blocks // 16) * 16
-    e = e if n > 1 else -(-e // 16) * 16
-    return n, b, Mx(m.elements.data_ptr(), m.scales.data_ptr(), e, s, _MX_TYPES[m.type])
+    n, width = m._elements.shape
+    b = width if m.type == "e4m3" else 2 * width
+    e = _require(index, name + ".elements", m._elements, m._elements.shape, torch.uint8)[0]
+    s = _require(index, name + ".scales", m._scales, (n, b // 32), torch.uint8)[0]
+    if n == 1:  # a single row's pitches, which no access uses: multiples of 16 that hold it
+        e, s = -(-width // 16) * 16, -(-b // 512) * 16
+    return n, b, Mx(m._elements.data_ptr(), m._scales.data_ptr(), e, s, _MX_TYPES[m.type])
 
 
 def mx_quantize(X, type="e2m1", out=None):
@@ -579,7 +612,7 @@ def mx_quantize(X, type="e2m1", out=None):
 def mx_dequantize(X, Y=None, out_dtype=None):
     """The values of a microscaled matrix, Y [n, b] in out_dtype (default bf16)."""
     torch = _torch()
-    index = _device_index(X.elements)
+    index = _mx_index(X)
     n, b, x = _mx(index, "X", X)
     ldy = b
     if Y is None:
@@ -590,7 +623,9 @@ def mx_dequantize(X, Y=None, out_dtype=None):
     return Y
 
 
+@functools.lru_cache(maxsize=1024)
 def mx_linear_workspace_size(type: str, n: int, b: int, c: int, out_dtype) -> int:
+    """Kept by its sizes, of which it is a function."""
     torch = _torch()
     out = ctypes.c_size_t(0)
     _check(lib().th_mx_linear_workspace_size(_MX_TYPES[type], n, b, c,
@@ -604,7 +639,7 @@ def mx_linear(X, W, bias=None, act="none", residual=None, Y=None, out_dtype=None
     ("e2m1"), bias [c] bf16; residual and Y [n, c] in out_dtype (bf16 or fp32, default the
     residual's or bf16). Y may be the residual. Forward only."""
     torch = _torch()
-    index = _device_index(X.elements)
+    index = _mx_index(X)
     n, b, x = _mx(index, "X", X)
     c, bw, w = _mx(index, "W", W)
     if bw != b:
@@ -781,22 +816,22 @@ def attention(Q, K, V, q_start=None, k_start=None, causal=True, scale=None, O=No
 
 
 def _paged_cache(index, k_cache, v_cache, pages, k_len):
-    """Host struct of a paged cache, and its dtype."""
+    """Host struct of a paged cache on GPU index."""
     torch = _torch()
-    npages, page, hk, d = k_cache.shape
+    shape = k_cache.shape
+    npages, page, hk, d = shape
     dtype = k_cache.dtype
-    k_s = _require(index, "k_cache", k_cache, (npages, page, hk, d), dtype)
-    v_s = _require(index, "v_cache", v_cache, (npages, page, hk, d), dtype)
+    kp, kt, kh, _ = _require(index, "k_cache", k_cache, shape, dtype)
+    vp, vt, vh, _ = _require(index, "v_cache", v_cache, shape, dtype)
+    if npages <= 1:  # strides of a dimension of one element, which no access uses: the dense ones
+        kp = vp = page * hk * d
+    if hk <= 1:
+        kh = vh = d
     nseq, width = pages.shape
     row = _row_pitch(_require(index, "pages", pages, (nseq, width), torch.int32), nseq, width)
-    if k_len.shape != (nseq,) or (nseq > 1 and k_len.stride(0) != 1):
-        raise ValueError(f"k_len must be contiguous with shape {(nseq,)}")
     _require(index, "k_len", k_len, (nseq,), torch.int32)
-    # strides of a dimension of one element, which no access uses, are given as the dense ones
-    k_s, v_s = ((s[0] if npages > 1 else page * hk * d, s[1], s[2] if hk > 1 else d)
-                for s in (k_s, v_s))
-    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), npages, page, hk, d, *k_s, *v_s,
-                      pages.data_ptr(), k_len.data_ptr(), nseq, width, row)
+    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), npages, page, hk, d, kp, kt, kh, vp, vt,
+                      vh, pages.data_ptr(), k_len.data_ptr(), nseq, width, row)
 
 
 def cache_store(K, V, k_cache, v_cache, pages, k_len, q_start=None):
@@ -828,6 +863,20 @@ def paged_attention_workspace_size(cache: PagedCache, params: PagedParams) -> in
     return out.value
 
 
+_paged_sizes = {}  # workspace sizes by all sizes that they follow from
+
+
+def _paged_workspace(cache, p) -> int:
+    key = (p.nq, p.hq, p.even, cache.hk, cache.d, cache.nseq, cache.width, cache.page_tokens)
+    nbytes = _paged_sizes.get(key)
+    if nbytes is None:
+        nbytes = paged_attention_workspace_size(cache, p)
+        if len(_paged_sizes) >= 1024:
+            _paged_sizes.clear()
+        _paged_sizes[key] = nbytes
+    return nbytes
+
+
 def paged_attention(Q, k_cache, v_cache, pages, k_len, q_start=None, causal=True, scale=None, O=None,
                     ws=None):
     """attention() of new tokens Q [nq, hq, d] (bf16) over a paged cache that holds their keys (see
@@ -853,7 +902,7 @@ def paged_attention(Q, k_cache, v_cache, pages, k_len, q_start=None, causal=True
     p = PagedParams(nq, hq, *q_s, *o_s, 1 if causal else 0, 1 if q_start is None else 0,
                     d ** -0.5 if scale is None else float(scale))
     if ws is None:
-        nbytes = paged_attention_workspace_size(cache, p)
+        nbytes = _paged_workspace(cache, p)
         ws = workspace(nbytes, Q.device) if nbytes else None
     at, nbytes = (None, 0) if ws is None else _workspace_on(index, ws)
     _call_on(index, lib().th_paged_attention, Q.data_ptr(), _dtype_code(Q), _addr(q_start), cache, p,
