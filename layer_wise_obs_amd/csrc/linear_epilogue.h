@@ -149,6 +149,9 @@ __device__ __forceinline__ void finish_tile(const LinEpilogue& ep, int64_t n, in
     constexpr bool f32 = decltype(F32)::value;
     constexpr int kRoom = 16 / (kPass * (f32 ? 2 : 1)), kHeld = WM < kRoom ? WM : kRoom;
     Out8<f32> res[kHeld][kPass];
+    float bias[8];  // once for all tokens: in the loop below every pass would wait for it
+#pragma unroll
+    for (int x = 0; x < 8; ++x) bias[x] = ep.bias && q + x < c ? bf16_to_f32(ep.bias[q + x]) : 0.f;
 #pragma unroll
     for (int i0 = 0; i0 < WM; i0 += kHeld) {
       if (ep.residual) {
@@ -169,7 +172,7 @@ __device__ __forceinline__ void finish_tile(const LinEpilogue& ep, int64_t n, in
             for (int x = 0; x < 8; ++x) v[x] = at[x];
             if (ep.bias) {
 #pragma unroll
-              for (int x = 0; x < 8; ++x) v[x] += q + x < c ? bf16_to_f32(ep.bias[q + x]) : 0.f;
+              for (int x = 0; x < 8; ++x) v[x] += bias[x];
             }
             activate8<NEAR && !f32>(v, ep.act);
 #pragma unroll

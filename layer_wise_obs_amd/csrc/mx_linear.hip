@@ -75,15 +75,15 @@ __device__ __forceinline__ void mx_part(const i32x8_t& v, i32x8_t& high, i32x8_t
   }
 }
 
-template <int XT, int FM, int FN, int GM, int GN, int RX, int RW, bool EXACT>
-__global__ __launch_bounds__(64 * GM * GN, 1) void mx_tile_kernel(MxOperand X, MxOperand W, int64_t n,
+template <int XT, int FM, int FN, int GM, int GN, int KS, int RX, int RW, bool EXACT>
+__global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand X, MxOperand W, int64_t n,
                                                                   int64_t b, int64_t c, int ntm, int ntn,
                                                                   int per_xcd, int steps_per_split,
                                                                   float* __restrict__ part,
                                                                   LinEpilogue ep) {
   constexpr bool kWide = XT == TH_MX_E4M3;  // X's rows of a step are two stages of 128 bytes
   constexpr int TM = 32 * FM * GM, TN = 32 * FN * GN;
-  constexpr int kWaves = GM * GN;
+  constexpr int kWaves = GM * GN * KS;
   constexpr int kXStage = TM * 128, kWStage = TN * 128;
   constexpr int kHalves = kWide ? 2 : 1;
   constexpr int kWAt = RX * kHalves * kXStage, kSAt = kWAt + RW * kWStage;  // in LDS
@@ -110,7 +110,8 @@ __global__ __launch_bounds__(64 * GM * GN, 1) void mx_tile_kernel(MxOperand X, M
   __shared__ __attribute__((aligned(1024))) unsigned char sm[kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / GN, wn = wave % GN;
+  const int kg = KS > 1 ? wave / (GM * GN) : 0;  // the wave's half of a step
+  const int wm = wave % (GM * GN) / GN, wn = wave % GN;
   const unsigned smb = lds_address(sm);
 
   // Loader: chunks of 1 KB (8 rows of 128 bytes), wave w those w + kWaves m of either operand. Lane
@@ -212,7 +213,7 @@ __global__ __launch_bounds__(64 * GM * GN, 1) void mx_tile_kernel(MxOperand X, M
   Frags f0, f1;
   int sa[2][FM], sb[2][FN];  // scales of the first and the second 128 k of a step
   // operand y of substep sub (64 k): the FN blocks of W, then the FM of X
-  auto read_one = [&](int it, int sub, int y, Frags& f) {
+  auto read_one = [&](int it, int sub, int y, Frags& f) __attribute__((always_inline)) {
     if (y < FN) {
       f.b[y].v = *(const i32x4_t*)(sm + kWAt + it % RW * kWStage + (wn * FN + y) * 4096 + (faddr ^ (sub << 5)));
     } else if constexpr (kWide) {
@@ -309,75 +310,142 @@ __global__ __launch_bounds__(64 * GM * GN, 1) void mx_tile_kernel(MxOperand X, M
   static_assert(RX == RW || (kWide && RX == 1 && RW == 2), "the order of the loads");
   static_assert(kLeft3 < 64 && kLeft1 < 64, "vmcnt immediates");
 
-  // prologue: the first scales, then steps 0 .. R-1 but for the last W, step 0 waited for
-  load_scales(0);
-  load_scales(1);
+  if constexpr (KS == 1) {
+    // prologue: the first scales, then steps 0 .. R-1 but for the last W, step 0 waited for
+    load_scales(0);
+    load_scales(1);
 #pragma unroll
-  for (int it = 0; it < RW; ++it) {
-    if (it < RX) {
+    for (int it = 0; it < RW; ++it) {
+      if (it < RX) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          stage_x(it, h);
+#pragma unroll
+          for (int m = 0; m < LX; ++m) issue_x(m);
+        }
+      }
+      if (it < RW - 1) {
+        stage_w(it);
+#pragma unroll
+        for (int m = 0; m < LW; ++m) issue_w(m);
+      }
+    }
+    __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((RW - 2) * LW + (RX - 1) * LX * kHalves) : "memory");
+    clear_past(0);
+    clear_past(1);
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < FM + FN; ++y) {
+      read_one(0, 0, y, f0);
+      read_scale(0, 0, y);
+    }
+    // A step of 256 k: four substeps, each reading the next one's operands. Before the last one the
+    // next step has landed, and the barrier frees this step's buffers (with 8 bits, another one
+    // before the second frees the first half of X). But for the scales' at its beginning a step
+    // has no branch: behind one the compiler puts the products before it, whose results nothing
+    // needs yet.
+    for (int it = 0; it < nk; ++it) {
+      if (it % 4 == 0) {  // into the buffers whose last reads lie before the last barrier
+        load_scales(it / 2 + 2);
+        load_scales(it / 2 + 3);
+      } else if (it % 4 == 3) {  // they have landed, and are read from this step's end on
+        clear_past(it / 2 + 1);
+        clear_past(it / 2 + 2);
+      }
+      shift_scales(0);
+      stage_w(it - 1 + RW);
+      products(f0, std::integral_constant<int, 0>{}, [&](int x) __attribute__((always_inline)) {
+        reads(x, it, 1, f1);
+        loads_w(x);
+      });
+      if constexpr (kWide) {
+        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft1) : "memory");
+        __syncthreads();
+        stage_x(it + RX, 0);
+      }
+      products(f1, std::integral_constant<int, 1>{}, [&](int x) __attribute__((always_inline)) {
+        reads(x, it, 2, f0);
+        scales(x, it, 1);
+        if constexpr (kWide) loads_x(x);
+      });
+      shift_scales(1);
+      products(f0, std::integral_constant<int, 2>{}, [&](int x) __attribute__((always_inline)) {
+        reads(x, it, 3, f1);
+      });
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft3) : "memory");
+      __syncthreads();
+      stage_x(it + RX, kHalves - 1);
+      products(f1, std::integral_constant<int, 3>{}, [&](int x) __attribute__((always_inline)) {
+        reads(x, it + 1, 0, f0);
+        scales(x, it + 1, 0);
+        loads_x(x);
+      });
+    }
+  } else {
+    // Two waves to a 32 x 32 block, either with half of a step's k: its two substeps, one barrier
+    // between them, which the next step's X and W have landed before.
+    static_assert(RX == RW && KS == 2, "one ring");
+    load_scales(0);
+    load_scales(1);
+#pragma unroll
+    for (int it = 0; it < RW; ++it) {
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         stage_x(it, h);
 #pragma unroll
         for (int m = 0; m < LX; ++m) issue_x(m);
       }
-    }
-    if (it < RW - 1) {
       stage_w(it);
 #pragma unroll
       for (int m = 0; m < LW; ++m) issue_w(m);
     }
-  }
-  __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((RW - 2) * LW + (RX - 1) * LX * kHalves) : "memory");
-  clear_past(0);
-  clear_past(1);
-  __syncthreads();
-#pragma unroll
-  for (int y = 0; y < FM + FN; ++y) {
-    read_one(0, 0, y, f0);
-    read_scale(0, 0, y);
-  }
-  // A step of 256 k: four substeps, each reading the next one's operands. Before the last one the
-  // next step has landed, and the barrier frees this step's buffers (with 8 bits, another one
-  // before the second frees the first half of X). But for the scales' at its beginning a step
-  // has no branch: behind one the compiler puts the products before it, whose results nothing
-  // needs yet.
-  for (int it = 0; it < nk; ++it) {
-    if (it % 4 == 0) {  // into the buffers whose last reads lie before the last barrier
-      load_scales(it / 2 + 2);
-      load_scales(it / 2 + 3);
-    } else if (it % 4 == 3) {  // they have landed, and are read from this step's end on
-      clear_past(it / 2 + 1);
-      clear_past(it / 2 + 2);
-    }
-    shift_scales(0);
-    stage_w(it - 1 + RW);
-    products(f0, std::integral_constant<int, 0>{}, [&](int x) __attribute__((always_inline)) {
-      reads(x, it, 1, f1);
-      loads_w(x);
-    });
-    if constexpr (kWide) {
-      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft1) : "memory");
-      __syncthreads();
-      stage_x(it + RX, 0);
-    }
-    products(f1, std::integral_constant<int, 1>{}, [&](int x) __attribute__((always_inline)) {
-      reads(x, it, 2, f0);
-      scales(x, it, 1);
-      if constexpr (kWide) loads_x(x);
-    });
-    shift_scales(1);
-    products(f0, std::integral_constant<int, 2>{}, [&](int x) __attribute__((always_inline)) {
-      reads(x, it, 3, f1);
-    });
-    __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft3) : "memory");
+    __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((RW - 1) * kStep) : "memory");
+    clear_past(0);
+    clear_past(1);
     __syncthreads();
-    stage_x(it + RX, kHalves - 1);
-    products(f1, std::integral_constant<int, 3>{}, [&](int x) __attribute__((always_inline)) {
-      reads(x, it + 1, 0, f0);
-      scales(x, it + 1, 0);
-      loads_x(x);
-    });
+    auto read_all = [&](int it, int c, Frags& f) __attribute__((always_inline)) {
+#pragma unroll
+      for (int y = 0; y < FM + FN; ++y) read_one(it, 2 * kg + c, y, f);
+    };
+    auto read_scales = [&](int it) __attribute__((always_inline)) {  // into the second set
+      const unsigned char* p = sm + scale_slot(it / 2) + (it % 2 * 2 + kg) * 4;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sb[1][j] = *(const int*)(p + (TM + (wn * FN + j) * 32 + r32) * 16);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) sa[1][i] = *(const int*)(p + ((wm * FM + i) * 32 + r32) * 16);
+    };
+    read_all(0, 0, f0);
+    read_scales(0);
+    for (int it = 0; it < nk; ++it) {
+      if (it % 4 == 0) {
+        load_scales(it / 2 + 2);
+        load_scales(it / 2 + 3);
+      } else if (it % 4 == 3) {
+        clear_past(it / 2 + 1);
+        clear_past(it / 2 + 2);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) sa[0][i] = sa[1][i];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sb[0][j] = sb[1][j];
+      shift_scales(0);
+      read_all(it, 1, f1);
+      products(f0, std::integral_constant<int, 0>{}, [](int) {});
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((RW - 2) * kStep) : "memory");
+      __syncthreads();
+      read_all(it + 1, 0, f0);
+      read_scales(it + 1);
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        stage_x(it + RX, h);
+#pragma unroll
+        for (int m = 0; m < LX; ++m) issue_x(m);
+      }
+      stage_w(it + RW);
+#pragma unroll
+      for (int m = 0; m < LW; ++m) issue_w(m);
+      products(f1, std::integral_constant<int, 1>{}, [](int) {});
+    }
   }
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();  // every wave's loads have landed: the stages may be reused
@@ -388,12 +456,35 @@ __global__ __launch_bounds__(64 * GM * GN, 1) void mx_tile_kernel(MxOperand X, M
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] += acc_low[i][j];
   }
+  if constexpr (KS > 1) {  // the second halves' sums, added by the waves of the first
+    static_assert(GM * GN * FM * FN * 4096 <= kLds, "sums fit the stages");
+    float* sums = (float*)sm + (wave % (GM * GN)) * FM * FN * 1024 + lane;
+    if (kg) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sums[((i * FN + j) * 16 + e) * 64] = acc[i][j][e];
+    }
+    __syncthreads();
+    if (kg) return;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] += sums[((i * FN + j) * 16 + e) * 64];
+    wave_sync();  // read before the strips take their place
+  }
   // Epilogue through LDS, one 32-token strip of the wave's block at a time: the lane holds
   // channel l % 32 of each block and tokens 8 (e / 4) + 4 (l / 32) + e % 4; read back, a lane has
   // 8 consecutive channels of one token.
   constexpr int kCols = 32 * FN, kPitch = kCols + 4;
-  static_assert(kWaves * 32 * kPitch * 4 <= kLds, "strips fit the stages");
-  float* strip = (float*)sm + wave * 32 * kPitch;
+  static_assert((KS > 1 ? GM * GN * FM * FN * 4096 : 0) + GM * GN * 32 * kPitch * 4 <= kLds,
+                "strips fit the stages");
+  // behind the sums of the second halves, which other waves may still read
+  float* strip = (float*)sm + (KS > 1 ? GM * GN * FM * FN * 1024 : 0) + wave * 32 * kPitch;
   constexpr int kLanes = kCols / 8;   // lanes per token
   constexpr int kTok = 64 / kLanes;   // tokens per pass
   constexpr int kPass = 32 / kTok;
@@ -515,7 +606,7 @@ struct MxTile {
 enum { kMx64 = 0, kMx128 = 1, kMx128x256 = 2, kMx256 = 3, kMxTiles = 4, kMxSkinny = 4 };
 constexpr int kMxUnits = 256;  // compute units
 constexpr MxTile kMxForms[kMxTiles] = {
-    {64, 64, 2 * kMxUnits, {0.27, 0.42, 0.95}, {0.44, 0.62, 1.17}, 5.0},   // 4 waves of 32 x 32
+    {64, 64, 2 * kMxUnits, {0.24, 0.42, 0.67}, {0.40, 0.62, 1.17}, 5.0},   // 4 (or 4 times 2) waves of 32 x 32
     {128, 128, 2 * kMxUnits, {0.52, 0.68, 1.48}, {1.15, 1.5, 2.7}, 5.0},   // 8 waves of 32 x 64
     {128, 256, kMxUnits, {0.70, 1.05, 2.6}, {1.1, 1.35, 2.8}, 6.0},        // 8 waves of 64 x 64
     {256, 256, kMxUnits, {1.1, 1.87, 4.3}, {2.1, 2.95, 5.7}, 6.0},         // 8 waves of 64 x 128
@@ -557,13 +648,13 @@ MxPlan plan_of(int xtype, int64_t n, int64_t b, int64_t c, bool exact, bool can_
   return best;
 }
 
-template <int XT, int FM, int FN, int GM, int GN, int RX, int RW, bool EXACT>
+template <int XT, int FM, int FN, int GM, int GN, int KS, int RX, int RW, bool EXACT>
 hipError_t launch_tiles(const MxOperand& X, const MxOperand& W, int64_t n, int64_t b, int64_t c,
                         const MxPlan& p, float* part, const LinEpilogue& ep, hipStream_t s) {
   const int ntm = (int)cdiv(n, 32 * FM * GM), ntn = (int)cdiv(c, 32 * FN * GN);
   const int per_xcd = (int)cdiv((int64_t)ntm * ntn, 8);
-  hipLaunchKernelGGL((mx_tile_kernel<XT, FM, FN, GM, GN, RX, RW, EXACT>),
-                     dim3((unsigned)(8 * per_xcd), (unsigned)p.splits), dim3(64 * GM * GN), 0, s, X, W, n, b,
+  hipLaunchKernelGGL((mx_tile_kernel<XT, FM, FN, GM, GN, KS, RX, RW, EXACT>),
+                     dim3((unsigned)(8 * per_xcd), (unsigned)p.splits), dim3(64 * GM * GN * KS), 0, s, X, W, n, b,
                      c, ntm, ntn, per_xcd, p.per, part, ep);
   return hipGetLastError();
 }
@@ -573,10 +664,10 @@ hipError_t launch_form(const MxOperand& X, const MxOperand& W, int64_t n, int64_
                        const MxPlan& p, float* part, const LinEpilogue& ep, hipStream_t s) {
   constexpr bool wide = XT == TH_MX_E4M3;
   switch (p.tile) {
-    case kMx64: return launch_tiles<XT, 1, 1, 2, 2, wide ? 3 : 4, wide ? 3 : 4, EXACT>(X, W, n, b, c, p, part, ep, s);
-    case kMx128: return launch_tiles<XT, 1, 2, 4, 2, wide ? 1 : 2, 2, EXACT>(X, W, n, b, c, p, part, ep, s);
-    case kMx128x256: return launch_tiles<XT, 2, 2, 2, 4, 2, 2, EXACT>(X, W, n, b, c, p, part, ep, s);
-    default: return launch_tiles<XT, 2, 4, 4, 2, wide ? 1 : 2, 2, EXACT>(X, W, n, b, c, p, part, ep, s);
+    case kMx64: return launch_tiles<XT, 1, 1, 2, 2, wide && !EXACT ? 1 : 2, wide ? 3 : 4, wide ? 3 : 4, EXACT>(X, W, n, b, c, p, part, ep, s);
+    case kMx128: return launch_tiles<XT, 1, 2, 4, 2, 1, wide ? 1 : 2, 2, EXACT>(X, W, n, b, c, p, part, ep, s);
+    case kMx128x256: return launch_tiles<XT, 2, 2, 2, 4, 1, 2, 2, EXACT>(X, W, n, b, c, p, part, ep, s);
+    default: return launch_tiles<XT, 2, 4, 4, 2, 1, wide ? 1 : 2, 2, EXACT>(X, W, n, b, c, p, part, ep, s);
   }
 }
 
