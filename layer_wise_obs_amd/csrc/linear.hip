@@ -423,6 +423,7 @@ hipError_t launch_linear(const unsigned short* X, int64_t ldx, const unsigned sh
   ep.ldy = ldy;
   ep.act = act;
   ep.y_f32 = ydt == TH_F32;
+  ep.past_cache = 0;
   const LinPlan p = plan_of(n, b, c, part != nullptr);
   float* raw = p.splits > 1 ? part : nullptr;
   hipError_t e;

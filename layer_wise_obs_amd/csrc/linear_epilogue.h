@@ -20,6 +20,7 @@ struct LinEpilogue {
   int64_t ldr, ldy;
   int act;       // th_activation
   int y_f32;     // Y and residual are fp32 (else bf16)
+  int past_cache;  // stores past the caches, which Y would not stay in (MX below only)
 };
 
 // z Phi(z), Phi(-|z|) = erfc(|z| / sqrt 2) / 2 = e^(-z^2/2) t Q(t), t = 1 / (1 + |z| / 2), Q
@@ -100,6 +101,7 @@ struct Out8<false> {
   __device__ __forceinline__ void load(const LinEpilogue& ep, int64_t t, int64_t q) {
     r = *(const bf16_out_t*)((const unsigned short*)ep.residual + t * ep.ldr + q);
   }
+  template <bool MX = false>
   __device__ __forceinline__ void put(float (&v)[8], const LinEpilogue& ep, int64_t t, int64_t q) const {
     if (ep.residual) {
 #pragma unroll
@@ -111,7 +113,11 @@ struct Out8<false> {
     bf16x8_t y;
 #pragma unroll
     for (int x = 0; x < 8; ++x) y[x] = (__bf16)v[x];
-    *(bf16_out_t*)((unsigned short*)ep.y + t * ep.ldy + q) = __builtin_bit_cast(u32x4_t, y);
+    bf16_out_t* to = (bf16_out_t*)((unsigned short*)ep.y + t * ep.ldy + q);
+    if (MX && ep.past_cache)
+      __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, y), to);
+    else
+      *to = __builtin_bit_cast(u32x4_t, y);
   }
 };
 template <>
@@ -122,6 +128,7 @@ struct Out8<true> {
     a = *(const f32_out_t*)r;
     b = *(const f32_out_t*)(r + 4);
   }
+  template <bool MX = false>
   __device__ __forceinline__ void put(float (&v)[8], const LinEpilogue& ep, int64_t t, int64_t q) const {
     if (ep.residual) {
 #pragma unroll
@@ -139,7 +146,7 @@ struct Out8<true> {
 // Epilogue of a wave's WM strips of 32 tokens, each kPass passes of the lanes' tokens:
 // write_strip(i) puts strip i into LDS, values(p) is then the lane's eight channels from q of
 // its token(i, p).
-template <int WM, int kPass, bool NEAR = false, class Token, class Values, class Write>
+template <int WM, int kPass, bool MX = false, class Token, class Values, class Write>
 __device__ __forceinline__ void finish_tile(const LinEpilogue& ep, int64_t n, int64_t c, int64_t q,
                                             Token&& token, Values&& values, Write&& write_strip) {
   const bool whole = q + 8 <= c;  // else fewer than eight channels, or none
@@ -174,7 +181,7 @@ __device__ __forceinline__ void finish_tile(const LinEpilogue& ep, int64_t n, in
 #pragma unroll
               for (int x = 0; x < 8; ++x) v[x] += bias[x];
             }
-            activate8<NEAR && !f32>(v, ep.act);
+            activate8<MX && !f32>(v, ep.act);
 #pragma unroll
             for (int x = 0; x < 8; ++x) at[x] = v[x];
           }
@@ -185,7 +192,7 @@ __device__ __forceinline__ void finish_tile(const LinEpilogue& ep, int64_t n, in
           const f32x4_t* vp = (const f32x4_t*)values(p);
           const f32x4_t lo = vp[0], hi = vp[1];
           float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          res[i][p].put(v, ep, token(i0 + i, p), q);
+          res[i][p].template put<MX>(v, ep, token(i0 + i, p), q);
         }
         if (!whole) {  // the last channels of a row
 #pragma unroll 1

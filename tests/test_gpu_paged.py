@@ -65,7 +65,10 @@ CASES = [
     ([(1, 33)] * 9 + [(3, 9000)] + [(0, 50)] * 3, 8, 2, 128, 32),
     ([(1, 100)] * 31 + [(1, 20000)] + [(1, 1)] * 32, 16, 2, 128, 16),  # one long among short
     ([(600, 700), (1, 1), (1, 5000), (50, 6000)], 4, 1, 80, 64),
-    ([(1, 40)], 64, 1, 64, 16), ([(2, 3000), (1, 9)], 33, 1, 64, 32)]  # groups past the few rows
+    ([(1, 40)], 64, 1, 64, 16), ([(2, 3000), (1, 9)], 33, 1, 64, 32),  # groups past the few rows
+    ([(100, 150)] + [(0, 5)] * 60 + [(1, 40)] * 20, 4, 2, 64, 16),  # few rows on average only
+    ([(0, 9)] * 50 + [(70, 6000)] + [(1, 2000)] * 30, 4, 1, 128, 32),
+    ([(33, 40)] * 70, 2, 1, 64, 16), ([(40, 900), (3, 2500)] * 40, 2, 2, 72, 64)]  # more than 64 longer ones
 
 
 @pytest.mark.parametrize("lens,hq,hk,d,page", CASES)
