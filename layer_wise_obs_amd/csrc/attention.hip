@@ -169,7 +169,8 @@ __device__ __forceinline__ void paged_sequence(const PagedArgs& a, int64_t s, in
 // room are cut into as many pieces as run at a time, one short piece each counted; more pairs into
 // twice as many, which evens out their lengths; so many that they even out by themselves, where
 // one is longer than a workgroup's share. Others: pieces of a share, or two where the row blocks
-// fill the units. @@
+// fill the units. (Shares of a half, a third and a fifth of these were slower over the sequences
+// tried: 64 tokens over 300001 keys, chunks of 4100 tokens over 40000, 256 tokens over 1000 each.)
 template <int TILE, bool FEW>
 __device__ __forceinline__ int paged_per(const PagedArgs& a, float tiles, float blocks) {
   if (a.slots == 0) return 1 << 26;  // more than any sequence has
@@ -209,7 +210,8 @@ __device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, unsigned at,
     if (s0 + lane < a.nseq) paged_sequence<BM>(a, s0 + lane, q0, q1, lk, blocks);
     who = lane;
     if (!FEW && a.nseq > 1 && a.nseq <= 64) {
-      // the ones with most keys first: a long piece that begins last keeps the others waiting (@@)
+      // the ones with most keys first: a long piece that begins last keeps the others waiting
+      // (chunks of 4100 tokens, 708 -> 652 us; few rows have pieces that are alike)
       const int all = a.nseq;
       int rank = 0;
       for (int j = 0; j < all; ++j) {
@@ -786,7 +788,9 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
 // cores are 9% busy). Everything else is as above.
 // Paged, a workgroup has two waves where there are more than compute units, so that a unit holds
 // two: the work before a workgroup's first and after its last tile (7 us and more) is beside the
-// other's loads. @@
+// other's loads. 64 tokens over 300001 keys in pages, 64 heads on 8: 253-260 us (4.8 TB/s) and 7
+// for the join; one token over 300 keys 12.0, the page numbers' loads before the keys' being the
+// rest to 10.1; 16 tokens over 1000 keys each, 32 heads, 67 where packed keys take 58.
 template <int D, int DC, bool PAD, int WAVES, class Args>
 __global__ __launch_bounds__(64 * WAVES, 1) void attention_few_kernel(Args a) {
   constexpr bool kPaged = std::is_same<Args, PagedArgs>::value;

@@ -12,7 +12,9 @@
 // 0.1048; 8 bits 0.0302 and 0.0269.)
 //
 // Bound by memory. Four lanes share a block, each moves eight elements (16 bytes of bf16, 32
-// of fp32); a workgroup's lanes follow the rows one after another.
+// of fp32); a workgroup's lanes follow the rows one after another. 11008 x 4096 from fp32 to 4
+// bits 30-32 us (6.6 TB/s, some of it from the last level cache), to bf16 from 4 bits 21-22; 65536 x
+// 4096 of 8 bits to bf16 148-158 (5.3-5.5 TB/s); 5 rows of 11008 2.4 and 2.8, a launch's time.
 #include "common.h"
 #include "mx.h"
 #include "row8.h"

@@ -19,10 +19,23 @@
 // the byte tells): either part's products lie within 13 places, and two products give
 // fp32's sum.
 //
-// Tiles as in linear.hip: (64 FM) tokens x (32 FN GN) channels on 2 x GN waves, each 32 FM x
-// 32 FN. Stages of 128 k are filled by direct global->LDS loads, S deep; 16-byte pieces of a
-// row are XOR-swizzled so that operand reads use all banks. Scales come 16 bytes (512 k) of a
-// row at a time, every fourth stage, into two buffers of their own.
+// A workgroup takes (32 FM GM) tokens x (32 FN GN) channels on GM x GN waves, each 32 FM x 32 FN
+// (times KS: few tiles of 64 x 64 get twice the waves, which halve a step's k between them: 777
+// tokens 2080 -> 1023 14.1 -> 12.0 us with e4m3, 256 tokens 4096 -> 4096 with an fp32 Y 20.8 ->
+// 16.4; with e4m3 and a bf16 Y, whose products take half the time, there is nothing to halve).
+// Steps are of 256 k: a row of 4 bits is then one cache line of 128 bytes (with 64 bytes of a row
+// at a time 872 us where this takes 840), one of 8 bits two, in halves. Direct global->LDS loads
+// fill RX steps of X and RW of W; 16-byte pieces of a row are XOR-swizzled so that operand reads
+// use all banks. Scales come 16 bytes (512 k) of a row at a time, every other step, into four
+// slots of their own. The step has no branch: with one, the compiler moved products behind it and
+// past the barrier (947 us). Operand reads and the next steps' loads stand between the products.
+//
+// Large products are bound by power: 32768 tokens 4096 -> 11008 with both of 4 bits take 810-890 us
+// by card (3.6-3.3 PFLOP/s), at 1.5 GHz with the matrix cores half busy, and 1.96 GHz with the
+// loads into LDS left out; with an e4m3 X and a bf16 Y 1085, with an fp32 Y 1960; 8192 tokens
+// 11008 -> 4096 173, 244 and 444. Of 840 us the epilogue is 111, the stores of Y 62 of it. Waves
+// of 64 x 128, eight to a tile: of 128 x 64 the same for 4 bits, 2234 against 2022 for the fp32 Y;
+// four waves of 128 x 128 892 against 839.
 #include "common.h"
 #include "lds_dma.h"
 #include "linear_epilogue.h"
@@ -34,7 +47,9 @@ namespace {
 
 constexpr int kMK = 256;         // contraction per step: whole cache lines of 4-bit rows
 constexpr int kMScaleSlots = 4;  // buffers of 16 bytes (512 k) of scales a row
-constexpr int kMGroup = 4;    // token tiles per group in the walk order
+// Token tiles per group in the walk order: 32768 tokens 4096 -> 11008 in groups of 2, 4, 8, 16
+// 853, 838, 878 and 901 us.
+constexpr int kMGroup = 4;
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
@@ -526,7 +541,8 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
 // v_mfma_scale_f32_16x16x128_f8f6f4 (lane l: channel l % 16, k 32 (l / 16) .. + 31), with its
 // scales 16 bytes (512 k) of a channel at a time; X comes from L2, in two parts where it is of
 // e4m3. The waves' sums meet in LDS and are added in the order of the waves. Workgroup x takes
-// the channels from 16 (first + x).
+// the channels from 16 (first + x). One token 4096 -> 4096: 4.8-5.1 us, of which its 9 MB take
+// 1.5; the rest is the launch and one chain of loads, products and joins.
 constexpr int kMsWaves = 8;
 
 template <int XT>
@@ -596,8 +612,10 @@ __global__ __launch_bounds__(64 * kMsWaves) void mx_skinny_kernel(MxOperand X, M
 // The tile kernel's forms. Its time is modelled as rounds of `slots` workgroups, each fixed +
 // steps * (microseconds a step, by kind: e2m1, e4m3, e4m3 in two parts): `full` with all slots
 // taken, and of forms with two workgroups per compute unit as soon as units are shared; between
-// `lone` and that, by their number, in the other forms. The join of splits takes 3 us and its
-// traffic at 4 TB/s. @@MODEL
+// `lone` and that, by their number, in the other forms. The join of splits takes 1.7 us and its
+// traffic at 4 TB/s. (Fitted to all forms' times, whole and in up to eight splits, at 17 to 6000
+// tokens through 512 -> 2048, 2080 -> 1023, 4096 -> 4096, 4096 -> 11008 and 11008 -> 4096, in every
+// kind: what it takes is as fast as the fastest in the mean, 5% slower at most.)
 struct MxTile {
   int tm, tn;
   int slots;
@@ -606,10 +624,10 @@ struct MxTile {
 enum { kMx64 = 0, kMx128 = 1, kMx128x256 = 2, kMx256 = 3, kMxTiles = 4, kMxSkinny = 4 };
 constexpr int kMxUnits = 256;  // compute units
 constexpr MxTile kMxForms[kMxTiles] = {
-    {64, 64, 2 * kMxUnits, {0.24, 0.42, 0.67}, {0.40, 0.62, 1.17}, 5.0},   // 4 (or 4 times 2) waves of 32 x 32
-    {128, 128, 2 * kMxUnits, {0.52, 0.68, 1.48}, {1.15, 1.5, 2.7}, 5.0},   // 8 waves of 32 x 64
-    {128, 256, kMxUnits, {0.70, 1.05, 2.6}, {1.1, 1.35, 2.8}, 6.0},        // 8 waves of 64 x 64
-    {256, 256, kMxUnits, {1.1, 1.87, 4.3}, {2.1, 2.95, 5.7}, 6.0},         // 8 waves of 64 x 128
+    {64, 64, 2 * kMxUnits, {0.27, 0.41, 0.63}, {0.48, 0.61, 1.16}, 5.2},    // 4 (or 4 times 2) waves of 32 x 32
+    {128, 128, 2 * kMxUnits, {0.62, 0.76, 1.54}, {1.24, 1.62, 3.55}, 4.9},  // 8 waves of 32 x 64
+    {128, 256, kMxUnits, {0.75, 1.18, 2.8}, {1.19, 1.49, 3.05}, 5.1},       // 8 waves of 64 x 64
+    {256, 256, kMxUnits, {1.09, 1.88, 4.3}, {1.89, 2.5, 4.65}, 8.2},        // 8 waves of 64 x 128
 };
 constexpr int64_t kMxSkinnyTokens = 16;
 
@@ -630,7 +648,7 @@ MxPlan plan_of(int xtype, int64_t n, int64_t b, int64_t c, bool exact, bool can_
     const int64_t tiles = cdiv(n, k.tm) * cdiv(c, k.tn);
     if (tiles >= ((int64_t)1 << 23) - 8) continue;  // a launch has less than 2^32 threads
     for (int64_t want : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (want > 1 && (!can_split || steps < 2 * want || tiles * want > 4 * k.slots)) break;
+      if (want > 1 && (!can_split || tiles * want > 4 * k.slots)) break;
       const int64_t per = want == 1 ? steps : cdiv(cdiv(steps, 2), want) * 2;
       const int64_t splits = cdiv(steps, per);
       const int64_t full = tiles * splits / k.slots, rest = tiles * splits % k.slots;
@@ -639,11 +657,12 @@ MxPlan plan_of(int xtype, int64_t n, int64_t b, int64_t c, bool exact, bool can_
         const double share = k.slots > kMxUnits ? (rest > kMxUnits ? 1.0 : 0.0) : (double)rest / k.slots;
         us += k.fixed + (double)per * (k.lone[kind] + (k.full[kind] - k.lone[kind]) * share);
       }
-      if (splits > 1) us += 3.0 + 8.0 * (double)splits * (double)n * (double)c / 4e6;
+      if (splits > 1) us += 1.7 + 8.0 * (double)splits * (double)n * (double)c / 4e6;
       if (us < least) {
         least = us;
         best = {t, (int)splits, (int)per};
       }
+      if (per <= 2) break;
     }
   }
   return best;
