@@ -19,16 +19,16 @@
 // the byte tells): either part's products lie within 13 places, and two products give
 // fp32's sum.
 //
-// A workgroup takes (32 FM GM) tokens x (32 FN GN) channels on GM x GN waves, each 32 FM x 32 FN
-// (times KS: few tiles of 64 x 64 get twice the waves, which halve a step's k between them: 777
-// tokens 2080 -> 1023 14.1 -> 12.0 us with e4m3, 256 tokens 4096 -> 4096 with an fp32 Y 20.8 ->
-// 16.4; with e4m3 and a bf16 Y, whose products take half the time, there is nothing to halve).
-// Steps are of 256 k: a row of 4 bits is then one cache line of 128 bytes (with 64 bytes of a row
-// at a time 872 us where this takes 840), one of 8 bits two, in halves. Direct global->LDS loads
-// fill RX steps of X and RW of W; 16-byte pieces of a row are XOR-swizzled so that operand reads
-// use all banks. Scales come 16 bytes (512 k) of a row at a time, every other step, into four
-// slots of their own. The step has no branch: with one, the compiler moved products behind it and
-// past the barrier (947 us). Operand reads and the next steps' loads stand between the products.
+// A workgroup takes (32 FM GM) tokens x (32 FN GN) channels on GM x GN waves, each 32 FM x 32 FN,
+// times KS: few tiles of 64 x 64 get twice the waves, which halve a step's k between them (777
+// tokens 2080 -> 1023 with e4m3 and an fp32 Y 14.1 -> 11.7 us, 256 tokens 4096 -> 4096 20.8 ->
+// 16.3; with e4m3 and a bf16 Y there is nothing to gain). Steps are of 256 k: a row of 4 bits is
+// then one cache line of 128 bytes (with 64 bytes of a row at a time 872 us where this takes 840),
+// one of 8 bits two, in halves. Direct global->LDS loads fill RX steps of X and RW of W; 16-byte
+// pieces of a row are XOR-swizzled so that operand reads use all banks. Scales come 16 bytes
+// (512 k) of a row at a time, two such every fourth step, into four slots of their own. But for
+// them a step has no branch: behind one the compiler moved products, past the barrier (947 us).
+// Operand reads and the next steps' loads stand between the products.
 //
 // Large products are bound by power: 32768 tokens 4096 -> 11008 with both of 4 bits take 810-890 us
 // by card (3.6-3.3 PFLOP/s), at 1.5 GHz with the matrix cores half busy, and 1.96 GHz with the
@@ -192,18 +192,31 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
   };
   auto issue_x = [&](int m) { lds_dma1(vx[m] - x_cut, xs, xbase + m * kWaves * 1024); };
   auto issue_w = [&](int m) { lds_dma1(vw[m] - w_cut, ws, wbase + m * kWaves * 1024); };
-  // Scales of blocks past b become 0 on either side: whatever numbers the pieces re-read, their
-  // products are below 2^-242 and count nothing. (A NaN among them is in its row already; as it is,
-  // such a scale might be 255.) By the wave that loaded them, once they have landed.
-  auto clear_past = [&](int u) {
-    if (s_begin / 2 + u != super_last) return;
-    const int blocks = (int)(b / kMxBlock) - super_last * 16;
-    for (int at = wave; at < kScaleLoads && blocks < 16; at += kWaves) {
-      unsigned* z = (unsigned*)(sm + scale_slot(u) + at * 1024 + lane * 16);
+  // A load's 64 rows of scales, as they landed 16 bytes (512 k) of a row, are put in the order in
+  // which the products want them, by the wave that loaded them: word 2 s + h of the rows one after
+  // another, of a row the blocks 8 s + h, 2, 4 and 6 further on, that is the scales of half h of the
+  // lanes in the four substeps of step s. (Read as they landed, a word of four blocks at a time,
+  // 32 rows are in 8 banks: LDS is busy for 1.55 cycles where it is for one now. In time that is 1%
+  // with an fp32 Y, and nothing where power is the limit.) Scales of blocks past b become 0 on either
+  // side: whatever numbers the pieces re-read, their products are below 2^-242 and count nothing. (A
+  // NaN among them is in its row already; as it is, such a scale might be 255.)
+  auto arrange = [&](int u) {
+    const int blocks = s_begin / 2 + u == super_last ? (int)(b / kMxBlock) - super_last * 16 : 16;
+    for (int at = wave; at < kScaleLoads; at += kWaves) {
+      unsigned char* chunk = sm + scale_slot(u) + at * 1024;
+      u32x4_t z = *(const u32x4_t*)(chunk + lane * 16);
+      if (blocks < 16) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int left = blocks - 4 * x;  // of this word's four
-        if (left < 4) z[x] = left <= 0 ? 0u : z[x] & (0xffffffffu >> (32 - 8 * left));
+        for (int x = 0; x < 4; ++x) {
+          const int left = blocks - 4 * x;  // of this word's four
+          if (left < 4) z[x] = left <= 0 ? 0u : z[x] & (0xffffffffu >> (32 - 8 * left));
+        }
+      }
+      unsigned* to = (unsigned*)chunk + lane;
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        to[128 * st] = __builtin_amdgcn_perm(z[2 * st + 1], z[2 * st], 0x06040200u);
+        to[128 * st + 64] = __builtin_amdgcn_perm(z[2 * st + 1], z[2 * st], 0x07050301u);
       }
     }
   };
@@ -226,7 +239,7 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
     MxFrag<TH_MX_E2M1> b[FN];
   };
   Frags f0, f1;
-  int sa[2][FM], sb[2][FN];  // scales of the first and the second 128 k of a step
+  int sa[FM], sb[FN], sa_next[FM], sb_next[FN];  // scales of a step; byte x is substep x's
   // operand y of substep sub (64 k): the FN blocks of W, then the FM of X
   auto read_one = [&](int it, int sub, int y, Frags& f) __attribute__((always_inline)) {
     if (y < FN) {
@@ -241,26 +254,27 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
           *(const i32x4_t*)(sm + it % RX * kXStage + (wm * FM + y - FN) * 4096 + (faddr ^ (sub << 5)));
     }
   };
-  // Scales of four blocks of 32 k, as they are; shifted, byte 2 (sub % 2) is substep sub's.
-  auto read_scale = [&](int it, int h, int y) {
-    const unsigned char* p = sm + scale_slot(it / 2) + (it % 2 * 2 + h) * 4;
+  auto read_scale = [&](int it, int y) {
+    const unsigned char* p = sm + scale_slot(it / 2) + it % 2 * 512 + half * 256 + r32 * 4;
+    const int row = y < FN ? TM + (wn * FN + y) * 32 : (wm * FM + y - FN) * 32;
+    const int scale = *(const int*)(p + row / 64 * 1024 + row % 64 * 4);
     if (y < FN)
-      sb[h][y] = *(const int*)(p + (TM + (wn * FN + y) * 32 + r32) * 16);
+      sb_next[y] = scale;
     else
-      sa[h][y - FN] = *(const int*)(p + ((wm * FM + y - FN) * 32 + r32) * 16);
+      sa_next[y - FN] = scale;
   };
-  auto shift_scales = [&](int h) {
+  auto take_scales = [&](int shift) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sa[h][i] = (int)((unsigned)sa[h][i] >> (8 * half));
+    for (int i = 0; i < FM; ++i) sa[i] = (int)((unsigned)sa_next[i] >> shift);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) sb[h][j] = (int)((unsigned)sb[h][j] >> (8 * half));
+    for (int j = 0; j < FN; ++j) sb[j] = (int)((unsigned)sb_next[j] >> shift);
   };
   // One substep's products, with reads and loads between them; the order is pinned.
   auto products = [&](const Frags& f, auto SUB, auto&& between) __attribute__((always_inline)) {
-    constexpr int h = decltype(SUB)::value / 2, byte = decltype(SUB)::value % 2 * 2;
+    constexpr int byte = decltype(SUB)::value;
     auto product = [&](const i32x8_t& x, f32x16_t& to, int i, int j) __attribute__((always_inline)) {
       to = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          x, f.b[j].wide(), to, kMxCode<XT>, kMxCode<TH_MX_E2M1>, byte, sa[h][i], byte, sb[h][j]);
+          x, f.b[j].wide(), to, kMxCode<XT>, kMxCode<TH_MX_E2M1>, byte, sa[i], byte, sb[j]);
       __builtin_amdgcn_sched_barrier(0);
     };
     __builtin_amdgcn_sched_barrier(0);
@@ -296,10 +310,10 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
     for (int y = 0; y < kReads; ++y)
       if (x * kReads + y < FM + FN) read_one(it, sub, x * kReads + y, f);
   };
-  auto scales = [&](int x, int it, int h) __attribute__((always_inline)) {
+  auto scales = [&](int x, int it) __attribute__((always_inline)) {
 #pragma unroll
     for (int y = 0; y < kReads; ++y)
-      if (x * kReads + y < FM + FN) read_scale(it, h, x * kReads + y);
+      if (x * kReads + y < FM + FN) read_scale(it, x * kReads + y);
   };
   auto loads_x = [&](int x) __attribute__((always_inline)) {
     if (x % kGapX == 0) {
@@ -346,13 +360,13 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
       }
     }
     __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((RW - 2) * LW + (RX - 1) * LX * kHalves) : "memory");
-    clear_past(0);
-    clear_past(1);
+    arrange(0);
+    arrange(1);
     __syncthreads();
 #pragma unroll
     for (int y = 0; y < FM + FN; ++y) {
       read_one(0, 0, y, f0);
-      read_scale(0, 0, y);
+      read_scale(0, y);
     }
     // A step of 256 k: four substeps, each reading the next one's operands. Before the last one the
     // next step has landed, and the barrier frees this step's buffers (with 8 bits, another one
@@ -364,10 +378,10 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
         load_scales(it / 2 + 2);
         load_scales(it / 2 + 3);
       } else if (it % 4 == 3) {  // they have landed, and are read from this step's end on
-        clear_past(it / 2 + 1);
-        clear_past(it / 2 + 2);
+        arrange(it / 2 + 1);
+        arrange(it / 2 + 2);
       }
-      shift_scales(0);
+      take_scales(0);
       stage_w(it - 1 + RW);
       products(f0, std::integral_constant<int, 0>{}, [&](int x) __attribute__((always_inline)) {
         reads(x, it, 1, f1);
@@ -380,10 +394,8 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
       }
       products(f1, std::integral_constant<int, 1>{}, [&](int x) __attribute__((always_inline)) {
         reads(x, it, 2, f0);
-        scales(x, it, 1);
         if constexpr (kWide) loads_x(x);
       });
-      shift_scales(1);
       products(f0, std::integral_constant<int, 2>{}, [&](int x) __attribute__((always_inline)) {
         reads(x, it, 3, f1);
       });
@@ -392,7 +404,7 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
       stage_x(it + RX, kHalves - 1);
       products(f1, std::integral_constant<int, 3>{}, [&](int x) __attribute__((always_inline)) {
         reads(x, it + 1, 0, f0);
-        scales(x, it + 1, 0);
+        scales(x, it + 1);
         loads_x(x);
       });
     }
@@ -415,19 +427,16 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
       for (int m = 0; m < LW; ++m) issue_w(m);
     }
     __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((RW - 1) * kStep) : "memory");
-    clear_past(0);
-    clear_past(1);
+    arrange(0);
+    arrange(1);
     __syncthreads();
     auto read_all = [&](int it, int c, Frags& f) __attribute__((always_inline)) {
 #pragma unroll
       for (int y = 0; y < FM + FN; ++y) read_one(it, 2 * kg + c, y, f);
     };
-    auto read_scales = [&](int it) __attribute__((always_inline)) {  // into the second set
-      const unsigned char* p = sm + scale_slot(it / 2) + (it % 2 * 2 + kg) * 4;
+    auto read_scales = [&](int it) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) sb[1][j] = *(const int*)(p + (TM + (wn * FN + j) * 32 + r32) * 16);
-#pragma unroll
-      for (int i = 0; i < FM; ++i) sa[1][i] = *(const int*)(p + ((wm * FM + i) * 32 + r32) * 16);
+      for (int y = 0; y < FM + FN; ++y) read_scale(it, y);
     };
     read_all(0, 0, f0);
     read_scales(0);
@@ -436,14 +445,10 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
         load_scales(it / 2 + 2);
         load_scales(it / 2 + 3);
       } else if (it % 4 == 3) {
-        clear_past(it / 2 + 1);
-        clear_past(it / 2 + 2);
+        arrange(it / 2 + 1);
+        arrange(it / 2 + 2);
       }
-#pragma unroll
-      for (int i = 0; i < FM; ++i) sa[0][i] = sa[1][i];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) sb[0][j] = sb[1][j];
-      shift_scales(0);
+      take_scales(16 * kg);
       read_all(it, 1, f1);
       products(f0, std::integral_constant<int, 0>{}, [](int) {});
       __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((RW - 2) * kStep) : "memory");
