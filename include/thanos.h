@@ -435,8 +435,9 @@ typedef struct {
  * k_len[s]-1. q_start NULL: every sequence has nq / nseq rows. A row whose key is before the
  * sequence's first, or whose page is not in [0, npages), is not stored, nor are rows before
  * q_start[0] and from q_start[nseq] on; start values outside [0, nq] are moved to its ends.
- * Where two rows have one place, either is left there. dt must be TH_BF16; d and alignment as in
- * th_paged_attention, also of K and V. Asynchronous. */
+ * Where two rows have one place (sequences that share a page), each element there is one of
+ * theirs. dt must be TH_BF16; d and alignment as in th_paged_attention, also of K and V.
+ * Asynchronous. */
 th_status th_cache_store(const void* K, int64_t k_token, int64_t k_head, const void* V,
                          int64_t v_token, int64_t v_head, th_dtype dt, int64_t nq,
                          const int32_t* q_start, const th_paged_cache* cache,
@@ -459,14 +460,16 @@ typedef struct {
 /* dt must be TH_BF16; 8 <= d <= 128, d % 8 == 0; hk divides hq; strides are multiples of 8
  * (k_token, v_token < 2^24), all >= 0, and Q, O, k, v 16-byte aligned; nq * hq / hk and
  * width * page_tokens < 2^31 - 2^16, npages < 2^31, nseq < 2^24; row blocks and pieces of
- * keys in one launch < 2^24. O must not overlap the inputs. Precision as in th_attention.
- * The host needs no lengths: how the keys are cut into pieces is found on the device from
- * the real ones, sequences of up to 32 rows (tokens times hq / hk) apart from longer ones,
- * so that batches of unlike sequences keep every compute unit busy, and a captured call
- * follows the lengths of each replay. workspace (optional, may be NULL with
- * workspace_bytes 0; 16-byte aligned) lets the keys be cut; size from
- * th_paged_attention_workspace_size. The order of all sums is fixed by the lengths, so
- * repeated calls give identical bits. Asynchronous. */
+ * keys in one launch < 2^24. O must not overlap the inputs. Precision as in th_attention:
+ * the weights enter the second product as a bf16 value and its rest where the sequences
+ * average no more than 32 rows (tokens times hq / hk), rounded to bf16 where they average
+ * more. With a q_start and nq > 2 nseq, sequences of more than 32 rows are rounded in the
+ * first case too. The host needs no lengths: how the keys are cut into pieces is found on the
+ * device from the real ones, few rows apart from many as above, so that batches of unlike
+ * sequences keep every compute unit busy, and a captured call follows the lengths of each
+ * replay. workspace (optional, may be NULL with workspace_bytes 0; 16-byte aligned) lets the
+ * keys be cut; size from th_paged_attention_workspace_size. The order of all sums is fixed by
+ * the lengths, so repeated calls give identical bits. Asynchronous. */
 th_status th_paged_attention_workspace_size(const th_paged_cache* cache, const th_paged_params* p,
                                             size_t* bytes /* host */);
 th_status th_paged_attention(const void* Q, th_dtype dt, const int32_t* q_start,
