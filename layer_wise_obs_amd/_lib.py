@@ -521,17 +521,18 @@ class MxMatrix:
     [n, b / 2] with element 2i in the low half of byte i) and scales (uint8 [n, b / 32]); a value is
     its element times 2^(scale - 127) of its 32. The scales' rows are a multiple of 16 bytes apart
     where mx_linear is to read them."""
-    __slots__ = ("type", "_elements", "_scales", "_new")
+    __slots__ = ("type", "_elements", "_scales", "_new", "_host")
 
     def __init__(self, type, elements, scales):
         if type not in _MX_TYPES:
             raise ValueError(f"type must be one of {sorted(_MX_TYPES)}, not {type!r}")
-        self.type, self._elements, self._scales, self._new = type, elements, scales, None
+        self.type, self._elements, self._scales = type, elements, scales
+        self._new = self._host = None
 
     @classmethod
     def empty(cls, n, b, type, device):
-        """A new one, both parts in one allocation; the tensors are made when they are asked for
-        (2 us less on the way to a kernel)."""
+        """A new one, both parts in one allocation, with its host struct; the tensors are made when
+        they are asked for (2 us less on the way to a kernel)."""
         torch = _torch()
         if type not in _MX_TYPES:
             raise ValueError(f"type must be one of {sorted(_MX_TYPES)}, not {type!r}")
@@ -541,7 +542,10 @@ class MxMatrix:
         pitch = -(-b // 512) * 16
         m = cls.__new__(cls)
         m.type, m._elements, m._scales = type, None, None
-        m._new = torch.empty(n * (width + pitch), dtype=torch.uint8, device=device), n, b, width, pitch
+        buf = torch.empty(n * (width + pitch), dtype=torch.uint8, device=device)
+        m._new, at = (buf, n, b, width, pitch), buf.data_ptr()
+        # its scales begin 16-byte aligned: rows of 16 bytes and more before them
+        m._host = Mx(at, at + n * width, width, pitch, _MX_TYPES[type])
         return m
 
     @property
@@ -577,12 +581,10 @@ def _mx_index(m) -> int:
 def _mx(index, name, m):
     """(n, b, host struct) of a microscaled matrix on GPU index."""
     if m._new is not None:
-        buf, n, b, width, pitch = m._new
+        buf, n, b, _, _ = m._new
         if buf.get_device() != index:
             raise ValueError(f"{name} must live on GPU {index}")
-        at = buf.data_ptr()
-        # its scales begin 16-byte aligned: rows of 16 bytes and more before them
-        return n, b, Mx(at, at + n * width, width, pitch, _MX_TYPES[m.type])
+        return n, b, m._host
     torch = _torch()
     n, width = m._elements.shape
     b = width if m.type == "e4m3" else 2 * width
