@@ -186,14 +186,26 @@ __device__ __forceinline__ int paged_per(const PagedArgs& a, float tiles, float 
   return (int)fminf(per, 0x1p26f);
 }
 
-// Inclusive sum over the lanes up to this one.
-__device__ __forceinline__ unsigned lanes_scan(unsigned v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const unsigned u = __shfl_up(v, d);
-    v += lane >= d ? u : 0u;
-  }
+// Inclusive sum over the lanes up to this one, of a full wave: within rows of 16 lanes, then the
+// last lane of a row to the next one and of the first half to the second. (Without LDS,
+// which shuffles take: 4 prompts of 2048 tokens 180 -> 175 us, 16 tokens over 1000 keys each 65.8 ->
+// 63.2, one over 300 12.3 -> 12.1.)
+template <class T>
+__device__ __forceinline__ T lanes_scan(T v) {
+  auto moved = [](T v, auto CONTROL, auto ROWS) __attribute__((always_inline)) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(CONTROL)::value,
+                                                             decltype(ROWS)::value, 0xf, false));
+  };
+  v += moved(v, std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xf>{});  // one lane up
+  v += moved(v, std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xf>{});  // two
+  v += moved(v, std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xf>{});
+  v += moved(v, std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xf>{});
+  v += moved(v, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});  // lane 15 of rows 0, 2
+  v += moved(v, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // lane 31
   return v;
+}
+__device__ __forceinline__ float lanes_sum(float v) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lanes_scan(v)), 63));
 }
 
 // Piece `at` of the work: sequences in order, their row blocks, the blocks' pieces; BY_SLOT: of
@@ -236,11 +248,8 @@ __device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, unsigned at,
     }
   }
   if (a.slots) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-      tiles += __shfl_xor(tiles, d);
-      all += __shfl_xor(all, d);
-    }
+    tiles = lanes_sum(tiles);
+    all = lanes_sum(all);
   }
   const int per = paged_per<TILE, FEW>(a, tiles, all);
   unsigned before = 0, cut = 0;  // pieces of the sequences before, and those among them with results
@@ -249,7 +258,7 @@ __device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, unsigned at,
     const unsigned of = (unsigned)(lk + TILE - 1) / TILE;
     const unsigned pieces = blocks ? (of ? (of - 1) / (unsigned)per + 1 : 1u) : 0u;
     const unsigned count = (unsigned)blocks * pieces, part = pieces > 1 ? count : 0u;
-    const unsigned upto = lanes_scan(count, lane), parts = a.slots ? lanes_scan(part, lane) : 0u;
+    const unsigned upto = lanes_scan(count), parts = a.slots ? lanes_scan(part) : 0u;
     const unsigned long long found = __ballot(BY_SLOT ? cut + parts > at : before + upto > at);
     if (found) {
       const int f = __ffsll(found) - 1;
@@ -790,7 +799,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
 // two: the work before a workgroup's first and after its last tile (7 us and more) is beside the
 // other's loads. 64 tokens over 300001 keys in pages, 64 heads on 8: 253-260 us (4.8 TB/s) and 7
 // for the join; one token over 300 keys 12.0, the page numbers' loads before the keys' being the
-// rest to 10.1; 16 tokens over 1000 keys each, 32 heads, 67 where packed keys take 58.
+// rest to 10.1; 16 tokens over 1000 keys each, 32 heads, 63 where packed keys take 54.
 template <int D, int DC, bool PAD, int WAVES, class Args>
 __global__ __launch_bounds__(64 * WAVES, 1) void attention_few_kernel(Args a) {
   constexpr bool kPaged = std::is_same<Args, PagedArgs>::value;
