@@ -460,13 +460,13 @@ typedef struct {
 /* dt must be TH_BF16; 8 <= d <= 128, d % 8 == 0; hk divides hq; strides are multiples of 8
  * (k_token, v_token < 2^24), all >= 0, and Q, O, k, v 16-byte aligned; nq * hq / hk and
  * width * page_tokens < 2^31 - 2^16, npages < 2^31, nseq < 2^24; row blocks and pieces of
- * keys in one launch < 2^24. O must not overlap the inputs. Precision as in th_attention:
- * the weights enter the second product as a bf16 value and its rest where the sequences
- * average no more than 32 rows (tokens times hq / hk), rounded to bf16 where they average
- * more. With a q_start and nq > 2 nseq, sequences of more than 32 rows are rounded in the
- * first case too. The host needs no lengths: how the keys are cut into pieces is found on the
- * device from the real ones, few rows apart from many as above, so that batches of unlike
- * sequences keep every compute unit busy, and a captured call follows the lengths of each
+ * keys in one launch < 2^24. O must not overlap the inputs. Scores, maxima, sums and O
+ * accumulate in fp32; the weights enter the second product as a bf16 value and its rest, also a
+ * bf16 value, so that 2^-16 of a weight is lost whatever the lengths of its sequence and of the
+ * others (th_attention loses 2^-8 where sequences average more than 32 rows). The host needs no
+ * lengths: how the keys are cut into pieces is found on the device from the real ones,
+ * sequences of up to 32 rows (tokens times hq / hk) apart from longer ones, so that batches of
+ * unlike sequences keep every compute unit busy, and a captured call follows the lengths of each
  * replay. workspace (optional, may be NULL with workspace_bytes 0; 16-byte aligned) lets the
  * keys be cut; size from th_paged_attention_workspace_size. The order of all sums is fixed by
  * the lengths, so repeated calls give identical bits. Asynchronous. */

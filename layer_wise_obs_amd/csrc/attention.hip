@@ -10,9 +10,16 @@
 // it moves when a score passes it by more than 8 (p <= 2^8 then), so most tiles
 // need no rescaling. m, l and O are fp32; p is rounded to bf16 for the matrix cores
 // (off by at most 2^-8 of itself, like the output's own rounding: against 64 bits 2.0e-3
-// rms instead of 1.65e-3). Products of what that rounding leaves, 2^-16 of p, too would
-// take 673 -> 1079 us for 16 sequences of 2048 tokens, 32 heads of 128 (92 registers
-// spill), 90 -> 104 for 24 prompts, heads of 80. The kernel for few rows below has them.
+// rms instead of 1.65e-3). Products of what that rounding leaves too would take 673 -> 1079 us
+// for 16 sequences of 2048 tokens, 32 heads of 128 (92 registers spill), 90 -> 104 for 24
+// prompts, heads of 80. The kernel for few rows below has them.
+// Over pages every row has them: p enters as a bf16 value and its rest, also a bf16 value, so that
+// 2^-16 of it is lost and not 2^-8 (error against 64 bits 1.66e-3 rms, the output's own rounding,
+// instead of 2.2e-3), and a row's precision does not hang on the other sequences of its call.
+// Half as many products again: 8 chunks of 4100 tokens over 65600 keys, 32 heads on 8, 636 -> 864 us,
+// 4 prompts of 2048 tokens 177 -> 237, one of 512 tokens over 32768 keys 283 -> 383. The weights
+// are kept in fp32 and made operands 32 keys at a time, the second 32's beside the last products of the
+// first (beside the first ones, 0.5% more): no more registers spill in the loop than without.
 //
 // A workgroup takes 128 rows of one sequence and key head, a row being a (token,
 // query head of the group) pair, so K and V are read once for all g heads and
@@ -636,40 +643,112 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
       for (int kb16 = 0; kb16 < 4; ++kb16)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const bf16x2_t p = pack2(exp2_fast(fmaf(s[kb16][rb][2 * x], a.c, ref)),
-                                   exp2_fast(fmaf(s[kb16][rb][2 * x + 1], a.c, ref)));
-          // the sum takes the rounded weights, which are the ones that V meets
-          l[rb] = __builtin_amdgcn_fdot2_f32_bf16(p, bf16x2_t{(__bf16)1.0f, (__bf16)1.0f}, l[rb],
-                                                  false);
-          pf[kb16 >> 1][rb][(kb16 & 1) * 4 + 2 * x] = p[0];
-          pf[kb16 >> 1][rb][(kb16 & 1) * 4 + 2 * x + 1] = p[1];
+          const float p0 = exp2_fast(fmaf(s[kb16][rb][2 * x], a.c, ref));
+          const float p1 = exp2_fast(fmaf(s[kb16][rb][2 * x + 1], a.c, ref));
+          if constexpr (kPaged) {  // s holds the weights as they are
+            s[kb16][rb][2 * x] = p0;
+            s[kb16][rb][2 * x + 1] = p1;
+            l[rb] += p0 + p1;
+          } else {
+            const bf16x2_t p = pack2(p0, p1);
+            // the sum takes the rounded weights, which are the ones that V meets
+            l[rb] = __builtin_amdgcn_fdot2_f32_bf16(p, bf16x2_t{(__bf16)1.0f, (__bf16)1.0f}, l[rb],
+                                                    false);
+            pf[kb16 >> 1][rb][(kb16 & 1) * 4 + 2 * x] = p[0];
+            pf[kb16 >> 1][rb][(kb16 & 1) * 4 + 2 * x + 1] = p[1];
+          }
         }
     }
+    // Paged: the weights of 32 keys from 32 kc as operands, and what their rounding leaves.
+    [[maybe_unused]] bf16x8_t pr[2][2];
+    [[maybe_unused]] auto operands = [&](int kc, int rb) __attribute__((always_inline)) {
+      u32x4_t wf, wr;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const f32x4_t& w = s[2 * kc + (x >> 1)][rb];
+        const float p0 = w[2 * (x & 1)], p1 = w[2 * (x & 1) + 1];
+        wf[x] = __builtin_bit_cast(unsigned, pack2(p0, p1));
+        wr[x] = __builtin_bit_cast(unsigned, pack2(p0 - __uint_as_float(wf[x] << 16),
+                                                   p1 - __uint_as_float(wf[x] & 0xffff0000u)));
+      }
+      pf[kc][rb] = __builtin_bit_cast(bf16x8_t, wf);
+      pr[kc][rb] = __builtin_bit_cast(bf16x8_t, wr);
+    };
     if constexpr (careful) {
-      if (masked) {
+      // element j % 8 of lanes 16 (j / 8) .. of 32 keys' values alone, and which key that is
+      auto alone = [&](const v8i16_t& v, int j) {
+        v8i16_t one;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) one[x] = quad == j >> 3 && x == (j & 7) ? v[x] : (short)0;
+        return __builtin_bit_cast(bf16x8_t, one);
+      };
+      auto key_of = [&](int kc, int j) { return kt + 32 * kc + 4 * (j >> 3) + (j & 3) + 16 * (j >> 2 & 1); };
+      if constexpr (kPaged) {
+        // first the weights, then their rests, whose products with an infinity are left out
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          auto add = [&](f32x4_t& to, const f32x4_t& z) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[e] += part == 0 || isfinite(z[e]) ? z[e] : 0.f;
+          };
+#pragma unroll
+          for (int kc = 0; kc < 2; ++kc) {
+            bf16x8_t w[2];
+#pragma unroll
+            for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const float p = s[2 * kc + (x >> 2)][rb][x & 3];
+                const __bf16 near = (__bf16)p;
+                w[rb][x] = part == 0 ? near : (__bf16)(p - (float)near);
+              }
+#pragma unroll
+            for (int cb = 0; cb < kCB; ++cb) {
+              const v8i16_t v = v_frag(kc, cb);
+              const f32x4_t zero = {};
+              if (masked) {
+#pragma unroll 1
+                for (int j = 0; j < 32; ++j) {
+                  const bf16x8_t one = alone(v, j);
+#pragma unroll
+                  for (int rb = 0; rb < 2; ++rb) {
+                    const f32x4_t z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one, w[rb], zero, 0, 0, 0);
+                    if (key_of(kc, j) < lim[rb]) add(o[cb][rb], z);
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int rb = 0; rb < 2; ++rb)
+                  add(o[cb][rb], __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                     __builtin_bit_cast(bf16x8_t, v), w[rb], zero, 0, 0, 0));
+              }
+            }
+          }
+        }
+        return;
+      } else if (masked) {
 #pragma unroll
         for (int kc = 0; kc < 2; ++kc)
 #pragma unroll
           for (int cb = 0; cb < kCB; ++cb) {
             const v8i16_t vx = v_frag(kc, cb);
 #pragma unroll 1
-            for (int j = 0; j < 32; ++j) {  // element j % 8 of lanes 16 (j / 8) ..
-              const int jq = j >> 3, jx = j & 7;
-              const int key = kt + 32 * kc + 4 * jq + (jx & 3) + 16 * (jx >> 2);
-              v8i16_t one;
-#pragma unroll
-              for (int x = 0; x < 8; ++x) one[x] = quad == jq && x == jx ? vx[x] : (short)0;
+            for (int j = 0; j < 32; ++j) {
+              const bf16x8_t one = alone(vx, j);
 #pragma unroll
               for (int rb = 0; rb < 2; ++rb) {
                 const f32x4_t zero = {};
-                const f32x4_t z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8_t, one), pf[kc][rb], zero, 0, 0, 0);
-                if (key < lim[rb]) o[cb][rb] += z;
+                const f32x4_t z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one, pf[kc][rb], zero, 0, 0, 0);
+                if (key_of(kc, j) < lim[rb]) o[cb][rb] += z;
               }
             }
           }
         return;
       }
+    }
+    if constexpr (kPaged) {
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb) operands(0, rb);
     }
 #pragma unroll
     for (int kc = 0; kc < 2; ++kc)
@@ -680,8 +759,17 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
         for (int rb = 0; rb < 2; ++rb)
           o[cb][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               __builtin_bit_cast(bf16x8_t, vf[cb]), pf[kc][rb], o[cb][rb], 0, 0, 0);
+        if constexpr (kPaged) {
+#pragma unroll
+          for (int rb = 0; rb < 2; ++rb)
+            o[cb][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8_t, vf[cb]), pr[kc][rb], o[cb][rb], 0, 0, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
         if (kc == 0) vf[cb] = v_frag(1, cb);
+        if constexpr (kPaged) {
+          if (kc == 0 && cb >= kCB - 2) operands(1, cb - (kCB - 2));
+        }
       }
   };
 
@@ -721,7 +809,18 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(Args a) {
     }
   };
   pass(std::integral_constant<bool, false>{});
-  if (__syncthreads_or((bad & 0x80008000u) != 0)) {
+  // Paged: an infinity that a row sees stays one times p, but is NaN times p's rest (0, or of the other
+  // sign): where anything is not finite, the second pass leaves such products of the rests out.
+  float zeros = 0.f;
+  if constexpr (kPaged) {
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+      for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zeros = fmaf(o[cb][rb][e], 0.f, zeros);
+  }
+  if (__syncthreads_or((bad & 0x80008000u) != 0 || zeros != 0.f)) {
     pass(std::integral_constant<bool, true>{});
     __syncthreads();  // a wave that is done puts its rows over tiles that others still read
   }
