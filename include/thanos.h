@@ -298,6 +298,13 @@ th_status th_mx_linear(const th_mx* X, const th_mx* W, int64_t n, int64_t b, int
                        void* Y, th_dtype ydt, int64_t ldy, void* workspace, size_t workspace_bytes,
                        th_stream_t stream);
 
+/* What a product of these sizes runs on (host only): the tokens and channels of a workgroup's
+ * tile and the pieces of its contraction, with the workspace of
+ * th_mx_linear_workspace_size or without one. */
+th_status th_debug_mx_linear_plan(int32_t xtype, int64_t n, int64_t b, int64_t c, th_dtype ydt,
+                                  int32_t workspace, int32_t* tokens, int32_t* channels,
+                                  int32_t* pieces);
+
 /* Root-mean-square norm of the rows of a residual stream, what the q/k/v and the
  * gate/up projections of a block read [BLOG, "The compression target: linear
  * layers"]: Y_tq = X_tq / sqrt(mean_q X_tq^2 + eps) * weight_q. X [n,b] (row pitch

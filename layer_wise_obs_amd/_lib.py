@@ -122,6 +122,7 @@ _SIG = {
     "th_mx_quantize": [_P, _I32, _I64, _I64, _I64, ctypes.POINTER(Mx), _P],
     "th_mx_dequantize": [ctypes.POINTER(Mx), _I64, _I64, _P, _I32, _I64, _P],
     "th_mx_linear_workspace_size": [_I32, _I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_size_t)],
+    "th_debug_mx_linear_plan": [_I32, _I64, _I64, _I64, _I32, _I32] + [ctypes.POINTER(_I32)] * 3,
     "th_mx_linear": [ctypes.POINTER(Mx), ctypes.POINTER(Mx), _I64, _I64, _I64, _P, _I32, _P, _I64, _P,
                      _I32, _I64, _P, ctypes.c_size_t, _P],
     "th_add_rms_norm": [_P, _I64, _P, _I64, _I32, _I64, _I64, _P, ctypes.c_double, _P, _I64, _P, _I32,
@@ -634,6 +635,16 @@ def mx_linear_workspace_size(type: str, n: int, b: int, c: int, out_dtype) -> in
                                              TH_F32 if out_dtype == torch.float32 else TH_BF16,
                                              ctypes.byref(out)))
     return out.value
+
+
+def debug_mx_linear_plan(type: str, n: int, b: int, c: int, out_dtype, ws=True):
+    """(tokens, channels, pieces): the tile of a workgroup and the pieces of the contraction that a
+    product of these sizes runs on, with a workspace or without one."""
+    out = [_I32(0) for _ in range(3)]
+    _check(lib().th_debug_mx_linear_plan(_MX_TYPES[type], n, b, c,
+                                         TH_F32 if out_dtype == _torch().float32 else TH_BF16,
+                                         1 if ws else 0, *(ctypes.byref(v) for v in out)))
+    return tuple(v.value for v in out)
 
 
 def mx_linear(X, W, bias=None, act="none", residual=None, Y=None, out_dtype=None, ws=None):

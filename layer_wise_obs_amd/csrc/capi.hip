@@ -963,6 +963,17 @@ th_status th_mx_linear_workspace_size(int32_t xtype, int64_t n, int64_t b, int64
   return TH_OK;
 }
 
+th_status th_debug_mx_linear_plan(int32_t xtype, int64_t n, int64_t b, int64_t c, th_dtype ydt,
+                                  int32_t workspace, int32_t* tokens, int32_t* channels,
+                                  int32_t* pieces) {
+  size_t bytes;
+  th_status st = th_mx_linear_workspace_size(xtype, n, b, c, ydt, &bytes);
+  if (st != TH_OK) return st;
+  if (!tokens || !channels || !pieces || n == 0) return fail(TH_ERR_INVALID_ARG, "bad arguments");
+  mx_linear_plan(xtype, n, b, c, ydt, workspace != 0, tokens, channels, pieces);
+  return TH_OK;
+}
+
 th_status th_mx_linear(const th_mx* X, const th_mx* W, int64_t n, int64_t b, int64_t c,
                        const void* bias, th_activation act, const void* residual, int64_t ldr,
                        void* Y, th_dtype ydt, int64_t ldy, void* workspace, size_t workspace_bytes,

@@ -260,6 +260,9 @@ hipError_t launch_mx_dequantize(const th_mx& x, int64_t n, int64_t b, void* Y, t
 // mx_linear.hip
 // workspace (floats) of the split contraction: 0 where it does not help
 size_t mx_linear_workspace_floats(int xtype, int64_t n, int64_t b, int64_t c, th_dtype ydt);
+// tile (tokens x channels) and pieces of the contraction
+void mx_linear_plan(int xtype, int64_t n, int64_t b, int64_t c, th_dtype ydt, bool can_split,
+                    int32_t* tokens, int32_t* channels, int32_t* pieces);
 hipError_t launch_mx_linear(const th_mx& X, const th_mx& W, int64_t n, int64_t b, int64_t c,
                             const unsigned short* bias, int act, const void* residual, int64_t ldr,
                             void* Y, th_dtype ydt, int64_t ldy, float* part, hipStream_t s);

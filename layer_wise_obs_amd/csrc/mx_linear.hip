@@ -703,6 +703,14 @@ size_t mx_linear_workspace_floats(int xtype, int64_t n, int64_t b, int64_t c, th
   return p.splits > 1 ? (size_t)p.splits * (size_t)n * (size_t)(cdiv(c, 8) * 8) : 0;
 }
 
+void mx_linear_plan(int xtype, int64_t n, int64_t b, int64_t c, th_dtype ydt, bool can_split,
+                    int32_t* tokens, int32_t* channels, int32_t* pieces) {
+  const MxPlan p = plan_of(xtype, n, b, c, ydt == TH_F32, can_split);
+  *tokens = p.tile == kMxSkinny ? (int32_t)kMxSkinnyTokens : kMxForms[p.tile].tm;
+  *channels = p.tile == kMxSkinny ? 16 : kMxForms[p.tile].tn;
+  *pieces = p.splits;
+}
+
 hipError_t launch_mx_linear(const th_mx& X, const th_mx& W, int64_t n, int64_t b, int64_t c,
                             const unsigned short* bias, int act, const void* residual, int64_t ldr,
                             void* Y, th_dtype ydt, int64_t ldy, float* part, hipStream_t s) {
