@@ -445,7 +445,7 @@ hipError_t launch_linear(const unsigned short* X, int64_t ldx, const unsigned sh
   }
   if (e != hipSuccess || !raw) return e;
   const int64_t items = n * cdiv(c, 8);
-  hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)cdiv(items, 256)), dim3(256), 0, s, raw,
+  hipLaunchKernelGGL(linear_join_kernel<false>, dim3((unsigned)cdiv(items, 256)), dim3(256), 0, s, raw,
                      p.splits, n, c, ep);
   return hipGetLastError();
 }

@@ -54,21 +54,52 @@ __device__ __forceinline__ float activate(float z, int act) {
   }
 }
 
-// z / (1 + e^-z) to 2 units and |z| 2^-23 of itself, for outputs that are rounded to bf16: a
-// division and expf would take five times as long.
-__device__ __forceinline__ float silu_near(float z) {
-  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+// z / (1 + e^-z) behind products of microscaled operands, by the value alone, whichever kernel forms
+// it. From z = -88.7 on e^-z passes fp32's range, where the result, -2.4e-37 there, is still one of
+// either type: below kSiluFar it is z e^z, e^z by its root, which is a normal number. NEAR, for outputs
+// that are rounded to bf16: to 4 units and |z| 2^-23 of itself, by the hardware's exponential and
+// reciprocal (a division and expf would take five times as long).
+constexpr float kSiluFar = -87.0f;
+template <bool NEAR>
+__device__ __forceinline__ float silu_near_zero(float z) {
+  return NEAR ? z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f))
+              : activate(z, TH_ACT_SILU);
+}
+__device__ __forceinline__ float silu_far(float z) {
+  const float e = expf(0.5f * z);
+  return z * e * e;
+}
+// The activation of a product of microscaled operands, F32: with an fp32 Y.
+template <bool F32>
+__device__ __forceinline__ float activate_mx(float z, int act) {
+  if (act != TH_ACT_SILU) return activate(z, act);
+  return z < kSiluFar ? silu_far(z) : silu_near_zero<!F32>(z);
 }
 
 // All of v, one decision for them.
-template <bool NEAR = false>
+template <bool MX, bool F32>
 __device__ __forceinline__ void activate8(float (&v)[8], int act) {
   if (act == TH_ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_RELU);
   } else if (act == TH_ACT_SILU) {
+    if constexpr (MX) {  // far ones are rare
+      float least = v[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = NEAR ? silu_near(v[i]) : activate(v[i], TH_ACT_SILU);
+      for (int i = 1; i < 8; ++i) least = fminf(least, v[i]);
+      if (__any(least < kSiluFar)) {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const float z = v[0], y = activate_mx<F32>(z, TH_ACT_SILU);
+#pragma unroll
+          for (int x = 0; x < 7; ++x) v[x] = v[x + 1];
+          v[7] = y;
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = MX ? silu_near_zero<!F32>(v[i]) : activate(v[i], TH_ACT_SILU);
   } else if (act == TH_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = activate(v[i], TH_ACT_GELU);
@@ -86,9 +117,14 @@ __device__ __forceinline__ void put1(float v, int64_t t, int64_t q, const LinEpi
   }
 }
 // Channel q of token t.
+template <bool MX = false>
 __device__ __forceinline__ void finish1(float v, int64_t t, int64_t q, const LinEpilogue& ep) {
   if (ep.bias) v += bf16_to_f32(ep.bias[q]);
-  put1(activate(v, ep.act), t, q, ep);
+  if constexpr (MX)
+    v = ep.y_f32 ? activate_mx<true>(v, ep.act) : activate_mx<false>(v, ep.act);
+  else
+    v = activate(v, ep.act);
+  put1(v, t, q, ep);
 }
 
 // Residuals of eight consecutive channels as they are in memory, and their sum with v
@@ -181,7 +217,7 @@ __device__ __forceinline__ void finish_tile(const LinEpilogue& ep, int64_t n, in
 #pragma unroll
               for (int x = 0; x < 8; ++x) v[x] += bias[x];
             }
-            activate8<MX && !f32>(v, ep.act);
+            activate8<MX, f32>(v, ep.act);
 #pragma unroll
             for (int x = 0; x < 8; ++x) at[x] = v[x];
           }
@@ -214,7 +250,8 @@ __device__ __forceinline__ void finish_tile(const LinEpilogue& ep, int64_t n, in
 
 // Sum of the splits' raw products in order, then the epilogue: 8 channels per thread,
 // those of a row's end one by one.
-static __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restrict__ part, int splits,
+template <bool MX>
+__global__ __launch_bounds__(256) void linear_join_kernel(const float* __restrict__ part, int splits,
                                                           int64_t n, int64_t c, LinEpilogue ep) {
   const int64_t per_row = cdiv(c, 8), cp = per_row * 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -235,7 +272,10 @@ static __global__ __launch_bounds__(256) void linear_join_kernel(const float* __
 #pragma unroll
     for (int x = 0; x < 8; ++x) v[x] += q + x < c ? bf16_to_f32(ep.bias[q + x]) : 0.f;
   }
-  activate8(v, ep.act);
+  if (ep.y_f32)
+    activate8<MX, true>(v, ep.act);
+  else
+    activate8<MX, false>(v, ep.act);
   if (q + 8 > c) {
 #pragma unroll
     for (int x = 0; x < 8; ++x)

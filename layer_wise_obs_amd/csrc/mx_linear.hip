@@ -610,7 +610,7 @@ __global__ __launch_bounds__(64 * kMsWaves) void mx_skinny_kernel(MxOperand X, M
     float v = red[0][t][q];
 #pragma unroll
     for (int w = 1; w < kMsWaves; ++w) v += red[w][t][q];
-    finish1(v, t, f0 + q, ep);
+    finish1<true>(v, t, f0 + q, ep);
   }
 }
 
@@ -748,7 +748,7 @@ hipError_t launch_mx_linear(const th_mx& X, const th_mx& W, int64_t n, int64_t b
                             : launch_form<TH_MX_E4M3, false>(x, w, n, b, c, p, raw, ep, s);
   if (e != hipSuccess || !raw) return e;
   const int64_t items = n * cdiv(c, 8);
-  hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)cdiv(items, 256)), dim3(256), 0, s, raw,
+  hipLaunchKernelGGL(linear_join_kernel<true>, dim3((unsigned)cdiv(items, 256)), dim3(256), 0, s, raw,
                      p.splits, n, c, ep);
   return hipGetLastError();
 }
