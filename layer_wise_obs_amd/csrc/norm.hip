@@ -287,7 +287,9 @@ __global__ __launch_bounds__(256) void add_rms_norm_kernel(const TI* X, int64_t 
   const double scale = 1.0 / sqrt(row_sum<W>(s, red) / (double)b + eps);
   // The products in fp32 are off by less than four units of their last place. Only where one
   // lies that near to a place where roundings to the output's type meet, or scales do (its last
-  // 16 bits tell: 1 in 7000), does fp64 have to decide: the wave then forms its eight again.
+  // 16 bits tell: 1 in 7000), does fp64 have to decide: the wave then forms its eight again. So it
+  // does where an element over the root is no normal number, or 0: its last places are lost, and a
+  // large weight would make them count.
   const float near = (float)scale;
   const bool far = !(near > 0x1p-100f && near < 0x1p100f);
   auto put = [&](const H& h, int64_t q) {
@@ -301,12 +303,15 @@ __global__ __launch_bounds__(256) void add_rms_norm_kernel(const TI* X, int64_t 
       return;
     }
     unsigned least = 0xffffffffu;
+    float small = 1.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      v.v[e] = h.at(e) * near * g.at(e);
+      const float x = h.at(e) * near;
+      small = fminf(small, fabsf(x));
+      v.v[e] = x * g.at(e);
       least = min(least, (__float_as_uint(v.v[e]) + (OUT == -1 ? 0x8004u : 4u)) << 16);
     }
-    if (__any(least <= 8u << 16 || far)) {
+    if (__any(least <= 8u << 16 || small < 0x1p-126f || far)) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v.v[e] = to_odd((double)h.at(e) * scale * (double)g.at(e));
     }
