@@ -521,7 +521,8 @@ class MxMatrix:
     """A microscaled matrix [n, b]: its type ("e4m3" or "e2m1"), elements (uint8 [n, b], or
     [n, b / 2] with element 2i in the low half of byte i) and scales (uint8 [n, b / 32]); a value is
     its element times 2^(scale - 127) of its 32. The scales' rows are a multiple of 16 bytes apart
-    where mx_linear is to read them."""
+    where mx_linear is to read them, and their memory holds the last (or only) row up to the next
+    multiple of 16 too."""
     __slots__ = ("type", "_elements", "_scales", "_new", "_host")
 
     def __init__(self, type, elements, scales):
@@ -579,8 +580,9 @@ def _mx_index(m) -> int:
     return _device_index(m._elements if m._new is None else m._new[0])
 
 
-def _mx(index, name, m):
-    """(n, b, host struct) of a microscaled matrix on GPU index."""
+def _mx(index, name, m, product=False):
+    """(n, b, host struct) of a microscaled matrix on GPU index; a product reads its rows of scales
+    up to the next multiple of 16 bytes, the last one's too."""
     if m._new is not None:
         buf, n, b, _, _ = m._new
         if buf.get_device() != index:
@@ -593,6 +595,10 @@ def _mx(index, name, m):
     s = _require(index, name + ".scales", m._scales, (n, b // 32), torch.uint8)[0]
     if n == 1:  # a single row's pitches, which no access uses: multiples of 16 that hold it
         e, s = -(-width // 16) * 16, -(-b // 512) * 16
+    if product and b % 512 and n:
+        t, row = m._scales, -(-b // 512) * 16
+        if t.storage_offset() + (n - 1) * t.stride(0) + row > t.untyped_storage().nbytes():
+            raise ValueError(f"{name}.scales must have memory for {row} bytes of the last row")
     return n, b, Mx(m._elements.data_ptr(), m._scales.data_ptr(), e, s, _MX_TYPES[m.type])
 
 
@@ -653,8 +659,8 @@ def mx_linear(X, W, bias=None, act="none", residual=None, Y=None, out_dtype=None
     residual's or bf16). Y may be the residual. Forward only."""
     torch = _torch()
     index = _mx_index(X)
-    n, b, x = _mx(index, "X", X)
-    c, bw, w = _mx(index, "W", W)
+    n, b, x = _mx(index, "X", X, True)
+    c, bw, w = _mx(index, "W", W, True)
     if bw != b:
         raise ValueError(f"W must have {b} columns, not {bw}")
     if out_dtype is None:
