@@ -140,7 +140,6 @@ __device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, int64_t slot,
 
 // ---------------------------------------------------------------- paged: the work
 
-constexpr float kAShare = 1.0f, kALeast = 10.0f;
 constexpr int kAFewRows = 32;  // rows of a sequence that the few-rows kernel takes in one block
 
 struct PagedWork {
@@ -175,9 +174,9 @@ __device__ __forceinline__ void paged_sequence(const PagedArgs& a, int64_t s, in
 // want no fewer.) Few rows: pieces of 320 keys at least; (row block, key head) pairs that leave
 // room are cut into as many pieces as run at a time, one short piece each counted; more pairs into
 // twice as many, which evens out their lengths; so many that they even out by themselves, where
-// one is longer than a workgroup's share. Others: pieces of a share, or two where the row blocks
-// fill the units. (Shares of a half, a third and a fifth of these were slower over the sequences
-// tried: 64 tokens over 300001 keys, chunks of 4100 tokens over 40000, 256 tokens over 1000 each.)
+// one is longer than a workgroup's share. Others: pieces of a workgroup's share, three tiles at least.
+// (Shares of a half, a third and a fifth of these were slower over the sequences tried: 64 tokens
+// over 300001 keys, chunks of 4100 tokens over 40000, 256 tokens over 1000 each.)
 template <int TILE, bool FEW>
 __device__ __forceinline__ int paged_per(const PagedArgs& a, float tiles, float blocks) {
   if (a.slots == 0) return 1 << 26;  // more than any sequence has
@@ -187,8 +186,7 @@ __device__ __forceinline__ int paged_per(const PagedArgs& a, float tiles, float 
     const float at_once = pairs <= kAUnits ? 2 * kAUnits - pairs : (pairs < 6 * kAUnits ? 4 * kAUnits : 2 * kAUnits);
     per = fmaxf(ceilf(work / at_once * (1.0f + 0x1p-20f)), 320 / TILE);
   } else {
-    const float share = work * (0.5f / kAUnits);
-    per = fmaxf(ceilf(fmaxf(share * kAShare, fminf(share, kALeast))), 3.0f);
+    per = fmaxf(ceilf(work * (0.5f / kAUnits)), 3.0f);
   }
   return (int)fminf(per, 0x1p26f);
 }
@@ -230,7 +228,10 @@ __device__ __forceinline__ PagedWork paged_work(const PagedArgs& a, unsigned at,
     who = lane;
     if (!FEW && a.nseq > 1 && a.nseq <= 64) {
       // the ones with most keys first: a long piece that begins last keeps the others waiting
-      // (chunks of 4100 tokens, 708 -> 652 us; few rows have pieces that are alike)
+      // (chunks of 4100 tokens with weights in one part, 708 -> 652 us; few rows have pieces that are
+      // alike). More than 64 are taken as they come: a lane has room for one, and batches that large
+      // gain little (called longest first: 65 chunks over 168447 keys, 32 heads on 8, 1671 -> 1632 us, 80
+      // over 272687 3516 -> 3456, 120 over 390515 5104 -> 4933).
       const int all = a.nseq;
       int rank = 0;
       for (int j = 0; j < all; ++j) {
@@ -1632,7 +1633,7 @@ PagedPlan plan_of(const th_paged_cache* c, const th_paged_params* p) {
   if (r.few) bound(r.many ? seqs : rows / 32 + seqs, 4 * kAUnits, 320, r.few_items, r.few_slots);
   if (r.many) {
     const int64_t longer = r.few ? std::min(seqs, rows / (kAFewRows + 1)) : seqs;
-    bound(rows / 128 + longer, (int64_t)(2 * kAUnits / kAShare), 3 * kAKT, r.many_items, r.many_slots);
+    bound(rows / 128 + longer, 2 * kAUnits, 3 * kAKT, r.many_items, r.many_slots);
   }
   return r;
 }
