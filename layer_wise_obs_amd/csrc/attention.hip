@@ -19,7 +19,8 @@
 // Half as many products again: 8 chunks of 4100 tokens over 65600 keys, 32 heads on 8, 636 -> 864 us,
 // 4 prompts of 2048 tokens 177 -> 237, one of 512 tokens over 32768 keys 283 -> 383. The weights
 // are kept in fp32 and made operands 32 keys at a time, the second 32's beside the last products of the
-// first (beside the first ones, 0.5% more): no more registers spill in the loop than without.
+// first (beside the first ones, 0.5% more): for heads of 128 the loop over the tiles then spills m's
+// two registers where they move, and three addresses for the last tile.
 //
 // A workgroup takes 128 rows of one sequence and key head, a row being a (token,
 // query head of the group) pair, so K and V are read once for all g heads and

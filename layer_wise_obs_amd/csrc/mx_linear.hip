@@ -547,7 +547,9 @@ __global__ __launch_bounds__(64 * GM * GN * KS, 1) void mx_tile_kernel(MxOperand
 // scales 16 bytes (512 k) of a channel at a time; X comes from L2, in two parts where it is of
 // e4m3. The waves' sums meet in LDS and are added in the order of the waves. Workgroup x takes
 // the channels from 16 (first + x). One token 4096 -> 4096: 4.8-5.1 us, of which its 9 MB take
-// 1.5; the rest is the launch and one chain of loads, products and joins.
+// 1.5; the rest is the launch and one chain of loads, products and joins. Longer contractions are
+// several turns of 512 k in series: one token 11008 -> 4096 8.1-8.3, 4096 -> 11008 8.9 (their bytes 4.0),
+// 16 tokens 12.2 and 12.7 (e2m1 X: 6.5 and 7.0, 8.5 and 9.6).
 constexpr int kMsWaves = 8;
 
 template <int XT>
@@ -722,7 +724,9 @@ hipError_t launch_mx_linear(const th_mx& X, const th_mx& W, int64_t n, int64_t b
   ep.ldy = ldy;
   ep.act = act;
   ep.y_f32 = ydt == TH_F32;
-  // (32768 tokens 4096 -> 11008, a Y of 721 MB: 835 -> 810 us; 67 MB: the same)
+  // bf16 Y of 2^27 and more outputs, 268 MB: the last level cache holds 256 MB. Past the caches and
+  // through them, tokens 4096 -> 11008: 12192 tokens 327 and 334 us, 32768 806 and 810 (another card 810
+  // and 835), 65536 1568 and 1582; below, 4096 to 16384 tokens, the same to 0.3%. An fp32 Y has no such form.
   ep.past_cache = n * c >= (int64_t)1 << 27;
   const MxOperand x = {(const unsigned char*)X.elements, (const unsigned char*)X.scales, X.ld, X.lds};
   const MxOperand w = {(const unsigned char*)W.elements, (const unsigned char*)W.scales, W.ld, W.lds};

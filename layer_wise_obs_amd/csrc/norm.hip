@@ -13,13 +13,15 @@
 // With the addition of the residual before it, h = x + r rounded to the stream's type, and an
 // output that may be microscaled (mx.h), what a product of 8- or 4-bit operands reads: the
 // second kernel. There sums, root and products are in 64 bits, so that y is rounded once, from
-// a value off by less than 2^-48 of itself: where it lies next to a border between two
+// a value off by (b / (2 T) + 20) 2^-53 of itself at most, T lanes to a row (64 up to 2048 columns, else
+// 256: 2^-48.2 at 4096, 2^-46.7 at 28672): where it lies next to a border between two
 // elements, or the block's largest next to one between two scales, fp32's error of 2^-23
 // decides for a step of 2^-4. Five 64-bit operations an element against 7 bytes are more than the
 // vector units have time for, so only the sum is in 64 bits everywhere; a wave's products are in
 // fp32, and again in 64 bits where one of them lies within 4 units of fp32 of a border. 65536 rows
 // of 4096 with the residual, bf16 to 8 bits: 532 -> 345-359 us by card (5.3 TB/s; a copy of 4 GiB
-// 4.7-4.9); 7 rows of 4096 from fp32 4.5, a launch's time.
+// 4.7-4.9); 7 rows of 4096 from fp32 4.5, of which a launch is 2.3 and the 64-bit sum's way over the
+// lanes 1 (rms_norm: 3.5).
 #include "common.h"
 #include "mx.h"
 #include "row8.h"
