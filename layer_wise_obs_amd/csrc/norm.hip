@@ -290,8 +290,8 @@ __global__ __launch_bounds__(256) void add_rms_norm_kernel(const TI* X, int64_t 
   // The products in fp32 are off by less than four units of their last place. Only where one
   // lies that near to a place where roundings to the output's type meet, or scales do (its last
   // 16 bits tell: 1 in 7000), does fp64 have to decide: the wave then forms its eight again. So it
-  // does where an element over the root is no normal number, or 0: its last places are lost, and a
-  // large weight would make them count.
+  // does where an element over the root is no normal number, or 0, beside a weight above 4: the places
+  // that are lost, 2^-150, would then count (weights up to 4 keep them below 4 units of any result).
   const float near = (float)scale;
   const bool far = !(near > 0x1p-100f && near < 0x1p100f);
   auto put = [&](const H& h, int64_t q) {
@@ -305,15 +305,16 @@ __global__ __launch_bounds__(256) void add_rms_norm_kernel(const TI* X, int64_t 
       return;
     }
     unsigned least = 0xffffffffu;
-    float small = 1.0f;
+    float small = 1.0f, large = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float x = h.at(e) * near;
       small = fminf(small, fabsf(x));
+      large = fmaxf(large, fabsf(g.at(e)));
       v.v[e] = x * g.at(e);
       least = min(least, (__float_as_uint(v.v[e]) + (OUT == -1 ? 0x8004u : 4u)) << 16);
     }
-    if (__any(least <= 8u << 16 || small < 0x1p-126f || far)) {
+    if (__any(least <= 8u << 16 || (small < 0x1p-126f && large > 4.0f) || far)) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v.v[e] = to_odd((double)h.at(e) * scale * (double)g.at(e));
     }
