@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from layer_wise_obs_amd import _lib as L
-from tests.test_gpu_mx import BF, DEV, F32, _check_product, _randn, _values
+from tests.test_gpu_mx import BF, DEV, F32, _check_product, _random_mx, _randn, _values
 from tests.test_mx_plan import JOINED, PAST_CACHE, WHOLE, WHOLE_K
 
 pytestmark = pytest.mark.gpu
@@ -45,6 +45,26 @@ def test_tiles_keep_blocks_of_no_numbers_in_their_rows_and_channels(tile, form):
     want[[2, n - 1]], want[:, [77, c - 1]] = True, True
     for ydt in (BF, F32):
         assert torch.equal(L.mx_linear(X, W, out_dtype=ydt).isnan().cpu(), want)
+
+
+@pytest.mark.parametrize("tile", list(WHOLE))
+@pytest.mark.parametrize("form", ["e4m3", "e2m1"])
+def test_scales_of_the_whole_range(tile, form):
+    """Blocks of X with scales from 2^-127 to 2^127, those of W the other way round up to 2^3: either
+    side's values may be past fp32's range, their products are not."""
+    n, c = WHOLE[tile]
+    b = 1056
+    print(f"[case] mx tile {tile} scales {form}", flush=True)
+    X, W = _random_mx(n, b, form, n), _random_mx(c, b, "e2m1", c)
+    g = np.random.default_rng(1)
+    scales = g.integers(0, 255, b // 32)
+    scales[:8] = 0, 1, 2, 3, 251, 252, 253, 254
+    other = np.clip(254 - scales + g.integers(-3, 4, b // 32), 0, 254)
+    X.scales.copy_(torch.from_numpy(np.tile(scales.astype(np.uint8), (n, 1))))
+    W.scales.copy_(torch.from_numpy(np.tile(other.astype(np.uint8), (c, 1))))
+    v = _values(X), _values(W)
+    for ydt in (BF, F32):
+        _check_product(L.mx_linear(X, W, out_dtype=ydt), X, W, None, "none", None, v)
 
 
 def _epilogues(n, b, c, form, act, pad):
